@@ -424,6 +424,101 @@ fno_status_t fno_model2d_set_graph(fno_model2d_t model, int on);
 /* Free the model (synchronises its device). NULL is a no-op. */
 fno_status_t fno_model2d_destroy(fno_model2d_t model);
 
+/* ---- training operators around a block ------------------------------------
+ * What a training step needs next to the layer and the channel mix: fields
+ * kept in 8 bits between forward and backward, and the norms before and after
+ * a block fused with its gate and residual scale. Arrays are contiguous, in
+ * `dtype`, on the current device; fields 16-byte aligned, parameters to their
+ * element; an output overlaps no other argument. Asynchronous on `stream`;
+ * nothing is allocated; results do not change from run to run. Argument
+ * errors are found on the host before any HIP call.
+ *
+ * 8-bit checkpoints. A field is rows of n contiguous values, each row cut into
+ * blocks of 32 (the last may be short). With M a block's largest magnitude its
+ * exponent is e = max(floor(log2 M) - 6, low), low = -24 for FNO_F16, else
+ * -126 (e = low where M = 0), and a value x is kept as
+ *   q = rint(x 2^-e) (ties to even), clamped to [-127, 127],
+ * so it reads back as q 2^e, off by at most M / 64 (half of 2^e unless the
+ * clamp acts), exactly representable in the storage type. A block holding an
+ * infinity or a NaN has e = 127 and reads back as NaN throughout.
+ * Layout: int8 codes [rows][32 nb], nb = ceil(n / 32), zero past n; then, from
+ * the next multiple of 256 bytes, int8 exponents [rows][nb]; the whole rounded
+ * up to 256 bytes (fno_checkpoint_bytes: n + n / 32 bytes a row, roughly).
+ * saved is 256-byte aligned. n <= 2^31, rows * n <= 2^40, else UNSUPPORTED. */
+fno_status_t fno_checkpoint_bytes(long rows, long n, size_t *bytes);
+fno_status_t fno_checkpoint_pack(const void *x, void *saved, long rows, long n,
+                                 fno_dtype_t dtype, void *stream);
+fno_status_t fno_checkpoint_unpack(const void *saved, void *y, long rows,
+                                   long n, fno_dtype_t dtype, void *stream);
+
+/* Norms after and before a block, with its gate and residual scale, over the
+ * channel axis of fields [batch][channels][pixels] (pixels = 1: tokens):
+ *   y = x + scale[c] gate[b][c] N_post(v),   u = N_pre(y),
+ *   N(h)[c] = (h[c] - m) / sqrt(mean_c((h - m)^2) + eps) w[c] + b[c],
+ * m = mean_c(h) for FNO_NORM_LAYER, 0 for FNO_NORM_RMS. x is the residual
+ * stream, v the block's output, u the next block's input. Sums and statistics
+ * in fp32; y's statistics are those of y before it is rounded.
+ * Every parameter may be NULL: w, gate and scale are then 1, b is 0. */
+typedef enum { FNO_NORM_RMS = 0, FNO_NORM_LAYER = 1 } fno_norm_kind_t;
+typedef struct {
+  int kind;            /* fno_norm_kind_t */
+  float eps;           /* a positive normal number */
+  const void *w_post;  /* [channels] */
+  const void *b_post;  /* [channels] */
+  const void *gate;    /* [batch][channels] */
+  const void *scale;   /* [channels] */
+  const void *w_pre;   /* [channels] */
+  const void *b_pre;   /* [channels] */
+} fno_norm_params_t;
+
+/* Where the gradients of the parameters go (shapes and dtype as the
+ * parameters'); NULL: not wanted. */
+typedef struct {
+  void *w_post, *b_post, *gate, *scale, *w_pre, *b_pre;
+} fno_norm_grads_t;
+
+/* u may be NULL (no norm follows). channels <= 512 (pixels > 1) or <= 8192
+ * (pixels = 1), batch <= 65535 where pixels > 1, else UNSUPPORTED.
+ * fno_norm_residual_save also leaves the 8-bit checkpoints of x and then of v
+ * in `saved` (fno_norm_residual_saved_bytes, 256-byte aligned), rows along
+ * the contiguous axis: [batch * channels][pixels], tokens [batch][channels]. */
+fno_status_t fno_norm_residual(const fno_norm_params_t *params, const void *x,
+                               const void *v, void *y, void *u, int batch,
+                               int channels, long pixels, fno_dtype_t dtype,
+                               void *stream);
+fno_status_t fno_norm_residual_saved_bytes(int batch, int channels,
+                                           long pixels, size_t *bytes);
+fno_status_t fno_norm_residual_save(const fno_norm_params_t *params,
+                                    const void *x, const void *v, void *y,
+                                    void *u, void *saved, int batch,
+                                    int channels, long pixels,
+                                    fno_dtype_t dtype, void *stream);
+
+/* Gradients at gy = dL/dy and gu = dL/du (NULL: none flows through u; the
+ * gradients of w_pre and b_pre must then be NULL): gx = dL/dx and gv = dL/dv
+ * (either may be NULL) and those of the parameters named in grads (NULL: none).
+ * The saved form reads x and v back from their checkpoints and is the gradient
+ * at those values. workspace: fno_norm_residual_workspace_bytes bytes, 16-byte
+ * aligned, needed when a parameter gradient is wanted; its contents do not
+ * matter before or after. INVALID_ARG also when nothing is wanted or a gradient
+ * is wanted of a parameter that is NULL. */
+fno_status_t fno_norm_residual_workspace_bytes(int batch, int channels,
+                                               long pixels, fno_dtype_t dtype,
+                                               size_t *bytes);
+fno_status_t fno_norm_residual_backward(const fno_norm_params_t *params,
+                                        const void *x, const void *v,
+                                        const void *gy, const void *gu,
+                                        void *gx, void *gv,
+                                        const fno_norm_grads_t *grads,
+                                        void *workspace, int batch,
+                                        int channels, long pixels,
+                                        fno_dtype_t dtype, void *stream);
+fno_status_t fno_norm_residual_backward_saved(
+    const fno_norm_params_t *params, const void *saved, const void *gy,
+    const void *gu, void *gx, void *gv, const fno_norm_grads_t *grads,
+    void *workspace, int batch, int channels, long pixels, fno_dtype_t dtype,
+    void *stream);
+
 #ifdef __cplusplus
 }
 #endif

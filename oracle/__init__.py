@@ -38,3 +38,4 @@ from .spectral import (  # noqa: F401
 )
 from .fno2d import fno2d_forward, fno_block2d, gelu  # noqa: F401
 from .backward import spectral_conv2d_backward, spectral_conv3d_backward  # noqa: F401
+from . import training  # noqa: F401

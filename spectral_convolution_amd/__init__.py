@@ -9,6 +9,11 @@ if libfno.so is missing, importing a function that needs it raises.
 import ctypes
 
 from ._lib import DTYPES, FnoError, check, lib  # noqa: F401
+from ._training import (  # noqa: F401
+    NormGrads, NormParams, fno_checkpoint_bytes, fno_checkpoint_empty, fno_checkpoint_pack, fno_checkpoint_unpack,
+    fno_norm_residual, fno_norm_residual_backward, fno_norm_residual_backward_saved, fno_norm_residual_save,
+    fno_norm_residual_saved_bytes, fno_norm_residual_saved_empty, fno_norm_residual_workspace_bytes,
+    fno_norm_residual_workspace_empty)
 
 __all__ = [
     "fno_plan_create", "fno_spectral_conv2d", "fno_spectral_conv3d",
@@ -20,6 +25,10 @@ __all__ = [
     "fno_model2d_destroy", "Model2d", "fno_model2d_set_graph", "fno_block2d", "fno_block2d_prepare",
     "fno_plan_saved_bytes", "fno_saved_empty", "fno_spectral_conv_forward_save",
     "fno_spectral_conv_backward_saved",
+    "fno_checkpoint_bytes", "fno_checkpoint_empty", "fno_checkpoint_pack", "fno_checkpoint_unpack",
+    "NormParams", "NormGrads", "fno_norm_residual", "fno_norm_residual_save", "fno_norm_residual_backward",
+    "fno_norm_residual_backward_saved", "fno_norm_residual_saved_bytes", "fno_norm_residual_saved_empty",
+    "fno_norm_residual_workspace_bytes", "fno_norm_residual_workspace_empty",
 ]
 
 

@@ -10,11 +10,28 @@ FNO_OK = 0
 STATUS_NAMES = {0: "FNO_OK", 1: "FNO_ERR_INVALID_ARG", 2: "FNO_ERR_UNSUPPORTED",
                 3: "FNO_ERR_OUT_OF_MEMORY", 4: "FNO_ERR_DEVICE"}
 DTYPES = {"f32": 0, "f16": 1, "bf16": 2}
+NORM_KINDS = {"rms": 0, "layer": 1}
 NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024  # FNO_NOALLOC_SCRATCH_BYTES
 
 # every symbol include/fno.h declares, with its ctypes signature
 _c_int, _c_void_p, _c_size_t = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t
 _IntP = ctypes.POINTER(ctypes.c_int)
+_c_long, _SizeP = ctypes.c_long, ctypes.POINTER(ctypes.c_size_t)
+
+
+class NormParamsStruct(ctypes.Structure):
+    """fno_norm_params_t"""
+    _fields_ = [("kind", _c_int), ("eps", ctypes.c_float)] + [
+        (n, _c_void_p) for n in ("w_post", "b_post", "gate", "scale", "w_pre", "b_pre")]
+
+
+class NormGradsStruct(ctypes.Structure):
+    """fno_norm_grads_t"""
+    _fields_ = [(n, _c_void_p) for n in ("w_post", "b_post", "gate", "scale", "w_pre", "b_pre")]
+
+
+_NormP, _NormG = ctypes.POINTER(NormParamsStruct), ctypes.POINTER(NormGradsStruct)
+_BCP = [_c_int, _c_int, _c_long, _c_int, _c_void_p]  # batch, channels, pixels, dtype, stream
 SIGNATURES = {
     "fno_plan_create": (_c_int, [ctypes.POINTER(_c_void_p), _c_int, _c_int, _c_int, _c_int,
                                  _IntP, _IntP, _c_int, _c_int]),
@@ -52,6 +69,15 @@ SIGNATURES = {
                                      _c_void_p]),
     "fno_model2d_set_graph": (_c_int, [_c_void_p, _c_int]),
     "fno_model2d_destroy": (_c_int, [_c_void_p]),
+    "fno_checkpoint_bytes": (_c_int, [_c_long, _c_long, _SizeP]),
+    "fno_checkpoint_pack": (_c_int, [_c_void_p, _c_void_p, _c_long, _c_long, _c_int, _c_void_p]),
+    "fno_checkpoint_unpack": (_c_int, [_c_void_p, _c_void_p, _c_long, _c_long, _c_int, _c_void_p]),
+    "fno_norm_residual": (_c_int, [_NormP] + [_c_void_p] * 4 + _BCP),
+    "fno_norm_residual_saved_bytes": (_c_int, [_c_int, _c_int, _c_long, _SizeP]),
+    "fno_norm_residual_save": (_c_int, [_NormP] + [_c_void_p] * 5 + _BCP),
+    "fno_norm_residual_workspace_bytes": (_c_int, [_c_int, _c_int, _c_long, _c_int, _SizeP]),
+    "fno_norm_residual_backward": (_c_int, [_NormP] + [_c_void_p] * 6 + [_NormG, _c_void_p] + _BCP),
+    "fno_norm_residual_backward_saved": (_c_int, [_NormP] + [_c_void_p] * 5 + [_NormG, _c_void_p] + _BCP),
 }
 
 _lib = None

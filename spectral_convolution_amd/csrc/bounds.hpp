@@ -28,6 +28,8 @@ struct ContractArgs;
 struct GradWArgs;
 struct WeightsArgs;
 struct FusedShape;
+struct CkArgs;
+struct NormArgs;
 
 namespace bounds {
 // [p, p + n) inside one live allocation of the recording runtime (n = 0: true)
@@ -55,6 +57,8 @@ void check_lift_fold(const void *P, const void *p, const void *w, const void *Wb
                      const void *af, const void *bf, int K, int J, int C, int dtype);
 void check_block_rows(const void *zg, const void *zexp, const void *tb, const void *x, const void *wb,
                       const void *bias, const void *y, int B, int Ci, int Co, int H, int W, int NN, int dtype);
+void check_checkpoint(const CkArgs &a, bool pack, int dtype);
+void check_norm(const NormArgs &a, bool fwd, int S, int dtype);
 
 }  // namespace fno
 

@@ -2,8 +2,8 @@
 // spread of shapes (matrix-core and VALU planes, 2D and 3D, the three dtypes,
 // ragged modes and channels, both launch shapes, the half exchange, the
 // backward pass (from x and from saved spectra), weight repacking, the
-// allocation-free entry, the FNO block
-// and the full FNO2d network). Each launch is checked by its launcher's
+// allocation-free entry, the FNO block, the full FNO2d network and the
+// training operators around a block). Each launch is checked by its launcher's
 // bounds hook against the recording runtime's allocations; the program exits
 // non-zero if any span or assumption was broken. Host code only.
 
@@ -134,6 +134,35 @@ void run_model(int B, int H, int W, int in, int ch, int layers, int m1, int m2, 
   for (Buf *b : bufs) delete b;
 }
 
+void run_checkpoint(long rows, long n, fno_dtype_t dt) {
+  size_t bytes = 0;
+  EXPECT(fno_checkpoint_bytes(rows, n, &bytes) == FNO_OK);
+  Buf x((size_t)rows * n * es_of(dt)), s(bytes);
+  EXPECT(fno_checkpoint_pack(x.p, s.p, rows, n, dt, nullptr) == FNO_OK);
+  EXPECT(fno_checkpoint_unpack(s.p, x.p, rows, n, dt, nullptr) == FNO_OK);
+}
+
+void run_norm(int B, int C, long P, int kind, bool params, fno_dtype_t dt) {
+  const size_t es = es_of(dt), n = (size_t)B * C * P * es, nc = C * es;
+  size_t sb = 0, wb = 0;
+  EXPECT(fno_norm_residual_saved_bytes(B, C, P, &sb) == FNO_OK);
+  EXPECT(fno_norm_residual_workspace_bytes(B, C, P, dt, &wb) == FNO_OK);
+  Buf x(n), v(n), y(n), u(n), gy(n), gu(n), gx(n), gv(n), saved(sb), ws(wb);
+  Buf p0(nc), p1(nc), p2(nc), p3(nc), p4(nc), pg(B * nc), g0(nc), g1(nc), g2(nc), g3(nc), g4(nc), gg(B * nc);
+  fno_norm_params_t p{kind, 1e-5f, p0.p, p1.p, pg.p, p2.p, p3.p, p4.p};
+  fno_norm_grads_t g{g0.p, g1.p, gg.p, g2.p, g3.p, g4.p};
+  if (!params) {
+    p = fno_norm_params_t{kind, 1e-5f, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr};
+    g = fno_norm_grads_t{};
+  }
+  EXPECT(fno_norm_residual(&p, x.p, v.p, y.p, u.p, B, C, P, dt, nullptr) == FNO_OK);
+  EXPECT(fno_norm_residual(&p, x.p, v.p, y.p, nullptr, B, C, P, dt, nullptr) == FNO_OK);
+  EXPECT(fno_norm_residual_save(&p, x.p, v.p, y.p, u.p, saved.p, B, C, P, dt, nullptr) == FNO_OK);
+  EXPECT(fno_norm_residual_backward(&p, x.p, v.p, gy.p, gu.p, gx.p, gv.p, &g, ws.p, B, C, P, dt, nullptr) == FNO_OK);
+  EXPECT(fno_norm_residual_backward_saved(&p, saved.p, gy.p, gu.p, gx.p, nullptr, params ? &g : nullptr, ws.p, B, C, P,
+                                          dt, nullptr) == FNO_OK);
+}
+
 }  // namespace
 
 int main() {
@@ -160,6 +189,16 @@ int main() {
   run_model(1, 64, 64, 3, 64, 4, 12, 12, 128, 1, FNO_BF16);
   run_model(2, 32, 32, 3, 16, 1, 4, 4, 8, 2, FNO_F32);
   run_model(2, 64, 64, 3, 16, 0, 4, 4, 8, 1, FNO_F16);
+  const long ck[][2] = {{1, 1}, {7, 31}, {96, 3721}, {5, 32}, {1280, 1000}, {3, 40000}};
+  for (const auto &c : ck)
+    for (fno_dtype_t dt : dts) run_checkpoint(c[0], c[1], dt);
+  struct N { int B, C; long P; };
+  const N nn[] = {{2, 4, 256}, {1, 1, 2}, {3, 7, 33}, {1, 16, 1000}, {20, 64, 4096}, {3, 48, 3721}, {2, 65, 100},
+                  {2, 130, 64}, {1, 256, 777}, {1, 512, 65}, {300, 8, 5}, {1, 1, 1}, {5, 64, 1}, {9, 257, 1},
+                  {700, 512, 1}, {3, 1025, 1}, {2, 3001, 1}, {2, 8192, 1}, {8192, 40, 1}};
+  for (const N &c : nn)
+    for (fno_dtype_t dt : dts)
+      for (int kind = 0; kind < 2; ++kind) run_norm(c.B, c.C, c.P, kind, kind == 0 || c.C != 64, dt);
   const long reports = check_reports();
   // the checker itself: spans past the end of a buffer must be reported
   {

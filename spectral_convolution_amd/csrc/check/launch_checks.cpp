@@ -334,4 +334,57 @@ void check_block_rows(const void *zg, const void *zexp, const void *tb, const vo
          dtype != DT_F32 && pow2_plane(W) && Ci >= 1 && Ci <= 64 && (NN == 1 || NN == 2));
 }
 
+void check_checkpoint(const CkArgs &a, bool pack, int dtype) {
+  const Ctx c{pack ? "fno_checkpoint_pack" : "fno_checkpoint_unpack"};
+  c.span("field", pack ? a.x : a.y, (size_t)a.rows * a.n * es_of(dtype));
+  c.span("codes", a.codes, (size_t)a.rows * a.nb * 32);
+  c.span("exponents", a.exps, (size_t)a.rows * a.nb);
+  c.need("blocks cover the row", a.nb == (a.n + 31) / 32);
+  c.need("codes 8-byte aligned", ((uintptr_t)a.codes & 7) == 0);
+  c.need("units of a row in 32 bits", 4 * a.nb + 1024 < (1L << 32));
+}
+
+void check_norm(const NormArgs &a, bool fwd, int S, int dtype) {
+  const Ctx c{fwd ? "fno_norm_fwd" : "fno_norm_bwd"};
+  const size_t es = es_of(dtype), n = (size_t)a.B * a.C * a.P * es, nc = (size_t)a.C * es, ng = (size_t)a.B * nc;
+  auto opt = [&](const char *what, const void *p, size_t bytes) {
+    if (p) c.span(what, p, bytes);
+  };
+  opt("w_post", a.w_post, nc);
+  opt("b_post", a.b_post, nc);
+  opt("gate", a.gate, ng);
+  opt("scale", a.scale, nc);
+  opt("w_pre", a.w_pre, nc);
+  opt("b_pre", a.b_pre, nc);
+  if (fwd || !a.vq) {
+    c.span("x", a.x, n);
+    c.span("v", a.v, n);
+  }
+  if (a.vq) {
+    const size_t rows = a.P == 1 ? a.B : (size_t)a.B * a.C, len = a.P == 1 ? a.C : a.P, nb = (len + 31) / 32;
+    c.span("codes of x", a.xq, rows * nb * 32);
+    c.span("exponents of x", a.xe, rows * nb);
+    c.span("codes of v", a.vq, rows * nb * 32);
+    c.span("exponents of v", a.ve, rows * nb);
+    c.need("codes 8-byte aligned", (((uintptr_t)a.xq | (uintptr_t)a.vq) & 7) == 0);
+  }
+  if (fwd) {
+    c.span("y", a.y, n);
+    opt("u", a.u, n);
+  } else {
+    c.span("gy", a.gy, n);
+    opt("gu", a.gu, n);
+    opt("gx", a.gx, n);
+    opt("gv", a.gv, n);
+    opt("g_w_post", a.g_w_post, nc);
+    opt("g_b_post", a.g_b_post, nc);
+    opt("g_gate", a.g_gate, ng);
+    opt("g_scale", a.g_scale, nc);
+    opt("g_w_pre", a.g_w_pre, nc);
+    opt("g_b_pre", a.g_b_pre, nc);
+    opt("runs' sums", a.part, (size_t)4 * a.C * S * (a.P == 1 ? 1 : a.B) * 4);
+  }
+  c.need("channels held by a workgroup", a.C >= 1 && a.C <= (a.P == 1 ? kNormMaxToken : kNormMaxField));
+}
+
 }  // namespace fno

@@ -1,0 +1,235 @@
+"""GPU parity of the training operators around a block against their float64
+definitions (oracle/training.py), at the sizes and values where they can go
+wrong: rows of one value, rows that end inside a block or a tile, odd channel
+counts, constant and empty-handed rows, poisoned values, absent parameters,
+gradients that are not wanted, other streams and captured graphs."""
+
+import numpy as np
+import pytest
+import torch
+
+import spectral_convolution_amd as fno
+from oracle import training as ref
+from training_util import DT, LOW, NORM_NAMES, close, f64, norm_case, stored
+
+pytestmark = pytest.mark.gpu
+DTYPES = ["f32", "f16", "bf16"]
+DEV = "cuda:0"
+
+
+def dev(t):
+    return None if t is None else t.to(DEV)
+
+
+# ------------------------------------------------------------- checkpoints
+
+def _parts(saved, rows, n):
+    nb = -(-n // 32)
+    off = -(-rows * nb * 32 // 256) * 256
+    b = saved.cpu().view(torch.int8)
+    return b[:rows * nb * 32].view(rows, -1).numpy(), b[off:off + rows * nb].view(rows, nb).numpy()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,n", [(1, 1), (7, 1), (3, 31), (2, 32), (5, 33), (1, 255), (9, 1000), (96, 3721),
+                                    (2, 8191), (300, 40), (4, 4096), (1, 100003)])
+def test_checkpoint(dtype, rows, n):
+    rng = np.random.default_rng(rows * 1000 + n)
+    x, x64 = stored(rng, (rows, n), dtype, spread=True)
+    saved = torch.full((fno.fno_checkpoint_bytes(rows, n),), 77, dtype=torch.uint8, device=DEV)
+    y = torch.full((rows, n), 3.0, dtype=DT[dtype], device=DEV)
+    fno.fno_checkpoint_pack(dev(x), saved)
+    fno.fno_checkpoint_unpack(saved, y)
+    q, e = ref.checkpoint(x64, LOW[dtype])
+    gq, ge = _parts(saved, rows, n)
+    assert (gq == q).all() and (ge == e).all()
+    assert (f64(y) == ref.checkpoint_values(q, e, n)).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_checkpoint_of_extreme_values(dtype):
+    fi = torch.finfo(DT[dtype])
+    tiny = 2.0 ** -24 if dtype == "f16" else (2.0 ** -149 if dtype == "f32" else 2.0 ** -133)
+    rows = [[0.0] * 40, [-0.0] * 40, [fi.max] * 40, [fi.min, fi.max, fi.tiny] + [1.0] * 37, [tiny] * 40,
+            [fi.tiny, -tiny, 3 * tiny] + [0.0] * 37, [fi.tiny] * 40,
+            [2.0 ** -6 * (127.5 + 1e-9)] + [1.0] * 39, [2.0 - float(fi.eps)] * 40, [-2.0] * 40,
+            [1.5 * 2.0 ** -6, 2.5 * 2.0 ** -6, 1.0, -1.5 * 2.0 ** -6, -2.5 * 2.0 ** -6] + [0.0] * 35]
+    x = torch.tensor(rows, dtype=torch.float64).to(DT[dtype])
+    x64 = x.double().numpy()
+    saved, y = fno.fno_checkpoint_empty(dev(x)), torch.empty_like(dev(x))
+    fno.fno_checkpoint_pack(dev(x), saved)
+    fno.fno_checkpoint_unpack(saved, y)
+    assert (f64(y) == ref.round_trip(x64, LOW[dtype])).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_checkpoint_of_poisoned_blocks(dtype):
+    x = torch.ones(4, 100)
+    x[0, 5], x[1, 40], x[2, 99] = float("nan"), float("inf"), -float("inf")
+    x = x.to(DT[dtype])
+    saved, y = fno.fno_checkpoint_empty(dev(x)), torch.empty_like(dev(x))
+    fno.fno_checkpoint_pack(dev(x), saved)
+    fno.fno_checkpoint_unpack(saved, y)
+    bad = np.zeros((4, 100), bool)
+    bad[0, :32] = bad[1, 32:64] = bad[2, 96:] = True
+    got = f64(y)
+    assert (np.isnan(got) == bad).all() and (got[~bad] == 1.0).all()
+
+
+def test_checkpoint_keeps_what_it_kept():
+    x, _ = stored(np.random.default_rng(2), (17, 333), "bf16", spread=True)
+    x = dev(x)
+    saved, y, again = fno.fno_checkpoint_empty(x), torch.empty_like(x), torch.empty_like(x)
+    fno.fno_checkpoint_pack(x, saved)
+    fno.fno_checkpoint_unpack(saved, y)
+    fno.fno_checkpoint_pack(y, saved)
+    fno.fno_checkpoint_unpack(saved, again)
+    assert torch.equal(y, again)
+
+
+# ------------------------------------------------------------------- norms
+
+# (B, C, P): P None is the token layout
+SHAPES = [(2, 4, 256), (1, 1, 2), (3, 7, 33), (2, 8, 64), (1, 13, 1000), (2, 16, 70), (3, 32, 31), (1, 33, 129),
+          (2, 48, 3721), (1, 64, 512), (1, 65, 100), (2, 128, 65), (1, 200, 257), (1, 256, 64), (1, 257, 97),
+          (1, 512, 40), (1, 1, None), (3, 5, None), (5, 64, None), (9, 257, None), (4, 500, None), (3, 512, None),
+          (2, 1000, None), (6, 1024, None), (3, 1025, None), (2, 3001, None), (2, 4096, None), (1, 8191, None),
+          (2, 8192, None), (1500, 40, None)]
+
+
+def _params(prm):
+    return {k: None if v is None else dev(v[0]) for k, v in prm.items()}
+
+
+def _run(dtype, kind, c, prm, saved_form, eps=1e-5, want=NORM_NAMES, use_u=True, stream=None):
+    x, v, gy, gu = (dev(c[k][0]) for k in ("x", "v", "gy", "gu"))
+    p = _params(prm)
+    N = fno.NormParams(kind, eps, **p)
+    y = torch.full_like(x, 7.0)
+    u = torch.full_like(x, 7.0) if use_u else None
+    gx, gv = torch.full_like(x, 7.0), torch.full_like(x, 7.0)
+    grads = {k: torch.full_like(p[k], 7.0) for k in want if p[k] is not None and (use_u or not k.endswith("_pre"))}
+    ws = torch.full_like(fno.fno_norm_residual_workspace_empty(x), 255)
+    if saved_form:
+        kept = torch.full_like(fno.fno_norm_residual_saved_empty(x), 99)
+        fno.fno_norm_residual_save(N, x, v, y, u, kept)
+        fno.fno_norm_residual_backward_saved(N, kept, gy, gu if use_u else None, gx, gv, fno.NormGrads(**grads), ws)
+    else:
+        fno.fno_norm_residual(N, x, v, y, u)
+        fno.fno_norm_residual_backward(N, x, v, gy, gu if use_u else None, gx, gv, fno.NormGrads(**grads), ws)
+    return y, u, gx, gv, grads
+
+
+def _check(dtype, kind, c, prm, saved_form, eps=1e-5, use_u=True, want=NORM_NAMES):
+    y, u, gx, gv, grads = _run(dtype, kind, c, prm, saved_form, eps, want, use_u)
+    p64 = {k: None if v is None else v[1] for k, v in prm.items()}
+    x, v, gy, gu = (c[k][1] for k in ("x", "v", "gy", "gu"))
+    yr, ur = ref.norm_residual(p64, kind, eps, x, v)
+    # one fp32 rounding of v's deviation from its mean shows as 2^-24 |mean| / deviation
+    rel = float(np.max(abs(v).max(1) / (np.std(v, axis=1) + eps ** 0.5))) if kind == "layer" else 1.0
+    extra = 8 * 2.0 ** -24 * rel
+    close("y", y, yr, dtype, extra=extra)
+    if use_u:
+        rely = float(np.max(abs(yr).max(1) / (np.std(yr, axis=1) + eps ** 0.5))) if kind == "layer" else 1.0
+        extra += 8 * 2.0 ** -24 * rely
+        close("u", u, ur, dtype, extra=extra)
+    xb, vb = (ref.round_trip(t, LOW[dtype]) for t in (x, v)) if saved_form else (x, v)
+    g = ref.norm_residual_backward(p64, kind, eps, xb, vb, gy, gu if use_u else None)
+    rms = lambda t: np.sqrt(np.mean(t ** 2))  # noqa: E731
+    for k, t in (("gx", gx), ("gv", gv)):
+        close(k, t, g[k][0], dtype, size=np.maximum(g[k][1], rms(g[k][0])), extra=extra)
+    for k, t in grads.items():
+        close("g_" + k, t, g[k][0], dtype, size=g[k][1] + abs(g[k][0]), extra=extra)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_norm(dtype, kind, shape):
+    B, C, P = shape
+    if C == 1 and kind == "layer":
+        pytest.skip("one channel has no deviation: see test_norm_of_constant_rows")
+    c, prm = norm_case(dtype, B, C, P, seed=B * 7919 + C)
+    _check(dtype, kind, c, prm, saved_form=False)
+    _check(dtype, kind, c, prm, saved_form=True)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("P", [None, 90])
+@pytest.mark.parametrize("absent", [("b_post", "b_pre"), ("gate",), ("scale", "w_post"), NORM_NAMES])
+def test_norm_with_absent_parameters(dtype, P, absent):
+    c, prm = norm_case(dtype, 3, 40, P, seed=11, absent=absent)
+    _check(dtype, "layer", c, prm, saved_form=False)
+    _check(dtype, "rms", c, prm, saved_form=True)
+
+
+@pytest.mark.parametrize("P", [None, 90])
+def test_norm_without_u(P):
+    c, prm = norm_case("f16", 2, 24, P, seed=12)
+    _check("f16", "layer", c, prm, saved_form=False, use_u=False)
+    _check("f16", "rms", c, prm, saved_form=True, use_u=False)
+
+
+@pytest.mark.parametrize("P", [None, 200])
+def test_norm_with_a_large_mean(P):
+    c, prm = norm_case("f32", 2, 96, P, seed=13, mean=1000.0)
+    _check("f32", "layer", c, prm, saved_form=False)
+
+
+@pytest.mark.parametrize("P", [None, 65])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+def test_norm_of_constant_rows(P, kind):
+    """v zero (or, for the layer norm, equal over the channels): v^ is 0 and y = x + scale gate b_post."""
+    c, prm = norm_case("f32", 2, 24, P, seed=14)
+    v = torch.full_like(c["v"][0], 2.5 if kind == "layer" else 0.0)
+    c["v"] = (v, v.double().numpy())
+    y, u, gx, gv, grads = _run("f32", kind, c, prm, False)
+    sg, b = prm["scale"][1] * prm["gate"][1], prm["b_post"][1]
+    want = c["x"][1] + (sg * b if P is None else (sg * b)[..., None])
+    close("y", y, want, "f32")
+    assert torch.isfinite(gv).all() and float(grads["w_post"].abs().max()) == 0.0
+
+
+@pytest.mark.parametrize("P", [None, 130])
+def test_norm_poison_stays_in_its_row(P):
+    c, prm = norm_case("f16", 2, 40, P, seed=15)
+    v = c["v"][0].clone()
+    v[(1, 3) if P is None else (1, 3, 100)] = float("nan")
+    c["v"] = (v, v.double().numpy())
+    y, u, gx, gv, _ = _run("f16", "layer", c, prm, False)
+    bad = np.zeros(tuple(v.shape), bool)
+    bad[(1,) if P is None else (1, slice(None), 100)] = True
+    for t in (y, u, gx, gv):
+        assert (np.isnan(f64(t)) == bad).all()
+
+
+@pytest.mark.parametrize("P", [None, 77])
+def test_norm_writes_only_what_is_wanted(P):
+    c, prm = norm_case("bf16", 2, 20, P, seed=16)
+    x, v, gy, gu = (dev(c[k][0]) for k in ("x", "v", "gy", "gu"))
+    p = _params(prm)
+    N = fno.NormParams("layer", 1e-5, **p)
+    gx, gv = torch.empty_like(x), torch.empty_like(x)
+    ws = fno.fno_norm_residual_workspace_empty(x)
+    full = {k: torch.empty_like(t) for k, t in p.items()}
+    fno.fno_norm_residual_backward(N, x, v, gy, gu, gx, gv, fno.NormGrads(**full), ws)
+    one, gate = torch.empty_like(x), torch.empty_like(p["gate"])
+    fno.fno_norm_residual_backward(N, x, v, gy, gu, one, None, None, None)
+    assert torch.equal(one, gx)
+    fno.fno_norm_residual_backward(N, x, v, gy, gu, None, one, fno.NormGrads(gate=gate), ws)
+    assert torch.equal(one, gv) and torch.equal(gate, full["gate"])
+    fno.fno_norm_residual_backward(N, x, v, gy, gu, None, None, fno.NormGrads(gate=gate.zero_()), ws)
+    assert torch.equal(gate, full["gate"])
+
+
+def test_norm_runs_on_the_given_stream_and_twice_alike():
+    c, prm = norm_case("f16", 3, 64, 5000, seed=17)
+    first = _run("f16", "layer", c, prm, True)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        second = _run("f16", "layer", c, prm, True)
+    s.synchronize()
+    for a, b in zip(first[:4], second[:4]):
+        assert torch.equal(a, b)
+    assert all(torch.equal(first[4][k], second[4][k]) for k in first[4])
