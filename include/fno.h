@@ -451,6 +451,38 @@ fno_status_t fno_checkpoint_pack(const void *x, void *saved, long rows, long n,
 fno_status_t fno_checkpoint_unpack(const void *saved, void *y, long rows,
                                    long n, fno_dtype_t dtype, void *stream);
 
+/* Channel mix of a training step, fno_channel_mix that also keeps what its
+ * backward needs in 8 bits: the checkpoint of x (rows [batch * c_in][pixels])
+ * and, with GELU and an add input, that of add (rows [batch * c_out][pixels])
+ * behind it, in `saved` (fno_channel_mix_saved_bytes, 256-byte aligned). y is
+ * that of x and add as given. act 0 or 1, bias and add may be NULL.
+ * c_in, c_out <= 128, else UNSUPPORTED. */
+fno_status_t fno_channel_mix_saved_bytes(int batch, int c_in, int c_out,
+                                         long pixels, int act, int has_add,
+                                         size_t *bytes);
+fno_status_t fno_channel_mix_save(const void *x, const void *A,
+                                  const void *bias, const void *add, void *y,
+                                  void *saved, int batch, int c_in, int c_out,
+                                  long pixels, int act, fno_dtype_t dtype,
+                                  void *stream);
+
+/* Its gradients at the kept x^ and add^, with z = A x^ + bias + add^ and
+ * gz = gy act'(z):
+ *   gx = A^T gz [batch][c_in][pixels],  gadd = gz [batch][c_out][pixels],
+ *   gA = sum gz x^^T [c_out][c_in],  gbias = sum gz [c_out]
+ * (sums over samples and pixels, in fp32). Each may be NULL, not all; bias as
+ * in the forward; has_add: whether the forward had an add input (gadd must be
+ * NULL otherwise). workspace: fno_channel_mix_workspace_bytes bytes, 16-byte
+ * aligned, needed for gA or gbias; its contents do not matter. */
+fno_status_t fno_channel_mix_workspace_bytes(int batch, int c_in, int c_out,
+                                             long pixels, fno_dtype_t dtype,
+                                             size_t *bytes);
+fno_status_t fno_channel_mix_backward_saved(
+    const void *saved, const void *A, const void *bias, const void *gy,
+    void *gx, void *gA, void *gbias, void *gadd, void *workspace, int batch,
+    int c_in, int c_out, long pixels, int act, int has_add, fno_dtype_t dtype,
+    void *stream);
+
 /* Norms after and before a block, with its gate and residual scale, over the
  * channel axis of fields [batch][channels][pixels] (pixels = 1: tokens):
  *   y = x + scale[c] gate[b][c] N_post(v),   u = N_pre(y),

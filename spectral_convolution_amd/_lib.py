@@ -72,6 +72,11 @@ SIGNATURES = {
     "fno_checkpoint_bytes": (_c_int, [_c_long, _c_long, _SizeP]),
     "fno_checkpoint_pack": (_c_int, [_c_void_p, _c_void_p, _c_long, _c_long, _c_int, _c_void_p]),
     "fno_checkpoint_unpack": (_c_int, [_c_void_p, _c_void_p, _c_long, _c_long, _c_int, _c_void_p]),
+    "fno_channel_mix_saved_bytes": (_c_int, [_c_int, _c_int, _c_int, _c_long, _c_int, _c_int, _SizeP]),
+    "fno_channel_mix_workspace_bytes": (_c_int, [_c_int, _c_int, _c_int, _c_long, _c_int, _SizeP]),
+    "fno_channel_mix_save": (_c_int, [_c_void_p] * 6 + [_c_int, _c_int, _c_int, _c_long, _c_int, _c_int, _c_void_p]),
+    "fno_channel_mix_backward_saved": (_c_int, [_c_void_p] * 9 + [_c_int, _c_int, _c_int, _c_long, _c_int, _c_int,
+                                                                  _c_int, _c_void_p]),
     "fno_norm_residual": (_c_int, [_NormP] + [_c_void_p] * 4 + _BCP),
     "fno_norm_residual_saved_bytes": (_c_int, [_c_int, _c_int, _c_long, _SizeP]),
     "fno_norm_residual_save": (_c_int, [_NormP] + [_c_void_p] * 5 + _BCP),

@@ -1,5 +1,6 @@
 """Binding of the training operators around a block (include/fno.h): 8-bit
-activation checkpoints and the norms with gate and residual scale. The names
+activation checkpoints, the channel mix that keeps them with its backward, and
+the norms with gate and residual scale. The names
 are re-exported by the package; like the rest of the binding these functions
 check and marshal arguments, every value is computed in the library's kernels.
 """
@@ -120,6 +121,81 @@ def fno_checkpoint_unpack(saved, y, stream=None):
               "fno_checkpoint_unpack")
 
 
+# --------------------------------------------------------------- channel mix
+
+def _fold(t, name):
+    """(dtype, batch, channels, pixels) of [B][C](...)."""
+    dt = _field_dtype(t, name)
+    if t.dim() < 2:
+        raise ValueError(f"{name} must be [batch][channels](...), got {tuple(t.shape)}")
+    P = 1
+    for s in t.shape[2:]:
+        P *= s
+    return dt, t.shape[0], t.shape[1], P
+
+
+def fno_channel_mix_saved_bytes(batch, c_in, c_out, pixels, act=0, has_add=False):
+    """Bytes of what fno_channel_mix_save keeps."""
+    return _bytes("fno_channel_mix_saved_bytes", batch, c_in, c_out, pixels, act, int(has_add))
+
+
+def fno_channel_mix_workspace_bytes(batch, c_in, c_out, pixels, dtype="f32"):
+    """Bytes of the backward's workspace."""
+    return _bytes("fno_channel_mix_workspace_bytes", batch, c_in, c_out, pixels, DTYPES[dtype])
+
+
+def fno_channel_mix_saved_empty(x, c_out, act=0, has_add=False):
+    """A device buffer (uint8 tensor) for what fno_channel_mix_save keeps."""
+    import torch
+    _, B, I, P = _fold(x, "x")
+    return torch.empty(fno_channel_mix_saved_bytes(B, I, c_out, P, act, has_add), dtype=torch.uint8, device=x.device)
+
+
+def fno_channel_mix_workspace_empty(x, c_out):
+    """A device buffer (uint8 tensor) for the backward of a mix of x."""
+    import torch
+    dt, B, I, P = _fold(x, "x")
+    return torch.empty(fno_channel_mix_workspace_bytes(B, I, c_out, P, dt), dtype=torch.uint8, device=x.device)
+
+
+def fno_channel_mix_save(x, A, bias, add, y, saved, act=0, stream=None):
+    """fno_channel_mix that also keeps x (and, with GELU, add) in 8 bits in `saved`."""
+    dt, B, I, P = _fold(x, "x")
+    _, By, O, Py = _fold(y, "y")
+    _check("y", y, (B, O) + tuple(x.shape[2:]), x)
+    _check("A", A, (O, I), x)
+    _check("bias", bias, (O,), x, optional=True)
+    _check("add", add, y.shape, x, optional=True)
+    _check_buffer("saved", saved, fno_channel_mix_saved_bytes(B, I, O, P, act, add is not None), 256, x.device)
+    with _on(x):
+        check(lib().fno_channel_mix_save(_ptr(x), _ptr(A), _ptr(bias), _ptr(add), _ptr(y), _ptr(saved), B, I, O, P, act,
+                                         DTYPES[dt], _stream(stream, x)), "fno_channel_mix_save")
+
+
+def fno_channel_mix_backward_saved(saved, A, bias, gy, gx, gA, gbias, gadd, workspace, act=0, has_add=False,
+                                   stream=None):
+    """Gradients of the channel mix at what its forward kept: gx, gA, gbias,
+    gadd, each None where not wanted. workspace: fno_channel_mix_workspace_empty."""
+    dt, B, O, P = _fold(gy, "gy")
+    if A.dim() != 2 or A.shape[0] != O:
+        raise ValueError(f"A shape {tuple(A.shape)} does not map to gy's {O} channels")
+    I = A.shape[1]
+    _check("A", A, (O, I), gy)
+    _check("bias", bias, (O,), gy, optional=True)
+    _check("gx", gx, (B, I) + tuple(gy.shape[2:]), gy, optional=True)
+    _check("gA", gA, (O, I), gy, optional=True)
+    _check("gbias", gbias, (O,), gy, optional=True)
+    _check("gadd", gadd, gy.shape, gy, optional=True)
+    _check_buffer("saved", saved, fno_channel_mix_saved_bytes(B, I, O, P, act, has_add), 256, gy.device)
+    if gA is not None or gbias is not None:
+        _check_buffer("workspace", workspace, fno_channel_mix_workspace_bytes(B, I, O, P, dt), 16, gy.device)
+    with _on(gy):
+        check(lib().fno_channel_mix_backward_saved(_ptr(saved), _ptr(A), _ptr(bias), _ptr(gy), _ptr(gx), _ptr(gA),
+                                                   _ptr(gbias), _ptr(gadd), _ptr(workspace), B, I, O, P, act,
+                                                   int(has_add), DTYPES[dt], _stream(stream, gy)),
+              "fno_channel_mix_backward_saved")
+
+
 # --------------------------------------------------------------------- norms
 
 class NormParams:
@@ -141,17 +217,6 @@ class NormGrads:
     def __init__(self, w_post=None, b_post=None, gate=None, scale=None, w_pre=None, b_pre=None):
         self.w_post, self.b_post, self.gate, self.scale = w_post, b_post, gate, scale
         self.w_pre, self.b_pre = w_pre, b_pre
-
-
-def _norm_shape(like, name):
-    dt = _field_dtype(like, name)
-    if like.dim() < 2:
-        raise ValueError(f"{name} must be [batch][channels](...), got {tuple(like.shape)}")
-    B, C = like.shape[:2]
-    P = 1
-    for s in like.shape[2:]:
-        P *= s
-    return dt, B, C, P
 
 
 def _norm_struct(obj, cls, like, B, C):
@@ -177,19 +242,19 @@ def fno_norm_residual_workspace_bytes(batch, channels, pixels, dtype="f32"):
 def fno_norm_residual_saved_empty(x):
     """A device buffer (uint8 tensor) for the checkpoints of a field or of tokens shaped like x."""
     import torch
-    _, B, C, P = _norm_shape(x, "x")
+    _, B, C, P = _fold(x, "x")
     return torch.empty(fno_norm_residual_saved_bytes(B, C, P), dtype=torch.uint8, device=x.device)
 
 
 def fno_norm_residual_workspace_empty(x):
     """A device buffer (uint8 tensor) for the backward of a call on x."""
     import torch
-    dt, B, C, P = _norm_shape(x, "x")
+    dt, B, C, P = _fold(x, "x")
     return torch.empty(fno_norm_residual_workspace_bytes(B, C, P, dt), dtype=torch.uint8, device=x.device)
 
 
 def _norm_forward(fn, prm, x, v, y, u, saved, stream):
-    dt, B, C, P = _norm_shape(x, "x")
+    dt, B, C, P = _fold(x, "x")
     _check("v", v, x.shape, x)
     _check("y", y, x.shape, x)
     _check("u", u, x.shape, x, optional=True)
@@ -214,7 +279,7 @@ def fno_norm_residual_save(params, x, v, y, u, saved, stream=None):
 
 
 def _norm_backward(fn, prm, first, gy, gu, gx, gv, grads, workspace, stream):
-    dt, B, C, P = _norm_shape(gy, "gy")
+    dt, B, C, P = _fold(gy, "gy")
     grads = NormGrads() if grads is None else grads
     for name, t in (("gu", gu), ("gx", gx), ("gv", gv)):
         _check(name, t, gy.shape, gy, optional=True)

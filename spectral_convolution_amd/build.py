@@ -19,8 +19,9 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfno.so")
 
 SOURCES = ["plane_kernels.hip", "plane_mfma.hip", "axis_kernels.hip", "contract.hip", "contract_mx.hip", "backward.hip", "weights.hip", "pointwise.hip", "fused.hip", "fno_api.cpp",
-           "fno_model.cpp", "checkpoint.hip", "norm.hip", "fno_train.cpp"]
-HEADERS = ["common.hpp", "fft_reg.hpp", "plane_common.hpp", "plane_valu.hpp", "plane_mfma.hpp", "contract.hpp", "checkpoint.hpp"]
+           "fno_model.cpp", "checkpoint.hip", "norm.hip", "mix_train.hip",
+           "fno_train.cpp"]
+HEADERS = ["common.hpp", "fft_reg.hpp", "plane_common.hpp", "plane_valu.hpp", "plane_mfma.hpp", "contract.hpp", "checkpoint.hpp", "gelu.hpp"]
 
 ARCH = "gfx950"
 CFLAGS = [

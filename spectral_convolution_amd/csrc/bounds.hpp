@@ -30,6 +30,7 @@ struct WeightsArgs;
 struct FusedShape;
 struct CkArgs;
 struct NormArgs;
+struct MixTrainArgs;
 
 namespace bounds {
 // [p, p + n) inside one live allocation of the recording runtime (n = 0: true)
@@ -58,6 +59,7 @@ void check_lift_fold(const void *P, const void *p, const void *w, const void *Wb
 void check_block_rows(const void *zg, const void *zexp, const void *tb, const void *x, const void *wb,
                       const void *bias, const void *y, int B, int Ci, int Co, int H, int W, int NN, int dtype);
 void check_checkpoint(const CkArgs &a, bool pack, int dtype);
+void check_mix_train(const MixTrainArgs &a, bool fwd, int S, size_t lds, int dtype);
 void check_norm(const NormArgs &a, bool fwd, int S, int dtype);
 
 }  // namespace fno

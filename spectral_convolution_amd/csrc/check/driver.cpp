@@ -163,6 +163,21 @@ void run_norm(int B, int C, long P, int kind, bool params, fno_dtype_t dt) {
                                           dt, nullptr) == FNO_OK);
 }
 
+void run_mix(int B, int I, int O, long P, int act, bool add, fno_dtype_t dt) {
+  const size_t es = es_of(dt), nx = (size_t)B * I * P * es, ny = (size_t)B * O * P * es;
+  size_t sb = 0, wb = 0;
+  EXPECT(fno_channel_mix_saved_bytes(B, I, O, P, act, add, &sb) == FNO_OK);
+  EXPECT(fno_channel_mix_workspace_bytes(B, I, O, P, dt, &wb) == FNO_OK);
+  Buf x(nx), A((size_t)O * I * es), bias(O * es), ad(ny), y(ny), saved(sb), gy(ny), gx(nx), gA((size_t)O * I * es),
+      gb(O * es), gadd(ny), ws(wb);
+  EXPECT(fno_channel_mix_save(x.p, A.p, bias.p, add ? ad.p : nullptr, y.p, saved.p, B, I, O, P, act, dt, nullptr) ==
+         FNO_OK);
+  EXPECT(fno_channel_mix_backward_saved(saved.p, A.p, bias.p, gy.p, gx.p, gA.p, gb.p, add ? gadd.p : nullptr, ws.p, B, I,
+                                        O, P, act, add, dt, nullptr) == FNO_OK);
+  EXPECT(fno_channel_mix_backward_saved(saved.p, A.p, nullptr, gy.p, gx.p, nullptr, nullptr, nullptr, nullptr, B, I, O,
+                                        P, act, add, dt, nullptr) == FNO_OK);
+}
+
 }  // namespace
 
 int main() {
@@ -199,6 +214,12 @@ int main() {
   for (const N &c : nn)
     for (fno_dtype_t dt : dts)
       for (int kind = 0; kind < 2; ++kind) run_norm(c.B, c.C, c.P, kind, kind == 0 || c.C != 64, dt);
+  struct M { int B, I, O; long P; };
+  const M mm[] = {{2, 4, 4, 256}, {1, 1, 1, 1}, {3, 5, 70, 33}, {2, 40, 72, 1001}, {1, 64, 64, 4096}, {1, 128, 128, 300},
+                  {2, 128, 3, 100}, {1, 17, 33, 7}, {4, 32, 32, 1024}, {70, 8, 16, 500}};
+  for (const M &c : mm)
+    for (fno_dtype_t dt : dts)
+      for (int k = 0; k < 4; ++k) run_mix(c.B, c.I, c.O, c.P, k & 1, (k & 2) != 0, dt);
   const long reports = check_reports();
   // the checker itself: spans past the end of a buffer must be reported
   {

@@ -387,4 +387,35 @@ void check_norm(const NormArgs &a, bool fwd, int S, int dtype) {
   c.need("channels held by a workgroup", a.C >= 1 && a.C <= (a.P == 1 ? kNormMaxToken : kNormMaxField));
 }
 
+void check_mix_train(const MixTrainArgs &a, bool fwd, int S, size_t lds, int dtype) {
+  const Ctx c{fwd ? "fno_mix_save" : "fno_mix_bwd"};
+  const size_t es = es_of(dtype), nx = (size_t)a.B * a.I * a.P * es, ny = (size_t)a.B * a.O * a.P * es;
+  const size_t nb = (a.P + 31) / 32, na = (size_t)a.O * a.I;
+  auto opt = [&](const char *what, const void *p, size_t bytes) {
+    if (p) c.span(what, p, bytes);
+  };
+  c.span("A", a.A, na * es);
+  opt("bias", a.bias, a.O * es);
+  c.span("codes of x", a.xq, (size_t)a.B * a.I * nb * 32);
+  c.span("exponents of x", a.xe, (size_t)a.B * a.I * nb);
+  opt("codes of add", a.aq, (size_t)a.B * a.O * nb * 32);
+  if (a.aq) c.span("exponents of add", a.ae, (size_t)a.B * a.O * nb);
+  c.need("codes 16-byte aligned", (((uintptr_t)a.xq | (uintptr_t)a.aq) & 15) == 0);
+  if (fwd) {
+    c.span("x", a.x, nx);
+    opt("add", a.add, ny);
+    c.span("y", a.y, ny);
+    c.need("add kept only where there is one", !a.aq || a.add);
+  } else {
+    c.span("gy", a.gy, ny);
+    opt("gx", a.gx, nx);
+    opt("gadd", a.gadd, ny);
+    opt("gA", a.gA, na * es);
+    opt("gbias", a.gbias, a.O * es);
+    opt("workgroups' sums", a.part, (size_t)S * (na + a.O) * 4);
+  }
+  c.need("1 <= channels <= 128", a.I >= 1 && a.I <= kMixTrainMax && a.O >= 1 && a.O <= kMixTrainMax);
+  c.need("LDS at most 160 KiB", lds <= kLdsMax);
+}
+
 }  // namespace fno

@@ -254,6 +254,21 @@ struct NormArgs {
   float *part;               // runs' sums; NULL when no parameter gradient is wanted
 };
 
+// Channel mix of a training step (mix_train.hip): [B][I][P] -> [B][O][P].
+struct MixTrainArgs {
+  const void *x, *add;  // forward (add may be NULL)
+  const void *A, *bias; // bias may be NULL
+  void *y;
+  uint8_t *xq, *aq;     // codes of x and add: written by the forward, read by the backward; aq NULL: add not kept
+  int8_t *xe, *ae;      // their exponents
+  const void *gy;
+  void *gx, *gadd, *gA, *gbias;  // NULL: not wanted
+  float *part;                   // workgroups' sums; NULL when neither gA nor gbias is wanted
+  int B, I, O;
+  long P;
+  int act;
+};
+
 bool fused_supported(const FusedShape &f);
 size_t fused_lds_bytes(const FusedShape &f, size_t lds_fwd, size_t lds_inv);
 // raises the kernel's LDS allowance and returns the largest co-resident grid
@@ -340,6 +355,10 @@ constexpr int kNormMaxToken = 8192;  // channels of a token (P = 1)
 size_t norm_workspace_bytes(int B, int C, long P, int dtype);
 hipError_t launch_norm_fwd(const NormArgs &a, int dtype, hipStream_t s);
 hipError_t launch_norm_bwd(const NormArgs &a, int dtype, hipStream_t s);
+constexpr int kMixTrainMax = 128;    // training channel mix: channels on either side
+size_t mix_train_workspace_bytes(int B, int I, int O, long P, int dtype);
+hipError_t launch_mix_save(const MixTrainArgs &a, int dtype, hipStream_t s);
+hipError_t launch_mix_bwd(const MixTrainArgs &a, int dtype, hipStream_t s);
 constexpr int kMixMaxIn = 128;   // channel mix: input channels
 constexpr int kProjMaxIn = 64;   // projection: input channels
 constexpr int kProjMaxHidden = 128;

@@ -1,7 +1,7 @@
 // fno_train.cpp - the C ABI of the training operators around a block: the
-// 8-bit activation checkpoints and the norms with gate and residual scale.
-// Arguments are checked on the host; the kernels are in checkpoint.hip and
-// norm.hip.
+// 8-bit activation checkpoints, the channel mix that keeps them with its
+// backward, and the norms with gate and residual scale. Arguments are checked
+// on the host; the kernels are in checkpoint.hip, mix_train.hip and norm.hip.
 
 #include <hip/hip_runtime.h>
 
@@ -192,9 +192,110 @@ fno_status_t norm_backward(const fno_norm_params_t *p, const void *x, const void
   return status_of(launch_norm_bwd(a, (int)dtype, (hipStream_t)stream));
 }
 
+// ---- channel mix
+
+fno_status_t mix_shape(int batch, int c_in, int c_out, long pixels, int act, int has_add, fno_dtype_t dtype) {
+  if (batch < 1 || c_in < 1 || c_out < 1 || pixels < 1 || (act != 0 && act != 1) || (has_add != 0 && has_add != 1) ||
+      !valid_dtype(dtype))
+    return FNO_ERR_INVALID_ARG;
+  if (c_in > kMixTrainMax || c_out > kMixTrainMax || pixels > kMaxRow || !values_in_range(batch, kMixTrainMax, pixels))
+    return FNO_ERR_UNSUPPORTED;
+  return FNO_OK;
+}
+
+// the kept inputs: the checkpoint of x, then (GELU with add) that of add
+struct MixSaved {
+  CkLayout x, add;
+  bool both;
+  size_t bytes;
+};
+MixSaved mix_saved(int batch, int c_in, int c_out, long pixels, int act, int has_add) {
+  MixSaved m;
+  m.x = ck_layout((long)batch * c_in, pixels);
+  m.add = ck_layout((long)batch * c_out, pixels);
+  m.both = act == 1 && has_add;
+  m.bytes = m.x.bytes + (m.both ? m.add.bytes : 0);
+  return m;
+}
+
+void mix_attach(MixTrainArgs &a, const void *saved, const MixSaved &m) {
+  void *s = const_cast<void *>(saved);
+  a.xq = at(s, 0), a.xe = reinterpret_cast<int8_t *>(at(s, m.x.exps));
+  if (m.both) a.aq = at(s, m.x.bytes), a.ae = reinterpret_cast<int8_t *>(at(s, m.x.bytes + m.add.exps));
+}
+
 }  // namespace
 
 extern "C" {
+
+fno_status_t fno_channel_mix_saved_bytes(int batch, int c_in, int c_out, long pixels, int act, int has_add,
+                                         size_t *bytes) {
+  if (!bytes) return FNO_ERR_INVALID_ARG;
+  const fno_status_t st = mix_shape(batch, c_in, c_out, pixels, act, has_add, FNO_F32);
+  if (st == FNO_OK) *bytes = mix_saved(batch, c_in, c_out, pixels, act, has_add).bytes;
+  return st;
+}
+
+fno_status_t fno_channel_mix_workspace_bytes(int batch, int c_in, int c_out, long pixels, fno_dtype_t dtype,
+                                             size_t *bytes) {
+  if (!bytes) return FNO_ERR_INVALID_ARG;
+  const fno_status_t st = mix_shape(batch, c_in, c_out, pixels, 0, 0, dtype);
+  if (st == FNO_OK) *bytes = mix_train_workspace_bytes(batch, c_in, c_out, pixels, (int)dtype);
+  return st;
+}
+
+fno_status_t fno_channel_mix_save(const void *x, const void *A, const void *bias, const void *add, void *y, void *saved,
+                                  int batch, int c_in, int c_out, long pixels, int act, fno_dtype_t dtype,
+                                  void *stream) {
+  if (!x || !A || !y || !saved) return FNO_ERR_INVALID_ARG;
+  const fno_status_t st = mix_shape(batch, c_in, c_out, pixels, act, add != nullptr, dtype);
+  if (st != FNO_OK) return st;
+  const size_t es = esize(dtype), nx = (size_t)batch * c_in * pixels * es, ny = (size_t)batch * c_out * pixels * es;
+  const MixSaved m = mix_saved(batch, c_in, c_out, pixels, act, add != nullptr);
+  Spans s;
+  s.in(x, nx, 16);
+  s.in(A, (size_t)c_out * c_in * es, es);
+  s.in(bias, c_out * es, es);
+  s.in(add, ny, 16);
+  s.out(y, ny, 16);
+  s.out(saved, m.bytes, 256);
+  if (!s.ok()) return FNO_ERR_INVALID_ARG;
+  MixTrainArgs a{};
+  a.x = x, a.add = add, a.A = A, a.bias = bias, a.y = y;
+  a.B = batch, a.I = c_in, a.O = c_out, a.P = pixels, a.act = act;
+  mix_attach(a, saved, m);
+  return status_of(launch_mix_save(a, (int)dtype, (hipStream_t)stream));
+}
+
+fno_status_t fno_channel_mix_backward_saved(const void *saved, const void *A, const void *bias, const void *gy, void *gx,
+                                            void *gA, void *gbias, void *gadd, void *workspace, int batch, int c_in,
+                                            int c_out, long pixels, int act, int has_add, fno_dtype_t dtype,
+                                            void *stream) {
+  if (!saved || !A || !gy || (!gx && !gA && !gbias && !gadd)) return FNO_ERR_INVALID_ARG;
+  if (((gA || gbias) && !workspace) || (gadd && !has_add)) return FNO_ERR_INVALID_ARG;
+  const fno_status_t st = mix_shape(batch, c_in, c_out, pixels, act, has_add, dtype);
+  if (st != FNO_OK) return st;
+  const size_t es = esize(dtype), nx = (size_t)batch * c_in * pixels * es, ny = (size_t)batch * c_out * pixels * es;
+  const MixSaved m = mix_saved(batch, c_in, c_out, pixels, act, has_add);
+  Spans s;
+  s.in(saved, m.bytes, 256);
+  s.in(A, (size_t)c_out * c_in * es, es);
+  s.in(bias, c_out * es, es);
+  s.in(gy, ny, 16);
+  s.out(gx, nx, 16);
+  s.out(gA, (size_t)c_out * c_in * es, es);
+  s.out(gbias, c_out * es, es);
+  s.out(gadd, ny, 16);
+  const bool sums = gA || gbias;
+  if (sums) s.out(workspace, mix_train_workspace_bytes(batch, c_in, c_out, pixels, (int)dtype), 16);
+  if (!s.ok()) return FNO_ERR_INVALID_ARG;
+  MixTrainArgs a{};
+  a.A = A, a.bias = bias, a.gy = gy, a.gx = gx, a.gadd = gadd, a.gA = gA, a.gbias = gbias;
+  a.part = sums ? static_cast<float *>(workspace) : nullptr;
+  a.B = batch, a.I = c_in, a.O = c_out, a.P = pixels, a.act = act;
+  mix_attach(a, saved, m);
+  return status_of(launch_mix_bwd(a, (int)dtype, (hipStream_t)stream));
+}
 
 fno_status_t fno_checkpoint_bytes(long rows, long n, size_t *bytes) {
   if (!bytes) return FNO_ERR_INVALID_ARG;

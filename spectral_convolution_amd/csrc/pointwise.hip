@@ -17,6 +17,7 @@
 #include <algorithm>
 
 #include "common.hpp"
+#include "gelu.hpp"
 
 namespace fno {
 
@@ -95,32 +96,6 @@ __device__ __forceinline__ void store4(void *p, size_t i, int n, bool al, const 
       }
     }
   }
-}
-
-__device__ __forceinline__ float gelu(float v) { return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f)); }
-
-// GELU for the half-precision kernels, whose outputs are rounded to 11 (fp16)
-// or 8 (bf16) significant bits: erf from Abramowitz & Stegun, Handbook of
-// Mathematical Functions, formula 7.1.28, erf(x) = 1 - (1 + a1 x + ... +
-// a6 x^6)^-16 for x >= 0 (absolute error below 3e-7; evaluated in fp32 it
-// stays below 2e-6), odd symmetry for x < 0. With r = 1 - erf(|v| / sqrt 2),
-// GELU(v) = max(v, 0) - |v| r / 2. One reciprocal on the transcendental
-// unit; formula 7.1.26 needs an exponential as well, which made the
-// projection (128 hidden GELUs per pixel) 21 us slower at B = 20, 256^2.
-__device__ __forceinline__ float gelu_half(float v) {
-  const float x = fabsf(v) * 0.70710678118654752f;
-  float p = fmaf(0.0000430638f, x, 0.0002765672f);
-  p = fmaf(p, x, 0.0001520143f);
-  p = fmaf(p, x, 0.0092705272f);
-  p = fmaf(p, x, 0.0422820123f);
-  p = fmaf(p, x, 0.0705230784f);
-  p = fmaf(p, x, 1.0f);
-  p = p * p;  // ^16 by four squarings; overflows to inf for large x, so r = 0
-  p = p * p;
-  p = p * p;
-  p = p * p;
-  const float r = __builtin_amdgcn_rcpf(p);
-  return fmaf(-0.5f * fabsf(v), r, fmaxf(v, 0.0f));
 }
 
 static constexpr int kPwThreads = 256;

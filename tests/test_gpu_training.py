@@ -233,3 +233,142 @@ def test_norm_runs_on_the_given_stream_and_twice_alike():
     for a, b in zip(first[:4], second[:4]):
         assert torch.equal(a, b)
     assert all(torch.equal(first[4][k], second[4][k]) for k in first[4])
+
+
+# ------------------------------------------------------------- channel mix
+
+def _mix_case(dtype, B, I, O, P, add, seed=0):
+    rng = np.random.default_rng(seed)
+    return dict(x=stored(rng, (B, I, P), dtype, spread=True), A=stored(rng, (O, I), dtype, I ** -0.5),
+                bias=stored(rng, (O,), dtype, 0.3), add=stored(rng, (B, O, P), dtype, spread=True) if add else None,
+                gy=stored(rng, (B, O, P), dtype, 0.5))
+
+
+def _mix_run(c, act, want=("gx", "gA", "gbias", "gadd")):
+    d = {k: None if t is None else dev(t[0]) for k, t in c.items()}
+    O, add = d["A"].shape[0], d["add"] is not None
+    y = torch.full_like(d["gy"], 7.0)
+    saved = torch.full_like(fno.fno_channel_mix_saved_empty(d["x"], O, act, add), 99)
+    fno.fno_channel_mix_save(d["x"], d["A"], d["bias"], d["add"], y, saved, act)
+    out = {"gx": d["x"], "gA": d["A"], "gbias": d["bias"], "gadd": d["add"]}
+    out = {k: torch.full_like(t, 7.0) if t is not None and k in want else None for k, t in out.items()}
+    ws = torch.full_like(fno.fno_channel_mix_workspace_empty(d["x"], O), 255)
+    fno.fno_channel_mix_backward_saved(saved, d["A"], d["bias"], d["gy"], out["gx"], out["gA"], out["gbias"], out["gadd"],
+                                       ws, act, add)
+    return y, out
+
+
+# GELU and its derivative: fp32 to a few roundings; 16-bit types to 1e-6 (the
+# published approximations' error in fp32), relative to |z| + 1
+ACT = {"f32": 0.0, "f16": 1e-6, "bf16": 1e-6}
+
+
+def _mix_check(dtype, B, I, O, P, act, add, seed=0):
+    c = _mix_case(dtype, B, I, O, P, add, seed)
+    y, out = _mix_run(c, act)
+    v = {k: None if t is None else t[1] for k, t in c.items()}
+    x, A, b, ad, gy = (v[k] for k in ("x", "A", "bias", "add", "gy"))
+    a0 = 0.0 if ad is None else abs(ad)
+    close("y", y, ref.channel_mix(x, A, b, ad, act), dtype, extra=ACT[dtype],
+          size=ref.mix_pre(abs(x), abs(A), abs(b), None) + a0 + 1)
+    xk = ref.round_trip(x, LOW[dtype])
+    adk = ref.round_trip(ad, LOW[dtype]) if add and act else ad
+    (gx, gA, gb, gz), _ = ref.channel_mix_backward(xk, A, b, adk, gy, act)
+    # gz: slope's error times gy, z's own error (slope of slope below 1) times gy
+    zs = ref.mix_pre(abs(xk), abs(A), abs(b), None) + a0 + 1
+    gzs = abs(gy) * (zs if act else 1.0)
+    close("gx", out["gx"], gx, dtype, extra=ACT[dtype], size=np.einsum("oi,bop->bip", abs(A), gzs))
+    close("gA", out["gA"], gA, dtype, extra=ACT[dtype], size=np.einsum("bop,bip->oi", gzs, abs(xk)))
+    close("gbias", out["gbias"], gb, dtype, extra=ACT[dtype], size=gzs.sum((0, 2)))
+    if add:
+        close("gadd", out["gadd"], gz, dtype, extra=ACT[dtype], size=gzs)
+
+
+MIXES = [(2, 4, 4, 256), (1, 1, 1, 1), (1, 2, 3, 31), (3, 5, 7, 33), (2, 16, 16, 64), (1, 17, 16, 65), (2, 16, 17, 300),
+         (1, 32, 32, 1024), (2, 33, 31, 127), (5, 40, 72, 201), (1, 64, 64, 129), (1, 65, 64, 100), (1, 64, 65, 100),
+         (1, 128, 128, 70), (2, 128, 3, 90), (2, 3, 128, 90), (1, 128, 20, 333), (1, 20, 100, 257), (9, 8, 48, 40)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("act,add", [(1, True), (1, False), (0, True), (0, False)])
+@pytest.mark.parametrize("shape", MIXES, ids=str)
+def test_mix(dtype, shape, act, add):
+    _mix_check(dtype, *shape, act, add, seed=sum(shape))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_mix_over_many_tiles(dtype):
+    _mix_check(dtype, 3, 24, 40, 20011, 1, True, seed=5)
+
+
+@pytest.mark.parametrize("want", [("gx",), ("gA",), ("gbias",), ("gadd",), ("gx", "gadd"), ("gA", "gbias")])
+def test_mix_writes_only_what_is_wanted(want):
+    c = _mix_case("f16", 2, 24, 40, 150, True, seed=6)
+    _, full = _mix_run(c, 1)
+    _, some = _mix_run(c, 1, want)
+    for k in full:
+        assert some[k] is None if k not in want else torch.equal(some[k], full[k]), k
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_mix_without_bias(dtype):
+    c = _mix_case(dtype, 2, 12, 20, 70, True, seed=7)
+    zero = torch.zeros_like(c["bias"][0])
+    with_zero = _mix_run({**c, "bias": (zero, None)}, 1)
+    none = _mix_run({**c, "bias": None}, 1)
+    assert torch.equal(with_zero[0], none[0])
+    assert all(torch.equal(with_zero[1][k], none[1][k]) for k in ("gx", "gA", "gadd"))
+
+
+def test_mix_large_and_saturated_z():
+    """Far out GELU is the identity or zero and its slope one or zero; nothing overflows on the way."""
+    c = _mix_case("f32", 1, 4, 4, 64, True, seed=8)
+    a = c["add"][0].clone()
+    a[0, :, :16], a[0, :, 16:32], a[0, :, 32:48], a[0, :, 48:] = 1e4, -1e4, 1e30, -1e30
+    c["add"] = (a, a.double().numpy())
+    y, out = _mix_run(c, 1)
+    gy = c["gy"][0].to(DEV)
+    up = (a > 0).to(DEV)
+    assert torch.isfinite(y).all() and (y[~up] == 0).all()
+    assert torch.equal(out["gadd"][up], gy[up]) and (out["gadd"][~up] == 0).all()
+
+
+def test_mix_poison():
+    """A NaN in x poisons its block of that channel, so z, and with it every gradient
+    through those pixels; other pixels stay what they are."""
+    c = _mix_case("f16", 1, 5, 6, 100, True, seed=9)
+    clean = _mix_run(c, 1)
+    x = c["x"][0].clone()
+    x[0, 2, 40] = float("nan")
+    y, out = _mix_run({**c, "x": (x, None)}, 1)
+    assert torch.isnan(y[0, :, 40]).all() and torch.equal(y[0, :, 41:], clean[0][0, :, 41:])
+    hit = torch.zeros(100, dtype=torch.bool, device=DEV)
+    hit[32:64] = True
+    for k in ("gx", "gadd"):
+        assert torch.isnan(out[k][0][:, hit]).all() and torch.equal(out[k][0][:, ~hit], clean[1][k][0][:, ~hit])
+
+
+def test_mix_twice_alike():
+    c = _mix_case("bf16", 4, 48, 64, 3000, True, seed=10)
+    (ya, a), (yb, b) = _mix_run(c, 1), _mix_run(c, 1)
+    assert torch.equal(ya, yb) and all(torch.equal(a[k], b[k]) for k in a)
+
+
+def test_mix_gradients_against_differences():
+    """The whole operator in fp32 against a central difference of its own forward, at values
+    that a checkpoint keeps exactly."""
+    c = _mix_case("f32", 2, 6, 5, 50, True, seed=11)
+    for k in ("x", "add"):
+        kept = torch.from_numpy(ref.round_trip(c[k][1], -126)).float()
+        c[k] = (kept, kept.double().numpy())
+    y, out = _mix_run(c, 1)
+    rng = np.random.default_rng(12)
+    h = 1e-4
+    for name, key in (("A", "gA"), ("bias", "gbias"), ("x", "gx"), ("add", "gadd")):
+        d = rng.standard_normal(c[name][1].shape)
+        loss = [(ref.channel_mix(*(c[k][1] + (s * h * d if k == name else 0) for k in ("x", "A", "bias", "add")), 1)
+                 * c["gy"][1]).sum() for s in (-1, 1)]
+        diff = (loss[1] - loss[0]) / (2 * h)
+        got = (f64(out[key]) * d).sum()
+        # h^2 of the third derivative, and fp32 sums
+        assert abs(got - diff) <= 1e-5 * (abs(f64(out[key]) * d)).sum()

@@ -225,3 +225,69 @@ def test_binding_refuses_host_tensors_and_mismatches():
         fno.fno_checkpoint_pack(x.double(), torch.zeros(4096, dtype=torch.uint8))
     with pytest.raises(TypeError):
         fno.fno_norm_residual_backward(prm, x, None, x, x, x, x, None, None)
+
+
+# ------------------------------------------------------------- channel mix
+
+def test_mix_sizes(L):
+    n = ctypes.c_size_t(7)
+    x, add = -(-6 * 128 // 256) * 256 + 256, -(-10 * 128 // 256) * 256 + 256
+    for act, has_add, want in ((0, 0, x), (0, 1, x), (1, 0, x), (1, 1, x + add)):
+        assert L.fno_channel_mix_saved_bytes(2, 3, 5, 100, act, has_add, ctypes.byref(n)) == OK and n.value == want
+    assert L.fno_channel_mix_saved_bytes(2, 3, 5, 100, 2, 0, ctypes.byref(n)) == INVALID
+    assert L.fno_channel_mix_saved_bytes(2, 3, 5, 100, 1, 0, None) == INVALID
+    assert L.fno_channel_mix_saved_bytes(2, 129, 5, 100, 1, 0, ctypes.byref(n)) == UNSUPPORTED
+    assert L.fno_channel_mix_workspace_bytes(2, 3, 129, 100, 0, ctypes.byref(n)) == UNSUPPORTED
+    assert L.fno_channel_mix_workspace_bytes(2, 3, 5, 0, 0, ctypes.byref(n)) == INVALID
+    assert L.fno_channel_mix_workspace_bytes(2, 3, 5, 100, 0, ctypes.byref(n)) == OK and 0 < n.value
+
+
+def test_mix_refusals(L):
+    keep, a = _buf(1 << 17)
+    at = {k: a + 8192 * i for i, k in enumerate(("x", "A", "bias", "add", "y", "saved", "gy", "gx", "gA", "gbias",
+                                                 "gadd", "ws"))}
+
+    def fwd(I=3, O=5, P=100, B=2, act=1, dtype=0, **kw):
+        d = {**at, **kw}
+        return L.fno_channel_mix_save(d["x"], d["A"], d["bias"], d["add"], d["y"], d["saved"], B, I, O, P, act, dtype,
+                                      None)
+
+    def bwd(I=3, O=5, P=100, B=2, act=1, has_add=1, dtype=0, **kw):
+        d = {**at, **kw}
+        return L.fno_channel_mix_backward_saved(d["saved"], d["A"], d["bias"], d["gy"], d["gx"], d["gA"], d["gbias"],
+                                                d["gadd"], d["ws"], B, I, O, P, act, has_add, dtype, None)
+
+    for k in ("x", "A", "y", "saved"):
+        assert fwd(**{k: None}) == INVALID
+    for k in ("gy", "A", "saved", "ws"):
+        assert bwd(**{k: None}) == INVALID
+    for f in (fwd, bwd):
+        for bad in (dict(I=0), dict(O=0), dict(P=0), dict(B=0), dict(act=2), dict(dtype=3)):
+            assert f(**bad) == INVALID
+        for far in (dict(I=129), dict(O=129), dict(P=(1 << 31) + 1)):
+            assert f(**far) == UNSUPPORTED
+        assert f(saved=at["saved"] + 128) == INVALID and f(A=at["A"] + 1) == INVALID
+    assert fwd(y=at["x"]) == INVALID and fwd(y=at["add"]) == INVALID and fwd(saved=at["x"]) == INVALID
+    assert fwd(x=at["x"] + 8) == INVALID
+    assert bwd(gx=None, gA=None, gbias=None, gadd=None) == INVALID
+    assert bwd(has_add=0) == INVALID                                     # gadd without an add input
+    assert bwd(has_add=2) == INVALID
+    assert bwd(gx=at["gy"]) == INVALID and bwd(gadd=at["gy"]) == INVALID and bwd(gA=at["A"]) == INVALID
+    assert bwd(ws=at["gx"]) == INVALID and bwd(ws=at["ws"] + 4) == INVALID
+
+
+def test_mix_binding_mismatches():
+    x, A = torch.zeros(2, 3, 40), torch.zeros(5, 3)
+    y, big = torch.zeros(2, 5, 40), torch.zeros(1 << 16, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="y shape"):
+        fno.fno_channel_mix_save(x, A, None, None, torch.zeros(2, 5, 41), big)
+    with pytest.raises(ValueError, match="A shape"):
+        fno.fno_channel_mix_save(x, A.t(), None, None, y, big)
+    with pytest.raises(ValueError, match="add dtype"):
+        fno.fno_channel_mix_save(x, A, None, y.half(), y, big)
+    with pytest.raises(ValueError, match="does not map"):
+        fno.fno_channel_mix_backward_saved(big, A.t(), None, y, x, None, None, None, None)
+    with pytest.raises(ValueError, match="saved holds"):
+        fno.fno_channel_mix_backward_saved(big[:8], A, None, y, x, None, None, None, None)
+    with pytest.raises(TypeError, match="workspace"):
+        fno.fno_channel_mix_backward_saved(big[-big.data_ptr() % 256:], A, None, y, x, A, None, None, None)
