@@ -11,55 +11,98 @@ from ._lib import DTYPES, NORM_KINDS, NormGradsStruct, NormParamsStruct, check, 
 
 _NORM_NAMES = ("w_post", "b_post", "gate", "scale", "w_pre", "b_pre")
 
-
-def _field_dtype(t, name):
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
-    names = {torch.float32: "f32", torch.float16: "f16", torch.bfloat16: "bf16"}
-    if t.dtype not in names:
-        raise ValueError(f"{name} dtype {t.dtype} is not one of float32, float16, bfloat16")
-    return names[t.dtype]
+# A call on a small field takes a few microseconds on the GPU, so the checks on
+# the way there are kept to a handful of attribute reads a tensor: _ptr() says yes
+# or hands over to _refuse(), which finds out what is wrong and says so.
+_torch = None
+_names = None
 
 
-def _check(name, t, shape, like, optional=False):
-    """t has `shape` and lives in like's dtype and device."""
-    import torch
-    if t is None:
-        if optional:
-            return
-        raise TypeError(f"{name} must be a torch tensor")
-    if not isinstance(t, torch.Tensor):
+def _t():
+    """torch, imported on first use (importing the binding does not import it)."""
+    global _torch, _names
+    if _torch is None:
+        import torch
+        _torch = torch
+        _names = {torch.float32: "f32", torch.float16: "f16", torch.bfloat16: "bf16"}
+    return _torch
+
+
+def _refuse(name, t, shape, dtype, dev, optional):
+    if not isinstance(t, _t().Tensor):
         raise TypeError(f"{name} must be a torch tensor" + (" or None" if optional else ""))
-    if t.dtype != like.dtype:
-        raise ValueError(f"{name} dtype {t.dtype} != {like.dtype}")
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, not on {like.device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} dtype {t.dtype} != {dtype}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} shape {tuple(t.shape)} != {tuple(shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the call's first field on device {dev}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _check_buffer(name, t, need, align, device):
-    import torch
-    if not isinstance(t, torch.Tensor):
+def _ptr(name, t, shape, dtype, dev, optional=False):
+    """Address of t, which has this shape and dtype, is contiguous and on device `dev`."""
+    if t is None and optional:
+        return None
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(name, t, shape, dtype, dev, optional)
+
+
+def _buffer(name, t, need, align, dev):
+    """Address of a buffer of at least `need` bytes at a multiple of `align`."""
+    if not isinstance(t, _t().Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
     have = t.numel() * t.element_size()
     if have < need:
         raise ValueError(f"{name} holds {have} bytes, the call needs {need}")
-    if t.data_ptr() % align:
+    p = t.data_ptr()
+    if p % align:
         raise ValueError(f"{name} must be {align}-byte aligned")
+    if t.get_device() != dev or not t.is_contiguous():
+        _refuse(name, t, t.shape, t.dtype, dev, False)
+    return p
 
 
-def _ptr(t):
-    from . import _ptr as ptr
-    return ptr(t)
+def _field(t, name):
+    """(dtype name, dtype, device, shape as a tuple) of a field."""
+    torch = _t()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    dt = _names.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"{name} dtype {t.dtype} is not one of float32, float16, bfloat16")
+    return dt, t.dtype, t.get_device(), tuple(t.shape)
 
 
-def _stream(stream, like):
-    from . import _stream as s
-    return s(stream, like.device)
+def _split(shape, name):
+    """(batch, channels, pixels) of [B][C](...)."""
+    if len(shape) < 2:
+        raise ValueError(f"{name} must be [batch][channels](...), got {shape}")
+    P = 1
+    for s in shape[2:]:
+        P *= s
+    return shape[0], shape[1], P
+
+
+def _call(fn, dev, stream, *args):
+    """Call the library with the tensors' device current, on `stream` or the current one."""
+    torch = _t()
+    if dev < 0:
+        raise ValueError(f"{fn}: the tensors must be on the GPU")
+    if torch._C._cuda_getDevice() != dev:
+        with torch.cuda.device(dev):
+            return _call(fn, dev, stream, *args)
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    st = getattr(lib(), fn)(*args, stream)
+    if st:
+        check(st, fn)
 
 
 def _bytes(fn, *args):
@@ -68,26 +111,19 @@ def _bytes(fn, *args):
     return n.value
 
 
-class _on:
-    """The tensor's device as the current one, where the library launches."""
-
-    def __init__(self, t):
-        self.t = t
-
-    def __enter__(self):
-        import torch
-        self.guard = torch.cuda.device(self.t.device)
-        return self.guard.__enter__()
-
-    def __exit__(self, *a):
-        return self.guard.__exit__(*a)
+def _empty(n, like):
+    torch = _t()
+    return torch.empty(n, dtype=torch.uint8, device=like.device)
 
 
 # --------------------------------------------------------------- checkpoints
 
-def _rows(t):
-    n = t.shape[-1] if t.dim() else 1
-    return (t.numel() // n if n else 0), n
+def _rows(shape):
+    n = shape[-1] if shape else 1
+    rows = 1
+    for s in shape[:-1]:
+        rows *= s
+    return rows, n
 
 
 def fno_checkpoint_bytes(rows, n):
@@ -97,42 +133,26 @@ def fno_checkpoint_bytes(rows, n):
 
 def fno_checkpoint_empty(x):
     """A device buffer (uint8 tensor) for the checkpoint of x (rows along its last axis)."""
-    import torch
-    return torch.empty(fno_checkpoint_bytes(*_rows(x)), dtype=torch.uint8, device=x.device)
+    return _empty(fno_checkpoint_bytes(*_rows(tuple(x.shape))), x)
 
 
 def fno_checkpoint_pack(x, saved, stream=None):
     """Keep x in 8 bits (blocks of 32 along its last axis) in `saved`."""
-    dt = _field_dtype(x, "x")
-    rows, n = _rows(x)
-    _check_buffer("saved", saved, fno_checkpoint_bytes(rows, n), 256, x.device)
-    with _on(x):
-        check(lib().fno_checkpoint_pack(_ptr(x), _ptr(saved), rows, n, DTYPES[dt], _stream(stream, x)),
-              "fno_checkpoint_pack")
+    dt, td, dev, shape = _field(x, "x")
+    rows, n = _rows(shape)
+    s = _buffer("saved", saved, fno_checkpoint_bytes(rows, n), 256, dev)
+    _call("fno_checkpoint_pack", dev, stream, _ptr("x", x, shape, td, dev), s, rows, n, DTYPES[dt])
 
 
 def fno_checkpoint_unpack(saved, y, stream=None):
     """Read the values kept in `saved` back into y (shape and dtype as packed)."""
-    dt = _field_dtype(y, "y")
-    rows, n = _rows(y)
-    _check_buffer("saved", saved, fno_checkpoint_bytes(rows, n), 256, y.device)
-    with _on(y):
-        check(lib().fno_checkpoint_unpack(_ptr(saved), _ptr(y), rows, n, DTYPES[dt], _stream(stream, y)),
-              "fno_checkpoint_unpack")
+    dt, td, dev, shape = _field(y, "y")
+    rows, n = _rows(shape)
+    s = _buffer("saved", saved, fno_checkpoint_bytes(rows, n), 256, dev)
+    _call("fno_checkpoint_unpack", dev, stream, s, _ptr("y", y, shape, td, dev), rows, n, DTYPES[dt])
 
 
 # --------------------------------------------------------------- channel mix
-
-def _fold(t, name):
-    """(dtype, batch, channels, pixels) of [B][C](...)."""
-    dt = _field_dtype(t, name)
-    if t.dim() < 2:
-        raise ValueError(f"{name} must be [batch][channels](...), got {tuple(t.shape)}")
-    P = 1
-    for s in t.shape[2:]:
-        P *= s
-    return dt, t.shape[0], t.shape[1], P
-
 
 def fno_channel_mix_saved_bytes(batch, c_in, c_out, pixels, act=0, has_add=False):
     """Bytes of what fno_channel_mix_save keeps."""
@@ -146,54 +166,47 @@ def fno_channel_mix_workspace_bytes(batch, c_in, c_out, pixels, dtype="f32"):
 
 def fno_channel_mix_saved_empty(x, c_out, act=0, has_add=False):
     """A device buffer (uint8 tensor) for what fno_channel_mix_save keeps."""
-    import torch
-    _, B, I, P = _fold(x, "x")
-    return torch.empty(fno_channel_mix_saved_bytes(B, I, c_out, P, act, has_add), dtype=torch.uint8, device=x.device)
+    B, I, P = _split(tuple(x.shape), "x")
+    return _empty(fno_channel_mix_saved_bytes(B, I, c_out, P, act, has_add), x)
 
 
 def fno_channel_mix_workspace_empty(x, c_out):
     """A device buffer (uint8 tensor) for the backward of a mix of x."""
-    import torch
-    dt, B, I, P = _fold(x, "x")
-    return torch.empty(fno_channel_mix_workspace_bytes(B, I, c_out, P, dt), dtype=torch.uint8, device=x.device)
+    dt, _, _, shape = _field(x, "x")
+    B, I, P = _split(shape, "x")
+    return _empty(fno_channel_mix_workspace_bytes(B, I, c_out, P, dt), x)
 
 
 def fno_channel_mix_save(x, A, bias, add, y, saved, act=0, stream=None):
     """fno_channel_mix that also keeps x (and, with GELU, add) in 8 bits in `saved`."""
-    dt, B, I, P = _fold(x, "x")
-    _, By, O, Py = _fold(y, "y")
-    _check("y", y, (B, O) + tuple(x.shape[2:]), x)
-    _check("A", A, (O, I), x)
-    _check("bias", bias, (O,), x, optional=True)
-    _check("add", add, y.shape, x, optional=True)
-    _check_buffer("saved", saved, fno_channel_mix_saved_bytes(B, I, O, P, act, add is not None), 256, x.device)
-    with _on(x):
-        check(lib().fno_channel_mix_save(_ptr(x), _ptr(A), _ptr(bias), _ptr(add), _ptr(y), _ptr(saved), B, I, O, P, act,
-                                         DTYPES[dt], _stream(stream, x)), "fno_channel_mix_save")
+    dt, td, dev, shape = _field(x, "x")
+    B, I, P = _split(shape, "x")
+    O = _split(_field(y, "y")[3], "y")[1]
+    out = (B, O) + shape[2:]
+    args = (_ptr("x", x, shape, td, dev), _ptr("A", A, (O, I), td, dev), _ptr("bias", bias, (O,), td, dev, True),
+            _ptr("add", add, out, td, dev, True), _ptr("y", y, out, td, dev),
+            _buffer("saved", saved, fno_channel_mix_saved_bytes(B, I, O, P, act, add is not None), 256, dev))
+    _call("fno_channel_mix_save", dev, stream, *args, B, I, O, P, act, DTYPES[dt])
 
 
 def fno_channel_mix_backward_saved(saved, A, bias, gy, gx, gA, gbias, gadd, workspace, act=0, has_add=False,
                                    stream=None):
     """Gradients of the channel mix at what its forward kept: gx, gA, gbias,
     gadd, each None where not wanted. workspace: fno_channel_mix_workspace_empty."""
-    dt, B, O, P = _fold(gy, "gy")
+    dt, td, dev, shape = _field(gy, "gy")
+    B, O, P = _split(shape, "gy")
+    if not isinstance(A, _t().Tensor):
+        raise TypeError("A must be a torch tensor")
     if A.dim() != 2 or A.shape[0] != O:
         raise ValueError(f"A shape {tuple(A.shape)} does not map to gy's {O} channels")
     I = A.shape[1]
-    _check("A", A, (O, I), gy)
-    _check("bias", bias, (O,), gy, optional=True)
-    _check("gx", gx, (B, I) + tuple(gy.shape[2:]), gy, optional=True)
-    _check("gA", gA, (O, I), gy, optional=True)
-    _check("gbias", gbias, (O,), gy, optional=True)
-    _check("gadd", gadd, gy.shape, gy, optional=True)
-    _check_buffer("saved", saved, fno_channel_mix_saved_bytes(B, I, O, P, act, has_add), 256, gy.device)
+    args = [_buffer("saved", saved, fno_channel_mix_saved_bytes(B, I, O, P, act, has_add), 256, dev),
+            _ptr("A", A, (O, I), td, dev), _ptr("bias", bias, (O,), td, dev, True), _ptr("gy", gy, shape, td, dev),
+            _ptr("gx", gx, (B, I) + shape[2:], td, dev, True), _ptr("gA", gA, (O, I), td, dev, True),
+            _ptr("gbias", gbias, (O,), td, dev, True), _ptr("gadd", gadd, shape, td, dev, True), None]
     if gA is not None or gbias is not None:
-        _check_buffer("workspace", workspace, fno_channel_mix_workspace_bytes(B, I, O, P, dt), 16, gy.device)
-    with _on(gy):
-        check(lib().fno_channel_mix_backward_saved(_ptr(saved), _ptr(A), _ptr(bias), _ptr(gy), _ptr(gx), _ptr(gA),
-                                                   _ptr(gbias), _ptr(gadd), _ptr(workspace), B, I, O, P, act,
-                                                   int(has_add), DTYPES[dt], _stream(stream, gy)),
-              "fno_channel_mix_backward_saved")
+        args[8] = _buffer("workspace", workspace, fno_channel_mix_workspace_bytes(B, I, O, P, dt), 16, dev)
+    _call("fno_channel_mix_backward_saved", dev, stream, *args, B, I, O, P, act, int(has_add), DTYPES[dt])
 
 
 # --------------------------------------------------------------------- norms
@@ -203,30 +216,43 @@ class NormParams:
     w_post, b_post, scale, w_pre, b_pre [C] and gate [B][C], each a tensor or
     None (weights, gate and scale then count as 1, biases as 0)."""
 
+    __slots__ = ("kind", "eps") + _NORM_NAMES
+
     def __init__(self, kind, eps, w_post=None, b_post=None, gate=None, scale=None, w_pre=None, b_pre=None):
         if kind not in NORM_KINDS:
             raise ValueError(f"kind must be one of {sorted(NORM_KINDS)}")
-        self.kind, self.eps = kind, float(eps)
+        self.kind, self.eps = kind, eps
         self.w_post, self.b_post, self.gate, self.scale = w_post, b_post, gate, scale
         self.w_pre, self.b_pre = w_pre, b_pre
+
+    def _struct(self, B, C, td, dev):
+        c = (C,)
+        return NormParamsStruct(
+            NORM_KINDS[self.kind], self.eps, _ptr("w_post", self.w_post, c, td, dev, True),
+            _ptr("b_post", self.b_post, c, td, dev, True), _ptr("gate", self.gate, (B, C), td, dev, True),
+            _ptr("scale", self.scale, c, td, dev, True), _ptr("w_pre", self.w_pre, c, td, dev, True),
+            _ptr("b_pre", self.b_pre, c, td, dev, True))
 
 
 class NormGrads:
     """Where the gradients of the parameters go; None: not wanted."""
 
+    __slots__ = _NORM_NAMES
+
     def __init__(self, w_post=None, b_post=None, gate=None, scale=None, w_pre=None, b_pre=None):
         self.w_post, self.b_post, self.gate, self.scale = w_post, b_post, gate, scale
         self.w_pre, self.b_pre = w_pre, b_pre
 
-
-def _norm_struct(obj, cls, like, B, C):
-    shapes = {n: (B, C) if n == "gate" else (C,) for n in _NORM_NAMES}
-    for n in _NORM_NAMES:
-        _check(n if cls is NormParamsStruct else f"gradient of {n}", getattr(obj, n), shapes[n], like, optional=True)
-    ptrs = {n: _ptr(getattr(obj, n)) for n in _NORM_NAMES}
-    if cls is NormParamsStruct:
-        return cls(NORM_KINDS[obj.kind], obj.eps, **ptrs)
-    return cls(**ptrs)
+    def _struct(self, B, C, td, dev):
+        """(the C struct, whether any gradient is wanted)"""
+        c = (C,)
+        p = (_ptr("gradient of w_post", self.w_post, c, td, dev, True),
+             _ptr("gradient of b_post", self.b_post, c, td, dev, True),
+             _ptr("gradient of gate", self.gate, (B, C), td, dev, True),
+             _ptr("gradient of scale", self.scale, c, td, dev, True),
+             _ptr("gradient of w_pre", self.w_pre, c, td, dev, True),
+             _ptr("gradient of b_pre", self.b_pre, c, td, dev, True))
+        return NormGradsStruct(*p), p != (None,) * 6
 
 
 def fno_norm_residual_saved_bytes(batch, channels, pixels):
@@ -241,36 +267,29 @@ def fno_norm_residual_workspace_bytes(batch, channels, pixels, dtype="f32"):
 
 def fno_norm_residual_saved_empty(x):
     """A device buffer (uint8 tensor) for the checkpoints of a field or of tokens shaped like x."""
-    import torch
-    _, B, C, P = _fold(x, "x")
-    return torch.empty(fno_norm_residual_saved_bytes(B, C, P), dtype=torch.uint8, device=x.device)
+    return _empty(fno_norm_residual_saved_bytes(*_split(tuple(x.shape), "x")), x)
 
 
 def fno_norm_residual_workspace_empty(x):
     """A device buffer (uint8 tensor) for the backward of a call on x."""
-    import torch
-    dt, B, C, P = _fold(x, "x")
-    return torch.empty(fno_norm_residual_workspace_bytes(B, C, P, dt), dtype=torch.uint8, device=x.device)
+    dt, _, _, shape = _field(x, "x")
+    return _empty(fno_norm_residual_workspace_bytes(*_split(shape, "x"), dt), x)
 
 
 def _norm_forward(fn, prm, x, v, y, u, saved, stream):
-    dt, B, C, P = _fold(x, "x")
-    _check("v", v, x.shape, x)
-    _check("y", y, x.shape, x)
-    _check("u", u, x.shape, x, optional=True)
-    st = _norm_struct(prm, NormParamsStruct, x, B, C)
-    args = [_ptr(x), _ptr(v), _ptr(y), _ptr(u)]
-    if fn == "fno_norm_residual_save":
-        _check_buffer("saved", saved, fno_norm_residual_saved_bytes(B, C, P), 256, x.device)
-        args.append(_ptr(saved))
-    with _on(x):
-        check(getattr(lib(), fn)(ctypes.byref(st), *args, B, C, P, DTYPES[dt], _stream(stream, x)), fn)
+    dt, td, dev, shape = _field(x, "x")
+    B, C, P = _split(shape, "x")
+    args = [_ptr("x", x, shape, td, dev), _ptr("v", v, shape, td, dev), _ptr("y", y, shape, td, dev),
+            _ptr("u", u, shape, td, dev, True)]
+    if saved is not False:
+        args.append(_buffer("saved", saved, fno_norm_residual_saved_bytes(B, C, P), 256, dev))
+    _call(fn, dev, stream, prm._struct(B, C, td, dev), *args, B, C, P, DTYPES[dt])
 
 
 def fno_norm_residual(params, x, v, y, u, stream=None):
     """y = x + scale gate N_post(v), u = N_pre(y) over the channels of
     [B][C](...) fields or [B][C] tokens; u may be None."""
-    _norm_forward("fno_norm_residual", params, x, v, y, u, None, stream)
+    _norm_forward("fno_norm_residual", params, x, v, y, u, False, stream)
 
 
 def fno_norm_residual_save(params, x, v, y, u, saved, stream=None):
@@ -278,32 +297,29 @@ def fno_norm_residual_save(params, x, v, y, u, saved, stream=None):
     _norm_forward("fno_norm_residual_save", params, x, v, y, u, saved, stream)
 
 
-def _norm_backward(fn, prm, first, gy, gu, gx, gv, grads, workspace, stream):
-    dt, B, C, P = _fold(gy, "gy")
-    grads = NormGrads() if grads is None else grads
-    for name, t in (("gu", gu), ("gx", gx), ("gv", gv)):
-        _check(name, t, gy.shape, gy, optional=True)
-    st = _norm_struct(prm, NormParamsStruct, gy, B, C)
-    gr = _norm_struct(grads, NormGradsStruct, gy, B, C)
-    if any(getattr(grads, n) is not None for n in _NORM_NAMES):
-        _check_buffer("workspace", workspace, fno_norm_residual_workspace_bytes(B, C, P, dt), 16, gy.device)
-    if fn == "fno_norm_residual_backward":
-        for name, t in zip("xv", first):
-            _check(name, t, gy.shape, gy)
+def _norm_backward(fn, prm, x, v, saved, gy, gu, gx, gv, grads, workspace, stream):
+    dt, td, dev, shape = _field(gy, "gy")
+    B, C, P = _split(shape, "gy")
+    args = [_ptr("gy", gy, shape, td, dev)] + [_ptr(n, t, shape, td, dev, True)
+                                               for n, t in (("gu", gu), ("gx", gx), ("gv", gv))]
+    if saved is False:
+        args = [_ptr("x", x, shape, td, dev), _ptr("v", v, shape, td, dev)] + args
     else:
-        _check_buffer("saved", first[0], fno_norm_residual_saved_bytes(B, C, P), 256, gy.device)
-    with _on(gy):
-        check(getattr(lib(), fn)(ctypes.byref(st), *(_ptr(t) for t in first), _ptr(gy), _ptr(gu), _ptr(gx), _ptr(gv),
-                                 ctypes.byref(gr), _ptr(workspace), B, C, P, DTYPES[dt], _stream(stream, gy)), fn)
+        args.insert(0, _buffer("saved", saved, fno_norm_residual_saved_bytes(B, C, P), 256, dev))
+    st = prm._struct(B, C, td, dev)
+    gr, any_ = (NormGradsStruct(), False) if grads is None else grads._struct(B, C, td, dev)
+    ws = _buffer("workspace", workspace, fno_norm_residual_workspace_bytes(B, C, P, dt), 16, dev) if any_ else None
+    _call(fn, dev, stream, st, *args, gr, ws, B, C, P, DTYPES[dt])
 
 
 def fno_norm_residual_backward(params, x, v, gy, gu, gx, gv, grads, workspace, stream=None):
     """Gradients of fno_norm_residual at gy = dL/dy, gu = dL/du (None: none
     through u): gx, gv (None: not wanted) and those named in grads (NormGrads or
     None). workspace: fno_norm_residual_workspace_empty."""
-    _norm_backward("fno_norm_residual_backward", params, (x, v), gy, gu, gx, gv, grads, workspace, stream)
+    _norm_backward("fno_norm_residual_backward", params, x, v, False, gy, gu, gx, gv, grads, workspace, stream)
 
 
 def fno_norm_residual_backward_saved(params, saved, gy, gu, gx, gv, grads, workspace, stream=None):
     """fno_norm_residual_backward at the x and v read back from `saved`."""
-    _norm_backward("fno_norm_residual_backward_saved", params, (saved,), gy, gu, gx, gv, grads, workspace, stream)
+    _norm_backward("fno_norm_residual_backward_saved", params, None, None, saved, gy, gu, gx, gv, grads, workspace,
+                   stream)
