@@ -510,7 +510,8 @@ typedef struct {
 } fno_norm_grads_t;
 
 /* u may be NULL (no norm follows). channels <= 512 (pixels > 1) or <= 8192
- * (pixels = 1), batch <= 65535 where pixels > 1, else UNSUPPORTED.
+ * (pixels = 1), batch <= 65535 where pixels > 1, pixels <= 2^27, else
+ * UNSUPPORTED.
  * fno_norm_residual_save also leaves the 8-bit checkpoints of x and then of v
  * in `saved` (fno_norm_residual_saved_bytes, 256-byte aligned), rows along
  * the contiguous axis: [batch * channels][pixels], tokens [batch][channels]. */

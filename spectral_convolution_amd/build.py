@@ -19,9 +19,9 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfno.so")
 
 SOURCES = ["plane_kernels.hip", "plane_mfma.hip", "axis_kernels.hip", "contract.hip", "contract_mx.hip", "backward.hip", "weights.hip", "pointwise.hip", "fused.hip", "fno_api.cpp",
-           "fno_model.cpp", "checkpoint.hip", "norm.hip", "mix_train.hip",
+           "fno_model.cpp", "checkpoint.hip", "norm.hip", "norm_f32.hip", "norm_f16.hip", "norm_bf16.hip", "mix_train.hip",
            "fno_train.cpp"]
-HEADERS = ["common.hpp", "fft_reg.hpp", "plane_common.hpp", "plane_valu.hpp", "plane_mfma.hpp", "contract.hpp", "checkpoint.hpp", "gelu.hpp"]
+HEADERS = ["common.hpp", "fft_reg.hpp", "plane_common.hpp", "plane_valu.hpp", "plane_mfma.hpp", "contract.hpp", "checkpoint.hpp", "gelu.hpp", "norm_common.hpp", "norm_field.hpp", "norm_token.hpp"]
 
 ARCH = "gfx950"
 CFLAGS = [
@@ -50,7 +50,7 @@ def _compile(src, verbose):
     return obj
 
 
-def build(verbose: bool = False, jobs: int = 4) -> str:
+def build(verbose: bool = False, jobs: int = 8) -> str:
     """Compile every source and link libfno.so; returns the library path."""
     os.makedirs(BUILD, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:

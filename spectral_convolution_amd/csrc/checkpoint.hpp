@@ -86,11 +86,15 @@ __device__ __forceinline__ ck_u32x4 ck_load(const void *p, size_t i, long n) {
   } else {
     const uint16_t *s = reinterpret_cast<const uint16_t *>(p) + i;
     if (n >= 8) return *reinterpret_cast<const ck_u32x4_any *>(s);
-    ck_u32x4 r{0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int e = 0; e < 7; ++e)
-      if (e < n) r[e >> 1] |= (uint32_t)s[e] << (16 * (e & 1));
-    return r;
+    // a row's tail: one element at a time through a 128-bit shift, small code
+    // where every access of a kernel has such a path
+    uint64_t lo = 0, hi = 0;
+#pragma unroll 1
+    for (int e = (int)n - 1; e >= 0; --e) {
+      hi = hi << 16 | lo >> 48;
+      lo = lo << 16 | s[e];
+    }
+    return ck_u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
   }
 }
 
@@ -110,10 +114,81 @@ __device__ __forceinline__ void ck_store(void *p, size_t i, long n, const ck_u32
     if (n >= 8) {
       *reinterpret_cast<ck_u32x4_any *>(d) = r;
     } else {
-#pragma unroll
-      for (int e = 0; e < 7; ++e)
-        if (e < n) d[e] = (uint16_t)(r[e >> 1] >> (16 * (e & 1)));
+      uint64_t lo = (uint64_t)r[1] << 32 | r[0], hi = (uint64_t)r[3] << 32 | r[2];
+#pragma unroll 1
+      for (int e = 0; e < (int)n; ++e) {
+        d[e] = (uint16_t)lo;
+        lo = lo >> 16 | hi << 48;
+        hi >>= 16;
+      }
     }
+  }
+}
+
+// 128-bit shifts by whole bytes; 16 or more leave nothing
+__device__ __forceinline__ ck_u32x4 ck_shift(const ck_u32x4 &r, int bytes, bool left) {
+  uint64_t lo = (uint64_t)r[1] << 32 | r[0], hi = (uint64_t)r[3] << 32 | r[2];
+  if (left) {  // as a right shift of the halves exchanged and mirrored
+    const bool far = bytes >= 8;
+    const int s = 8 * (bytes & 7);
+    uint64_t h = far ? lo : hi, l = far ? 0 : lo;
+    h = h << s | (s ? l >> (64 - s) : 0);
+    l <<= s;
+    lo = bytes >= 16 ? 0 : l;
+    hi = bytes >= 16 ? 0 : h;
+  } else {
+    const bool far = bytes >= 8;
+    const int s = 8 * (bytes & 7);
+    uint64_t l = far ? hi : lo, h = far ? 0 : hi;
+    l = l >> s | (s ? h << (64 - s) : 0);
+    h >>= s;
+    lo = bytes >= 16 ? 0 : l;
+    hi = bytes >= 16 ? 0 : h;
+  }
+  return ck_u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+}
+
+// The elements at i .. of a row that ends before element `end` of a field of
+// `total` elements, zeros past the row's end (all zeros for i >= end). Where 16
+// bytes from i would pass the end, the last 16 bytes of the row (or, in a
+// field's first few elements, its first) are read and moved into place: one
+// access on every path, so the tails of a kernel need no branches of their
+// own and never read outside the field. TINY: the field may be smaller than 16
+// bytes in all.
+template <int DT, bool TINY>
+__device__ __forceinline__ ck_u32x4 ck_load_row(const void *p, long i, long end, long total) {
+  constexpr int V = ck_vec<DT>(), ES = DT == DT_F32 ? 4 : 2;
+  if (TINY && total < V) return ck_load<DT>(p, i < end ? i : 0, end - i);
+  const long at = min(i, max(end - V, 0L));
+  ck_u32x4 r = *reinterpret_cast<const ck_u32x4_any *>(static_cast<const char *>(p) + at * ES);
+  if (end < V) r = ck_shift(r, (int)(V - end) * ES, true);  // drop what follows the row
+  return ck_shift(r, (int)min(16L, (i - min(i, end - V)) * ES), false);
+}
+
+// the first n of the elements to p[i] .. (n <= 0: none)
+template <int DT>
+__device__ __forceinline__ void ck_store_row(void *p, size_t i, long n, const ck_u32x4 &r) {
+  typedef unsigned u32_any __attribute__((aligned(2)));
+  typedef unsigned u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
+  constexpr int V = ck_vec<DT>(), ES = DT == DT_F32 ? 4 : 2;
+  char *d = static_cast<char *>(p) + i * ES;
+  if (n >= V) {
+    *reinterpret_cast<ck_u32x4_any *>(d) = r;
+  } else if (n > 0) {
+    const int bytes = (int)n * ES;
+    uint32_t a = r[0], b = r[1];
+    if (bytes & 8) {
+      *reinterpret_cast<u32x2_any *>(d) = u32x2_any{a, b};
+      d += 8;
+      a = r[2];
+      b = r[3];
+    }
+    if (bytes & 4) {
+      *reinterpret_cast<u32_any *>(d) = a;
+      d += 4;
+      a = b;
+    }
+    if (ES == 2 && (bytes & 2)) *reinterpret_cast<uint16_t *>(d) = (uint16_t)a;
   }
 }
 

@@ -252,6 +252,7 @@ struct NormArgs {
   void *gx, *gv;             // NULL: not wanted
   void *g_w_post, *g_b_post, *g_gate, *g_scale, *g_w_pre, *g_b_pre;  // NULL: not wanted
   float *part;               // runs' sums; NULL when no parameter gradient is wanted
+  int per;                   // fields: tiles of a run (set by the launcher)
 };
 
 // Channel mix of a training step (mix_train.hip): [B][I][P] -> [B][O][P].
@@ -351,6 +352,7 @@ hipError_t launch_block_rows(const uint16_t *zg, const signed char *zexp, const 
                              int act, int dtype, hipStream_t s);
 hipError_t launch_checkpoint(const CkArgs &a, bool pack, int dtype, hipStream_t s);
 constexpr int kNormMaxField = 512;   // norms: channels of a field (P > 1)
+constexpr long kNormMaxPixels = 1L << 27;  // lane offsets of 7 rows fit 32 bits
 constexpr int kNormMaxToken = 8192;  // channels of a token (P = 1)
 size_t norm_workspace_bytes(int B, int C, long P, int dtype);
 hipError_t launch_norm_fwd(const NormArgs &a, int dtype, hipStream_t s);

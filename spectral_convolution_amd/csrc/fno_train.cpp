@@ -100,7 +100,7 @@ fno_status_t norm_shape(const fno_norm_params_t *p, int batch, int channels, lon
     return FNO_ERR_INVALID_ARG;
   if (batch < 1 || channels < 1 || pixels < 1 || !valid_dtype(dtype)) return FNO_ERR_INVALID_ARG;
   if (channels > (pixels == 1 ? kNormMaxToken : kNormMaxField)) return FNO_ERR_UNSUPPORTED;
-  if ((pixels > 1 && batch > 65535) || pixels > kMaxRow || !values_in_range(batch, channels, pixels))
+  if ((pixels > 1 && batch > 65535) || pixels > kNormMaxPixels || !values_in_range(batch, channels, pixels))
     return FNO_ERR_UNSUPPORTED;
   return FNO_OK;
 }

@@ -1,0 +1,17 @@
+// norm_bf16.hip - the norm kernels of bf16 fields and tokens (norm.hip launches them).
+
+#include "norm_field.hpp"
+#include "norm_token.hpp"
+
+namespace fno {
+
+const void *norm_kernel_bf16(bool tok, int kind, bool fwd, int C, int &threads, int &rpg) {
+  if (tok)
+    return kind == kLayer ? tok_kernel<DT_BF16, kLayer>(fwd, C, threads, rpg) : tok_kernel<DT_BF16, kRms>(fwd, C, threads, rpg);
+  const int w = field_waves(C);
+  threads = w == 1 ? 256 : 64 * w;
+  rpg = w == 1 ? 4 : 1;
+  return kind == kLayer ? field_kernel<DT_BF16, kLayer>(fwd, C) : field_kernel<DT_BF16, kRms>(fwd, C);
+}
+
+}  // namespace fno

@@ -1,0 +1,509 @@
+// norm_field.hpp - forward and backward of the norms around a block on fields
+// (norm.hip has the mathematics and the design).
+#pragma once
+
+#include "norm_common.hpp"
+
+namespace fno {
+
+// {scale gate w_post, scale gate b_post, w_pre, b_pre} of the channels of sample b
+template <int DT>
+__device__ __forceinline__ void norm_table(const NormArgs &a, int b, int n, float4 *tab) {
+  for (int c = threadIdx.x; c < n; c += blockDim.x) {
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (c < a.C) {
+      const float sg = param(a.scale, DT, c, 1.f) * param(a.gate, DT, (size_t)b * a.C + c, 1.f);
+      t = make_float4(sg * param(a.w_post, DT, c, 1.f), sg * param(a.b_post, DT, c, 0.f), param(a.w_pre, DT, c, 1.f),
+                      param(a.b_pre, DT, c, 0.f));
+    }
+    tab[c] = t;
+  }
+}
+
+// The pieces of a tile that a wave holds: its k-th group of 8 channels is group
+// k WPT + (wave in tile), so only the last one can reach past the channels. Lane l
+// has the 16 bytes of channel l / 8 of each group and of pixels V (l % 8) .. of the tile: a
+// uniform base (sample, group, tile) plus one 32-bit offset that no loop
+// changes, so an access takes no address registers of its own (P <= 2^27
+// keeps 7 rows inside 32 bits).
+template <int DT, int CPT, int WPT>
+struct FieldTile {
+  static constexpr int V = ck_vec<DT>(), PX = 8 * V, ES = DT == DT_F32 ? 4 : 2;
+  long P, nb, rows;  // row length, its blocks, rows of the whole field
+  int sample, channels;
+  int first;      // the wave's first group
+  int last;       // its last group, or the field's where it has none
+  int cl, clast;  // channel within a group, within the last one (clamped to the field's)
+  int pl;
+  bool ok;        // the lane's channel of the last group exists
+  uint32_t off, off_last, code, code_last, exp, exp_last;
+
+  __device__ __forceinline__ FieldTile(const NormArgs &a, int b, int lane, int w) {
+    P = a.P;
+    nb = (P + kCkBlock - 1) / kCkBlock;
+    sample = b;
+    channels = a.C;
+    rows = (long)a.B * a.C;
+    first = w;
+    const int g = (CPT - 1) * WPT + w;
+    last = min(g, (a.C - 1) / 8);
+    cl = lane >> 3;
+    pl = lane & 7;
+    clast = min(cl, a.C - 1 - 8 * last);
+    ok = 8 * g + cl < a.C;
+    off = (uint32_t)cl * (uint32_t)P * ES + 16u * pl;
+    off_last = (uint32_t)clast * (uint32_t)P * ES + 16u * pl;
+    code = (uint32_t)cl * (uint32_t)nb * kCkBlock + (uint32_t)V * pl;
+    code_last = (uint32_t)clast * (uint32_t)nb * kCkBlock + (uint32_t)V * pl;
+    exp = (uint32_t)cl * (uint32_t)nb + (uint32_t)V * pl / kCkBlock;
+    exp_last = (uint32_t)clast * (uint32_t)nb + (uint32_t)V * pl / kCkBlock;
+  }
+  // The tile being worked on: uniform byte offsets of the wave's first and last
+  // groups in a field, its codes and its exponents. The lane offsets (and
+  // the row length) pass through an opaque move, or the compiler adds them to
+  // every base ahead of the loop and keeps the sums (40 register pairs in the
+  // backward, spilled).
+  size_t f0, f1, c0, c1, e0, e1;
+  __device__ __forceinline__ void at(int t) {
+    asm volatile("" : "+v"(off), "+v"(off_last), "+v"(code), "+v"(code_last), "+v"(exp), "+v"(exp_last));
+    uint32_t p = (uint32_t)P;
+    asm volatile("" : "+v"(p));
+    P = __builtin_amdgcn_readfirstlane(p);
+    nb = (P + kCkBlock - 1) / kCkBlock;
+    const size_t r = (size_t)sample * channels;
+    const size_t first_row = r + 8 * first, last_row = r + 8 * last;
+    f0 = (first_row * P + (long)t * PX) * ES;
+    f1 = (last_row * P + (long)t * PX) * ES;
+    c0 = first_row * nb * kCkBlock + (long)t * PX;
+    c1 = last_row * nb * kCkBlock + (long)t * PX;
+    e0 = first_row * nb + (long)t * (PX / kCkBlock);
+    e1 = last_row * nb + (long)t * (PX / kCkBlock);
+  }
+  __device__ __forceinline__ size_t field_at(int k) const { return k < CPT - 1 ? f0 + (size_t)k * 8 * WPT * P * ES : f1; }
+  __device__ __forceinline__ size_t code_at(int k) const { return k < CPT - 1 ? c0 + (size_t)k * 8 * WPT * nb * kCkBlock : c1; }
+  __device__ __forceinline__ size_t exp_at(int k) const { return k < CPT - 1 ? e0 + (size_t)k * 8 * WPT * nb : e1; }
+  __device__ __forceinline__ size_t row(int k) const {
+    return (size_t)sample * channels + 8 * (k < CPT - 1 ? k * WPT + first : last);
+  }
+  // whether the lane's channel of group k exists, and its place in the channel table
+  __device__ __forceinline__ bool has(int k) const { return k < CPT - 1 || ok; }
+  __device__ __forceinline__ int channel(int k) const { return 8 * (k * WPT + first) + cl; }
+
+  __device__ __forceinline__ ck_u32x4 only(int k, const ck_u32x4 &r) const {
+    return k < CPT - 1 || ok ? r : ck_u32x4{0u, 0u, 0u, 0u};
+  }
+  // The addresses of a row's last tile are computed there, not kept from before
+  // the loop over the tiles: two registers for each access of the kernel.
+  static __device__ __forceinline__ int here(int c) {
+    asm volatile("" : "+v"(c));
+    return c;
+  }
+  // a tile that lies within the row
+  __device__ __forceinline__ ck_u32x4 load(const void *f, int t, int k) const {
+    const char *s = static_cast<const char *>(f) + field_at(k);
+    return only(k, *reinterpret_cast<const ck_u32x4_any *>(s + (k < CPT - 1 ? off : off_last)));
+  }
+  // the row's last tile, zeros past its end
+  __device__ __forceinline__ ck_u32x4 load_end(const void *f, int t, int k) const {
+    const long r = (long)row(k) + here(k < CPT - 1 ? cl : clast);
+    return only(k, ck_load_row<DT, CPT == 1>(f, r * P + (long)t * PX + pl * V, (r + 1) * P, P * rows));
+  }
+  __device__ __forceinline__ void store(void *f, int t, int k, bool whole, const ck_u32x4 &r) const {
+    if (!has(k)) return;
+    if (whole) {
+      char *d = static_cast<char *>(f) + field_at(k);
+      *reinterpret_cast<ck_u32x4_any *>(d + (k < CPT - 1 ? off : off_last)) = r;
+    } else {
+      ck_store_row<DT>(f, (row(k) + here(cl)) * P + (long)t * PX + pl * V, P - ((long)t * PX + pl * V), r);
+    }
+  }
+  // whether the lane's piece begins inside the row's blocks
+  __device__ __forceinline__ bool coded(int t) const { return (long)t * PX + pl * V < nb * kCkBlock; }
+  __device__ __forceinline__ ck_u32x4 decode(const uint8_t *q, const int8_t *e, int t, int k) const {
+    const uint8_t *s = q + code_at(k);
+    uint2 c = make_uint2(0u, 0u);
+    int x = 0;
+    if (coded(t)) {
+      if constexpr (DT == DT_F32) c.x = *reinterpret_cast<const uint32_t *>(s + (k < CPT - 1 ? code : code_last));
+      else c = *reinterpret_cast<const uint2 *>(s + (k < CPT - 1 ? code : code_last));
+      x = (e + exp_at(k))[k < CPT - 1 ? exp : exp_last];
+    }
+    return only(k, ck_decode<DT>(c, x));
+  }
+  __device__ __forceinline__ void encode(const ck_u32x4 &r, uint8_t *q, int8_t *e, int t, int k) const {
+    constexpr int L = kCkBlock / V;  // lanes of a block
+    const int ex = ck_exponent<DT>(ck_groupmax<L>(ck_maxkey<DT>(r)));
+    const uint2 c = ck_codes<DT>(r, ex);
+    if (!has(k) || !coded(t)) return;
+    uint8_t *d = q + code_at(k);
+    if constexpr (DT == DT_F32) *reinterpret_cast<uint32_t *>(d + code) = c.x;
+    else *reinterpret_cast<uint2 *>(d + code) = c;
+    if (pl % L == 0) (e + exp_at(k))[exp] = (int8_t)ex;
+  }
+};
+
+template <int DT, int CPT, int WPT, int KIND>
+__global__ __launch_bounds__(norm_threads<WPT>()) void fno_norm_fwd(NormArgs a) {
+  constexpr int V = ck_vec<DT>(), PX = 8 * V, WAVES = norm_threads<WPT>() / 64, TPG = WAVES / WPT, NC = 8 * CPT * WPT;
+  __shared__ float4 tab[NC];
+  __shared__ float red[WPT > 1 ? 2 * WAVES * 2 * PX : 1];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), b = blockIdx.y;
+  norm_table<DT>(a, b, NC, tab);
+  __syncthreads();
+  const int t0 = blockIdx.x * a.per, t1 = min((int)((a.P + PX - 1) / PX), t0 + a.per);
+  FieldTile<DT, CPT, WPT> tile(a, b, lane, wave % WPT);
+  const float invC = 1.f / (float)a.C;
+  int turn = 0;
+  for (int t = t0 + wave / WPT; t < t1; t += TPG) {
+    const bool whole = (t + 1L) * PX <= a.P;
+    tile.at(t);
+    ck_u32x4 vr[CPT], xr[CPT];
+    if (whole) {
+#pragma unroll
+      for (int k = 0; k < CPT; ++k) {
+        vr[k] = tile.load(a.v, t, k);
+        xr[k] = tile.load(a.x, t, k);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < CPT; ++k) {
+        vr[k] = tile.load_end(a.v, t, k);
+        xr[k] = tile.load_end(a.x, t, k);
+      }
+    }
+    if (a.vq) {
+#pragma unroll
+      for (int k = 0; k < CPT; ++k) {
+        tile.encode(vr[k], a.vq, a.ve, t, k);
+        tile.encode(xr[k], a.xq, a.xe, t, k);
+      }
+    }
+    fresh<DT>(vr);
+    float s[1][V], o[1][V / 4], m[V], r[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) m[e] = 0.f;
+    if constexpr (KIND == kLayer) {
+      channel_sum<V, CPT, false>(s[0], [&](int k, int e) { return ck_get<DT>(vr[k], e); });
+      fold<V>(s[0], o[0]);
+      Join<1, V, WPT>::run(o, red, turn, wave, lane);
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i) o[0][i] /= (float)a.C;
+      unfold<V>(o[0], m);
+      fresh<DT>(vr);
+    }
+    channel_sum<V, CPT, true>(s[0], [&](int k, int e) {
+      const float d = ck_get<DT>(vr[k], e) - m[e];
+      return KIND == kLayer && !tile.has(k) ? 0.f : d;
+    });
+    fold<V>(s[0], o[0]);
+    Join<1, V, WPT>::run(o, red, turn, wave, lane);
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) o[0][i] = rsq(fmaf(o[0][i], invC, a.eps));
+    unfold<V>(o[0], r);
+    fresh<DT>(vr);
+    float y[CPT][V];
+#pragma unroll
+    for (int k = 0; k < CPT; ++k) {
+      const float4 w = tab[tile.channel(k)];
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        y[k][e] = ck_get<DT>(xr[k], e) + fmaf((ck_get<DT>(vr[k], e) - m[e]) * r[e], w.x, w.y);
+      tile.store(a.y, t, k, whole, ck_raw<DT>(y[k]));
+    }
+    if (a.u) {
+      if constexpr (KIND == kLayer) {
+        channel_sum<V, CPT, false>(s[0], [&](int k, int e) { return y[k][e]; });
+        fold<V>(s[0], o[0]);
+        Join<1, V, WPT>::run(o, red, turn, wave, lane);
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) o[0][i] /= (float)a.C;
+        unfold<V>(o[0], m);
+      }
+      channel_sum<V, CPT, true>(s[0], [&](int k, int e) {
+        const float d = y[k][e] - m[e];
+        return KIND == kLayer && !tile.has(k) ? 0.f : d;
+      });
+      fold<V>(s[0], o[0]);
+      Join<1, V, WPT>::run(o, red, turn, wave, lane);
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i) o[0][i] = rsq(fmaf(o[0][i], invC, a.eps));
+      unfold<V>(o[0], r);
+#pragma unroll
+      for (int k = 0; k < CPT; ++k) {
+          const float4 w = tab[tile.channel(k)];
+        float u[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) u[e] = fmaf((y[k][e] - m[e]) * r[e], w.z, w.w);
+        tile.store(a.u, t, k, whole, ck_raw<DT>(u));
+      }
+    }
+  }
+}
+
+// Backward of a field. The wave's registers hold v, gy and gu as stored and y
+// (then gx) in fp32; v^ is formed again from v where it is needed.
+template <int DT, int CPT, int WPT, int KIND>
+__global__ __launch_bounds__(norm_threads<WPT>()) __attribute__((amdgpu_waves_per_eu(2))) void fno_norm_bwd(NormArgs a) {
+  constexpr int V = ck_vec<DT>(), PX = 8 * V, WAVES = norm_threads<WPT>() / 64, TPG = WAVES / WPT, NC = 8 * CPT * WPT;
+  __shared__ float4 tab[NC];
+  __shared__ float4 accs[CPT * 64 * WAVES];
+  __shared__ float red[WPT > 1 ? 2 * WAVES * 2 * PX : 1];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), b = blockIdx.y;
+  norm_table<DT>(a, b, NC, tab);
+  __syncthreads();
+  const int t0 = blockIdx.x * a.per, t1 = min((int)((a.P + PX - 1) / PX), t0 + a.per);
+  FieldTile<DT, CPT, WPT> tile(a, b, lane, wave % WPT);
+  const float invC = 1.f / (float)a.C;
+  int turn = 0;
+  float *acc = reinterpret_cast<float *>(accs) + threadIdx.x;  // this thread's sums: acc[(4 k + q) threads]
+#pragma unroll
+  for (int i = 0; i < 4 * CPT; ++i) acc[i * (64 * WAVES)] = 0.f;
+  auto add = [&](int k, int q, float v) {
+    __hip_atomic_fetch_add(acc + (4 * k + q) * (64 * WAVES), v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT);
+  };
+  for (int t = t0 + wave / WPT; t < t1; t += TPG) {
+    const bool whole = (t + 1L) * PX <= a.P;
+    tile.at(t);
+    ck_u32x4 vr[CPT], xr[CPT], gyr[CPT], gur[CPT];
+    if (a.vq) {
+#pragma unroll
+      for (int k = 0; k < CPT; ++k) {
+        vr[k] = tile.decode(a.vq, a.ve, t, k);
+        xr[k] = tile.decode(a.xq, a.xe, t, k);
+      }
+    } else if (whole) {
+#pragma unroll
+      for (int k = 0; k < CPT; ++k) {
+        vr[k] = tile.load(a.v, t, k);
+        xr[k] = tile.load(a.x, t, k);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < CPT; ++k) {
+        vr[k] = tile.load_end(a.v, t, k);
+        xr[k] = tile.load_end(a.x, t, k);
+      }
+    }
+    const void *gu = a.gu ? a.gu : a.gy;  // without gu its values are not used
+    if (whole) {
+#pragma unroll
+      for (int k = 0; k < CPT; ++k) {
+        gur[k] = tile.load(gu, t, k);
+        gyr[k] = tile.load(a.gy, t, k);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < CPT; ++k) {
+        gur[k] = tile.load_end(gu, t, k);
+        gyr[k] = tile.load_end(a.gy, t, k);
+      }
+    }
+    fresh<DT>(vr);
+    float s[1][V], o[1][V / 4], m[V], r[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) m[e] = 0.f;
+    if constexpr (KIND == kLayer) {
+      channel_sum<V, CPT, false>(s[0], [&](int k, int e) { return ck_get<DT>(vr[k], e); });
+      fold<V>(s[0], o[0]);
+      Join<1, V, WPT>::run(o, red, turn, wave, lane);
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i) o[0][i] /= (float)a.C;
+      unfold<V>(o[0], m);
+      fresh<DT>(vr);
+    }
+    channel_sum<V, CPT, true>(s[0], [&](int k, int e) {
+      const float d = ck_get<DT>(vr[k], e) - m[e];
+      return KIND == kLayer && !tile.has(k) ? 0.f : d;
+    });
+    fold<V>(s[0], o[0]);
+    Join<1, V, WPT>::run(o, red, turn, wave, lane);
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) o[0][i] = rsq(fmaf(o[0][i], invC, a.eps));
+    unfold<V>(o[0], r);
+    fresh<DT>(vr);
+    float y[CPT][V];
+    if (a.gu) {
+      float my[V], ry[V];
+#pragma unroll
+      for (int k = 0; k < CPT; ++k) {
+        const float4 w = tab[tile.channel(k)];
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          y[k][e] = ck_get<DT>(xr[k], e) + fmaf((ck_get<DT>(vr[k], e) - m[e]) * r[e], w.x, w.y);
+        channel_done();
+      }
+#pragma unroll
+      for (int e = 0; e < V; ++e) my[e] = 0.f;
+      if constexpr (KIND == kLayer) {
+        channel_sum<V, CPT, false>(s[0], [&](int k, int e) { return y[k][e]; });
+        fold<V>(s[0], o[0]);
+        Join<1, V, WPT>::run(o, red, turn, wave, lane);
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) o[0][i] /= (float)a.C;
+        unfold<V>(o[0], my);
+      }
+      channel_sum<V, CPT, true>(s[0], [&](int k, int e) {
+        const float d = y[k][e] - my[e];
+        return KIND == kLayer && !tile.has(k) ? 0.f : d;
+      });
+      fold<V>(s[0], o[0]);
+      Join<1, V, WPT>::run(o, red, turn, wave, lane);
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i) o[0][i] = rsq(fmaf(o[0][i], invC, a.eps));
+      unfold<V>(o[0], ry);
+      float q[2][V], oq[2][V / 4];
+#pragma unroll
+      for (int e = 0; e < V; ++e) q[0][e] = q[1][e] = 0.f;
+#pragma unroll
+      for (int k = 0; k < CPT; ++k) {
+        const float wp = tab[tile.channel(k)].z;
+        float sU = 0.f, sV = 0.f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const float gu = ck_get<DT>(gur[k], e), yh = (y[k][e] - my[e]) * ry[e];
+          y[k][e] = yh;
+          sU = fmaf(gu, yh, sU);
+          sV += gu;
+          q[0][e] = fmaf(gu * wp, yh, q[0][e]);
+          if (KIND == kLayer) q[1][e] = fmaf(gu, wp, q[1][e]);
+        }
+        add(k, 2, sU);
+        add(k, 3, sV);
+        channel_done();
+      }
+      fresh<DT>(gur);
+      fold<V>(q[0], oq[0]);
+      if (KIND == kLayer) fold<V>(q[1], oq[1]);
+      else
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) oq[1][i] = 0.f;
+      Join<2, V, WPT>::run(oq, red, turn, wave, lane);
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i) {
+        oq[0][i] *= invC;
+        oq[1][i] *= invC;
+      }
+      unfold<V>(oq[0], q[0]);
+      if (KIND == kLayer) unfold<V>(oq[1], q[1]);
+#pragma unroll
+      for (int k = 0; k < CPT; ++k) {
+        const float wp = tab[tile.channel(k)].z;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          float g = fmaf(-y[k][e], q[0][e], ck_get<DT>(gur[k], e) * wp);
+          if (KIND == kLayer) g -= q[1][e];
+          y[k][e] = fmaf(ry[e], g, ck_get<DT>(gyr[k], e));
+        }
+        channel_done();
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < CPT; ++k)
+#pragma unroll
+        for (int e = 0; e < V; ++e) y[k][e] = ck_get<DT>(gyr[k], e);
+    }
+    // y holds gx
+    fresh<DT>(vr);
+    float q[2][V], oq[2][V / 4];
+#pragma unroll
+    for (int e = 0; e < V; ++e) q[0][e] = q[1][e] = 0.f;
+#pragma unroll
+    for (int k = 0; k < CPT; ++k) {
+      const float w = tab[tile.channel(k)].x;
+      if (a.gx) tile.store(a.gx, t, k, whole, ck_raw<DT>(y[k]));
+      float sT = 0.f, sG = 0.f;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float vh = (ck_get<DT>(vr[k], e) - m[e]) * r[e], g = y[k][e];
+        sT = fmaf(g, vh, sT);
+        sG += g;
+        q[0][e] = fmaf(g * w, vh, q[0][e]);
+        if (KIND == kLayer) q[1][e] = fmaf(g, w, q[1][e]);
+      }
+      add(k, 0, sT);
+      add(k, 1, sG);
+      channel_done();
+    }
+    fresh<DT>(vr);
+    fold<V>(q[0], oq[0]);
+    if (KIND == kLayer) fold<V>(q[1], oq[1]);
+    else
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i) oq[1][i] = 0.f;
+    Join<2, V, WPT>::run(oq, red, turn, wave, lane);
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) {
+      oq[0][i] *= invC;
+      oq[1][i] *= invC;
+    }
+    unfold<V>(oq[0], q[0]);
+    if (KIND == kLayer) unfold<V>(oq[1], q[1]);
+    if (a.gv) {
+#pragma unroll
+      for (int k = 0; k < CPT; ++k) {
+          const float w = tab[tile.channel(k)].x;
+        float gv[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const float vh = (ck_get<DT>(vr[k], e) - m[e]) * r[e];
+          float g = fmaf(-vh, q[0][e], y[k][e] * w);
+          if (KIND == kLayer) g -= q[1][e];
+          gv[e] = r[e] * g;
+        }
+        tile.store(a.gv, t, k, whole, ck_raw<DT>(gv));
+      }
+    }
+  }
+  if (!a.part) return;
+  // the run's sums: over a channel's 8 lanes, then over the workgroup's tiles
+  float tot[CPT][4];
+#pragma unroll
+  for (int k = 0; k < CPT; ++k)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) tot[k][q] = sum8(acc[(4 * k + q) * (64 * WAVES)]);
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < CPT; ++k)
+    if ((lane & 7) == 0) accs[(wave / WPT) * NC + tile.channel(k)] = make_float4(tot[k][0], tot[k][1], tot[k][2], tot[k][3]);
+  __syncthreads();
+  for (int i = threadIdx.x; i < 4 * NC; i += blockDim.x) {
+    const int c = i >> 2, q = i & 3;
+    if (c >= a.C) continue;
+    float t = 0.f;
+#pragma unroll
+    for (int g = 0; g < TPG; ++g) t += reinterpret_cast<const float *>(accs + g * NC + c)[q];
+    a.part[(((size_t)q * a.C + c) * a.B + b) * gridDim.x + blockIdx.x] = t;
+  }
+}
+
+// The variant for C channels: groups of 8 spread over 1, 2, 4 or 8 waves, at most
+// 8 groups a wave. Exactly ceil(groups / waves) of them, so that no group but a wave's last is
+// ever empty.
+template <int DT, int KIND, int WPT>
+const void *field_pick(bool fwd, int cpt) {
+#define FNO_PICK(CPT) (fwd ? (const void *)fno_norm_fwd<DT, CPT, WPT, KIND> : (const void *)fno_norm_bwd<DT, CPT, WPT, KIND>)
+  if constexpr (WPT == 1) {
+    if (cpt == 1) return FNO_PICK(1);
+    if (cpt == 2) return FNO_PICK(2);
+    if (cpt == 3) return FNO_PICK(3);
+    if (cpt == 4) return FNO_PICK(4);
+  }
+  if (cpt <= 5) return FNO_PICK(5);
+  if (cpt == 6) return FNO_PICK(6);
+  if (cpt == 7) return FNO_PICK(7);
+  return FNO_PICK(8);
+#undef FNO_PICK
+}
+
+inline int field_waves(int C) { return C <= 64 ? 1 : C <= 128 ? 2 : C <= 256 ? 4 : 8; }
+
+template <int DT, int KIND>
+const void *field_kernel(bool fwd, int C) {
+  const int w = field_waves(C), cpt = ((C + 7) / 8 + w - 1) / w;
+  if (w == 1) return field_pick<DT, KIND, 1>(fwd, cpt);
+  if (w == 2) return field_pick<DT, KIND, 2>(fwd, cpt);
+  if (w == 4) return field_pick<DT, KIND, 4>(fwd, cpt);
+  return field_pick<DT, KIND, 8>(fwd, cpt);
+}
+
+}  // namespace fno
