@@ -125,44 +125,17 @@ __device__ __forceinline__ void ck_store(void *p, size_t i, long n, const ck_u32
   }
 }
 
-// 128-bit shifts by whole bytes; 16 or more leave nothing
-__device__ __forceinline__ ck_u32x4 ck_shift(const ck_u32x4 &r, int bytes, bool left) {
+// 128 bits moved down by whole bytes, zeros from above (16 or more: all)
+__device__ __forceinline__ ck_u32x4 ck_shift(const ck_u32x4 &r, int bytes) {
   uint64_t lo = (uint64_t)r[1] << 32 | r[0], hi = (uint64_t)r[3] << 32 | r[2];
-  if (left) {  // as a right shift of the halves exchanged and mirrored
-    const bool far = bytes >= 8;
-    const int s = 8 * (bytes & 7);
-    uint64_t h = far ? lo : hi, l = far ? 0 : lo;
-    h = h << s | (s ? l >> (64 - s) : 0);
-    l <<= s;
-    lo = bytes >= 16 ? 0 : l;
-    hi = bytes >= 16 ? 0 : h;
-  } else {
-    const bool far = bytes >= 8;
-    const int s = 8 * (bytes & 7);
-    uint64_t l = far ? hi : lo, h = far ? 0 : hi;
-    l = l >> s | (s ? h << (64 - s) : 0);
-    h >>= s;
-    lo = bytes >= 16 ? 0 : l;
-    hi = bytes >= 16 ? 0 : h;
-  }
+  const bool far = bytes >= 8;
+  const int s = 8 * (bytes & 7);
+  lo = far ? hi : lo;
+  hi = far ? 0 : hi;
+  lo = lo >> s | (s ? hi << (64 - s) : 0);
+  hi >>= s;
+  if (bytes >= 16) lo = hi = 0;
   return ck_u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
-}
-
-// The elements at i .. of a row that ends before element `end` of a field of
-// `total` elements, zeros past the row's end (all zeros for i >= end). Where 16
-// bytes from i would pass the end, the last 16 bytes of the row (or, in a
-// field's first few elements, its first) are read and moved into place: one
-// access on every path, so the tails of a kernel need no branches of their
-// own and never read outside the field. TINY: the field may be smaller than 16
-// bytes in all.
-template <int DT, bool TINY>
-__device__ __forceinline__ ck_u32x4 ck_load_row(const void *p, long i, long end, long total) {
-  constexpr int V = ck_vec<DT>(), ES = DT == DT_F32 ? 4 : 2;
-  if (TINY && total < V) return ck_load<DT>(p, i < end ? i : 0, end - i);
-  const long at = min(i, max(end - V, 0L));
-  ck_u32x4 r = *reinterpret_cast<const ck_u32x4_any *>(static_cast<const char *>(p) + at * ES);
-  if (end < V) r = ck_shift(r, (int)(V - end) * ES, true);  // drop what follows the row
-  return ck_shift(r, (int)min(16L, (i - min(i, end - V)) * ES), false);
 }
 
 // the first n of the elements to p[i] .. (n <= 0: none)

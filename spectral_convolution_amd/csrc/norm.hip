@@ -132,13 +132,15 @@ const void *pick(const NormArgs &a, bool fwd, int dtype, int &threads, int &rpg)
   return norm_kernel_bf16(tok, a.kind, fwd, a.C, threads, rpg);
 }
 
-// Runs per sample (fields) or in all (tokens). Backward: about 1024 in all,
-// two rounds of the workgroups the chip holds at two waves per SIMD.
-constexpr long kNormRuns = 1024;
+// Runs per sample (fields) or in all (tokens): at most `most` of them. A
+// field's run is a whole number of rounds of the workgroup's waves and short,
+// so that the last workgroups to finish are not far behind the rest (the chip
+// holds 512 of the backward's: 1040 long ones took three rounds, not two).
+constexpr long kFieldRuns = 4096, kTokenRuns = 1024;
 long norm_runs(const NormArgs &a, int dtype, int rpg, long most, int *per = nullptr) {
   if (a.P == 1) return std::min((a.B + (long)rpg - 1) / rpg, most);
   const long px = dtype == DT_F32 ? 32 : 64, nt = (a.P + px - 1) / px;
-  const long s = std::min((nt + rpg - 1) / rpg, std::max(1L, (most + a.B - 1) / a.B)), p = (nt + s - 1) / s;
+  const long s = std::max(1L, most / a.B), p = ((nt + s - 1) / s + rpg - 1) / rpg * rpg;
   if (per) *per = (int)p;
   return (nt + p - 1) / p;
 }
@@ -150,7 +152,7 @@ size_t norm_workspace_bytes(int B, int C, long P, int dtype) {
   a.B = B, a.C = C, a.P = P;
   int threads, rpg;
   (void)pick(a, false, dtype, threads, rpg);
-  const long S = norm_runs(a, dtype, rpg, kNormRuns);
+  const long S = norm_runs(a, dtype, rpg, P == 1 ? kTokenRuns : kFieldRuns);
   return (size_t)4 * C * S * (P == 1 ? 1 : B) * 4;
 }
 
@@ -159,7 +161,7 @@ hipError_t launch_norm_fwd(const NormArgs &a, int dtype, hipStream_t s) {
   int threads, rpg;
   const void *k = pick(a, true, dtype, threads, rpg);
   NormArgs arg = a;
-  const long S = norm_runs(a, dtype, rpg, 4 * kNormRuns, &arg.per);
+  const long S = norm_runs(a, dtype, rpg, kFieldRuns, &arg.per);
   const dim3 grid((unsigned)S, a.P == 1 ? 1u : (unsigned)a.B);
   void *args[] = {(void *)&arg};
   return hipLaunchKernel(k, grid, dim3((unsigned)threads), args, 0, s);
@@ -169,7 +171,7 @@ hipError_t launch_norm_bwd(const NormArgs &a, int dtype, hipStream_t s) {
   int threads, rpg;
   const void *k = pick(a, false, dtype, threads, rpg);
   NormArgs arg = a;
-  int S = (int)norm_runs(a, dtype, rpg, kNormRuns, &arg.per);
+  int S = (int)norm_runs(a, dtype, rpg, a.P == 1 ? kTokenRuns : kFieldRuns, &arg.per);
   FNO_BOUNDS(check_norm(a, false, S, dtype);)
   const bool tok = a.P == 1;
   const dim3 grid((unsigned)S, tok ? 1u : (unsigned)a.B);

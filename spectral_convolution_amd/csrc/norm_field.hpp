@@ -29,7 +29,7 @@ __device__ __forceinline__ void norm_table(const NormArgs &a, int b, int n, floa
 template <int DT, int CPT, int WPT>
 struct FieldTile {
   static constexpr int V = ck_vec<DT>(), PX = 8 * V, ES = DT == DT_F32 ? 4 : 2;
-  long P, nb, rows;  // row length, its blocks, rows of the whole field
+  long P, nb;  // row length and its blocks
   int sample, channels;
   int first;      // the wave's first group
   int last;       // its last group, or the field's where it has none
@@ -43,7 +43,6 @@ struct FieldTile {
     nb = (P + kCkBlock - 1) / kCkBlock;
     sample = b;
     channels = a.C;
-    rows = (long)a.B * a.C;
     first = w;
     const int g = (CPT - 1) * WPT + w;
     last = min(g, (a.C - 1) / 8);
@@ -82,9 +81,6 @@ struct FieldTile {
   __device__ __forceinline__ size_t field_at(int k) const { return k < CPT - 1 ? f0 + (size_t)k * 8 * WPT * P * ES : f1; }
   __device__ __forceinline__ size_t code_at(int k) const { return k < CPT - 1 ? c0 + (size_t)k * 8 * WPT * nb * kCkBlock : c1; }
   __device__ __forceinline__ size_t exp_at(int k) const { return k < CPT - 1 ? e0 + (size_t)k * 8 * WPT * nb : e1; }
-  __device__ __forceinline__ size_t row(int k) const {
-    return (size_t)sample * channels + 8 * (k < CPT - 1 ? k * WPT + first : last);
-  }
   // whether the lane's channel of group k exists, and its place in the channel table
   __device__ __forceinline__ bool has(int k) const { return k < CPT - 1 || ok; }
   __device__ __forceinline__ int channel(int k) const { return 8 * (k * WPT + first) + cl; }
@@ -92,21 +88,33 @@ struct FieldTile {
   __device__ __forceinline__ ck_u32x4 only(int k, const ck_u32x4 &r) const {
     return k < CPT - 1 || ok ? r : ck_u32x4{0u, 0u, 0u, 0u};
   }
-  // The addresses of a row's last tile are computed there, not kept from before
-  // the loop over the tiles: two registers for each access of the kernel.
-  static __device__ __forceinline__ int here(int c) {
-    asm volatile("" : "+v"(c));
-    return c;
-  }
   // a tile that lies within the row
   __device__ __forceinline__ ck_u32x4 load(const void *f, int t, int k) const {
     const char *s = static_cast<const char *>(f) + field_at(k);
     return only(k, *reinterpret_cast<const ck_u32x4_any *>(s + (k < CPT - 1 ? off : off_last)));
   }
-  // the row's last tile, zeros past its end
-  __device__ __forceinline__ ck_u32x4 load_end(const void *f, int t, int k) const {
-    const long r = (long)row(k) + here(k < CPT - 1 ? cl : clast);
-    return only(k, ck_load_row<DT, CPT == 1>(f, r * P + (long)t * PX + pl * V, (r + 1) * P, P * rows));
+  // The row's last tile, zeros past its end: a lane that would pass it reads the
+  // row's last 16 bytes instead (`back` elements before its own) and shifts
+  // them into place. Rows shorter than 16 bytes are read by the element.
+  struct End {
+    uint32_t off, off_last;  // lane offsets from 16 bytes before the tile
+    int back;                // in bytes, 16 and more: nothing of the piece is in the row
+    long n;
+  };
+  __device__ __forceinline__ End end(int t) const {
+    End x;
+    x.n = P - ((long)t * PX + pl * V);
+    const int b = (int)max(0L, V - x.n) * ES;
+    x.off = off + 16 - b;
+    x.off_last = off_last + 16 - b;
+    x.back = min(b, 16);
+    return x;
+  }
+  __device__ __forceinline__ ck_u32x4 load_end(const void *f, const End &x, int k) const {
+    const char *s = static_cast<const char *>(f) + field_at(k);
+    if (P < V) return only(k, ck_load<DT>(s + (k < CPT - 1 ? off : off_last), 0, x.n));
+    const ck_u32x4 r = *reinterpret_cast<const ck_u32x4_any *>(s - 16 + (k < CPT - 1 ? x.off : x.off_last));
+    return only(k, ck_shift(r, x.back));
   }
   __device__ __forceinline__ void store(void *f, int t, int k, bool whole, const ck_u32x4 &r) const {
     if (!has(k)) return;
@@ -114,7 +122,7 @@ struct FieldTile {
       char *d = static_cast<char *>(f) + field_at(k);
       *reinterpret_cast<ck_u32x4_any *>(d + (k < CPT - 1 ? off : off_last)) = r;
     } else {
-      ck_store_row<DT>(f, (row(k) + here(cl)) * P + (long)t * PX + pl * V, P - ((long)t * PX + pl * V), r);
+      ck_store_row<DT>(static_cast<char *>(f) + field_at(k) + (k < CPT - 1 ? off : off_last), 0, P - ((long)t * PX + pl * V), r);
     }
   }
   // whether the lane's piece begins inside the row's blocks
@@ -165,10 +173,12 @@ __global__ __launch_bounds__(norm_threads<WPT>()) void fno_norm_fwd(NormArgs a) 
         xr[k] = tile.load(a.x, t, k);
       }
     } else {
+      const auto end = tile.end(t);
 #pragma unroll
       for (int k = 0; k < CPT; ++k) {
-        vr[k] = tile.load_end(a.v, t, k);
-        xr[k] = tile.load_end(a.x, t, k);
+        vr[k] = tile.load_end(a.v, end, k);
+        xr[k] = tile.load_end(a.x, end, k);
+        channel_done();
       }
     }
     if (a.vq) {
@@ -240,11 +250,19 @@ __global__ __launch_bounds__(norm_threads<WPT>()) void fno_norm_fwd(NormArgs a) 
   }
 }
 
-// Backward of a field. The wave's registers hold v, gy and gu as stored and y
-// (then gx) in fp32; v^ is formed again from v where it is needed.
+// Backward of a field, in passes over the wave's registers, each ending in a
+// sum over the channels:
+//   v's mean (layer norm) and deviation;
+//   y's mean and that of g = gu w_pre (layer norm);  y's deviation and g . (y - m');
+//   gx, its sums over pixels and h . v^, h = gx scale gate w_post (and h's mean);
+//   gv.
+// x, v, gy and gu stay as stored and y is formed from them again in each
+// pass: kept in fp32 it would spill, and a spilled value read back after a
+// store waits for that store (measured 46 us a tile instead of 12).
 template <int DT, int CPT, int WPT, int KIND>
 __global__ __launch_bounds__(norm_threads<WPT>()) __attribute__((amdgpu_waves_per_eu(2))) void fno_norm_bwd(NormArgs a) {
   constexpr int V = ck_vec<DT>(), PX = 8 * V, WAVES = norm_threads<WPT>() / 64, TPG = WAVES / WPT, NC = 8 * CPT * WPT;
+  constexpr int NQ = KIND == kLayer ? 2 : 1;
   __shared__ float4 tab[NC];
   __shared__ float4 accs[CPT * 64 * WAVES];
   __shared__ float red[WPT > 1 ? 2 * WAVES * 2 * PX : 1];
@@ -278,10 +296,12 @@ __global__ __launch_bounds__(norm_threads<WPT>()) __attribute__((amdgpu_waves_pe
         xr[k] = tile.load(a.x, t, k);
       }
     } else {
+      const auto end = tile.end(t);
 #pragma unroll
       for (int k = 0; k < CPT; ++k) {
-        vr[k] = tile.load_end(a.v, t, k);
-        xr[k] = tile.load_end(a.x, t, k);
+        vr[k] = tile.load_end(a.v, end, k);
+        xr[k] = tile.load_end(a.x, end, k);
+        channel_done();
       }
     }
     const void *gu = a.gu ? a.gu : a.gy;  // without gu its values are not used
@@ -292,165 +312,160 @@ __global__ __launch_bounds__(norm_threads<WPT>()) __attribute__((amdgpu_waves_pe
         gyr[k] = tile.load(a.gy, t, k);
       }
     } else {
+      const auto end = tile.end(t);
 #pragma unroll
       for (int k = 0; k < CPT; ++k) {
-        gur[k] = tile.load_end(gu, t, k);
-        gyr[k] = tile.load_end(a.gy, t, k);
+        gur[k] = tile.load_end(gu, end, k);
+        gyr[k] = tile.load_end(a.gy, end, k);
+        channel_done();
       }
     }
+    float m[V], r[V], my[V], ry[V], q[2][V];
+    // joins NQ sums over the channels: each lane then holds `out` of its pixels
+    auto all = [&](auto &s, auto &&f) {
+      constexpr int N = sizeof(s) / sizeof(s[0]);
+      float o[N][V / 4];
+#pragma unroll
+      for (int i = 0; i < N; ++i) fold<V>(s[i], o[i]);
+      Join<N, V, WPT>::run(o, red, turn, wave, lane);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+#pragma unroll
+        for (int j = 0; j < V / 4; ++j) o[i][j] = f(i, o[i][j]);
+        unfold<V>(o[i], s[i]);
+      }
+    };
+    auto mean = [&](int, float s) { return s / (float)a.C; };
+    auto scale = [&](int, float s) { return s * invC; };
+    auto zero = [&](auto &s) {
+#pragma unroll
+      for (int i = 0; i < (int)(sizeof(s) / sizeof(s[0])); ++i)
+#pragma unroll
+        for (int e = 0; e < V; ++e) s[i][e] = 0.f;
+    };
+    float s1[1][V], s2[NQ][V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) m[e] = my[e] = 0.f;
     fresh<DT>(vr);
-    float s[1][V], o[1][V / 4], m[V], r[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) m[e] = 0.f;
     if constexpr (KIND == kLayer) {
-      channel_sum<V, CPT, false>(s[0], [&](int k, int e) { return ck_get<DT>(vr[k], e); });
-      fold<V>(s[0], o[0]);
-      Join<1, V, WPT>::run(o, red, turn, wave, lane);
+      channel_sum<V, CPT, false>(s1[0], [&](int k, int e) { return ck_get<DT>(vr[k], e); });
+      all(s1, mean);
 #pragma unroll
-      for (int i = 0; i < V / 4; ++i) o[0][i] /= (float)a.C;
-      unfold<V>(o[0], m);
+      for (int e = 0; e < V; ++e) m[e] = s1[0][e];
       fresh<DT>(vr);
     }
-    channel_sum<V, CPT, true>(s[0], [&](int k, int e) {
+    channel_sum<V, CPT, true>(s1[0], [&](int k, int e) {
       const float d = ck_get<DT>(vr[k], e) - m[e];
       return KIND == kLayer && !tile.has(k) ? 0.f : d;
     });
-    fold<V>(s[0], o[0]);
-    Join<1, V, WPT>::run(o, red, turn, wave, lane);
+    all(s1, [&](int, float s) { return rsq(fmaf(s, invC, a.eps)); });
 #pragma unroll
-    for (int i = 0; i < V / 4; ++i) o[0][i] = rsq(fmaf(o[0][i], invC, a.eps));
-    unfold<V>(o[0], r);
-    fresh<DT>(vr);
-    float y[CPT][V];
+    for (int e = 0; e < V; ++e) r[e] = s1[0][e];
+    auto y = [&](int k, int e, const float4 &w) {
+      return ck_get<DT>(xr[k], e) + fmaf((ck_get<DT>(vr[k], e) - m[e]) * r[e], w.x, w.y);
+    };
     if (a.gu) {
-      float my[V], ry[V];
+      if constexpr (KIND == kLayer) {
+        zero(s2);
+        fresh<DT>(vr);
+        fresh<DT>(xr);
+        fresh<DT>(gur);
+#pragma unroll
+        for (int k = 0; k < CPT; ++k) {
+          const float4 w = tab[tile.channel(k)];
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            s2[0][e] += y(k, e, w);
+            s2[NQ - 1][e] = fmaf(ck_get<DT>(gur[k], e), w.z, s2[NQ - 1][e]);
+          }
+          channel_done();
+        }
+        all(s2, mean);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          my[e] = s2[0][e];
+          q[1][e] = s2[NQ - 1][e];
+        }
+      }
+      float s[2][V];
+      zero(s);
+      fresh<DT>(vr);
+      fresh<DT>(xr);
+      fresh<DT>(gur);
 #pragma unroll
       for (int k = 0; k < CPT; ++k) {
         const float4 w = tab[tile.channel(k)];
 #pragma unroll
-        for (int e = 0; e < V; ++e)
-          y[k][e] = ck_get<DT>(xr[k], e) + fmaf((ck_get<DT>(vr[k], e) - m[e]) * r[e], w.x, w.y);
+        for (int e = 0; e < V; ++e) {
+          float d = y(k, e, w) - my[e];
+          if (KIND == kLayer && !tile.has(k)) d = 0.f;
+          s[0][e] = fmaf(d, d, s[0][e]);
+          s[1][e] = fmaf(ck_get<DT>(gur[k], e) * w.z, d, s[1][e]);
+        }
         channel_done();
       }
+      all(s, [&](int i, float v) { return i == 0 ? rsq(fmaf(v, invC, a.eps)) : v * invC; });
 #pragma unroll
-      for (int e = 0; e < V; ++e) my[e] = 0.f;
-      if constexpr (KIND == kLayer) {
-        channel_sum<V, CPT, false>(s[0], [&](int k, int e) { return y[k][e]; });
-        fold<V>(s[0], o[0]);
-        Join<1, V, WPT>::run(o, red, turn, wave, lane);
-#pragma unroll
-        for (int i = 0; i < V / 4; ++i) o[0][i] /= (float)a.C;
-        unfold<V>(o[0], my);
+      for (int e = 0; e < V; ++e) {
+        ry[e] = s[0][e];
+        q[0][e] = s[1][e] * s[0][e];  // mean(g y^)
       }
-      channel_sum<V, CPT, true>(s[0], [&](int k, int e) {
-        const float d = y[k][e] - my[e];
-        return KIND == kLayer && !tile.has(k) ? 0.f : d;
-      });
-      fold<V>(s[0], o[0]);
-      Join<1, V, WPT>::run(o, red, turn, wave, lane);
+    }
+    float gx[CPT][V];
+    zero(s2);
+    fresh<DT>(vr);
+    fresh<DT>(xr);
+    fresh<DT>(gur);
 #pragma unroll
-      for (int i = 0; i < V / 4; ++i) o[0][i] = rsq(fmaf(o[0][i], invC, a.eps));
-      unfold<V>(o[0], ry);
-      float q[2][V], oq[2][V / 4];
-#pragma unroll
-      for (int e = 0; e < V; ++e) q[0][e] = q[1][e] = 0.f;
-#pragma unroll
-      for (int k = 0; k < CPT; ++k) {
-        const float wp = tab[tile.channel(k)].z;
+    for (int k = 0; k < CPT; ++k) {
+      const float4 w = tab[tile.channel(k)];
+      float sT = 0.f, sG = 0.f;
+      if (a.gu) {
         float sU = 0.f, sV = 0.f;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          const float gu = ck_get<DT>(gur[k], e), yh = (y[k][e] - my[e]) * ry[e];
-          y[k][e] = yh;
+          const float gu = ck_get<DT>(gur[k], e), yh = (y(k, e, w) - my[e]) * ry[e];
           sU = fmaf(gu, yh, sU);
           sV += gu;
-          q[0][e] = fmaf(gu * wp, yh, q[0][e]);
-          if (KIND == kLayer) q[1][e] = fmaf(gu, wp, q[1][e]);
+          float g = fmaf(-yh, q[0][e], gu * w.z);
+          if (KIND == kLayer) g -= q[1][e];
+          gx[k][e] = fmaf(ry[e], g, ck_get<DT>(gyr[k], e));
         }
         add(k, 2, sU);
         add(k, 3, sV);
-        channel_done();
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) gx[k][e] = ck_get<DT>(gyr[k], e);
       }
-      fresh<DT>(gur);
-      fold<V>(q[0], oq[0]);
-      if (KIND == kLayer) fold<V>(q[1], oq[1]);
-      else
-#pragma unroll
-        for (int i = 0; i < V / 4; ++i) oq[1][i] = 0.f;
-      Join<2, V, WPT>::run(oq, red, turn, wave, lane);
-#pragma unroll
-      for (int i = 0; i < V / 4; ++i) {
-        oq[0][i] *= invC;
-        oq[1][i] *= invC;
-      }
-      unfold<V>(oq[0], q[0]);
-      if (KIND == kLayer) unfold<V>(oq[1], q[1]);
-#pragma unroll
-      for (int k = 0; k < CPT; ++k) {
-        const float wp = tab[tile.channel(k)].z;
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          float g = fmaf(-y[k][e], q[0][e], ck_get<DT>(gur[k], e) * wp);
-          if (KIND == kLayer) g -= q[1][e];
-          y[k][e] = fmaf(ry[e], g, ck_get<DT>(gyr[k], e));
-        }
-        channel_done();
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < CPT; ++k)
-#pragma unroll
-        for (int e = 0; e < V; ++e) y[k][e] = ck_get<DT>(gyr[k], e);
-    }
-    // y holds gx
-    fresh<DT>(vr);
-    float q[2][V], oq[2][V / 4];
-#pragma unroll
-    for (int e = 0; e < V; ++e) q[0][e] = q[1][e] = 0.f;
-#pragma unroll
-    for (int k = 0; k < CPT; ++k) {
-      const float w = tab[tile.channel(k)].x;
-      if (a.gx) tile.store(a.gx, t, k, whole, ck_raw<DT>(y[k]));
-      float sT = 0.f, sG = 0.f;
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float vh = (ck_get<DT>(vr[k], e) - m[e]) * r[e], g = y[k][e];
+        const float vh = (ck_get<DT>(vr[k], e) - m[e]) * r[e], g = gx[k][e];
         sT = fmaf(g, vh, sT);
         sG += g;
-        q[0][e] = fmaf(g * w, vh, q[0][e]);
-        if (KIND == kLayer) q[1][e] = fmaf(g, w, q[1][e]);
+        s2[0][e] = fmaf(g * w.x, vh, s2[0][e]);
+        if (KIND == kLayer) s2[NQ - 1][e] = fmaf(g, w.x, s2[NQ - 1][e]);
       }
       add(k, 0, sT);
       add(k, 1, sG);
+      if (a.gx) tile.store(a.gx, t, k, whole, ck_raw<DT>(gx[k]));
       channel_done();
     }
-    fresh<DT>(vr);
-    fold<V>(q[0], oq[0]);
-    if (KIND == kLayer) fold<V>(q[1], oq[1]);
-    else
-#pragma unroll
-      for (int i = 0; i < V / 4; ++i) oq[1][i] = 0.f;
-    Join<2, V, WPT>::run(oq, red, turn, wave, lane);
-#pragma unroll
-    for (int i = 0; i < V / 4; ++i) {
-      oq[0][i] *= invC;
-      oq[1][i] *= invC;
-    }
-    unfold<V>(oq[0], q[0]);
-    if (KIND == kLayer) unfold<V>(oq[1], q[1]);
+    all(s2, scale);
     if (a.gv) {
+      fresh<DT>(vr);
 #pragma unroll
       for (int k = 0; k < CPT; ++k) {
-          const float w = tab[tile.channel(k)].x;
+        const float w = tab[tile.channel(k)].x;
         float gv[V];
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           const float vh = (ck_get<DT>(vr[k], e) - m[e]) * r[e];
-          float g = fmaf(-vh, q[0][e], y[k][e] * w);
-          if (KIND == kLayer) g -= q[1][e];
+          float g = fmaf(-vh, s2[0][e], gx[k][e] * w);
+          if (KIND == kLayer) g -= s2[NQ - 1][e];
           gv[e] = r[e] * g;
         }
         tile.store(a.gv, t, k, whole, ck_raw<DT>(gv));
+        channel_done();
       }
     }
   }
