@@ -456,7 +456,8 @@ fno_status_t fno_checkpoint_unpack(const void *saved, void *y, long rows,
  * and, with GELU and an add input, that of add (rows [batch * c_out][pixels])
  * behind it, in `saved` (fno_channel_mix_saved_bytes, 256-byte aligned). y is
  * that of x and add as given. act 0 or 1, bias and add may be NULL.
- * c_in, c_out <= 128, else UNSUPPORTED. */
+ * c_in, c_out <= 128, pixels <= 2^26 and batch * pixels <= 2^36, else
+ * UNSUPPORTED. */
 fno_status_t fno_channel_mix_saved_bytes(int batch, int c_in, int c_out,
                                          long pixels, int act, int has_add,
                                          size_t *bytes);

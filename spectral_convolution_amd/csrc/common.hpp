@@ -268,6 +268,7 @@ struct MixTrainArgs {
   int B, I, O;
   long P;
   int act;
+  int tpb, tiles, per;  // tiles of a sample, in all, of a workgroup (set by the launcher)
 };
 
 bool fused_supported(const FusedShape &f);
@@ -358,6 +359,7 @@ size_t norm_workspace_bytes(int B, int C, long P, int dtype);
 hipError_t launch_norm_fwd(const NormArgs &a, int dtype, hipStream_t s);
 hipError_t launch_norm_bwd(const NormArgs &a, int dtype, hipStream_t s);
 constexpr int kMixTrainMax = 128;    // training channel mix: channels on either side
+constexpr long kMixTrainPixels = 1L << 26, kMixTrainTiles = 1L << 30;  // lane offsets and tile numbers in 32 bits
 size_t mix_train_workspace_bytes(int B, int I, int O, long P, int dtype);
 hipError_t launch_mix_save(const MixTrainArgs &a, int dtype, hipStream_t s);
 hipError_t launch_mix_bwd(const MixTrainArgs &a, int dtype, hipStream_t s);

@@ -198,7 +198,8 @@ fno_status_t mix_shape(int batch, int c_in, int c_out, long pixels, int act, int
   if (batch < 1 || c_in < 1 || c_out < 1 || pixels < 1 || (act != 0 && act != 1) || (has_add != 0 && has_add != 1) ||
       !valid_dtype(dtype))
     return FNO_ERR_INVALID_ARG;
-  if (c_in > kMixTrainMax || c_out > kMixTrainMax || pixels > kMaxRow || !values_in_range(batch, kMixTrainMax, pixels))
+  if (c_in > kMixTrainMax || c_out > kMixTrainMax || pixels > kMixTrainPixels ||
+      (pixels + 63) / 64 > kMixTrainTiles / batch)
     return FNO_ERR_UNSUPPORTED;
   return FNO_OK;
 }

@@ -25,77 +25,11 @@
 
 #include <algorithm>
 
-#include "checkpoint.hpp"
-#include "gelu.hpp"
+#include "mix_train.hpp"
 
 namespace fno {
 
 namespace {
-
-constexpr int kMtThreads = 256;
-
-// 16 consecutive elements of a row
-template <int DT>
-struct Px16 {
-  static constexpr int N = DT == DT_F32 ? 4 : 2, V = ck_vec<DT>();
-  ck_u32x4 r[N];
-  __device__ __forceinline__ void load(const void *p, size_t i, long n) {
-#pragma unroll
-    for (int k = 0; k < N; ++k) r[k] = ck_load<DT>(p, i + k * V, n - k * V);
-  }
-  __device__ __forceinline__ float get(int e) const { return ck_get<DT>(r[e / V], e % V); }
-  __device__ __forceinline__ uint32_t key() const {
-    uint32_t m = ck_maxkey<DT>(r[0]);
-#pragma unroll
-    for (int k = 1; k < N; ++k) m = max(m, ck_maxkey<DT>(r[k]));
-    return m;
-  }
-  __device__ __forceinline__ ck_u32x4 codes(int e) const {
-    ck_u32x4 q;
-    if constexpr (DT == DT_F32) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) q[k] = ck_codes<DT>(r[k], e).x;
-    } else {
-      const uint2 a = ck_codes<DT>(r[0], e), b = ck_codes<DT>(r[1], e);
-      q = ck_u32x4{a.x, a.y, b.x, b.y};
-    }
-    return q;
-  }
-};
-
-template <int DT>
-__device__ __forceinline__ void store16(void *p, size_t i, long n, const float (&v)[16]) {
-  constexpr int V = ck_vec<DT>();
-#pragma unroll
-  for (int k = 0; k < 16 / V; ++k) ck_store<DT>(p, i + k * V, n - k * V, ck_raw<DT>(v + k * V));
-}
-
-template <int DT>
-__device__ __forceinline__ float mt_load1(const void *p, size_t i) {
-  if constexpr (DT == DT_F32) return reinterpret_cast<const float *>(p)[i];
-  else if constexpr (DT == DT_F16) return (float)reinterpret_cast<const _Float16 *>(p)[i];
-  else return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(p)[i] << 16);
-}
-
-// 16 codes of a row's piece at pixel p (zeros past the row's blocks) and their exponent
-struct Code16 {
-  ck_u32x4 q;
-  int e;
-  __device__ __forceinline__ void load(const uint8_t *codes, const int8_t *exps, size_t row, long p, long nb, bool ok) {
-    q = ck_u32x4{0u, 0u, 0u, 0u};
-    e = 0;
-    if (ok && p < nb * kCkBlock) {
-      q = *reinterpret_cast<const ck_u32x4 *>(codes + row * nb * kCkBlock + p);
-      e = exps[row * nb + p / kCkBlock];
-    }
-  }
-  __device__ __forceinline__ float get(int k, float step) const { return ck_value(q[k >> 2], k & 3, step); }
-};
-
-template <int DT>
-__device__ __forceinline__ float mt_gelu(float z) { return DT == DT_F32 ? gelu(z) : gelu_half(z); }
-template <int DT>
-__device__ __forceinline__ float mt_slope(float z) { return DT == DT_F32 ? gelu_slope(z) : gelu_slope_half(z); }
 
 template <int OT, int IT>
 struct MtGeom {
@@ -129,39 +63,40 @@ __device__ __forceinline__ void mt_z(const float *xs, int pb, int lane, const fl
 
 }  // namespace
 
-template <int DT, int OT, int IT>
+template <int OT, int IT>
 __global__ __launch_bounds__(kMtThreads) void fno_mix_save(MixTrainArgs a) {
   using G = MtGeom<OT, IT>;
   extern __shared__ float4 lds4[];
   float *xs = reinterpret_cast<float *>(lds4);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, n = lane & 15;
   const int ow = wave % G::WO, pb = 64 * (wave / G::WO);
-  const long P = a.P, tpb = (P + G::PT - 1) / G::PT, nt = tpb * a.B, nb = (P + kCkBlock - 1) / kCkBlock;
+  const long P = a.P, nb = (P + kCkBlock - 1) / kCkBlock;
   float wf[G::OTW][IT * 4], bias[G::OTW];
 #pragma unroll
   for (int m = 0; m < G::OTW; ++m) {
     const int o = 16 * (ow + G::WO * m) + n;
-    bias[m] = a.bias && o < a.O ? mt_load1<DT>(a.bias, o) : 0.f;
+    bias[m] = a.bias && o < a.O ? mt_load1<DT_F32>(a.bias, o) : 0.f;
 #pragma unroll
     for (int kk = 0; kk < IT * 4; ++kk) {
       const int i = 4 * kk + g;
-      wf[m][kk] = o < a.O && i < a.I ? mt_load1<DT>(a.A, (size_t)o * a.I + i) : 0.f;
+      wf[m][kk] = o < a.O && i < a.I ? mt_load1<DT_F32>(a.A, (size_t)o * a.I + i) : 0.f;
     }
   }
-  const long per = (nt + gridDim.x - 1) / gridDim.x, t0 = blockIdx.x * per, t1 = min(nt, t0 + per);
-  for (long t = t0; t < t1; ++t) {
-    const long b = t / tpb, p0 = (t - b * tpb) * G::PT;
+  const int t0 = blockIdx.x * a.per, t1 = min(a.tiles, t0 + a.per);
+  for (int t = t0; t < t1; ++t) {
+    const int b = t / a.tpb;
+    const long p0 = (long)(t - b * a.tpb) * G::PT;
 #pragma unroll
     for (int k = 0; k < G::NU; ++k) {
       const int u = tid + k * kMtThreads, i = u / (G::PT / 16), pu = 16 * (u % (G::PT / 16));
       if (G::UNITS % kMtThreads != 0 && u >= G::UNITS) break;  // whole pairs of lanes
       const long p = p0 + pu;
       const size_t row = (size_t)b * a.I + i;
-      Px16<DT> v;
+      Px16<DT_F32> v;
       v.load(a.x, row * P + p, i < a.I ? P - p : 0);
       uint32_t key = v.key();
       key = max(key, ck_dpp<kDppXor1>(key));
-      const int e = ck_exponent<DT>(key);
+      const int e = ck_exponent<DT_F32>(key);
       if (i < a.I && p < nb * kCkBlock) {
         *reinterpret_cast<ck_u32x4 *>(a.xq + row * nb * kCkBlock + p) = v.codes(e);
         if (p % kCkBlock == 0) a.xe[row * nb + p / kCkBlock] = (int8_t)e;
@@ -180,12 +115,12 @@ __global__ __launch_bounds__(kMtThreads) void fno_mix_save(MixTrainArgs a) {
       const int o = 16 * (ow + G::WO * m) + n;
       const bool ok = o < a.O;
       const size_t row = (size_t)b * a.O + o;
-      Px16<DT> ad;
+      Px16<DT_F32> ad;
       ad.load(a.add, row * P + p, a.add && ok ? P - p : 0);
       if (a.aq) {
         uint32_t key = ad.key();
         const auto s = __builtin_amdgcn_permlane16_swap(key, key, false, false);  // the block's other 16 pixels
-        const int e = ck_exponent<DT>(max(s[0], s[1]));
+        const int e = ck_exponent<DT_F32>(max(s[0], s[1]));
         if (ok && p < nb * kCkBlock) {
           *reinterpret_cast<ck_u32x4 *>(a.aq + row * nb * kCkBlock + p) = ad.codes(e);
           if (p % kCkBlock == 0) a.ae[row * nb + p / kCkBlock] = (int8_t)e;
@@ -195,15 +130,15 @@ __global__ __launch_bounds__(kMtThreads) void fno_mix_save(MixTrainArgs a) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
         const float v = z[m][e & 3][e >> 2] + bias[m] + ad.get(e);
-        y[e] = a.act ? mt_gelu<DT>(v) : v;
+        y[e] = a.act ? mt_gelu<DT_F32>(v) : v;
       }
-      if (ok) store16<DT>(a.y, row * P + p, P - p, y);
+      if (ok) store16<DT_F32>(a.y, row * P + p, P - p, y);
     }
     __syncthreads();
   }
 }
 
-template <int DT, int OT, int IT>
+template <int OT, int IT>
 __global__ __launch_bounds__(kMtThreads) void fno_mix_bwd(MixTrainArgs a) {
   using G = MtGeom<OT, IT>;
   constexpr int WI = IT < 4 ? IT : 4, ITW = IT / WI;  // gx: waves over c_in, tiles of each
@@ -211,18 +146,18 @@ __global__ __launch_bounds__(kMtThreads) void fno_mix_bwd(MixTrainArgs a) {
   float *xs = reinterpret_cast<float *>(lds4), *gs = xs + G::XS / 4;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, n = lane & 15;
   const int ow = wave % G::WO, pb = 64 * (wave / G::WO), iw = wave % WI;
-  const long P = a.P, tpb = (P + G::PT - 1) / G::PT, nt = tpb * a.B, nb = (P + kCkBlock - 1) / kCkBlock;
+  const long P = a.P, nb = (P + kCkBlock - 1) / kCkBlock;
   float wf[G::OTW][IT * 4], wt[ITW][OT * 4], bias[G::OTW], gb[G::OTW];
   v4f ga[G::OTW][IT];
 #pragma unroll
   for (int m = 0; m < G::OTW; ++m) {
     const int o = 16 * (ow + G::WO * m) + n;
     gb[m] = 0.f;
-    bias[m] = a.bias && o < a.O ? mt_load1<DT>(a.bias, o) : 0.f;
+    bias[m] = a.bias && o < a.O ? mt_load1<DT_F32>(a.bias, o) : 0.f;
 #pragma unroll
     for (int kk = 0; kk < IT * 4; ++kk) {
       const int i = 4 * kk + g;
-      wf[m][kk] = o < a.O && i < a.I ? mt_load1<DT>(a.A, (size_t)o * a.I + i) : 0.f;
+      wf[m][kk] = o < a.O && i < a.I ? mt_load1<DT_F32>(a.A, (size_t)o * a.I + i) : 0.f;
     }
 #pragma unroll
     for (int it = 0; it < IT; ++it) ga[m][it] = v4f{0.f, 0.f, 0.f, 0.f};
@@ -232,11 +167,12 @@ __global__ __launch_bounds__(kMtThreads) void fno_mix_bwd(MixTrainArgs a) {
 #pragma unroll
     for (int kk = 0; kk < OT * 4; ++kk) {
       const int o = 4 * kk + g, i = 16 * (iw + WI * m) + n;
-      wt[m][kk] = o < a.O && i < a.I ? mt_load1<DT>(a.A, (size_t)o * a.I + i) : 0.f;
+      wt[m][kk] = o < a.O && i < a.I ? mt_load1<DT_F32>(a.A, (size_t)o * a.I + i) : 0.f;
     }
-  const long per = (nt + gridDim.x - 1) / gridDim.x, t0 = blockIdx.x * per, t1 = min(nt, t0 + per);
-  for (long t = t0; t < t1; ++t) {
-    const long b = t / tpb, p0 = (t - b * tpb) * G::PT;
+  const int t0 = blockIdx.x * a.per, t1 = min(a.tiles, t0 + a.per);
+  for (int t = t0; t < t1; ++t) {
+    const int b = t / a.tpb;
+    const long p0 = (long)(t - b * a.tpb) * G::PT;
 #pragma unroll
     for (int k = 0; k < G::NU; ++k) {
       const int u = tid + k * kMtThreads, i = u / (G::PT / 16), pu = 16 * (u % (G::PT / 16));
@@ -259,7 +195,7 @@ __global__ __launch_bounds__(kMtThreads) void fno_mix_bwd(MixTrainArgs a) {
       const int o = 16 * (ow + G::WO * m) + n;
       const bool ok = o < a.O;
       const size_t row = (size_t)b * a.O + o;
-      Px16<DT> gy;
+      Px16<DT_F32> gy;
       gy.load(a.gy, row * P + p, ok ? P - p : 0);
       float gz[16];
 #pragma unroll
@@ -269,9 +205,9 @@ __global__ __launch_bounds__(kMtThreads) void fno_mix_bwd(MixTrainArgs a) {
         c.load(a.aq, a.ae, row, p, nb, a.aq && ok);
         const float s = ck_step(c.e);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) gz[e] *= mt_slope<DT>(z[m][e & 3][e >> 2] + bias[m] + c.get(e, s));
+        for (int e = 0; e < 16; ++e) gz[e] *= mt_slope<DT_F32>(z[m][e & 3][e >> 2] + bias[m] + c.get(e, s));
       }
-      if (a.gadd && ok) store16<DT>(a.gadd, row * P + p, P - p, gz);
+      if (a.gadd && ok) store16<DT_F32>(a.gadd, row * P + p, P - p, gz);
       float *d = gs + (16 * (ow + G::WO * m) + n) * G::PITCH + pb + 16 * g;
 #pragma unroll
       for (int q = 0; q < 4; ++q)
@@ -310,7 +246,7 @@ __global__ __launch_bounds__(kMtThreads) void fno_mix_bwd(MixTrainArgs a) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) v[e] = acc[e & 3][e >> 2];
           const long q = p0 + sb + 16 * g;
-          if (i < a.I) store16<DT>(a.gx, ((size_t)b * a.I + i) * P + q, P - q, v);
+          if (i < a.I) store16<DT_F32>(a.gx, ((size_t)b * a.I + i) * P + q, P - q, v);
         }
       }
     }
@@ -318,52 +254,7 @@ __global__ __launch_bounds__(kMtThreads) void fno_mix_bwd(MixTrainArgs a) {
     // its gz overwrite gs only after the next barrier
   }
   if (!a.part) return;
-  // this workgroup's sums, the pixel parts added through LDS
-  float *out = a.part + (size_t)blockIdx.x * ((size_t)a.O * a.I + a.O);
-  __syncthreads();
-#pragma unroll
-  for (int m = 0; m < G::OTW; ++m) {
-    float v = gb[m];
-    v += __shfl_xor(v, 16);
-    v += __shfl_xor(v, 32);
-    gb[m] = v;
-  }
-  constexpr int RO = OT * 16, RI = IT * 16 + 1;  // a row of gA and its gbias
-  const int part = wave / G::WO;
-#pragma unroll
-  for (int m = 0; m < G::OTW; ++m) {
-    const int ot = ow + G::WO * m;
-#pragma unroll
-    for (int it = 0; it < IT; ++it)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int o = 16 * ot + 4 * g + j, i = 16 * it + n;
-        if constexpr (G::WP == 1) {
-          if (o < a.O && i < a.I) out[(size_t)o * a.I + i] = ga[m][it][j];
-        } else {
-          xs[(part * RO + o) * RI + i] = ga[m][it][j];
-        }
-      }
-    if (g == 0) {
-      if constexpr (G::WP == 1) {
-        if (16 * ot + n < a.O) out[(size_t)a.O * a.I + 16 * ot + n] = gb[m];
-      } else {
-        xs[(part * RO + 16 * ot + n) * RI + IT * 16] = gb[m];
-      }
-    }
-  }
-  if constexpr (G::WP > 1) {
-    static_assert(G::WP * RO * RI * 4 <= G::XS + G::GS, "the parts' sums fit the tiles' LDS");
-    __syncthreads();
-    for (int u = tid; u < RO * RI; u += kMtThreads) {
-      const int o = u / RI, i = u - o * RI;
-      float v = 0.f;
-#pragma unroll
-      for (int w = 0; w < G::WP; ++w) v += xs[(w * RO + o) * RI + i];
-      if (o < a.O && i < a.I) out[(size_t)o * a.I + i] = v;
-      if (o < a.O && i == IT * 16) out[(size_t)a.O * a.I + o] = v;
-    }
-  }
+  mt_finish<OT, IT, G::WO, G::WP>(a, ga, gb, xs, wave, lane);
 }
 
 // gA and gbias from the workgroups' sums part[S][O I + O]: 32 elements a
@@ -393,38 +284,39 @@ __global__ __launch_bounds__(1024) void fno_mix_params(MixTrainArgs a, int S) {
 
 namespace {
 
-struct MtPick {
-  const void *fwd, *bwd;
-  int pt;
-  size_t lds_fwd, lds_bwd;
-};
-
-template <int DT, int OT, int IT>
+template <int OT, int IT>
 MtPick mt_pick3() {
   using G = MtGeom<OT, IT>;
-  return {(const void *)fno_mix_save<DT, OT, IT>, (const void *)fno_mix_bwd<DT, OT, IT>, G::PT, (size_t)G::XS,
+  return {(const void *)fno_mix_save<OT, IT>, (const void *)fno_mix_bwd<OT, IT>, G::PT, (size_t)G::XS,
           (size_t)(G::XS + G::GS)};
 }
-template <int DT, int OT>
+template <int OT>
 MtPick mt_pick2(int I) {
-  return I <= 16 ? mt_pick3<DT, OT, 1>() : I <= 32 ? mt_pick3<DT, OT, 2>() : I <= 64 ? mt_pick3<DT, OT, 4>()
-                                                                                     : mt_pick3<DT, OT, 8>();
-}
-template <int DT>
-MtPick mt_pick1(int O, int I) {
-  return O <= 16 ? mt_pick2<DT, 1>(I) : O <= 32 ? mt_pick2<DT, 2>(I) : O <= 64 ? mt_pick2<DT, 4>(I) : mt_pick2<DT, 8>(I);
+  return I <= 16 ? mt_pick3<OT, 1>() : I <= 32 ? mt_pick3<OT, 2>() : I <= 64 ? mt_pick3<OT, 4>() : mt_pick3<OT, 8>();
 }
 MtPick mt_pick(int O, int I, int dtype) {
-  return dtype == DT_F32 ? mt_pick1<DT_F32>(O, I) : dtype == DT_F16 ? mt_pick1<DT_F16>(O, I) : mt_pick1<DT_BF16>(O, I);
+  if (dtype == DT_F16) return mix_train_f16(O, I);
+  if (dtype == DT_BF16) return mix_train_bf16(O, I);
+  return O <= 16 ? mt_pick2<1>(I) : O <= 32 ? mt_pick2<2>(I) : O <= 64 ? mt_pick2<4>(I) : mt_pick2<8>(I);
 }
 
 constexpr long kMtRuns = 1024;  // workgroups, each a contiguous run of tiles
-long mt_runs(int B, long P, int pt) { return std::min(B * ((P + pt - 1) / pt), kMtRuns); }
+
+// workgroups of a call; fills the tiling in
+int mt_runs(MixTrainArgs &a, int pt) {
+  a.tpb = (int)((a.P + pt - 1) / pt);
+  a.tiles = a.B * a.tpb;
+  const int most = (int)std::min((long)a.tiles, kMtRuns);
+  a.per = (a.tiles + most - 1) / most;
+  return (a.tiles + a.per - 1) / a.per;
+}
 
 }  // namespace
 
 size_t mix_train_workspace_bytes(int B, int I, int O, long P, int dtype) {
-  return (size_t)mt_runs(B, P, mt_pick(O, I, dtype).pt) * ((size_t)O * I + O) * 4;
+  MixTrainArgs a{};
+  a.B = B, a.P = P;
+  return (size_t)mt_runs(a, mt_pick(O, I, dtype).pt) * ((size_t)O * I + O) * 4;
 }
 
 hipError_t launch_mix_save(const MixTrainArgs &a, int dtype, hipStream_t s) {
@@ -433,15 +325,15 @@ hipError_t launch_mix_save(const MixTrainArgs &a, int dtype, hipStream_t s) {
   if (hipError_t e = raise_lds_cap(k.fwd, k.lds_fwd); e != hipSuccess) return e;
   MixTrainArgs arg = a;
   void *args[] = {(void *)&arg};
-  return hipLaunchKernel(k.fwd, dim3((unsigned)mt_runs(a.B, a.P, k.pt)), dim3(kMtThreads), args, k.lds_fwd, s);
+  return hipLaunchKernel(k.fwd, dim3((unsigned)mt_runs(arg, k.pt)), dim3(kMtThreads), args, k.lds_fwd, s);
 }
 
 hipError_t launch_mix_bwd(const MixTrainArgs &a, int dtype, hipStream_t s) {
   const MtPick k = mt_pick(a.O, a.I, dtype);
-  int S = (int)mt_runs(a.B, a.P, k.pt);
+  MixTrainArgs arg = a;
+  int S = mt_runs(arg, k.pt);
   FNO_BOUNDS(check_mix_train(a, false, S, k.lds_bwd, dtype);)
   if (hipError_t e = raise_lds_cap(k.bwd, k.lds_bwd); e != hipSuccess) return e;
-  MixTrainArgs arg = a;
   void *args[] = {(void *)&arg};
   hipError_t e = hipLaunchKernel(k.bwd, dim3((unsigned)S), dim3(kMtThreads), args, k.lds_bwd, s);
   if (e != hipSuccess || !a.part) return e;

@@ -1,0 +1,138 @@
+// mix_train.hpp - pieces shared by the kernels of the training channel mix
+// (mix_train.hip).
+#pragma once
+
+#include "checkpoint.hpp"
+#include "gelu.hpp"
+
+namespace fno {
+
+constexpr int kMtThreads = 256;
+
+// 16 consecutive elements of a row
+template <int DT>
+struct Px16 {
+  static constexpr int N = DT == DT_F32 ? 4 : 2, V = ck_vec<DT>();
+  ck_u32x4 r[N];
+  __device__ __forceinline__ void load(const void *p, size_t i, long n) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) r[k] = ck_load<DT>(p, i + k * V, n - k * V);
+  }
+  __device__ __forceinline__ float get(int e) const { return ck_get<DT>(r[e / V], e % V); }
+  __device__ __forceinline__ uint32_t key() const {
+    uint32_t m = ck_maxkey<DT>(r[0]);
+#pragma unroll
+    for (int k = 1; k < N; ++k) m = max(m, ck_maxkey<DT>(r[k]));
+    return m;
+  }
+  __device__ __forceinline__ ck_u32x4 codes(int e) const {
+    ck_u32x4 q;
+    if constexpr (DT == DT_F32) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) q[k] = ck_codes<DT>(r[k], e).x;
+    } else {
+      const uint2 a = ck_codes<DT>(r[0], e), b = ck_codes<DT>(r[1], e);
+      q = ck_u32x4{a.x, a.y, b.x, b.y};
+    }
+    return q;
+  }
+};
+
+template <int DT>
+__device__ __forceinline__ void store16(void *p, size_t i, long n, const float (&v)[16]) {
+  constexpr int V = ck_vec<DT>();
+#pragma unroll
+  for (int k = 0; k < 16 / V; ++k) ck_store<DT>(p, i + k * V, n - k * V, ck_raw<DT>(v + k * V));
+}
+
+template <int DT>
+__device__ __forceinline__ float mt_load1(const void *p, size_t i) {
+  if constexpr (DT == DT_F32) return reinterpret_cast<const float *>(p)[i];
+  else if constexpr (DT == DT_F16) return (float)reinterpret_cast<const _Float16 *>(p)[i];
+  else return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(p)[i] << 16);
+}
+
+// 16 codes of a row's piece at pixel p (zeros past the row's blocks) and their exponent
+struct Code16 {
+  ck_u32x4 q;
+  int e;
+  __device__ __forceinline__ void load(const uint8_t *codes, const int8_t *exps, size_t row, long p, long nb, bool ok) {
+    q = ck_u32x4{0u, 0u, 0u, 0u};
+    e = 0;
+    if (ok && p < nb * kCkBlock) {
+      q = *reinterpret_cast<const ck_u32x4 *>(codes + row * nb * kCkBlock + p);
+      e = exps[row * nb + p / kCkBlock];
+    }
+  }
+  __device__ __forceinline__ float get(int k, float step) const { return ck_value(q[k >> 2], k & 3, step); }
+};
+
+template <int DT>
+__device__ __forceinline__ float mt_gelu(float z) { return DT == DT_F32 ? gelu(z) : gelu_half(z); }
+template <int DT>
+__device__ __forceinline__ float mt_slope(float z) { return DT == DT_F32 ? gelu_slope(z) : gelu_slope_half(z); }
+
+// The workgroup's sums of gA (ga[m][it]: rows 16 (ow + WO m) + 4 (lane / 16) + j,
+// columns 16 it + lane % 16) and gbias (gb[m], a lane's share of row
+// 16 (ow + WO m) + lane % 16) to the workspace, the WP pixel parts added through LDS
+// (WP OT 16 (IT 16 + 1) floats, where WP > 1).
+template <int OT, int IT, int WO, int WP>
+__device__ __forceinline__ void mt_finish(const MixTrainArgs &a, v4f (&ga)[OT / WO][IT], float (&gb)[OT / WO], float *xs,
+                                          int wave, int lane) {
+  const int g = lane >> 4, n = lane & 15, ow = wave % WO;
+  float *out = a.part + (size_t)blockIdx.x * ((size_t)a.O * a.I + a.O);
+  __syncthreads();
+#pragma unroll
+  for (int m = 0; m < OT / WO; ++m) {
+    float v = gb[m];
+    v += __shfl_xor(v, 16);
+    v += __shfl_xor(v, 32);
+    gb[m] = v;
+  }
+  constexpr int RO = OT * 16, RI = IT * 16 + 1;  // a row of gA and its gbias
+  const int part = wave / WO;
+#pragma unroll
+  for (int m = 0; m < OT / WO; ++m) {
+    const int ot = ow + WO * m;
+#pragma unroll
+    for (int it = 0; it < IT; ++it)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int o = 16 * ot + 4 * g + j, i = 16 * it + n;
+        if constexpr (WP == 1) {
+          if (o < a.O && i < a.I) out[(size_t)o * a.I + i] = ga[m][it][j];
+        } else {
+          xs[(part * RO + o) * RI + i] = ga[m][it][j];
+        }
+      }
+    if (g == 0) {
+      if constexpr (WP == 1) {
+        if (16 * ot + n < a.O) out[(size_t)a.O * a.I + 16 * ot + n] = gb[m];
+      } else {
+        xs[(part * RO + 16 * ot + n) * RI + IT * 16] = gb[m];
+      }
+    }
+  }
+  if constexpr (WP > 1) {
+    __syncthreads();
+    for (int u = threadIdx.x; u < RO * RI; u += kMtThreads) {
+      const int o = u / RI, i = u - o * RI;
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < WP; ++w) v += xs[(w * RO + o) * RI + i];
+      if (o < a.O && i < a.I) out[(size_t)o * a.I + i] = v;
+      if (o < a.O && i == IT * 16) out[(size_t)a.O * a.I + o] = v;
+    }
+  }
+}
+
+// a call's kernels, their tile and LDS
+struct MtPick {
+  const void *fwd, *bwd;
+  int pt;
+  size_t lds_fwd, lds_bwd;
+};
+MtPick mix_train_f16(int O, int I);
+MtPick mix_train_bf16(int O, int I);
+
+}  // namespace fno

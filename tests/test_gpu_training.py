@@ -372,3 +372,28 @@ def test_mix_gradients_against_differences():
         got = (f64(out[key]) * d).sum()
         # h^2 of the third derivative, and fp32 sums
         assert abs(got - diff) <= 1e-5 * (abs(f64(out[key]) * d)).sum()
+
+
+@pytest.mark.parametrize("scale_x,scale_gy", [(2.0 ** -18, 1.0), (1.0, 2.0 ** -12), (2.0 ** 7, 2.0 ** 14)])
+def test_mix_at_the_ends_of_fp16(scale_x, scale_gy):
+    """Subnormal inputs are used as they are; gz near the type's largest does not overflow on its way to gA
+    and gx (weights and x small enough that those are finite)."""
+    c = _mix_case("f16", 1, 20, 24, 100, True, seed=13)
+    for k, s in (("x", scale_x), ("add", min(scale_x, 1.0)), ("gy", scale_gy)):
+        t = (c[k][0].double().clamp(-3.9, 3.9) * s).half()
+        c[k] = (t, t.double().numpy())
+    small = (c["A"][0].double() / 64).half()
+    c["A"] = (small, small.double().numpy())
+    if scale_x > 1:
+        tiny = (c["x"][0].double() * 2.0 ** -20).half()
+        c["x"] = (tiny, tiny.double().numpy())
+    y, out = _mix_run(c, 1)
+    v = {k: t[1] for k, t in c.items()}
+    xk, adk = ref.round_trip(v["x"], -24), ref.round_trip(v["add"], -24)
+    (gx, gA, gb, gz), _ = ref.channel_mix_backward(xk, v["A"], v["bias"], adk, v["gy"], 1)
+    zs = ref.mix_pre(abs(xk), abs(v["A"]), abs(v["bias"]), None) + abs(v["add"]) + 1
+    gzs = abs(v["gy"]) * zs
+    # fp16's largest, 65504, bounds the outputs that can be compared
+    assert max(abs(gx).max(), abs(gA).max()) < 65504
+    close("gx", out["gx"], gx, "f16", extra=ACT["f16"], size=np.einsum("oi,bop->bip", abs(v["A"]), gzs))
+    close("gA", out["gA"], gA, "f16", extra=ACT["f16"], size=np.einsum("bop,bip->oi", gzs, abs(xk)))
