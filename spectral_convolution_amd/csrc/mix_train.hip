@@ -7,9 +7,9 @@
 //             gx = A^T gz,  gA = sum over pixels of gz x^T,  gbias = sum gz,  gadd = gz
 // for every sample and pixel, [batch][channels][pixels], act none or GELU.
 //
-// A workgroup of 4 waves takes tiles of 64 WP pixels and all channels (c_out
-// in OT, c_in in IT tiles of 16): the WO = min(4, OT) waves of a 64-pixel part
-// share the output channels, the WP = 4 / WO parts go side by side. The
+// A workgroup takes tiles of 64 WP pixels and all channels (c_out in OT, c_in in
+// IT tiles of 16): the OT waves of a 64-pixel part have one tile of the output
+// channels each, WP parts go side by side to make four waves (eight where OT is). The
 // channels' values are staged in LDS, [channel][pixel], once; every product
 // runs on matrix cores with fp32 accumulation:
 //   z   D[pixel][o], from x (A operand) and A^T (B operand, in registers)
@@ -33,53 +33,49 @@ namespace {
 
 template <int OT, int IT>
 struct MtGeom {
-  static constexpr int WO = OT < 4 ? OT : 4, WP = 4 / WO, OTW = OT / WO;
+  static constexpr int WAVES = OT == 8 ? 8 : 4, THREADS = 64 * WAVES;
+  static constexpr int WO = OT, WP = WAVES / WO, WI = IT < WAVES ? IT : WAVES, ITW = IT / WI;
   static constexpr int PT = 64 * WP, PITCH = PT + 4;   // floats
   static constexpr int XS = IT * 16 * PITCH * 4, GS = OT * 16 * PITCH * 4;
-  static constexpr int UNITS = IT * 16 * (PT / 16), NU = (UNITS + kMtThreads - 1) / kMtThreads;
+  static constexpr int UNITS = IT * 16 * (PT / 16), NU = (UNITS + THREADS - 1) / THREADS;
 };
 
 // z of 16 pixels of the wave's output channels: zv[m][4 j + pt], without bias
 template <int OT, int IT>
-__device__ __forceinline__ void mt_z(const float *xs, int pb, int lane, const float (&wf)[MtGeom<OT, IT>::OTW][IT * 4],
-                                     v4f (&z)[MtGeom<OT, IT>::OTW][4]) {
+__device__ __forceinline__ void mt_z(const float *xs, int pb, int lane, const float (&wf)[IT * 4],
+                                     v4f (&z)[4]) {
   using G = MtGeom<OT, IT>;
   const int g = lane >> 4, n = lane & 15;
 #pragma unroll
-  for (int m = 0; m < G::OTW; ++m)
-#pragma unroll
-    for (int pt = 0; pt < 4; ++pt) z[m][pt] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int pt = 0; pt < 4; ++pt) z[pt] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int kk = 0; kk < IT * 4; ++kk) {
     const float4 a = *reinterpret_cast<const float4 *>(xs + (4 * kk + g) * G::PITCH + pb + 4 * n);
     const float av[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-    for (int m = 0; m < G::OTW; ++m)
-#pragma unroll
       for (int pt = 0; pt < 4; ++pt)
-        z[m][pt] = __builtin_amdgcn_mfma_f32_16x16x4f32(av[pt], wf[m][kk], z[m][pt], 0, 0, 0);
+        z[pt] = __builtin_amdgcn_mfma_f32_16x16x4f32(av[pt], wf[kk], z[pt], 0, 0, 0);
   }
 }
 
 }  // namespace
 
 template <int OT, int IT>
-__global__ __launch_bounds__(kMtThreads) void fno_mix_save(MixTrainArgs a) {
+__global__ __launch_bounds__((MtGeom<OT, IT>::THREADS)) void fno_mix_save(MixTrainArgs a) {
   using G = MtGeom<OT, IT>;
   extern __shared__ float4 lds4[];
   float *xs = reinterpret_cast<float *>(lds4);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, n = lane & 15;
   const int ow = wave % G::WO, pb = 64 * (wave / G::WO);
   const long P = a.P, nb = (P + kCkBlock - 1) / kCkBlock;
-  float wf[G::OTW][IT * 4], bias[G::OTW];
-#pragma unroll
-  for (int m = 0; m < G::OTW; ++m) {
-    const int o = 16 * (ow + G::WO * m) + n;
-    bias[m] = a.bias && o < a.O ? mt_load1<DT_F32>(a.bias, o) : 0.f;
+  float wf[IT * 4], bias;
+  {
+    const int o = 16 * (ow) + n;
+    bias = a.bias && o < a.O ? mt_load1<DT_F32>(a.bias, o) : 0.f;
 #pragma unroll
     for (int kk = 0; kk < IT * 4; ++kk) {
       const int i = 4 * kk + g;
-      wf[m][kk] = o < a.O && i < a.I ? mt_load1<DT_F32>(a.A, (size_t)o * a.I + i) : 0.f;
+      wf[kk] = o < a.O && i < a.I ? mt_load1<DT_F32>(a.A, (size_t)o * a.I + i) : 0.f;
     }
   }
   const int t0 = blockIdx.x * a.per, t1 = min(a.tiles, t0 + a.per);
@@ -88,8 +84,8 @@ __global__ __launch_bounds__(kMtThreads) void fno_mix_save(MixTrainArgs a) {
     const long p0 = (long)(t - b * a.tpb) * G::PT;
 #pragma unroll
     for (int k = 0; k < G::NU; ++k) {
-      const int u = tid + k * kMtThreads, i = u / (G::PT / 16), pu = 16 * (u % (G::PT / 16));
-      if (G::UNITS % kMtThreads != 0 && u >= G::UNITS) break;  // whole pairs of lanes
+      const int u = tid + k * G::THREADS, i = u / (G::PT / 16), pu = 16 * (u % (G::PT / 16));
+      if (G::UNITS % G::THREADS != 0 && u >= G::UNITS) break;  // whole pairs of lanes
       const long p = p0 + pu;
       const size_t row = (size_t)b * a.I + i;
       Px16<DT_F32> v;
@@ -107,12 +103,11 @@ __global__ __launch_bounds__(kMtThreads) void fno_mix_save(MixTrainArgs a) {
         reinterpret_cast<float4 *>(d)[q] = make_float4(v.get(4 * q), v.get(4 * q + 1), v.get(4 * q + 2), v.get(4 * q + 3));
     }
     __syncthreads();
-    v4f z[G::OTW][4];
+    v4f z[4];
     mt_z<OT, IT>(xs, pb, lane, wf, z);
     const long p = p0 + pb + 16 * g;
-#pragma unroll
-    for (int m = 0; m < G::OTW; ++m) {
-      const int o = 16 * (ow + G::WO * m) + n;
+    {
+      const int o = 16 * (ow) + n;
       const bool ok = o < a.O;
       const size_t row = (size_t)b * a.O + o;
       Px16<DT_F32> ad;
@@ -129,7 +124,7 @@ __global__ __launch_bounds__(kMtThreads) void fno_mix_save(MixTrainArgs a) {
       float y[16];
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        const float v = z[m][e & 3][e >> 2] + bias[m] + ad.get(e);
+        const float v = z[e & 3][e >> 2] + bias + ad.get(e);
         y[e] = a.act ? mt_gelu<DT_F32>(v) : v;
       }
       if (ok) store16<DT_F32>(a.y, row * P + p, P - p, y);
@@ -139,34 +134,32 @@ __global__ __launch_bounds__(kMtThreads) void fno_mix_save(MixTrainArgs a) {
 }
 
 template <int OT, int IT>
-__global__ __launch_bounds__(kMtThreads) void fno_mix_bwd(MixTrainArgs a) {
+__global__ __launch_bounds__((MtGeom<OT, IT>::THREADS)) void fno_mix_bwd(MixTrainArgs a) {
   using G = MtGeom<OT, IT>;
-  constexpr int WI = IT < 4 ? IT : 4, ITW = IT / WI;  // gx: waves over c_in, tiles of each
   extern __shared__ float4 lds4[];
   float *xs = reinterpret_cast<float *>(lds4), *gs = xs + G::XS / 4;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, n = lane & 15;
-  const int ow = wave % G::WO, pb = 64 * (wave / G::WO), iw = wave % WI;
+  const int ow = wave % G::WO, pb = 64 * (wave / G::WO), iw = wave % G::WI;
   const long P = a.P, nb = (P + kCkBlock - 1) / kCkBlock;
-  float wf[G::OTW][IT * 4], wt[ITW][OT * 4], bias[G::OTW], gb[G::OTW];
-  v4f ga[G::OTW][IT];
-#pragma unroll
-  for (int m = 0; m < G::OTW; ++m) {
-    const int o = 16 * (ow + G::WO * m) + n;
-    gb[m] = 0.f;
-    bias[m] = a.bias && o < a.O ? mt_load1<DT_F32>(a.bias, o) : 0.f;
+  float wf[IT * 4], wt[G::ITW][OT * 4], bias, gb;
+  v4f ga[IT];
+  {
+    const int o = 16 * (ow) + n;
+    gb = 0.f;
+    bias = a.bias && o < a.O ? mt_load1<DT_F32>(a.bias, o) : 0.f;
 #pragma unroll
     for (int kk = 0; kk < IT * 4; ++kk) {
       const int i = 4 * kk + g;
-      wf[m][kk] = o < a.O && i < a.I ? mt_load1<DT_F32>(a.A, (size_t)o * a.I + i) : 0.f;
+      wf[kk] = o < a.O && i < a.I ? mt_load1<DT_F32>(a.A, (size_t)o * a.I + i) : 0.f;
     }
 #pragma unroll
-    for (int it = 0; it < IT; ++it) ga[m][it] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int it = 0; it < IT; ++it) ga[it] = v4f{0.f, 0.f, 0.f, 0.f};
   }
 #pragma unroll
-  for (int m = 0; m < ITW; ++m)
+  for (int m = 0; m < G::ITW; ++m)
 #pragma unroll
     for (int kk = 0; kk < OT * 4; ++kk) {
-      const int o = 4 * kk + g, i = 16 * (iw + WI * m) + n;
+      const int o = 4 * kk + g, i = 16 * (iw + G::WI * m) + n;
       wt[m][kk] = o < a.O && i < a.I ? mt_load1<DT_F32>(a.A, (size_t)o * a.I + i) : 0.f;
     }
   const int t0 = blockIdx.x * a.per, t1 = min(a.tiles, t0 + a.per);
@@ -175,8 +168,8 @@ __global__ __launch_bounds__(kMtThreads) void fno_mix_bwd(MixTrainArgs a) {
     const long p0 = (long)(t - b * a.tpb) * G::PT;
 #pragma unroll
     for (int k = 0; k < G::NU; ++k) {
-      const int u = tid + k * kMtThreads, i = u / (G::PT / 16), pu = 16 * (u % (G::PT / 16));
-      if (G::UNITS % kMtThreads != 0 && u >= G::UNITS) break;
+      const int u = tid + k * G::THREADS, i = u / (G::PT / 16), pu = 16 * (u % (G::PT / 16));
+      if (G::UNITS % G::THREADS != 0 && u >= G::UNITS) break;
       Code16 c;
       c.load(a.xq, a.xe, (size_t)b * a.I + i, p0 + pu, nb, i < a.I);
       const float s = ck_step(c.e);
@@ -187,12 +180,11 @@ __global__ __launch_bounds__(kMtThreads) void fno_mix_bwd(MixTrainArgs a) {
             make_float4(c.get(4 * q, s), c.get(4 * q + 1, s), c.get(4 * q + 2, s), c.get(4 * q + 3, s));
     }
     __syncthreads();
-    v4f z[G::OTW][4];
+    v4f z[4];
     if (a.act) mt_z<OT, IT>(xs, pb, lane, wf, z);
     const long p = p0 + pb + 16 * g;
-#pragma unroll
-    for (int m = 0; m < G::OTW; ++m) {
-      const int o = 16 * (ow + G::WO * m) + n;
+    {
+      const int o = 16 * (ow) + n;
       const bool ok = o < a.O;
       const size_t row = (size_t)b * a.O + o;
       Px16<DT_F32> gy;
@@ -205,34 +197,34 @@ __global__ __launch_bounds__(kMtThreads) void fno_mix_bwd(MixTrainArgs a) {
         c.load(a.aq, a.ae, row, p, nb, a.aq && ok);
         const float s = ck_step(c.e);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) gz[e] *= mt_slope<DT_F32>(z[m][e & 3][e >> 2] + bias[m] + c.get(e, s));
+        for (int e = 0; e < 16; ++e) gz[e] *= mt_slope<DT_F32>(z[e & 3][e >> 2] + bias + c.get(e, s));
       }
       if (a.gadd && ok) store16<DT_F32>(a.gadd, row * P + p, P - p, gz);
-      float *d = gs + (16 * (ow + G::WO * m) + n) * G::PITCH + pb + 16 * g;
+      float *d = gs + (16 * (ow) + n) * G::PITCH + pb + 16 * g;
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         reinterpret_cast<float4 *>(d)[q] = make_float4(gz[4 * q], gz[4 * q + 1], gz[4 * q + 2], gz[4 * q + 3]);
       if (a.part) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) gb[m] += gz[e];
+        for (int e = 0; e < 16; ++e) gb += gz[e];
 #pragma unroll
         for (int it = 0; it < IT; ++it)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const float4 xv = *reinterpret_cast<const float4 *>(xs + (16 * it + n) * G::PITCH + pb + 16 * g + 4 * q);
-            ga[m][it] = __builtin_amdgcn_mfma_f32_16x16x4f32(gz[4 * q], xv.x, ga[m][it], 0, 0, 0);
-            ga[m][it] = __builtin_amdgcn_mfma_f32_16x16x4f32(gz[4 * q + 1], xv.y, ga[m][it], 0, 0, 0);
-            ga[m][it] = __builtin_amdgcn_mfma_f32_16x16x4f32(gz[4 * q + 2], xv.z, ga[m][it], 0, 0, 0);
-            ga[m][it] = __builtin_amdgcn_mfma_f32_16x16x4f32(gz[4 * q + 3], xv.w, ga[m][it], 0, 0, 0);
+            ga[it] = __builtin_amdgcn_mfma_f32_16x16x4f32(gz[4 * q], xv.x, ga[it], 0, 0, 0);
+            ga[it] = __builtin_amdgcn_mfma_f32_16x16x4f32(gz[4 * q + 1], xv.y, ga[it], 0, 0, 0);
+            ga[it] = __builtin_amdgcn_mfma_f32_16x16x4f32(gz[4 * q + 2], xv.z, ga[it], 0, 0, 0);
+            ga[it] = __builtin_amdgcn_mfma_f32_16x16x4f32(gz[4 * q + 3], xv.w, ga[it], 0, 0, 0);
           }
       }
     }
     __syncthreads();
     if (a.gx) {
 #pragma unroll
-      for (int m = 0; m < ITW; ++m) {
-        const int i = 16 * (iw + WI * m) + n;
-        for (int sb = 64 * (wave / WI); sb < G::PT; sb += 64 * (4 / WI)) {
+      for (int m = 0; m < G::ITW; ++m) {
+        const int i = 16 * (iw + G::WI * m) + n;
+        for (int sb = 64 * (wave / G::WI); sb < G::PT; sb += 64 * (G::WAVES / G::WI)) {
           v4f acc[4] = {v4f{0.f, 0.f, 0.f, 0.f}, v4f{0.f, 0.f, 0.f, 0.f}, v4f{0.f, 0.f, 0.f, 0.f}, v4f{0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
           for (int kk = 0; kk < OT * 4; ++kk) {
@@ -254,7 +246,7 @@ __global__ __launch_bounds__(kMtThreads) void fno_mix_bwd(MixTrainArgs a) {
     // its gz overwrite gs only after the next barrier
   }
   if (!a.part) return;
-  mt_finish<OT, IT, G::WO, G::WP>(a, ga, gb, xs, wave, lane);
+  mt_finish<OT, IT, G::WP, G::THREADS>(a, ga, gb, xs, wave, lane);
 }
 
 // gA and gbias from the workgroups' sums part[S][O I + O]: 32 elements a
@@ -287,8 +279,8 @@ namespace {
 template <int OT, int IT>
 MtPick mt_pick3() {
   using G = MtGeom<OT, IT>;
-  return {(const void *)fno_mix_save<OT, IT>, (const void *)fno_mix_bwd<OT, IT>, G::PT, (size_t)G::XS,
-          (size_t)(G::XS + G::GS)};
+  return {(const void *)fno_mix_save<OT, IT>, (const void *)fno_mix_bwd<OT, IT>, G::PT, G::PT, (size_t)G::XS,
+          (size_t)(G::XS + G::GS), G::THREADS, G::THREADS, 1024 / G::WAVES * 2};
 }
 template <int OT>
 MtPick mt_pick2(int I) {
@@ -300,23 +292,26 @@ MtPick mt_pick(int O, int I, int dtype) {
   return O <= 16 ? mt_pick2<1>(I) : O <= 32 ? mt_pick2<2>(I) : O <= 64 ? mt_pick2<4>(I) : mt_pick2<8>(I);
 }
 
-constexpr long kMtRuns = 1024;  // workgroups, each a contiguous run of tiles
-
-// workgroups of a call; fills the tiling in
-int mt_runs(MixTrainArgs &a, int pt) {
+// Workgroups of a call, each a contiguous run of tiles; fills the tiling in. The
+// backward takes as many as the chip holds at once: with a few more, the last
+// ones run alone (1024 of 768: 382 us against 300 at 32 x 64 x 64 channels, 256^2).
+int mt_runs(MixTrainArgs &a, int pt, long most) {
   a.tpb = (int)((a.P + pt - 1) / pt);
   a.tiles = a.B * a.tpb;
-  const int most = (int)std::min((long)a.tiles, kMtRuns);
-  a.per = (a.tiles + most - 1) / most;
+  const int m = (int)std::min((long)a.tiles, most);
+  a.per = (a.tiles + m - 1) / m;
   return (a.tiles + a.per - 1) / a.per;
 }
+
+constexpr long kMtForward = 2048;
 
 }  // namespace
 
 size_t mix_train_workspace_bytes(int B, int I, int O, long P, int dtype) {
   MixTrainArgs a{};
   a.B = B, a.P = P;
-  return (size_t)mt_runs(a, mt_pick(O, I, dtype).pt) * ((size_t)O * I + O) * 4;
+  const MtPick k = mt_pick(O, I, dtype);
+  return (size_t)mt_runs(a, k.pt_bwd, k.resident) * ((size_t)O * I + O) * 4;
 }
 
 hipError_t launch_mix_save(const MixTrainArgs &a, int dtype, hipStream_t s) {
@@ -325,17 +320,17 @@ hipError_t launch_mix_save(const MixTrainArgs &a, int dtype, hipStream_t s) {
   if (hipError_t e = raise_lds_cap(k.fwd, k.lds_fwd); e != hipSuccess) return e;
   MixTrainArgs arg = a;
   void *args[] = {(void *)&arg};
-  return hipLaunchKernel(k.fwd, dim3((unsigned)mt_runs(arg, k.pt)), dim3(kMtThreads), args, k.lds_fwd, s);
+  return hipLaunchKernel(k.fwd, dim3((unsigned)mt_runs(arg, k.pt_fwd, kMtForward)), dim3((unsigned)k.threads_fwd), args, k.lds_fwd, s);
 }
 
 hipError_t launch_mix_bwd(const MixTrainArgs &a, int dtype, hipStream_t s) {
   const MtPick k = mt_pick(a.O, a.I, dtype);
   MixTrainArgs arg = a;
-  int S = mt_runs(arg, k.pt);
+  int S = mt_runs(arg, k.pt_bwd, k.resident);
   FNO_BOUNDS(check_mix_train(a, false, S, k.lds_bwd, dtype);)
   if (hipError_t e = raise_lds_cap(k.bwd, k.lds_bwd); e != hipSuccess) return e;
   void *args[] = {(void *)&arg};
-  hipError_t e = hipLaunchKernel(k.bwd, dim3((unsigned)S), dim3(kMtThreads), args, k.lds_bwd, s);
+  hipError_t e = hipLaunchKernel(k.bwd, dim3((unsigned)S), dim3((unsigned)k.threads_bwd), args, k.lds_bwd, s);
   if (e != hipSuccess || !a.part) return e;
   void *pargs[] = {(void *)&arg, (void *)&S};
   const void *pk = dtype == DT_F32 ? (const void *)fno_mix_params<DT_F32>

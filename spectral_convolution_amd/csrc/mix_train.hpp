@@ -7,8 +7,6 @@
 
 namespace fno {
 
-constexpr int kMtThreads = 256;
-
 // 16 consecutive elements of a row
 template <int DT>
 struct Px16 {
@@ -72,65 +70,52 @@ __device__ __forceinline__ float mt_gelu(float z) { return DT == DT_F32 ? gelu(z
 template <int DT>
 __device__ __forceinline__ float mt_slope(float z) { return DT == DT_F32 ? gelu_slope(z) : gelu_slope_half(z); }
 
-// The workgroup's sums of gA (ga[m][it]: rows 16 (ow + WO m) + 4 (lane / 16) + j,
-// columns 16 it + lane % 16) and gbias (gb[m], a lane's share of row
-// 16 (ow + WO m) + lane % 16) to the workspace, the WP pixel parts added through LDS
+// The workgroup's sums of gA (ga[it]: rows 16 ow + 4 (lane / 16) + j, columns
+// 16 it + lane % 16, ow = wave % OT) and gbias (gb, a lane's share of row
+// 16 ow + lane % 16) to the workspace, the WP pixel parts added through LDS
 // (WP OT 16 (IT 16 + 1) floats, where WP > 1).
-template <int OT, int IT, int WO, int WP>
-__device__ __forceinline__ void mt_finish(const MixTrainArgs &a, v4f (&ga)[OT / WO][IT], float (&gb)[OT / WO], float *xs,
-                                          int wave, int lane) {
-  const int g = lane >> 4, n = lane & 15, ow = wave % WO;
+template <int OT, int IT, int WP, int THREADS>
+__device__ __forceinline__ void mt_finish(const MixTrainArgs &a, const v4f (&ga)[IT], float gb, float *lds, int wave,
+                                          int lane) {
+  constexpr int RO = OT * 16, RI = IT * 16 + 1;  // rows; a row of gA and its gbias
+  const int g = lane >> 4, n = lane & 15, ow = wave % OT, part = wave / OT;
   float *out = a.part + (size_t)blockIdx.x * ((size_t)a.O * a.I + a.O);
+  gb += __shfl_xor(gb, 16);
+  gb += __shfl_xor(gb, 32);
   __syncthreads();
 #pragma unroll
-  for (int m = 0; m < OT / WO; ++m) {
-    float v = gb[m];
-    v += __shfl_xor(v, 16);
-    v += __shfl_xor(v, 32);
-    gb[m] = v;
-  }
-  constexpr int RO = OT * 16, RI = IT * 16 + 1;  // a row of gA and its gbias
-  const int part = wave / WO;
+  for (int it = 0; it < IT; ++it)
 #pragma unroll
-  for (int m = 0; m < OT / WO; ++m) {
-    const int ot = ow + WO * m;
-#pragma unroll
-    for (int it = 0; it < IT; ++it)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int o = 16 * ot + 4 * g + j, i = 16 * it + n;
-        if constexpr (WP == 1) {
-          if (o < a.O && i < a.I) out[(size_t)o * a.I + i] = ga[m][it][j];
-        } else {
-          xs[(part * RO + o) * RI + i] = ga[m][it][j];
-        }
-      }
-    if (g == 0) {
-      if constexpr (WP == 1) {
-        if (16 * ot + n < a.O) out[(size_t)a.O * a.I + 16 * ot + n] = gb[m];
-      } else {
-        xs[(part * RO + 16 * ot + n) * RI + IT * 16] = gb[m];
-      }
+    for (int j = 0; j < 4; ++j) {
+      const int o = 16 * ow + 4 * g + j, i = 16 * it + n;
+      if constexpr (WP > 1) lds[(part * RO + o) * RI + i] = ga[it][j];
+      else if (o < a.O && i < a.I) out[(size_t)o * a.I + i] = ga[it][j];
     }
+  if (g == 0) {
+    if constexpr (WP > 1) lds[(part * RO + 16 * ow + n) * RI + IT * 16] = gb;
+    else if (16 * ow + n < a.O) out[(size_t)a.O * a.I + 16 * ow + n] = gb;
   }
   if constexpr (WP > 1) {
     __syncthreads();
-    for (int u = threadIdx.x; u < RO * RI; u += kMtThreads) {
+    for (int u = threadIdx.x; u < RO * RI; u += THREADS) {
       const int o = u / RI, i = u - o * RI;
       float v = 0.f;
 #pragma unroll
-      for (int w = 0; w < WP; ++w) v += xs[(w * RO + o) * RI + i];
+      for (int w = 0; w < WP; ++w) v += lds[(w * RO + o) * RI + i];
       if (o < a.O && i < a.I) out[(size_t)o * a.I + i] = v;
       if (o < a.O && i == IT * 16) out[(size_t)a.O * a.I + o] = v;
     }
   }
 }
 
-// a call's kernels, their tile and LDS
+// a call's kernels; of each its tile's pixels, LDS and threads, and how many of the
+// backward's workgroups the chip holds at once
 struct MtPick {
   const void *fwd, *bwd;
-  int pt;
+  int pt_fwd, pt_bwd;
   size_t lds_fwd, lds_bwd;
+  int threads_fwd, threads_bwd;
+  int resident;
 };
 MtPick mix_train_f16(int O, int I);
 MtPick mix_train_bf16(int O, int I);

@@ -26,14 +26,24 @@ typedef short mt_s16x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 mt_h8 __attribute__((ext_vector_type(8)));
 typedef __bf16 mt_b8 __attribute__((ext_vector_type(8)));
 
-template <int OT, int IT>
+// WAVES in a workgroup. Backward: four, or eight for eight tiles of c_out, so that
+// a wave has one of them; its registers (a row of gA, a tile's inputs ahead)
+// fit three waves a SIMD up to 16 tiles of gA, where few waves do not stage many
+// rows of x. Forward: eight from four tiles of c_out on, tiles of 128 pixels: with
+// 64, a row's piece of the codes is half a line, and evicted as such.
+template <int OT>
+constexpr int mh_waves(bool fwd) { return OT == 8 || (fwd && OT == 4) ? 8 : 4; }
+
+template <int OT, int IT, bool FWD>
 struct MhGeom {
-  static constexpr int WO = OT < 4 ? OT : 4, WP = 4 / WO, OTW = OT / WO;  // waves over c_out, over pixels; tiles of a wave
-  static constexpr int WI = IT < 4 ? IT : 4, ITW = IT / WI;               // gx: waves over c_in; tiles of a wave
+  static constexpr int WAVES = mh_waves<OT>(FWD), THREADS = 64 * WAVES;
+  static constexpr int PER_EU = OT * IT <= 16 && IT <= 2 * OT ? 3 : 2;
+  static constexpr int WO = OT, WP = WAVES / WO;                       // waves over c_out, over pixels
+  static constexpr int WI = IT < WAVES ? IT : WAVES, ITW = IT / WI;    // gx: waves over c_in; tiles of a wave
   static constexpr int KI = (IT + 1) / 2, KO = (OT + 1) / 2;              // 32-channel steps
   static constexpr int PT = 64 * WP, PITCH = PT + 4;                      // pixels of a tile; halves of an LDS row
   static constexpr int XS = KI * 32 * PITCH * 2, GS = KO * 32 * PITCH * 2;
-  static constexpr int UNITS = IT * 16 * (PT / 16), NU = (UNITS + kMtThreads - 1) / kMtThreads;
+  static constexpr int UNITS = IT * 16 * (PT / 16), NU = (UNITS + THREADS - 1) / THREADS;
   static constexpr int SUMS = WP > 1 ? WP * OT * 16 * (IT * 16 + 1) * 4 : 0;
   static constexpr int LDS_FWD = 2 * XS, LDS_BWD = XS + 2 * GS > SUMS ? XS + 2 * GS : SUMS;
 };
@@ -138,42 +148,44 @@ template <int DT>
 __device__ __forceinline__ float mh_join(float hi, float lo) { return DT == DT_F16 ? fmaf(lo, 0x1p-10f, hi + hi) : hi; }
 
 // zero the LDS rows past the channels' tiles (half of a 32-channel step): never written again
-template <int T, int K, int PITCH>
+template <int T, int K, int PITCH, int THREADS>
 __device__ __forceinline__ void mh_clear(uint16_t *s) {
   if constexpr (16 * T < 32 * K)
-    for (int v = threadIdx.x; v < (32 * K - 16 * T) * PITCH; v += kMtThreads) s[16 * T * PITCH + v] = 0;
+    for (int v = threadIdx.x; v < (32 * K - 16 * T) * PITCH; v += THREADS) s[16 * T * PITCH + v] = 0;
 }
 
 template <int DT, int OT, int IT>
-__global__ __launch_bounds__(kMtThreads) void fno_mix_save_half(MixTrainArgs a) {
-  using G = MhGeom<OT, IT>;
+__global__ __launch_bounds__((MhGeom<OT, IT, true>::THREADS)) void fno_mix_save_half(MixTrainArgs a) {
+  using G = MhGeom<OT, IT, true>;
   extern __shared__ float4 lds4[];
   uint16_t *xs0 = reinterpret_cast<uint16_t *>(lds4);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4, n = lane & 15;
   const int ow = wave % G::WO, pb = 64 * (wave / G::WO);
   const long P = a.P, nb = (P + kCkBlock - 1) / kCkBlock;
   const uint16_t *A = reinterpret_cast<const uint16_t *>(a.A);
-  ck_u32x4 wf[G::OTW][G::KI];
-  float bias[G::OTW];
-#pragma unroll
-  for (int m = 0; m < G::OTW; ++m) {
-    const int o = 16 * (ow + G::WO * m) + n;
-    bias[m] = a.bias && o < a.O ? mt_load1<DT>(a.bias, o) : 0.f;
+  ck_u32x4 wf[G::KI];
+  float bias;
+  {
+    const int o = 16 * (ow) + n;
+    bias = a.bias && o < a.O ? mt_load1<DT>(a.bias, o) : 0.f;
 #pragma unroll
     for (int k = 0; k < G::KI; ++k)
-      wf[m][k] = mh_weights(A, o, a.O, a.I, k, lane, [&](int c, int s) { return c * a.I + s; });
+      wf[k] = mh_weights(A, o, a.O, a.I, k, lane, [&](int c, int s) { return c * a.I + s; });
   }
-  mh_clear<IT, G::KI, G::PITCH>(xs0);
-  mh_clear<IT, G::KI, G::PITCH>(xs0 + G::XS / 2);
+  mh_clear<IT, G::KI, G::PITCH, G::THREADS>(xs0);
+  mh_clear<IT, G::KI, G::PITCH, G::THREADS>(xs0 + G::XS / 2);
   const int t0 = blockIdx.x * a.per, t1 = min(a.tiles, t0 + a.per);
-  Px16<DT> xv[G::NU];
+  // the next tile's x and add, in flight over a whole tile's work
+  Px16<DT> xv[G::NU], nadd;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) nadd.r[q] = ck_u32x4{0u, 0u, 0u, 0u};
   auto fetch = [&](int t) {
     const int b = t / a.tpb;
     const long p0 = (long)(t - b * a.tpb) * G::PT;
 #pragma unroll
     for (int k = 0; k < G::NU; ++k) {
-      const int u = tid + k * kMtThreads, i = u / (G::PT / 16), pu = 16 * (u % (G::PT / 16));
-      const bool ok = (G::UNITS % kMtThreads == 0 || u < G::UNITS) && i < a.I;
+      const int u = tid + k * G::THREADS, i = u / (G::PT / 16), pu = 16 * (u % (G::PT / 16));
+      const bool ok = (G::UNITS % G::THREADS == 0 || u < G::UNITS) && i < a.I;
       const size_t row = (size_t)b * a.I + (ok ? i : 0);
       if (p0 + G::PT <= P) {
         xv[k].load(a.x, row * P + p0 + pu, 16);
@@ -184,6 +196,13 @@ __global__ __launch_bounds__(kMtThreads) void fno_mix_save_half(MixTrainArgs a) 
         xv[k].load(a.x, row * P + p0 + pu, ok ? P - p0 - pu : 0);
       }
     }
+    if (a.add)
+      {
+        const int o = 16 * (ow) + n;
+        const long p = p0 + pb + 16 * g;
+        const size_t row = (size_t)b * a.O + min(o, a.O - 1);
+        nadd.load(a.add, row * P + p, p0 + G::PT <= P ? 16 : o < a.O ? P - p : 0);
+      }
   };
   if (t0 < t1) fetch(t0);
   for (int t = t0; t < t1; ++t) {
@@ -193,8 +212,8 @@ __global__ __launch_bounds__(kMtThreads) void fno_mix_save_half(MixTrainArgs a) 
     uint16_t *xs = xs0 + (t & 1) * (G::XS / 2);  // the other buffer may still be read by a slower wave
 #pragma unroll
     for (int k = 0; k < G::NU; ++k) {
-      const int u = tid + k * kMtThreads, i = u / (G::PT / 16), pu = 16 * (u % (G::PT / 16));
-      if (G::UNITS % kMtThreads != 0 && u >= G::UNITS) break;  // whole pairs of lanes
+      const int u = tid + k * G::THREADS, i = u / (G::PT / 16), pu = 16 * (u % (G::PT / 16));
+      if (G::UNITS % G::THREADS != 0 && u >= G::UNITS) break;  // whole pairs of lanes
       const long p = p0 + pu;
       uint32_t key = xv[k].key();
       key = max(key, ck_dpp<kDppXor1>(key));
@@ -208,52 +227,38 @@ __global__ __launch_bounds__(kMtThreads) void fno_mix_save_half(MixTrainArgs a) 
       mh_write16(d, xv[k].r[0]);
       mh_write16(d + 8, xv[k].r[1]);
     }
-    // add's values, in flight over the barrier and the product
     const long p = p0 + pb + 16 * g;
-    Px16<DT> ad[G::OTW];
-#pragma unroll
-    for (int m = 0; m < G::OTW; ++m) {
-      const int o = 16 * (ow + G::WO * m) + n;
-#pragma unroll
-      for (int q = 0; q < 2; ++q) ad[m].r[q] = ck_u32x4{0u, 0u, 0u, 0u};
-      if (a.add) {
-        const size_t row = (size_t)b * a.O + min(o, a.O - 1);
-        ad[m].load(a.add, row * P + p, whole ? 16 : o < a.O ? P - p : 0);
-      }
-    }
+    Px16<DT> ad;
+    ad = nadd;
     __syncthreads();
     if (t + 1 < t1) fetch(t + 1);
-    v4f z[G::OTW][4];
+    v4f z[4];
 #pragma unroll
-    for (int m = 0; m < G::OTW; ++m)
-#pragma unroll
-      for (int pt = 0; pt < 4; ++pt) z[m][pt] = v4f{bias[m], bias[m], bias[m], bias[m]};
+      for (int pt = 0; pt < 4; ++pt) z[pt] = v4f{bias, bias, bias, bias};
 #pragma unroll
     for (int k = 0; k < G::KI; ++k)
 #pragma unroll
       for (int pt = 0; pt < 4; ++pt) {
         const ck_u32x4 xa = mh_pixels<G::PITCH>(xs, k, pb, pt, lane);
-#pragma unroll
-        for (int m = 0; m < G::OTW; ++m) z[m][pt] = mh_mma<DT>(xa, wf[m][k], z[m][pt]);
+        z[pt] = mh_mma<DT>(xa, wf[k], z[pt]);
       }
-#pragma unroll
-    for (int m = 0; m < G::OTW; ++m) {
-      const int o = 16 * (ow + G::WO * m) + n;
+    {
+      const int o = 16 * (ow) + n;
       const bool ok = o < a.O;
       const size_t row = (size_t)b * a.O + o;
       if (a.aq) {
-        uint32_t key = ad[m].key();
+        uint32_t key = ad.key();
         const auto s = __builtin_amdgcn_permlane16_swap(key, key, false, false);  // the block's other 16 pixels
         const int e = ck_exponent<DT>(max(s[0], s[1]));
         if (ok && p < nb * kCkBlock) {
-          *reinterpret_cast<ck_u32x4 *>(a.aq + row * nb * kCkBlock + p) = ad[m].codes(e);
+          *reinterpret_cast<ck_u32x4 *>(a.aq + row * nb * kCkBlock + p) = ad.codes(e);
           if ((g & 1) == 0) a.ae[row * nb + p / kCkBlock] = (int8_t)e;
         }
       }
       float y[16];
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        const float v = z[m][e >> 2][e & 3] + ad[m].get(e);
+        const float v = z[e >> 2][e & 3] + ad.get(e);
         y[e] = a.act ? mt_gelu<DT>(v) : v;
       }
       if (ok) store16<DT>(a.y, row * P + p, whole ? 16 : P - p, y);
@@ -262,46 +267,62 @@ __global__ __launch_bounds__(kMtThreads) void fno_mix_save_half(MixTrainArgs a) 
 }
 
 template <int DT, int OT, int IT>
-__global__ __launch_bounds__(kMtThreads) void fno_mix_bwd_half(MixTrainArgs a) {
-  using G = MhGeom<OT, IT>;
+__global__ __launch_bounds__((MhGeom<OT, IT, false>::THREADS))
+    __attribute__((amdgpu_waves_per_eu(MhGeom<OT, IT, false>::PER_EU))) void fno_mix_bwd_half(MixTrainArgs a) {
+  using G = MhGeom<OT, IT, false>;
   extern __shared__ float4 lds4[];
   uint16_t *xs = reinterpret_cast<uint16_t *>(lds4), *gh = xs + G::XS / 2, *gl = gh + G::GS / 2;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4, n = lane & 15;
   const int ow = wave % G::WO, pb = 64 * (wave / G::WO), iw = wave % G::WI;
   const long P = a.P, nb = (P + kCkBlock - 1) / kCkBlock;
   const uint16_t *A = reinterpret_cast<const uint16_t *>(a.A);
-  ck_u32x4 wf[G::OTW][G::KI], wt[G::ITW][G::KO];
-  float bias[G::OTW], gb[G::OTW];
+  ck_u32x4 wf[G::KI], wt[G::ITW][G::KO];
+  float bias, gb;
   constexpr int NS = mh_sums<DT>();
-  v4f ga[NS][G::OTW][IT];
-#pragma unroll
-  for (int m = 0; m < G::OTW; ++m) {
-    const int o = 16 * (ow + G::WO * m) + n;
-    gb[m] = 0.f;
-    bias[m] = a.bias && o < a.O ? mt_load1<DT>(a.bias, o) : 0.f;
+  v4f ga[NS][IT];
+  {
+    const int o = 16 * (ow) + n;
+    gb = 0.f;
+    bias = a.bias && o < a.O ? mt_load1<DT>(a.bias, o) : 0.f;
 #pragma unroll
     for (int k = 0; k < G::KI; ++k)
-      wf[m][k] = mh_weights(A, o, a.O, a.I, k, lane, [&](int c, int s) { return c * a.I + s; });
+      wf[k] = mh_weights(A, o, a.O, a.I, k, lane, [&](int c, int s) { return c * a.I + s; });
 #pragma unroll
-    for (int it = 0; it < IT; ++it) ga[0][m][it] = ga[NS - 1][m][it] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int it = 0; it < IT; ++it) ga[0][it] = ga[NS - 1][it] = v4f{0.f, 0.f, 0.f, 0.f};
   }
 #pragma unroll
   for (int m = 0; m < G::ITW; ++m)
 #pragma unroll
     for (int k = 0; k < G::KO; ++k)
       wt[m][k] = mh_weights(A, 16 * (iw + G::WI * m) + n, a.I, a.O, k, lane, [&](int c, int s) { return s * a.I + c; });
-  mh_clear<IT, G::KI, G::PITCH>(xs);
-  mh_clear<OT, G::KO, G::PITCH>(gh);
-  mh_clear<OT, G::KO, G::PITCH>(gl);
+  mh_clear<IT, G::KI, G::PITCH, G::THREADS>(xs);
+  mh_clear<OT, G::KO, G::PITCH, G::THREADS>(gh);
+  mh_clear<OT, G::KO, G::PITCH, G::THREADS>(gl);
   const int t0 = blockIdx.x * a.per, t1 = min(a.tiles, t0 + a.per);
-  Code16 xc[G::NU];
+  // the next tile's codes of x and add and its gy, in flight over a whole tile's work
+  Code16 xc[G::NU], nac;
+  Px16<DT> ngy;
   auto fetch = [&](int t) {
     const int b = t / a.tpb;
     const long p0 = (long)(t - b * a.tpb) * G::PT;
 #pragma unroll
     for (int k = 0; k < G::NU; ++k) {
-      const int u = tid + k * kMtThreads, i = u / (G::PT / 16), pu = 16 * (u % (G::PT / 16));
-      xc[k].load(a.xq, a.xe, (size_t)b * a.I + i, p0 + pu, nb, (G::UNITS % kMtThreads == 0 || u < G::UNITS) && i < a.I);
+      const int u = tid + k * G::THREADS, i = u / (G::PT / 16), pu = 16 * (u % (G::PT / 16));
+      xc[k].load(a.xq, a.xe, (size_t)b * a.I + i, p0 + pu, nb, (G::UNITS % G::THREADS == 0 || u < G::UNITS) && i < a.I);
+    }
+    const long p = p0 + pb + 16 * g;
+    {
+      const int o = 16 * (ow) + n;
+      const size_t row = (size_t)b * a.O + min(o, a.O - 1);
+      if (p0 + G::PT <= P) {
+        ngy.load(a.gy, row * P + p, 16);
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          if (o >= a.O) ngy.r[q] = ck_u32x4{0u, 0u, 0u, 0u};
+      } else {
+        ngy.load(a.gy, row * P + p, o < a.O ? P - p : 0);
+      }
+      nac.load(a.aq, a.ae, row, p, nb, a.aq && o < a.O);
     }
   };
   if (t0 < t1) fetch(t0);
@@ -310,27 +331,16 @@ __global__ __launch_bounds__(kMtThreads) void fno_mix_bwd_half(MixTrainArgs a) {
     const long p0 = (long)(t - b * a.tpb) * G::PT;
     const bool whole = p0 + G::PT <= P;
     const long p = p0 + pb + 16 * g;
-    // gy and add's codes, in flight while x is staged
-    Px16<DT> gy[G::OTW];
-    Code16 ac[G::OTW];
-#pragma unroll
-    for (int m = 0; m < G::OTW; ++m) {
-      const int o = 16 * (ow + G::WO * m) + n;
-      const size_t row = (size_t)b * a.O + min(o, a.O - 1);
-      if (whole) {
-        gy[m].load(a.gy, row * P + p, 16);
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-          if (o >= a.O) gy[m].r[q] = ck_u32x4{0u, 0u, 0u, 0u};
-      } else {
-        gy[m].load(a.gy, row * P + p, o < a.O ? P - p : 0);
-      }
-      ac[m].load(a.aq, a.ae, row, p, nb, a.aq && o < a.O);
+    Px16<DT> gy;
+    Code16 ac;
+    {
+      gy = ngy;
+      ac = nac;
     }
 #pragma unroll
     for (int k = 0; k < G::NU; ++k) {
-      const int u = tid + k * kMtThreads, i = u / (G::PT / 16), pu = 16 * (u % (G::PT / 16));
-      if (G::UNITS % kMtThreads != 0 && u >= G::UNITS) break;
+      const int u = tid + k * G::THREADS, i = u / (G::PT / 16), pu = 16 * (u % (G::PT / 16));
+      if (G::UNITS % G::THREADS != 0 && u >= G::UNITS) break;
       const float s = ck_step(xc[k].e);
       uint2 *d = reinterpret_cast<uint2 *>(xs + i * G::PITCH + pu);
 #pragma unroll
@@ -338,38 +348,34 @@ __global__ __launch_bounds__(kMtThreads) void fno_mix_bwd_half(MixTrainArgs a) {
     }
     __syncthreads();
     if (t + 1 < t1) fetch(t + 1);
-    v4f z[G::OTW][4];
+    v4f z[4];
     if (a.act) {
 #pragma unroll
-      for (int m = 0; m < G::OTW; ++m)
-#pragma unroll
-        for (int pt = 0; pt < 4; ++pt) z[m][pt] = v4f{bias[m], bias[m], bias[m], bias[m]};
+        for (int pt = 0; pt < 4; ++pt) z[pt] = v4f{bias, bias, bias, bias};
 #pragma unroll
       for (int k = 0; k < G::KI; ++k)
 #pragma unroll
         for (int pt = 0; pt < 4; ++pt) {
           const ck_u32x4 xa = mh_pixels<G::PITCH>(xs, k, pb, pt, lane);
-#pragma unroll
-          for (int m = 0; m < G::OTW; ++m) z[m][pt] = mh_mma<DT>(xa, wf[m][k], z[m][pt]);
+          z[pt] = mh_mma<DT>(xa, wf[k], z[pt]);
         }
     }
-#pragma unroll
-    for (int m = 0; m < G::OTW; ++m) {
-      const int o = 16 * (ow + G::WO * m) + n;
+    {
+      const int o = 16 * (ow) + n;
       float gz[16];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) gz[e] = gy[m].get(e);
+      for (int e = 0; e < 16; ++e) gz[e] = gy.get(e);
       if (a.act) {
-        const float s = ck_step(ac[m].e);
+        const float s = ck_step(ac.e);
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          gz[e] *= mt_slope<DT>(fmaf((float)(int8_t)(ac[m].q[e >> 2] >> (8 * (e & 3))), s, z[m][e >> 2][e & 3]));
+          gz[e] *= mt_slope<DT>(fmaf((float)(int8_t)(ac.q[e >> 2] >> (8 * (e & 3))), s, z[e >> 2][e & 3]));
       }
       if (a.gadd && o < a.O) store16<DT>(a.gadd, ((size_t)b * a.O + o) * P + p, whole ? 16 : P - p, gz);
       uint32_t hi[8], lo[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) mh_split<DT>(gz[2 * e], gz[2 * e + 1], hi[e], lo[e]);
-      const int at = (16 * (ow + G::WO * m) + n) * G::PITCH + pb + 16 * g;
+      const int at = (16 * (ow) + n) * G::PITCH + pb + 16 * g;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         reinterpret_cast<uint2 *>(gh + at)[q] = make_uint2(hi[2 * q], hi[2 * q + 1]);
@@ -377,7 +383,7 @@ __global__ __launch_bounds__(kMtThreads) void fno_mix_bwd_half(MixTrainArgs a) {
       }
       if (a.part) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) gb[m] += gz[e];
+        for (int e = 0; e < 16; ++e) gb += gz[e];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const ck_u32x4 h{hi[4 * k], hi[4 * k + 1], hi[4 * k + 2], hi[4 * k + 3]};
@@ -385,8 +391,8 @@ __global__ __launch_bounds__(kMtThreads) void fno_mix_bwd_half(MixTrainArgs a) {
 #pragma unroll
           for (int it = 0; it < IT; ++it) {
             const ck_u32x4 xv = mh_read16(xs + (16 * it + n) * G::PITCH + pb + 16 * g + 8 * k);
-            ga[0][m][it] = mh_mma<DT>(h, xv, ga[0][m][it]);
-            ga[NS - 1][m][it] = mh_mma<DT>(l, xv, ga[NS - 1][m][it]);
+            ga[0][it] = mh_mma<DT>(h, xv, ga[0][it]);
+            ga[NS - 1][it] = mh_mma<DT>(l, xv, ga[NS - 1][it]);
           }
         }
       }
@@ -396,7 +402,7 @@ __global__ __launch_bounds__(kMtThreads) void fno_mix_bwd_half(MixTrainArgs a) {
 #pragma unroll
       for (int m = 0; m < G::ITW; ++m) {
         const int i = 16 * (iw + G::WI * m) + n;
-        for (int sb = 64 * (wave / G::WI); sb < G::PT; sb += 64 * (4 / G::WI)) {
+        for (int sb = 64 * (wave / G::WI); sb < G::PT; sb += 64 * (G::WAVES / G::WI)) {
           v4f acc[NS][4];
 #pragma unroll
           for (int q = 0; q < NS; ++q)
@@ -422,19 +428,26 @@ __global__ __launch_bounds__(kMtThreads) void fno_mix_bwd_half(MixTrainArgs a) {
   }
   if (!a.part) return;
 #pragma unroll
-  for (int m = 0; m < G::OTW; ++m)
-#pragma unroll
     for (int it = 0; it < IT; ++it)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) ga[0][m][it][j] = mh_join<DT>(ga[0][m][it][j], ga[NS - 1][m][it][j]);
-  mt_finish<OT, IT, G::WO, G::WP>(a, ga[0], gb, reinterpret_cast<float *>(lds4), wave, lane);
+      for (int j = 0; j < 4; ++j) ga[0][it][j] = mh_join<DT>(ga[0][it][j], ga[NS - 1][it][j]);
+  mt_finish<OT, IT, G::WP, G::THREADS>(a, ga[0], gb, reinterpret_cast<float *>(lds4), wave, lane);
 }
 
 template <int DT, int OT, int IT>
 MtPick mh_pick3() {
-  using G = MhGeom<OT, IT>;
-  return {(const void *)fno_mix_save_half<DT, OT, IT>, (const void *)fno_mix_bwd_half<DT, OT, IT>, G::PT,
-          (size_t)G::LDS_FWD, (size_t)G::LDS_BWD};
+  using F = MhGeom<OT, IT, true>;
+  using G = MhGeom<OT, IT, false>;
+  constexpr int by_lds = 160 * 1024 / G::LDS_BWD, by_regs = 4 * G::PER_EU / G::WAVES;
+  return {(const void *)fno_mix_save_half<DT, OT, IT>,
+          (const void *)fno_mix_bwd_half<DT, OT, IT>,
+          F::PT,
+          G::PT,
+          (size_t)F::LDS_FWD,
+          (size_t)G::LDS_BWD,
+          F::THREADS,
+          G::THREADS,
+          256 * (by_lds < by_regs ? by_lds : by_regs)};
 }
 template <int DT, int OT>
 MtPick mh_pick2(int I) {
