@@ -6,6 +6,7 @@ check and marshal arguments, every value is computed in the library's kernels.
 """
 
 import ctypes
+import functools
 
 from ._lib import DTYPES, NORM_KINDS, NormGradsStruct, NormParamsStruct, check, lib
 
@@ -105,7 +106,9 @@ def _call(fn, dev, stream, *args):
         check(st, fn)
 
 
+@functools.lru_cache(maxsize=1024)
 def _bytes(fn, *args):
+    """A size that the library computes from a shape (a call asks for the same ones every time)."""
     n = ctypes.c_size_t()
     check(getattr(lib(), fn)(*args, ctypes.byref(n)), fn)
     return n.value

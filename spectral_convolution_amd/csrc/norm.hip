@@ -119,17 +119,18 @@ __global__ __launch_bounds__(1024) void fno_norm_tok_params(NormArgs a, int S) {
 // ------------------------------------------------------------------ launch
 
 // the kernel of a call, its threads and the tiles (rows) a workgroup has at a time
-const void *norm_kernel_f32(bool tok, int kind, bool fwd, int C, int &threads, int &rpg);
-const void *norm_kernel_f16(bool tok, int kind, bool fwd, int C, int &threads, int &rpg);
-const void *norm_kernel_bf16(bool tok, int kind, bool fwd, int C, int &threads, int &rpg);
+const void *norm_kernel_f32(bool tok, int kind, bool fwd, int C, long tiles, int &threads, int &rpg);
+const void *norm_kernel_f16(bool tok, int kind, bool fwd, int C, long tiles, int &threads, int &rpg);
+const void *norm_kernel_bf16(bool tok, int kind, bool fwd, int C, long tiles, int &threads, int &rpg);
 
 namespace {
 
 const void *pick(const NormArgs &a, bool fwd, int dtype, int &threads, int &rpg) {
   const bool tok = a.P == 1;
-  if (dtype == DT_F32) return norm_kernel_f32(tok, a.kind, fwd, a.C, threads, rpg);
-  if (dtype == DT_F16) return norm_kernel_f16(tok, a.kind, fwd, a.C, threads, rpg);
-  return norm_kernel_bf16(tok, a.kind, fwd, a.C, threads, rpg);
+  const long px = dtype == DT_F32 ? 32 : 64, tiles = a.B * ((a.P + px - 1) / px);
+  if (dtype == DT_F32) return norm_kernel_f32(tok, a.kind, fwd, a.C, tiles, threads, rpg);
+  if (dtype == DT_F16) return norm_kernel_f16(tok, a.kind, fwd, a.C, tiles, threads, rpg);
+  return norm_kernel_bf16(tok, a.kind, fwd, a.C, tiles, threads, rpg);
 }
 
 // Runs per sample (fields) or in all (tokens): at most `most` of them. A

@@ -491,13 +491,13 @@ __global__ __launch_bounds__(norm_threads<WPT>()) __attribute__((amdgpu_waves_pe
   }
 }
 
-// The variant for C channels: groups of 8 spread over 1, 2, 4 or 8 waves, at most
-// 8 groups a wave. Exactly ceil(groups / waves) of them, so that no group but a wave's last is
-// ever empty.
+// The variant for C channels: groups of 8 spread over `waves` waves, at most 8
+// groups a wave and exactly ceil(groups / waves) of them, so that no group but
+// a wave's last is ever empty.
 template <int DT, int KIND, int WPT>
 const void *field_pick(bool fwd, int cpt) {
 #define FNO_PICK(CPT) (fwd ? (const void *)fno_norm_fwd<DT, CPT, WPT, KIND> : (const void *)fno_norm_bwd<DT, CPT, WPT, KIND>)
-  if constexpr (WPT == 1) {
+  if constexpr (WPT == 1 || WPT == 4) {
     if (cpt == 1) return FNO_PICK(1);
     if (cpt == 2) return FNO_PICK(2);
     if (cpt == 3) return FNO_PICK(3);
@@ -510,11 +510,17 @@ const void *field_pick(bool fwd, int cpt) {
 #undef FNO_PICK
 }
 
-inline int field_waves(int C) { return C <= 64 ? 1 : C <= 128 ? 2 : C <= 256 ? 4 : 8; }
+// Waves that share a tile: one up to 64 channels, and no more than the registers
+// ask for where there are tiles enough to fill the chip. With fewer than 512
+// tiles a call is as long as one wave's work, so four share it.
+inline int field_waves(int C, long tiles) {
+  if (C > 8 && C <= 128 && tiles < 512) return 4;
+  return C <= 64 ? 1 : C <= 128 ? 2 : C <= 256 ? 4 : 8;
+}
 
 template <int DT, int KIND>
-const void *field_kernel(bool fwd, int C) {
-  const int w = field_waves(C), cpt = ((C + 7) / 8 + w - 1) / w;
+const void *field_kernel(bool fwd, int C, int w) {
+  const int cpt = ((C + 7) / 8 + w - 1) / w;
   if (w == 1) return field_pick<DT, KIND, 1>(fwd, cpt);
   if (w == 2) return field_pick<DT, KIND, 2>(fwd, cpt);
   if (w == 4) return field_pick<DT, KIND, 4>(fwd, cpt);
