@@ -90,7 +90,7 @@ __device__ __forceinline__ void unfold(const float (&o)[V / 4], float (&s)[V]) {
 
 // The scheduler may not mix the channels of a phase: converting all of them
 // ahead of their use doubles the registers held.
-__device__ __forceinline__ void channel_done() { __builtin_amdgcn_sched_barrier(0); }
+__device__ __forceinline__ void channel_done() { __builtin_amdgcn_sched_barrier(0x4 | 0x10 | 0x80); }
 
 // s[e] = sum over a lane's channels k of h(k, e), or of its square
 template <int V, int CPT, bool SQUARE, typename F>

@@ -91,7 +91,7 @@ struct FieldTile {
   // a tile that lies within the row
   __device__ __forceinline__ ck_u32x4 load(const void *f, int t, int k) const {
     const char *s = static_cast<const char *>(f) + field_at(k);
-    return only(k, *reinterpret_cast<const ck_u32x4_any *>(s + (k < CPT - 1 ? off : off_last)));
+    return only(k, __builtin_nontemporal_load(reinterpret_cast<const ck_u32x4_any *>(s + (k < CPT - 1 ? off : off_last))));
   }
   // The row's last tile, zeros past its end: a lane that would pass it reads the
   // row's last 16 bytes instead (`back` elements before its own) and shifts
@@ -120,7 +120,7 @@ struct FieldTile {
     if (!has(k)) return;
     if (whole) {
       char *d = static_cast<char *>(f) + field_at(k);
-      *reinterpret_cast<ck_u32x4_any *>(d + (k < CPT - 1 ? off : off_last)) = r;
+      __builtin_nontemporal_store((ck_u32x4_any)r, reinterpret_cast<ck_u32x4_any *>(d + (k < CPT - 1 ? off : off_last)));
     } else {
       ck_store_row<DT>(static_cast<char *>(f) + field_at(k) + (k < CPT - 1 ? off : off_last), 0, P - ((long)t * PX + pl * V), r);
     }
@@ -491,12 +491,12 @@ __global__ __launch_bounds__(norm_threads<WPT>()) __attribute__((amdgpu_waves_pe
   }
 }
 
-// The variant for C channels: groups of 8 spread over `waves` waves, at most 8
-// groups a wave and exactly ceil(groups / waves) of them, so that no group but
-// a wave's last is ever empty.
+// The variant for C channels: groups of 8 spread over `waves` waves, exactly
+// ceil(groups / waves) of them each, so that no group but a wave's last is ever
+// empty.
 template <int DT, int KIND, int WPT>
-const void *field_pick(bool fwd, int cpt) {
-#define FNO_PICK(CPT) (fwd ? (const void *)fno_norm_fwd<DT, CPT, WPT, KIND> : (const void *)fno_norm_bwd<DT, CPT, WPT, KIND>)
+const void *field_fwd(int cpt) {
+#define FNO_PICK(CPT) (const void *)fno_norm_fwd<DT, CPT, WPT, KIND>
   if constexpr (WPT == 1 || WPT == 4) {
     if (cpt == 1) return FNO_PICK(1);
     if (cpt == 2) return FNO_PICK(2);
@@ -509,22 +509,40 @@ const void *field_pick(bool fwd, int cpt) {
   return FNO_PICK(8);
 #undef FNO_PICK
 }
+template <int DT, int KIND, int WPT>
+const void *field_bwd(int cpt) {
+#define FNO_PICK(CPT) (const void *)fno_norm_bwd<DT, CPT, WPT, KIND>
+  if constexpr (WPT != 2) {
+    if (cpt == 1) return FNO_PICK(1);
+    if (cpt == 2) return FNO_PICK(2);
+  }
+  if (cpt <= 3) return FNO_PICK(3);
+  if constexpr (WPT == 8) {
+    if (cpt == 5) return FNO_PICK(5);
+    if (cpt == 6) return FNO_PICK(6);
+    if (cpt == 7) return FNO_PICK(7);
+    if (cpt == 8) return FNO_PICK(8);
+  }
+  return FNO_PICK(4);
+#undef FNO_PICK
+}
 
-// Waves that share a tile: one up to 64 channels, and no more than the registers
-// ask for where there are tiles enough to fill the chip. With fewer than 512
-// tiles a call is as long as one wave's work, so four share it.
-inline int field_waves(int C, long tiles) {
+// Waves that share a tile: forward one up to 64 channels, backward (four
+// fields) up to 32. With fewer than 512 tiles a call is as long as one
+// wave's work, so four share it.
+inline int field_waves(bool fwd, int C, long tiles) {
   if (C > 8 && C <= 128 && tiles < 512) return 4;
-  return C <= 64 ? 1 : C <= 128 ? 2 : C <= 256 ? 4 : 8;
+  const int one = fwd ? 64 : 32;
+  return C <= one ? 1 : C <= 2 * one ? 2 : C <= 4 * one ? 4 : 8;
 }
 
 template <int DT, int KIND>
 const void *field_kernel(bool fwd, int C, int w) {
   const int cpt = ((C + 7) / 8 + w - 1) / w;
-  if (w == 1) return field_pick<DT, KIND, 1>(fwd, cpt);
-  if (w == 2) return field_pick<DT, KIND, 2>(fwd, cpt);
-  if (w == 4) return field_pick<DT, KIND, 4>(fwd, cpt);
-  return field_pick<DT, KIND, 8>(fwd, cpt);
+  if (w == 1) return fwd ? field_fwd<DT, KIND, 1>(cpt) : field_bwd<DT, KIND, 1>(cpt);
+  if (w == 2) return fwd ? field_fwd<DT, KIND, 2>(cpt) : field_bwd<DT, KIND, 2>(cpt);
+  if (w == 4) return fwd ? field_fwd<DT, KIND, 4>(cpt) : field_bwd<DT, KIND, 4>(cpt);
+  return fwd ? field_fwd<DT, KIND, 8>(cpt) : field_bwd<DT, KIND, 8>(cpt);
 }
 
 }  // namespace fno
