@@ -10,11 +10,12 @@ import ctypes
 
 from ._lib import DTYPES, FnoError, check, lib  # noqa: F401
 from ._training import (  # noqa: F401
-    NormGrads, NormParams, fno_channel_mix_backward_saved, fno_channel_mix_save, fno_channel_mix_saved_bytes,
-    fno_channel_mix_saved_empty, fno_channel_mix_workspace_bytes, fno_channel_mix_workspace_empty, fno_checkpoint_bytes, fno_checkpoint_empty, fno_checkpoint_pack, fno_checkpoint_unpack,
-    fno_norm_residual, fno_norm_residual_backward, fno_norm_residual_backward_saved, fno_norm_residual_save,
-    fno_norm_residual_saved_bytes, fno_norm_residual_saved_empty, fno_norm_residual_workspace_bytes,
-    fno_norm_residual_workspace_empty)
+    NormGrads, NormParams, channel_mix, fno_channel_mix_backward_saved, fno_channel_mix_save,
+    fno_channel_mix_saved_bytes, fno_channel_mix_saved_empty, fno_channel_mix_workspace_bytes,
+    fno_channel_mix_workspace_empty, fno_checkpoint_bytes, fno_checkpoint_empty, fno_checkpoint_pack,
+    fno_checkpoint_unpack, fno_norm_residual, fno_norm_residual_backward, fno_norm_residual_backward_saved,
+    fno_norm_residual_save, fno_norm_residual_saved_bytes, fno_norm_residual_saved_empty,
+    fno_norm_residual_workspace_bytes, fno_norm_residual_workspace_empty, norm_residual)
 
 __all__ = [
     "fno_plan_create", "fno_spectral_conv2d", "fno_spectral_conv3d",
@@ -31,7 +32,7 @@ __all__ = [
     "fno_channel_mix_saved_empty", "fno_channel_mix_workspace_bytes", "fno_channel_mix_workspace_empty",
     "NormParams", "NormGrads", "fno_norm_residual", "fno_norm_residual_save", "fno_norm_residual_backward",
     "fno_norm_residual_backward_saved", "fno_norm_residual_saved_bytes", "fno_norm_residual_saved_empty",
-    "fno_norm_residual_workspace_bytes", "fno_norm_residual_workspace_empty",
+    "fno_norm_residual_workspace_bytes", "fno_norm_residual_workspace_empty", "channel_mix", "norm_residual",
 ]
 
 

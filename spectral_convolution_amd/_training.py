@@ -326,3 +326,25 @@ def fno_norm_residual_backward_saved(params, saved, gy, gu, gx, gv, grads, works
     """fno_norm_residual_backward at the x and v read back from `saved`."""
     _norm_backward("fno_norm_residual_backward_saved", params, None, None, saved, gy, gu, gx, gv, grads, workspace,
                    stream)
+
+
+# ------------------------------------------------- differentiable functions
+
+def channel_mix(x, A, bias=None, add=None, act=0):
+    """y = act(A x + bias + add), differentiable in all four; x (and, with
+    GELU, add) is kept for the backward in 8 bits."""
+    from ._training_autograd import ChannelMixFunction
+    if not isinstance(A, _t().Tensor) or A.dim() != 2:
+        raise ValueError("A must be a [c_out][c_in] tensor")
+    return ChannelMixFunction.apply(x, A, bias, add, act)
+
+
+def norm_residual(x, v, params, with_u=True, keep="8bit"):
+    """(y, u) of fno_norm_residual (u None unless with_u), differentiable in x, v
+    and the parameters (NormParams); x and v are kept for the backward in 8 bits
+    (keep "8bit") or as they are ("whole")."""
+    from ._training_autograd import NormResidualFunction
+    if keep not in ("8bit", "whole"):
+        raise ValueError('keep must be "8bit" or "whole"')
+    return NormResidualFunction.apply(x, v, params.kind, params.eps, keep, with_u,
+                                      *(getattr(params, k) for k in _NORM_NAMES))

@@ -264,7 +264,8 @@ __global__ __launch_bounds__(norm_threads<WPT>()) __attribute__((amdgpu_waves_pe
   constexpr int V = ck_vec<DT>(), PX = 8 * V, WAVES = norm_threads<WPT>() / 64, TPG = WAVES / WPT, NC = 8 * CPT * WPT;
   constexpr int NQ = KIND == kLayer ? 2 : 1;
   __shared__ float4 tab[NC];
-  __shared__ float4 accs[CPT * 64 * WAVES];
+  constexpr bool HELD = CPT <= 2;  // the run's sums: in registers, or in LDS where those are needed
+  __shared__ float4 accs[CPT * WAVES * (HELD ? 8 : 64)];
   __shared__ float red[WPT > 1 ? 2 * WAVES * 2 * PX : 1];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), b = blockIdx.y;
   norm_table<DT>(a, b, NC, tab);
@@ -273,12 +274,15 @@ __global__ __launch_bounds__(norm_threads<WPT>()) __attribute__((amdgpu_waves_pe
   FieldTile<DT, CPT, WPT> tile(a, b, lane, wave % WPT);
   const float invC = 1.f / (float)a.C;
   int turn = 0;
-  float *acc = reinterpret_cast<float *>(accs) + threadIdx.x;  // this thread's sums: acc[(4 k + q) threads]
-#pragma unroll
-  for (int i = 0; i < 4 * CPT; ++i) acc[i * (64 * WAVES)] = 0.f;
-  auto add = [&](int k, int q, float v) {
-    __hip_atomic_fetch_add(acc + (4 * k + q) * (64 * WAVES), v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT);
+  // this thread's sums {T, G, U, V} of its k-th channel. Private, so read, added to
+  // and written back: LDS atomics took a third of the kernel's time.
+  float4 held[HELD ? CPT : 1];
+  auto sums = [&](int k) -> float4 & {
+    if constexpr (HELD) return held[k];
+    else return accs[k * (64 * WAVES) + threadIdx.x];
   };
+#pragma unroll
+  for (int k = 0; k < CPT; ++k) sums(k) = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int t = t0 + wave / WPT; t < t1; t += TPG) {
     const bool whole = (t + 1L) * PX <= a.P;
     tile.at(t);
@@ -419,6 +423,7 @@ __global__ __launch_bounds__(norm_threads<WPT>()) __attribute__((amdgpu_waves_pe
 #pragma unroll
     for (int k = 0; k < CPT; ++k) {
       const float4 w = tab[tile.channel(k)];
+      float4 sum = sums(k);
       float sT = 0.f, sG = 0.f;
       if (a.gu) {
         float sU = 0.f, sV = 0.f;
@@ -431,8 +436,8 @@ __global__ __launch_bounds__(norm_threads<WPT>()) __attribute__((amdgpu_waves_pe
           if (KIND == kLayer) g -= q[1][e];
           gx[k][e] = fmaf(ry[e], g, ck_get<DT>(gyr[k], e));
         }
-        add(k, 2, sU);
-        add(k, 3, sV);
+        sum.z += sU;
+        sum.w += sV;
       } else {
 #pragma unroll
         for (int e = 0; e < V; ++e) gx[k][e] = ck_get<DT>(gyr[k], e);
@@ -445,8 +450,9 @@ __global__ __launch_bounds__(norm_threads<WPT>()) __attribute__((amdgpu_waves_pe
         s2[0][e] = fmaf(g * w.x, vh, s2[0][e]);
         if (KIND == kLayer) s2[NQ - 1][e] = fmaf(g, w.x, s2[NQ - 1][e]);
       }
-      add(k, 0, sT);
-      add(k, 1, sG);
+      sum.x += sT;
+      sum.y += sG;
+      sums(k) = sum;
       if (a.gx) tile.store(a.gx, t, k, whole, ck_raw<DT>(gx[k]));
       channel_done();
     }
@@ -471,15 +477,16 @@ __global__ __launch_bounds__(norm_threads<WPT>()) __attribute__((amdgpu_waves_pe
   }
   if (!a.part) return;
   // the run's sums: over a channel's 8 lanes, then over the workgroup's tiles
-  float tot[CPT][4];
+  float4 tot[CPT];
 #pragma unroll
-  for (int k = 0; k < CPT; ++k)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) tot[k][q] = sum8(acc[(4 * k + q) * (64 * WAVES)]);
+  for (int k = 0; k < CPT; ++k) {
+    const float4 sum = sums(k);
+    tot[k] = make_float4(sum8(sum.x), sum8(sum.y), sum8(sum.z), sum8(sum.w));
+  }
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < CPT; ++k)
-    if ((lane & 7) == 0) accs[(wave / WPT) * NC + tile.channel(k)] = make_float4(tot[k][0], tot[k][1], tot[k][2], tot[k][3]);
+    if ((lane & 7) == 0) accs[(wave / WPT) * NC + tile.channel(k)] = tot[k];
   __syncthreads();
   for (int i = threadIdx.x; i < 4 * NC; i += blockDim.x) {
     const int c = i >> 2, q = i & 3;
