@@ -501,9 +501,9 @@ __global__ __launch_bounds__(norm_threads<WPT>()) __attribute__((amdgpu_waves_pe
 // The variant for C channels: groups of 8 spread over `waves` waves, exactly
 // ceil(groups / waves) of them each, so that no group but a wave's last is ever
 // empty.
-template <int DT, int KIND, int WPT>
-const void *field_fwd(int cpt) {
-#define FNO_PICK(CPT) (const void *)fno_norm_fwd<DT, CPT, WPT, KIND>
+template <int DT, int KIND, int WPT, bool FWD>
+const void *field_pick(int cpt) {
+#define FNO_PICK(CPT) (FWD ? (const void *)fno_norm_fwd<DT, CPT, WPT, KIND> : (const void *)fno_norm_bwd<DT, CPT, WPT, KIND>)
   if constexpr (WPT == 1 || WPT == 4) {
     if (cpt == 1) return FNO_PICK(1);
     if (cpt == 2) return FNO_PICK(2);
@@ -516,40 +516,24 @@ const void *field_fwd(int cpt) {
   return FNO_PICK(8);
 #undef FNO_PICK
 }
-template <int DT, int KIND, int WPT>
-const void *field_bwd(int cpt) {
-#define FNO_PICK(CPT) (const void *)fno_norm_bwd<DT, CPT, WPT, KIND>
-  if constexpr (WPT != 2) {
-    if (cpt == 1) return FNO_PICK(1);
-    if (cpt == 2) return FNO_PICK(2);
-  }
-  if (cpt <= 3) return FNO_PICK(3);
-  if constexpr (WPT == 8) {
-    if (cpt == 5) return FNO_PICK(5);
-    if (cpt == 6) return FNO_PICK(6);
-    if (cpt == 7) return FNO_PICK(7);
-    if (cpt == 8) return FNO_PICK(8);
-  }
-  return FNO_PICK(4);
-#undef FNO_PICK
-}
 
-// Waves that share a tile: forward one up to 64 channels, backward (four
-// fields) up to 32. With fewer than 512 tiles a call is as long as one
-// wave's work, so four share it.
-inline int field_waves(bool fwd, int C, long tiles) {
+// Waves that share a tile: as few as hold its channels, 64 each. In the
+// backward that leaves two waves a SIMD instead of three from 40 channels on,
+// yet two waves that share a tile wait for each other four times a tile (64
+// channels, fp16: 193 us with one wave, 226 with two). With fewer than 512
+// tiles a call is as long as one wave's work, so four share it.
+inline int field_waves(int C, long tiles) {
   if (C > 8 && C <= 128 && tiles < 512) return 4;
-  const int one = fwd ? 64 : 32;
-  return C <= one ? 1 : C <= 2 * one ? 2 : C <= 4 * one ? 4 : 8;
+  return C <= 64 ? 1 : C <= 128 ? 2 : C <= 256 ? 4 : 8;
 }
 
-template <int DT, int KIND>
-const void *field_kernel(bool fwd, int C, int w) {
+template <int DT, int KIND, bool FWD>
+const void *field_kernel(int C, int w) {
   const int cpt = ((C + 7) / 8 + w - 1) / w;
-  if (w == 1) return fwd ? field_fwd<DT, KIND, 1>(cpt) : field_bwd<DT, KIND, 1>(cpt);
-  if (w == 2) return fwd ? field_fwd<DT, KIND, 2>(cpt) : field_bwd<DT, KIND, 2>(cpt);
-  if (w == 4) return fwd ? field_fwd<DT, KIND, 4>(cpt) : field_bwd<DT, KIND, 4>(cpt);
-  return fwd ? field_fwd<DT, KIND, 8>(cpt) : field_bwd<DT, KIND, 8>(cpt);
+  return w == 1   ? field_pick<DT, KIND, 1, FWD>(cpt)
+         : w == 2 ? field_pick<DT, KIND, 2, FWD>(cpt)
+         : w == 4 ? field_pick<DT, KIND, 4, FWD>(cpt)
+                  : field_pick<DT, KIND, 8, FWD>(cpt);
 }
 
 }  // namespace fno
