@@ -13,6 +13,8 @@ def _dense(t):
     """t as the kernels take a field: contiguous, on a 16-byte boundary."""
     if t is None:
         return None
+    if not t.is_cuda:
+        raise ValueError(f"fields must be on the GPU, got one on {t.device}")
     t = t.contiguous()
     return t.clone() if t.data_ptr() % 16 else t
 

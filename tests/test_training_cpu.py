@@ -291,3 +291,35 @@ def test_mix_binding_mismatches():
         fno.fno_channel_mix_backward_saved(big[:8], A, None, y, x, None, None, None, None)
     with pytest.raises(TypeError, match="workspace"):
         fno.fno_channel_mix_backward_saved(big[-big.data_ptr() % 256:], A, None, y, x, A, None, None, None)
+
+
+# ------------------------------------------------- differentiable functions
+
+def test_differentiable_functions_refuse():
+    x, A = torch.zeros(2, 3, 5), torch.zeros(4, 3)
+    with pytest.raises(ValueError, match="on the GPU"):
+        fno.channel_mix(x, A)
+    with pytest.raises(ValueError, match="c_out"):
+        fno.channel_mix(x, torch.zeros(4))
+    prm = fno.NormParams("rms", 1e-5)
+    with pytest.raises(ValueError, match="keep"):
+        fno.norm_residual(x, x, prm, keep="4bit")
+    with pytest.raises(ValueError, match="on the GPU"):
+        fno.norm_residual(x, x, prm)
+
+
+def test_example_data_is_the_heat_equations():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "train_conditioned_fno2d.py")
+    spec = importlib.util.spec_from_file_location("train_conditioned_fno2d", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    a, tau, s = m.heat_batch(np.random.default_rng(1), 3, (16, 24))
+    assert a.shape == s.shape == (3, 1, 16, 24) and (0 <= tau).all() and (tau < 1).all()
+    assert np.allclose(a.mean((2, 3)), s.mean((2, 3)))
+    # one mode by hand: 2 periods along the second axis
+    k2 = (2 * math.pi * 2) ** 2
+    fa, fs = np.fft.fft2(a)[..., 0, 2], np.fft.fft2(s)[..., 0, 2]
+    assert np.allclose(fs[:, 0], fa[:, 0] * np.exp(-m.TAU * tau * k2))
