@@ -119,60 +119,64 @@ __global__ __launch_bounds__(1024) void fno_norm_params(NormArgs a, int S) {
   put<DT>(a.g_scale, c, t[4]);
 }
 
-// Parameter gradients of tokens from part[S][4][C]: 32 channels a workgroup,
-// 32 slices of the runs.
+// Parameter gradients of tokens from part[S][4][C]: 32 channels and two of the
+// four sums a workgroup, 32 slices of the runs.
 template <int DT>
 __global__ __launch_bounds__(1024) void fno_norm_tok_params(NormArgs a, int S) {
-  __shared__ float red[4][32][33];
-  const int l = threadIdx.x & 31, sl = threadIdx.x >> 5, c = blockIdx.x * 32 + l;
-  float v[4] = {0.f, 0.f, 0.f, 0.f};
+  __shared__ float red[2][32][33];
+  const int l = threadIdx.x & 31, sl = threadIdx.x >> 5, c = blockIdx.x * 32 + l, half = blockIdx.y;
+  float v[2] = {0.f, 0.f};
   if (c < a.C) {
-#pragma unroll 4
+#pragma unroll 8
     for (int i = sl; i < S; i += 32)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) v[q] += a.part[((size_t)i * 4 + q) * a.C + c];
+      for (int q = 0; q < 2; ++q) v[q] += a.part[((size_t)i * 4 + 2 * half + q) * a.C + c];
   }
 #pragma unroll
-  for (int q = 0; q < 4; ++q) red[q][sl][l] = v[q];
+  for (int q = 0; q < 2; ++q) red[q][sl][l] = v[q];
   __syncthreads();
   if (threadIdx.x >= 32 || c >= a.C) return;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
+  for (int q = 0; q < 2; ++q) {
     v[q] = 0.f;
     for (int i = 0; i < 32; ++i) v[q] += red[q][i][l];
+  }
+  if (half == 1) {
+    put<DT>(a.g_w_pre, c, v[0]);
+    put<DT>(a.g_b_pre, c, v[1]);
+    return;
   }
   const float w = param(a.w_post, DT, c, 1.f), bp = param(a.b_post, DT, c, 0.f), sc = param(a.scale, DT, c, 1.f);
   put<DT>(a.g_w_post, c, sc * v[0]);
   put<DT>(a.g_b_post, c, sc * v[1]);
-  put<DT>(a.g_w_pre, c, v[2]);
-  put<DT>(a.g_b_pre, c, v[3]);
   put<DT>(a.g_scale, c, fmaf(w, v[0], bp * v[1]));
 }
 
 // ------------------------------------------------------------------ launch
 
-// the kernel of a call, its threads and the tiles (rows) a workgroup has at a time
-const void *norm_kernel_f32(bool tok, int kind, bool fwd, int C, long tiles, int &threads, int &rpg);
-const void *norm_kernel_f16(bool tok, int kind, bool fwd, int C, long tiles, int &threads, int &rpg);
-const void *norm_kernel_bf16(bool tok, int kind, bool fwd, int C, long tiles, int &threads, int &rpg);
+NormPick norm_kernel_f32(bool tok, int kind, bool fwd, int C, long tiles);
+NormPick norm_kernel_f16(bool tok, int kind, bool fwd, int C, long tiles);
+NormPick norm_kernel_bf16(bool tok, int kind, bool fwd, int C, long tiles);
 
 namespace {
 
-const void *pick(const NormArgs &a, bool fwd, int dtype, int &threads, int &rpg) {
+NormPick pick(const NormArgs &a, bool fwd, int dtype) {
   const bool tok = a.P == 1;
   const long px = dtype == DT_F32 ? 32 : 64, tiles = a.B * ((a.P + px - 1) / px);
-  if (dtype == DT_F32) return norm_kernel_f32(tok, a.kind, fwd, a.C, tiles, threads, rpg);
-  if (dtype == DT_F16) return norm_kernel_f16(tok, a.kind, fwd, a.C, tiles, threads, rpg);
-  return norm_kernel_bf16(tok, a.kind, fwd, a.C, tiles, threads, rpg);
+  if (dtype == DT_F32) return norm_kernel_f32(tok, a.kind, fwd, a.C, tiles);
+  if (dtype == DT_F16) return norm_kernel_f16(tok, a.kind, fwd, a.C, tiles);
+  return norm_kernel_bf16(tok, a.kind, fwd, a.C, tiles);
 }
 
 // Runs per sample (fields) or in all (tokens): at most `most` of them. A
 // field's run is a whole number of rounds of the workgroup's waves and short,
 // so that the last workgroups to finish are not far behind the rest (the chip
-// holds 512 of the backward's: 1040 long ones took three rounds, not two).
-constexpr long kFieldRuns = 4096, kTokenRuns = 1024;
-long norm_runs(const NormArgs &a, int dtype, int rpg, long most, int *per = nullptr) {
-  if (a.P == 1) return std::min((a.B + (long)rpg - 1) / rpg, most);
+// holds 512 of the backward's: 1040 long ones took three rounds, not two). Tokens:
+// as many as the chip holds at two waves a SIMD; each leaves 4 C sums to be added.
+constexpr long kFieldRuns = 4096, kTokenRuns = 512;
+long norm_runs(const NormArgs &a, int dtype, const NormPick &k, long most, int *per = nullptr) {
+  const int rpg = k.rpg;
+  if (a.P == 1) return std::min((a.B + (long)rpg - 1) / rpg, most * 256 / k.threads);
   const long px = dtype == DT_F32 ? 32 : 64, nt = (a.P + px - 1) / px;
   const long s = std::max(1L, most / a.B), p = ((nt + s - 1) / s + rpg - 1) / rpg * rpg;
   if (per) *per = (int)p;
@@ -184,39 +188,37 @@ long norm_runs(const NormArgs &a, int dtype, int rpg, long most, int *per = null
 size_t norm_workspace_bytes(int B, int C, long P, int dtype) {
   NormArgs a{};
   a.B = B, a.C = C, a.P = P;
-  int threads, rpg;
-  (void)pick(a, false, dtype, threads, rpg);
-  const long S = norm_runs(a, dtype, rpg, P == 1 ? kTokenRuns : kFieldRuns);
+  const long S = norm_runs(a, dtype, pick(a, false, dtype), P == 1 ? kTokenRuns : kFieldRuns);
   return (size_t)4 * C * S * (P == 1 ? 1 : B) * 4;
 }
 
 hipError_t launch_norm_fwd(const NormArgs &a, int dtype, hipStream_t s) {
   FNO_BOUNDS(check_norm(a, true, 0, dtype);)
-  int threads, rpg;
-  const void *k = pick(a, true, dtype, threads, rpg);
+  const NormPick k = pick(a, true, dtype);
   NormArgs arg = a;
-  const long S = norm_runs(a, dtype, rpg, kFieldRuns, &arg.per);
+  const long S = norm_runs(a, dtype, k, kFieldRuns, &arg.per);
   const dim3 grid((unsigned)S, a.P == 1 ? 1u : (unsigned)a.B);
   void *args[] = {(void *)&arg};
-  return hipLaunchKernel(k, grid, dim3((unsigned)threads), args, 0, s);
+  return hipLaunchKernel(k.kernel, grid, dim3((unsigned)k.threads), args, k.lds, s);
 }
 
 hipError_t launch_norm_bwd(const NormArgs &a, int dtype, hipStream_t s) {
-  int threads, rpg;
-  const void *k = pick(a, false, dtype, threads, rpg);
+  const NormPick k = pick(a, false, dtype);
   NormArgs arg = a;
-  int S = (int)norm_runs(a, dtype, rpg, a.P == 1 ? kTokenRuns : kFieldRuns, &arg.per);
+  int S = (int)norm_runs(a, dtype, k, a.P == 1 ? kTokenRuns : kFieldRuns, &arg.per);
   FNO_BOUNDS(check_norm(a, false, S, dtype);)
   const bool tok = a.P == 1;
   const dim3 grid((unsigned)S, tok ? 1u : (unsigned)a.B);
   void *args[] = {(void *)&arg};
-  hipError_t e = hipLaunchKernel(k, grid, dim3((unsigned)threads), args, 0, s);
+  if (hipError_t e = raise_lds_cap(k.kernel, k.lds); e != hipSuccess) return e;
+  hipError_t e = hipLaunchKernel(k.kernel, grid, dim3((unsigned)k.threads), args, k.lds, s);
   if (e != hipSuccess || !a.part) return e;
   void *pargs[] = {(void *)&arg, (void *)&S};
 #define FNO_PICK(DT) (tok ? (const void *)fno_norm_tok_params<DT> : (const void *)fno_norm_params<DT>)
   const void *pk = dtype == DT_F32 ? FNO_PICK(DT_F32) : dtype == DT_F16 ? FNO_PICK(DT_F16) : FNO_PICK(DT_BF16);
 #undef FNO_PICK
-  return hipLaunchKernel(pk, dim3((unsigned)(tok ? (a.C + 31) / 32 : a.C)), dim3(1024), pargs, 0, s);
+  const dim3 pgrid(tok ? (a.C + 31) / 32 : a.C, tok ? 2 : 1);
+  return hipLaunchKernel(pk, pgrid, dim3(1024), pargs, 0, s);
 }
 
 }  // namespace fno

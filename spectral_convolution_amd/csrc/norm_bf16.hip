@@ -5,14 +5,10 @@
 
 namespace fno {
 
-const void *norm_kernel_bf16(bool tok, int kind, bool fwd, int C, long tiles, int &threads, int &rpg) {
-  if (tok)
-    return kind == kLayer ? tok_kernel<DT_BF16, kLayer>(fwd, C, threads, rpg) : tok_kernel<DT_BF16, kRms>(fwd, C, threads, rpg);
+NormPick norm_kernel_bf16(bool tok, int kind, bool fwd, int C, long tiles) {
+  if (tok) return kind == kLayer ? tok_kernel<DT_BF16, kLayer>(fwd, C) : tok_kernel<DT_BF16, kRms>(fwd, C);
   const int w = field_waves(C, tiles);
-  threads = w == 1 ? 256 : 64 * w;
-  rpg = w == 1 ? 4 : 1;
-  if (fwd) return kind == kLayer ? field_kernel<DT_BF16, kLayer, true>(C, w) : field_kernel<DT_BF16, kRms, true>(C, w);
-  return kind == kLayer ? field_kernel<DT_BF16, kLayer, false>(C, w) : field_kernel<DT_BF16, kRms, false>(C, w);
+  return kind == kLayer ? field_kernel<DT_BF16, kLayer>(fwd, C, w) : field_kernel<DT_BF16, kRms>(fwd, C, w);
 }
 
 }  // namespace fno

@@ -5,6 +5,14 @@
 
 namespace fno {
 
+// a call's kernel, its threads, the tiles (rows) a workgroup has at a time and
+// the LDS it is launched with
+struct NormPick {
+  const void *kernel;
+  int threads, rpg;
+  size_t lds;
+};
+
 constexpr int kRms = 0;
 constexpr int kLayer = 1;
 

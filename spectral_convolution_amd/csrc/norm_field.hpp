@@ -528,12 +528,18 @@ inline int field_waves(int C, long tiles) {
 }
 
 template <int DT, int KIND, bool FWD>
-const void *field_kernel(int C, int w) {
+NormPick field_kernel(int C, int w) {
   const int cpt = ((C + 7) / 8 + w - 1) / w;
-  return w == 1   ? field_pick<DT, KIND, 1, FWD>(cpt)
-         : w == 2 ? field_pick<DT, KIND, 2, FWD>(cpt)
-         : w == 4 ? field_pick<DT, KIND, 4, FWD>(cpt)
-                  : field_pick<DT, KIND, 8, FWD>(cpt);
+  const void *k = w == 1   ? field_pick<DT, KIND, 1, FWD>(cpt)
+                  : w == 2 ? field_pick<DT, KIND, 2, FWD>(cpt)
+                  : w == 4 ? field_pick<DT, KIND, 4, FWD>(cpt)
+                           : field_pick<DT, KIND, 8, FWD>(cpt);
+  return {k, w == 1 ? 256 : 64 * w, w == 1 ? 4 : 1, 0};
+}
+
+template <int DT, int KIND>
+NormPick field_kernel(bool fwd, int C, int w) {
+  return fwd ? field_kernel<DT, KIND, true>(C, w) : field_kernel<DT, KIND, false>(C, w);
 }
 
 }  // namespace fno

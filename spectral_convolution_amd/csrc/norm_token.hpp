@@ -30,7 +30,7 @@ __device__ __forceinline__ void norm_encode(const ck_u32x4 &r, uint8_t *q, int8_
 }
 
 template <int NT>
-constexpr int tok_threads() { return NT > 256 ? NT : 256; }
+constexpr int tok_threads() { return NT > 64 ? NT : 256; }
 
 // sums of NQ values over a row's NT threads
 template <int NT, int NQ>
@@ -55,33 +55,48 @@ __device__ __forceinline__ void row_sum(float (&s)[NQ], float *red, int &turn) {
   }
 }
 
-// the elements' squared distance from m; elements past n do not count
-template <int V>
-__device__ __forceinline__ float dev2(const float *h, float m, long n) {
-  float s = 0.f;
-#pragma unroll
-  for (int e = 0; e < V; ++e) {
-    const float d = e < n ? h[e] - m : 0.f;
-    s = fmaf(d, d, s);
-  }
-  return s;
-}
-
-// parameter values of 16 bytes' worth of channels, `none` where there is no parameter
+// 16 bytes of a row of C channels for channel c on. A lane that would pass the
+// row's end reads its last 16 bytes; tok_fix moves them into place once all of a
+// row's loads are on their way (element by element, each load waited for, that lane
+// took longer than the rest of the row: 76 us instead of 21 at 16000 x 100, bf16).
+// Rows shorter than 16 bytes are read by the element.
 template <int DT>
-__device__ __forceinline__ void tok_param(const void *p, size_t i, long n, float none, float *v) {
+__device__ __forceinline__ ck_u32x4 tok_load(const void *p, size_t row, int c, int C) {
+  constexpr int V = ck_vec<DT>(), ES = DT == DT_F32 ? 4 : 2;
+  if (C < V) return ck_load<DT>(p, row, c == 0 ? C : 0);
+  return *reinterpret_cast<const ck_u32x4_any *>(static_cast<const char *>(p) + (row + min(c, C - V)) * ES);
+}
+
+// the same of a parameter, `none` for each channel where there is no parameter
+template <int DT>
+__device__ __forceinline__ ck_u32x4 tok_param(const void *p, size_t row, int c, int C, float none) {
   constexpr int V = ck_vec<DT>();
-  if (p) {
-    const ck_u32x4 r = ck_load<DT>(p, i, n);
+  if (p) return tok_load<DT>(p, row, c, C);
+  float v[V];
 #pragma unroll
-    for (int e = 0; e < V; ++e) v[e] = ck_get<DT>(r, e);
-  } else {
+  for (int e = 0; e < V; ++e) v[e] = C >= V || e < C ? none : 0.f;
+  return ck_raw<DT>(v);
+}
+
+// what tok_load and tok_param gave, in place, zeros past the row's end
+template <int DT, int NT, int CH>
+__device__ __forceinline__ void tok_fix(ck_u32x4 (&r)[CH], int t, int C) {
+  constexpr int V = ck_vec<DT>(), ES = DT == DT_F32 ? 4 : 2;
+  if (C == NT * CH * V) return;
 #pragma unroll
-    for (int e = 0; e < V; ++e) v[e] = none;
+  for (int j = 0; j < CH; ++j) {
+    const int c = (j * NT + t) * V;
+    if (C % V == 0 || C < V) {
+      if (c >= C) r[j] = ck_u32x4{0u, 0u, 0u, 0u};
+    } else {
+      r[j] = ck_shift(r[j], min(max(c - (C - V), 0), V) * ES);
+    }
   }
 }
 
-// NT threads hold a row, CH 16-byte pieces each
+// NT threads hold a row, CH 16-byte pieces each. Parameters are loaded where they
+// are used: held from the start they cost more in waves than their latency does (8192
+// x 1024 bf16: 29.4 us instead of 26.3).
 template <int DT, int NT, int CH, int KIND>
 __global__ __launch_bounds__(tok_threads<NT>()) void fno_norm_tok_fwd(NormArgs a) {
   constexpr int V = ck_vec<DT>(), RPG = tok_threads<NT>() / NT;
@@ -90,14 +105,22 @@ __global__ __launch_bounds__(tok_threads<NT>()) void fno_norm_tok_fwd(NormArgs a
   const float invC = 1.f / (float)C;
   const long nb = (C + kCkBlock - 1) / kCkBlock;
   int turn = 0;
+  auto get = [&](ck_u32x4 (&r)[CH], const void *p, float none) {
+#pragma unroll
+    for (int j = 0; j < CH; ++j) r[j] = tok_param<DT>(p, 0, (j * NT + t) * V, C, none);
+  };
   for (long b = (long)blockIdx.x * RPG + threadIdx.x / NT; b < a.B; b += (long)gridDim.x * RPG) {
-    ck_u32x4 vr[CH], xr[CH];
+    ck_u32x4 vr[CH], xr[CH], gr[CH];
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-      const long c = (long)(j * NT + t) * V;
-      vr[j] = ck_load<DT>(a.v, (size_t)b * C + c, C - c);
-      xr[j] = ck_load<DT>(a.x, (size_t)b * C + c, C - c);
+      const int c = (j * NT + t) * V;
+      vr[j] = tok_load<DT>(a.v, (size_t)b * C, c, C);
+      xr[j] = tok_load<DT>(a.x, (size_t)b * C, c, C);
+      gr[j] = tok_param<DT>(a.gate, (size_t)b * C, c, C, 1.f);
     }
+    tok_fix<DT, NT, CH>(vr, t, C);
+    tok_fix<DT, NT, CH>(xr, t, C);
+    tok_fix<DT, NT, CH>(gr, t, C);
     if (a.vq) {
 #pragma unroll
       for (int j = 0; j < CH; ++j) {
@@ -106,72 +129,77 @@ __global__ __launch_bounds__(tok_threads<NT>()) void fno_norm_tok_fwd(NormArgs a
         norm_encode<DT>(xr[j], a.xq, a.xe, b, c, nb);
       }
     }
-    float h[CH][V], s[1], m = 0.f;
+    // mean (layer norm) and inverse deviation of h(j, e)
+    auto stats = [&](auto &&h, float &m, float &r) {
+      float s[1] = {0.f};
+      m = 0.f;
+      if constexpr (KIND == kLayer) {
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+#pragma unroll
+          for (int e = 0; e < V; ++e) s[0] += h(j, e);
+        row_sum<NT, 1>(s, red, turn);
+        m = s[0] / (float)C;
+        s[0] = 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < CH; ++j)
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const float d = h(j, e) - m;
+          s[0] += KIND == kRms || (j * NT + t) * V + e < C ? d * d : 0.f;
+        }
+      row_sum<NT, 1>(s, red, turn);
+      r = rsq(fmaf(s[0], invC, a.eps));
+    };
+    float y[CH][V], m, r;
+    stats([&](int j, int e) { return ck_get<DT>(vr[j], e); }, m, r);
+    ck_u32x4 sc[CH], w[CH], bp[CH];
+    get(sc, a.scale, 1.f);
+    get(w, a.w_post, 1.f);
+    get(bp, a.b_post, 0.f);
+    tok_fix<DT, NT, CH>(sc, t, C);
+    tok_fix<DT, NT, CH>(w, t, C);
+    tok_fix<DT, NT, CH>(bp, t, C);
 #pragma unroll
     for (int j = 0; j < CH; ++j)
 #pragma unroll
-      for (int e = 0; e < V; ++e) h[j][e] = ck_get<DT>(vr[j], e);
-    if constexpr (KIND == kLayer) {
-      s[0] = 0.f;
-#pragma unroll
-      for (int j = 0; j < CH; ++j)
-#pragma unroll
-        for (int e = 0; e < V; ++e) s[0] += h[j][e];
-      row_sum<NT, 1>(s, red, turn);
-      m = s[0] / (float)C;
+      for (int e = 0; e < V; ++e)
+        y[j][e] = fmaf(ck_get<DT>(sc[j], e) * ck_get<DT>(gr[j], e),
+                       fmaf((ck_get<DT>(vr[j], e) - m) * r, ck_get<DT>(w[j], e), ck_get<DT>(bp[j], e)), ck_get<DT>(xr[j], e));
+    if (a.u) {  // ahead of y's stores, which they would wait for
+      get(w, a.w_pre, 1.f);
+      get(bp, a.b_pre, 0.f);
+      tok_fix<DT, NT, CH>(w, t, C);
+      tok_fix<DT, NT, CH>(bp, t, C);
     }
-    s[0] = 0.f;
-#pragma unroll
-    for (int j = 0; j < CH; ++j) s[0] += dev2<V>(h[j], m, C - (long)(j * NT + t) * V);
-    row_sum<NT, 1>(s, red, turn);
-    const float r = rsq(fmaf(s[0], invC, a.eps));
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-      const long c = (long)(j * NT + t) * V, n = C - c;
-      float g[V], sc[V], w[V], bp[V];
-      tok_param<DT>(a.gate, (size_t)b * C + c, n, 1.f, g);
-      tok_param<DT>(a.scale, c, n, 1.f, sc);
-      tok_param<DT>(a.w_post, c, n, 1.f, w);
-      tok_param<DT>(a.b_post, c, n, 0.f, bp);
-#pragma unroll
-      for (int e = 0; e < V; ++e)
-        h[j][e] = ck_get<DT>(xr[j], e) + sc[e] * g[e] * fmaf((h[j][e] - m) * r, w[e], bp[e]);
-      ck_store<DT>(a.y, (size_t)b * C + c, n, ck_raw<DT>(h[j]));
+      const int c = (j * NT + t) * V;
+      ck_store_row<DT>(a.y, (size_t)b * C + c, C - c, ck_raw<DT>(y[j]));
     }
     if (!a.u) continue;
-    m = 0.f;
-    if constexpr (KIND == kLayer) {
-      s[0] = 0.f;
-#pragma unroll
-      for (int j = 0; j < CH; ++j)
-#pragma unroll
-        for (int e = 0; e < V; ++e) s[0] += e < C - (long)(j * NT + t) * V ? h[j][e] : 0.f;
-      row_sum<NT, 1>(s, red, turn);
-      m = s[0] / (float)C;
-    }
-    s[0] = 0.f;
-#pragma unroll
-    for (int j = 0; j < CH; ++j) s[0] += dev2<V>(h[j], m, C - (long)(j * NT + t) * V);
-    row_sum<NT, 1>(s, red, turn);
-    const float ry = rsq(fmaf(s[0], invC, a.eps));
+    stats([&](int j, int e) { return y[j][e]; }, m, r);
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-      const long c = (long)(j * NT + t) * V, n = C - c;
-      float w[V], bp[V];
-      tok_param<DT>(a.w_pre, c, n, 1.f, w);
-      tok_param<DT>(a.b_pre, c, n, 0.f, bp);
 #pragma unroll
-      for (int e = 0; e < V; ++e) h[j][e] = fmaf((h[j][e] - m) * ry, w[e], bp[e]);
-      ck_store<DT>(a.u, (size_t)b * C + c, n, ck_raw<DT>(h[j]));
+      for (int e = 0; e < V; ++e) y[j][e] = fmaf((y[j][e] - m) * r, ck_get<DT>(w[j], e), ck_get<DT>(bp[j], e));
+      const int c = (j * NT + t) * V;
+      ck_store_row<DT>(a.u, (size_t)b * C + c, C - c, ck_raw<DT>(y[j]));
     }
   }
 }
 
-// Backward of tokens; the column sums of a workgroup's rows (gate T, gate G, U, V)
-// stay in registers and go to part[workgroup][4][C].
+// Backward of tokens, in the passes of a field's (norm_field.hpp). A row's
+// fields and gate stay as stored and are converted again in each pass; scale,
+// w_post, b_post and w_pre wait in LDS, a thread's own 16 bytes each; the column
+// sums of a workgroup's rows (gate T, gate G, U, V) stay in registers and go
+// to part[workgroup][4][C]. Stores come last in a row, so that no load waits
+// for one.
 template <int DT, int NT, int CH, int KIND>
-__global__ __launch_bounds__(tok_threads<NT>()) void fno_norm_tok_bwd(NormArgs a) {
+__global__ __launch_bounds__(tok_threads<NT>()) __attribute__((amdgpu_waves_per_eu(2))) void fno_norm_tok_bwd(NormArgs a) {
   constexpr int V = ck_vec<DT>(), RPG = tok_threads<NT>() / NT;
+  extern __shared__ ck_u32x4 prm[];  // [4][CH][NT]
   __shared__ float red[NT > 64 ? 4 * (NT / 64) : 1];
   __shared__ float sums[RPG > 1 ? RPG * NT * V : 1];
   const int t = threadIdx.x % NT, C = a.C;
@@ -185,143 +213,168 @@ __global__ __launch_bounds__(tok_threads<NT>()) void fno_norm_tok_bwd(NormArgs a
     for (int j = 0; j < CH; ++j)
 #pragma unroll
       for (int e = 0; e < V; ++e) acc[q][j][e] = 0.f;
-  for (long b = (long)blockIdx.x * RPG + threadIdx.x / NT; b < a.B; b += (long)gridDim.x * RPG) {
-    ck_u32x4 vr[CH], xr[CH], gyr[CH], gur[CH];
+  if (threadIdx.x < NT) {
+    ck_u32x4 p[4][CH];
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-      const long c = (long)(j * NT + t) * V, n = C - c;
+      const int c = (j * NT + t) * V;
+      p[0][j] = tok_param<DT>(a.scale, 0, c, C, 1.f);
+      p[1][j] = tok_param<DT>(a.w_post, 0, c, C, 1.f);
+      p[2][j] = tok_param<DT>(a.b_post, 0, c, C, 0.f);
+      p[3][j] = tok_param<DT>(a.w_pre, 0, c, C, 1.f);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      tok_fix<DT, NT, CH>(p[q], t, C);
+#pragma unroll
+      for (int j = 0; j < CH; ++j) prm[(q * CH + j) * NT + t] = p[q][j];
+    }
+  }
+  __syncthreads();
+  for (long b = (long)blockIdx.x * RPG + threadIdx.x / NT; b < a.B; b += (long)gridDim.x * RPG) {
+    ck_u32x4 vr[CH], xr[CH], gyr[CH], gur[CH], gr[CH];
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+      const int c = (j * NT + t) * V;
       if (a.vq) {
         vr[j] = norm_decode<DT>(a.vq, a.ve, b, c, nb);
         xr[j] = norm_decode<DT>(a.xq, a.xe, b, c, nb);
       } else {
-        vr[j] = ck_load<DT>(a.v, (size_t)b * C + c, n);
-        xr[j] = ck_load<DT>(a.x, (size_t)b * C + c, n);
+        vr[j] = tok_load<DT>(a.v, (size_t)b * C, c, C);
+        xr[j] = tok_load<DT>(a.x, (size_t)b * C, c, C);
       }
-      gyr[j] = ck_load<DT>(a.gy, (size_t)b * C + c, n);
+      gr[j] = tok_param<DT>(a.gate, (size_t)b * C, c, C, 1.f);
       gur[j] = ck_u32x4{0u, 0u, 0u, 0u};
-      if (a.gu) gur[j] = ck_load<DT>(a.gu, (size_t)b * C + c, n);
+      if (a.gu) gur[j] = tok_load<DT>(a.gu, (size_t)b * C, c, C);
+      gyr[j] = tok_load<DT>(a.gy, (size_t)b * C, c, C);
     }
-    float vh[CH][V], y[CH][V], s[1], m = 0.f;
+    if (!a.vq) {
+      tok_fix<DT, NT, CH>(vr, t, C);
+      tok_fix<DT, NT, CH>(xr, t, C);
+    }
+    tok_fix<DT, NT, CH>(gr, t, C);
+    tok_fix<DT, NT, CH>(gur, t, C);
+    tok_fix<DT, NT, CH>(gyr, t, C);
+    auto at = [&](int q, int j) { return prm[(q * CH + j) * NT + t]; };
+    auto in = [&](int j, int e) { return (j * NT + t) * V + e < C; };
+    float s[1] = {0.f}, m = 0.f;
+    if constexpr (KIND == kLayer) {
+#pragma unroll
+      for (int j = 0; j < CH; ++j)
+#pragma unroll
+        for (int e = 0; e < V; ++e) s[0] += ck_get<DT>(vr[j], e);
+      row_sum<NT, 1>(s, red, turn);
+      m = s[0] / (float)C;
+      s[0] = 0.f;
+    }
 #pragma unroll
     for (int j = 0; j < CH; ++j)
 #pragma unroll
-      for (int e = 0; e < V; ++e) vh[j][e] = ck_get<DT>(vr[j], e);
-    if constexpr (KIND == kLayer) {
-      s[0] = 0.f;
-#pragma unroll
-      for (int j = 0; j < CH; ++j)
-#pragma unroll
-        for (int e = 0; e < V; ++e) s[0] += vh[j][e];
-      row_sum<NT, 1>(s, red, turn);
-      m = s[0] / (float)C;
-    }
-    s[0] = 0.f;
-#pragma unroll
-    for (int j = 0; j < CH; ++j) s[0] += dev2<V>(vh[j], m, C - (long)(j * NT + t) * V);
+      for (int e = 0; e < V; ++e) {
+        const float d = ck_get<DT>(vr[j], e) - m;
+        s[0] += KIND == kRms || in(j, e) ? d * d : 0.f;
+      }
     row_sum<NT, 1>(s, red, turn);
     const float r = rsq(fmaf(s[0], invC, a.eps));
-    float q[2];
+    float y[CH][V], q[2];  // y, then gx
+    fresh<DT>(vr);
     if (a.gu) {
 #pragma unroll
       for (int j = 0; j < CH; ++j) {
-        const long c = (long)(j * NT + t) * V, n = C - c;
-        float g[V], sc[V], w[V], bp[V];
-        tok_param<DT>(a.gate, (size_t)b * C + c, n, 1.f, g);
-        tok_param<DT>(a.scale, c, n, 1.f, sc);
-        tok_param<DT>(a.w_post, c, n, 1.f, w);
-        tok_param<DT>(a.b_post, c, n, 0.f, bp);
+        const ck_u32x4 sc = at(0, j), w = at(1, j), bp = at(2, j);
 #pragma unroll
         for (int e = 0; e < V; ++e)
-          y[j][e] = ck_get<DT>(xr[j], e) + sc[e] * g[e] * fmaf((vh[j][e] - m) * r, w[e], bp[e]);
+          y[j][e] = fmaf(ck_get<DT>(sc, e) * ck_get<DT>(gr[j], e),
+                         fmaf((ck_get<DT>(vr[j], e) - m) * r, ck_get<DT>(w, e), ck_get<DT>(bp, e)), ck_get<DT>(xr[j], e));
+        channel_done();
       }
       float my = 0.f;
-      if constexpr (KIND == kLayer) {
-        s[0] = 0.f;
-#pragma unroll
-        for (int j = 0; j < CH; ++j)
-#pragma unroll
-          for (int e = 0; e < V; ++e) s[0] += e < C - (long)(j * NT + t) * V ? y[j][e] : 0.f;
-        row_sum<NT, 1>(s, red, turn);
-        my = s[0] / (float)C;
-      }
-      s[0] = 0.f;
-#pragma unroll
-      for (int j = 0; j < CH; ++j) s[0] += dev2<V>(y[j], my, C - (long)(j * NT + t) * V);
-      row_sum<NT, 1>(s, red, turn);
-      const float ry = rsq(fmaf(s[0], invC, a.eps));
       q[0] = q[1] = 0.f;
-      float gp[CH][V];
+      if constexpr (KIND == kLayer) {
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+          const ck_u32x4 w = at(3, j);
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            q[0] += y[j][e];
+            q[1] = fmaf(ck_get<DT>(gur[j], e), ck_get<DT>(w, e), q[1]);
+          }
+        }
+        row_sum<NT, 2>(q, red, turn);
+        my = q[0] / (float)C;
+      }
+      const float mg = q[1] * invC;  // mean of g = gu w_pre
+      q[0] = q[1] = 0.f;
 #pragma unroll
       for (int j = 0; j < CH; ++j) {
-        const long c = (long)(j * NT + t) * V, n = C - c;
-        tok_param<DT>(a.w_pre, c, n, 1.f, gp[j]);
+        const ck_u32x4 w = at(3, j);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          const float gu = ck_get<DT>(gur[j], e);
-          y[j][e] = (y[j][e] - my) * ry;
-          acc[2][j][e] = fmaf(gu, y[j][e], acc[2][j][e]);
-          acc[3][j][e] += gu;
-          gp[j][e] *= gu;
-          q[0] = fmaf(gp[j][e], y[j][e], q[0]);
-          if (KIND == kLayer) q[1] += gp[j][e];
+          const float d = KIND == kRms || in(j, e) ? y[j][e] - my : 0.f;
+          y[j][e] = d;
+          q[0] = fmaf(d, d, q[0]);
+          q[1] = fmaf(ck_get<DT>(gur[j], e) * ck_get<DT>(w, e), d, q[1]);
         }
       }
       row_sum<NT, 2>(q, red, turn);
-      q[0] *= invC;
-      q[1] *= invC;
+      const float ry = rsq(fmaf(q[0], invC, a.eps)), gy = q[1] * invC * ry;  // gy = mean(g y^)
 #pragma unroll
-      for (int j = 0; j < CH; ++j)
+      for (int j = 0; j < CH; ++j) {
+        const ck_u32x4 w = at(3, j);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          float g = fmaf(-y[j][e], q[0], gp[j][e]);
-          if (KIND == kLayer) g -= q[1];
+          const float gu = ck_get<DT>(gur[j], e), yh = y[j][e] * ry;
+          acc[2][j][e] = fmaf(gu, yh, acc[2][j][e]);
+          acc[3][j][e] += gu;
+          float g = fmaf(-yh, gy, gu * ck_get<DT>(w, e));
+          if (KIND == kLayer) g -= mg;
           y[j][e] = fmaf(ry, g, ck_get<DT>(gyr[j], e));
         }
+        channel_done();
+      }
     } else {
 #pragma unroll
       for (int j = 0; j < CH; ++j)
 #pragma unroll
         for (int e = 0; e < V; ++e) y[j][e] = ck_get<DT>(gyr[j], e);
     }
-    // y holds gx, h below the gradient of v^
-    float h[CH][V];
+    fresh<DT>(vr);
     q[0] = q[1] = 0.f;
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-      const long c = (long)(j * NT + t) * V, n = C - c;
-      if (a.gx) ck_store<DT>(a.gx, (size_t)b * C + c, n, ck_raw<DT>(y[j]));
-      float g[V], sc[V], w[V], bp[V], gg[V];
-      tok_param<DT>(a.gate, (size_t)b * C + c, n, 1.f, g);
-      tok_param<DT>(a.scale, c, n, 1.f, sc);
-      tok_param<DT>(a.w_post, c, n, 1.f, w);
-      tok_param<DT>(a.b_post, c, n, 0.f, bp);
+      const ck_u32x4 sc = at(0, j), w = at(1, j);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float vv = e < n ? (vh[j][e] - m) * r : 0.f, gx = e < n ? y[j][e] : 0.f;
-        vh[j][e] = vv;
-        gg[e] = gx * sc[e] * fmaf(vv, w[e], bp[e]);
-        acc[0][j][e] = fmaf(gx * g[e], vv, acc[0][j][e]);
-        acc[1][j][e] = fmaf(gx, g[e], acc[1][j][e]);
-        h[j][e] = gx * sc[e] * g[e] * w[e];
-        q[0] = fmaf(h[j][e], vv, q[0]);
-        if (KIND == kLayer) q[1] += h[j][e];
+        const float vh = (ck_get<DT>(vr[j], e) - m) * r, gx = y[j][e], g = ck_get<DT>(gr[j], e), wv = ck_get<DT>(w, e);
+        acc[0][j][e] = fmaf(gx * g, vh, acc[0][j][e]);
+        acc[1][j][e] = fmaf(gx, g, acc[1][j][e]);
+        const float h = gx * (ck_get<DT>(sc, e) * g * wv);
+        q[0] = fmaf(h, vh, q[0]);
+        if (KIND == kLayer) q[1] += h;
       }
-      if (a.g_gate) ck_store<DT>(a.g_gate, (size_t)b * C + c, n, ck_raw<DT>(gg));
+      channel_done();
     }
     row_sum<NT, 2>(q, red, turn);
-    if (!a.gv) continue;
-    q[0] *= invC;
-    q[1] *= invC;
+    const float hv = q[0] * invC, mh = q[1] * invC;
+    fresh<DT>(vr);
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-      const long c = (long)(j * NT + t) * V;
+      const int c = (j * NT + t) * V;
+      const size_t to = (size_t)b * C + c;
+      if (a.gx) ck_store_row<DT>(a.gx, to, C - c, ck_raw<DT>(y[j]));
+      const ck_u32x4 sc = at(0, j), w = at(1, j), bp = at(2, j);
+      float gg[V], gv[V];
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        float g = fmaf(-vh[j][e], q[0], h[j][e]);
-        if (KIND == kLayer) g -= q[1];
-        h[j][e] = r * g;
+        const float vh = (ck_get<DT>(vr[j], e) - m) * r, gs = y[j][e] * ck_get<DT>(sc, e), wv = ck_get<DT>(w, e);
+        gg[e] = gs * fmaf(vh, wv, ck_get<DT>(bp, e));
+        float g = fmaf(-vh, hv, gs * (ck_get<DT>(gr[j], e) * wv));
+        if (KIND == kLayer) g -= mh;
+        gv[e] = r * g;
       }
-      ck_store<DT>(a.gv, (size_t)b * C + c, C - c, ck_raw<DT>(h[j]));
+      if (a.g_gate) ck_store_row<DT>(a.g_gate, to, C - c, ck_raw<DT>(gg));
+      if (a.gv) ck_store_row<DT>(a.gv, to, C - c, ck_raw<DT>(gv));
+      channel_done();
     }
   }
   if (!a.part) return;
@@ -352,26 +405,32 @@ __global__ __launch_bounds__(tok_threads<NT>()) void fno_norm_tok_bwd(NormArgs a
     }
 }
 
+template <int DT, int KIND, bool FWD, int NT, int CH>
+NormPick tok_pick() {
+  if constexpr (FWD) return {(const void *)fno_norm_tok_fwd<DT, NT, CH, KIND>, tok_threads<NT>(), tok_threads<NT>() / NT, 0};
+  else return {(const void *)fno_norm_tok_bwd<DT, NT, CH, KIND>, tok_threads<NT>(), tok_threads<NT>() / NT, (size_t)64 * CH * NT};
+}
+
 template <int DT, int KIND>
-const void *tok_kernel(bool fwd, int C, int &threads, int &rpg) {
-#define FNO_PICK(NT, CH)                                       \
-  (threads = tok_threads<NT>(), rpg = tok_threads<NT>() / NT,  \
-   fwd ? (const void *)fno_norm_tok_fwd<DT, NT, CH, KIND> : (const void *)fno_norm_tok_bwd<DT, NT, CH, KIND>)
+NormPick tok_kernel(bool fwd, int C) {
+  // Forward: one piece a thread, so that many waves have loads in flight (8192 x 1024
+  // bf16: 23.3 us with one, 27.8 with two). Backward: two where that needs no more
+  // threads than 512, as each workgroup leaves sums to add (1024 x 8192 fp16: 72 us
+  // with 512 threads, 105 with 1024); four spill.
   if constexpr (DT == DT_F32) {
-    if (C <= 256) return FNO_PICK(64, 1);
-    if (C <= 512) return FNO_PICK(64, 2);
-    if (C <= 1024) return FNO_PICK(64, 4);
-    if (C <= 2048) return FNO_PICK(256, 2);
-    if (C <= 4096) return FNO_PICK(256, 4);
-    return FNO_PICK(512, 4);
+    if (C <= 256) return fwd ? tok_pick<DT, KIND, true, 64, 1>() : tok_pick<DT, KIND, false, 64, 1>();
+    if (C <= 512) return fwd ? tok_pick<DT, KIND, true, 128, 1>() : tok_pick<DT, KIND, false, 128, 1>();
+    if (C <= 1024) return fwd ? tok_pick<DT, KIND, true, 256, 1>() : tok_pick<DT, KIND, false, 256, 1>();
+    if (C <= 2048) return fwd ? tok_pick<DT, KIND, true, 512, 1>() : tok_pick<DT, KIND, false, 256, 2>();
+    if (C <= 4096) return fwd ? tok_pick<DT, KIND, true, 1024, 1>() : tok_pick<DT, KIND, false, 512, 2>();
+    return fwd ? tok_pick<DT, KIND, true, 1024, 2>() : tok_pick<DT, KIND, false, 512, 4>();
   } else {
-    if (C <= 512) return FNO_PICK(64, 1);
-    if (C <= 1024) return FNO_PICK(64, 2);
-    if (C <= 2048) return FNO_PICK(256, 1);
-    if (C <= 4096) return FNO_PICK(256, 2);
-    return FNO_PICK(512, 2);
+    if (C <= 512) return fwd ? tok_pick<DT, KIND, true, 64, 1>() : tok_pick<DT, KIND, false, 64, 1>();
+    if (C <= 1024) return fwd ? tok_pick<DT, KIND, true, 128, 1>() : tok_pick<DT, KIND, false, 64, 2>();
+    if (C <= 2048) return fwd ? tok_pick<DT, KIND, true, 256, 1>() : tok_pick<DT, KIND, false, 256, 1>();
+    if (C <= 4096) return fwd ? tok_pick<DT, KIND, true, 512, 1>() : tok_pick<DT, KIND, false, 512, 1>();
+    return fwd ? tok_pick<DT, KIND, true, 1024, 1>() : tok_pick<DT, KIND, false, 512, 2>();
   }
-#undef FNO_PICK
 }
 
 }  // namespace fno
