@@ -78,20 +78,19 @@ __device__ __forceinline__ ck_u32x4 tok_param(const void *p, size_t row, int c, 
   return ck_raw<DT>(v);
 }
 
-// what tok_load and tok_param gave, in place, zeros past the row's end
+// what tok_load and tok_param gave for channel c on, in place, zeros past the row's end
+template <int DT>
+__device__ __forceinline__ ck_u32x4 tok_fix1(const ck_u32x4 &r, int c, int C) {
+  constexpr int V = ck_vec<DT>(), ES = DT == DT_F32 ? 4 : 2;
+  if (C % V == 0 || C < V) return c < C ? r : ck_u32x4{0u, 0u, 0u, 0u};
+  return ck_shift(r, min(max(c - (C - V), 0), V) * ES);
+}
 template <int DT, int NT, int CH>
 __device__ __forceinline__ void tok_fix(ck_u32x4 (&r)[CH], int t, int C) {
-  constexpr int V = ck_vec<DT>(), ES = DT == DT_F32 ? 4 : 2;
+  constexpr int V = ck_vec<DT>();
   if (C == NT * CH * V) return;
 #pragma unroll
-  for (int j = 0; j < CH; ++j) {
-    const int c = (j * NT + t) * V;
-    if (C % V == 0 || C < V) {
-      if (c >= C) r[j] = ck_u32x4{0u, 0u, 0u, 0u};
-    } else {
-      r[j] = ck_shift(r[j], min(max(c - (C - V), 0), V) * ES);
-    }
-  }
+  for (int j = 0; j < CH; ++j) r[j] = tok_fix1<DT>(r[j], (j * NT + t) * V, C);
 }
 
 // NT threads hold a row, CH 16-byte pieces each. Parameters are loaded where they
@@ -105,9 +104,10 @@ __global__ __launch_bounds__(tok_threads<NT>()) void fno_norm_tok_fwd(NormArgs a
   const float invC = 1.f / (float)C;
   const long nb = (C + kCkBlock - 1) / kCkBlock;
   int turn = 0;
-  auto get = [&](ck_u32x4 (&r)[CH], const void *p, float none) {
-#pragma unroll
-    for (int j = 0; j < CH; ++j) r[j] = tok_param<DT>(p, 0, (j * NT + t) * V, C, none);
+  auto get = [&](const void *p, int j, float none) {
+    const int c = (j * NT + t) * V;
+    const ck_u32x4 r = tok_param<DT>(p, 0, c, C, none);
+    return C == NT * CH * V ? r : tok_fix1<DT>(r, c, C);
   };
   for (long b = (long)blockIdx.x * RPG + threadIdx.x / NT; b < a.B; b += (long)gridDim.x * RPG) {
     ck_u32x4 vr[CH], xr[CH], gr[CH];
@@ -154,27 +154,20 @@ __global__ __launch_bounds__(tok_threads<NT>()) void fno_norm_tok_fwd(NormArgs a
     };
     float y[CH][V], m, r;
     stats([&](int j, int e) { return ck_get<DT>(vr[j], e); }, m, r);
-    ck_u32x4 sc[CH], w[CH], bp[CH];
-    get(sc, a.scale, 1.f);
-    get(w, a.w_post, 1.f);
-    get(bp, a.b_post, 0.f);
-    tok_fix<DT, NT, CH>(sc, t, C);
-    tok_fix<DT, NT, CH>(w, t, C);
-    tok_fix<DT, NT, CH>(bp, t, C);
-#pragma unroll
-    for (int j = 0; j < CH; ++j)
-#pragma unroll
-      for (int e = 0; e < V; ++e)
-        y[j][e] = fmaf(ck_get<DT>(sc[j], e) * ck_get<DT>(gr[j], e),
-                       fmaf((ck_get<DT>(vr[j], e) - m) * r, ck_get<DT>(w[j], e), ck_get<DT>(bp[j], e)), ck_get<DT>(xr[j], e));
-    if (a.u) {  // ahead of y's stores, which they would wait for
-      get(w, a.w_pre, 1.f);
-      get(bp, a.b_pre, 0.f);
-      tok_fix<DT, NT, CH>(w, t, C);
-      tok_fix<DT, NT, CH>(bp, t, C);
+    // with one piece u's parameters are loaded ahead of y's store, which they would wait for
+    constexpr bool EARLY = CH == 1;
+    ck_u32x4 wu, bu;
+    if (EARLY && a.u) {
+      wu = get(a.w_pre, 0, 1.f);
+      bu = get(a.b_pre, 0, 0.f);
     }
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
+      const ck_u32x4 sc = get(a.scale, j, 1.f), w = get(a.w_post, j, 1.f), bp = get(a.b_post, j, 0.f);
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        y[j][e] = fmaf(ck_get<DT>(sc, e) * ck_get<DT>(gr[j], e),
+                       fmaf((ck_get<DT>(vr[j], e) - m) * r, ck_get<DT>(w, e), ck_get<DT>(bp, e)), ck_get<DT>(xr[j], e));
       const int c = (j * NT + t) * V;
       ck_store_row<DT>(a.y, (size_t)b * C + c, C - c, ck_raw<DT>(y[j]));
     }
@@ -182,8 +175,9 @@ __global__ __launch_bounds__(tok_threads<NT>()) void fno_norm_tok_fwd(NormArgs a
     stats([&](int j, int e) { return y[j][e]; }, m, r);
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
+      const ck_u32x4 w = EARLY ? wu : get(a.w_pre, j, 1.f), bp = EARLY ? bu : get(a.b_pre, j, 0.f);
 #pragma unroll
-      for (int e = 0; e < V; ++e) y[j][e] = fmaf((y[j][e] - m) * r, ck_get<DT>(w[j], e), ck_get<DT>(bp[j], e));
+      for (int e = 0; e < V; ++e) y[j][e] = fmaf((y[j][e] - m) * r, ck_get<DT>(w, e), ck_get<DT>(bp, e));
       const int c = (j * NT + t) * V;
       ck_store_row<DT>(a.u, (size_t)b * C + c, C - c, ck_raw<DT>(y[j]));
     }
@@ -423,7 +417,7 @@ NormPick tok_kernel(bool fwd, int C) {
     if (C <= 1024) return fwd ? tok_pick<DT, KIND, true, 256, 1>() : tok_pick<DT, KIND, false, 256, 1>();
     if (C <= 2048) return fwd ? tok_pick<DT, KIND, true, 512, 1>() : tok_pick<DT, KIND, false, 256, 2>();
     if (C <= 4096) return fwd ? tok_pick<DT, KIND, true, 1024, 1>() : tok_pick<DT, KIND, false, 512, 2>();
-    return fwd ? tok_pick<DT, KIND, true, 1024, 2>() : tok_pick<DT, KIND, false, 512, 4>();
+    return fwd ? tok_pick<DT, KIND, true, 512, 4>() : tok_pick<DT, KIND, false, 512, 4>();
   } else {
     if (C <= 512) return fwd ? tok_pick<DT, KIND, true, 64, 1>() : tok_pick<DT, KIND, false, 64, 1>();
     if (C <= 1024) return fwd ? tok_pick<DT, KIND, true, 128, 1>() : tok_pick<DT, KIND, false, 64, 2>();
