@@ -45,6 +45,13 @@ struct MtGeom {
   static constexpr int LDS_FWD = (AHEAD ? 2 : 1) * XS;
 };
 
+// A[o][i], 0 past the channels; the address is clamped and the value selected, so
+// that a wave's loads follow each other without a wait
+__device__ __forceinline__ float mt_weight(const MixTrainArgs &a, int o, int i) {
+  const float v = mt_load1<DT_F32>(a.A, (size_t)min(o, a.O - 1) * a.I + min(i, a.I - 1));
+  return o < a.O && i < a.I ? v : 0.f;
+}
+
 // z of 16 pixels of the wave's output channels: zv[m][4 j + pt], without bias
 template <int OT, int IT>
 __device__ __forceinline__ void mt_z(const float *xs, int pb, int lane, const float (&wf)[IT * 4],
@@ -76,11 +83,11 @@ __global__ __launch_bounds__((MtGeom<OT, IT>::THREADS)) void fno_mix_save(MixTra
   float wf[IT * 4], bias;
   {
     const int o = 16 * (ow) + n;
-    bias = a.bias && o < a.O ? mt_load1<DT_F32>(a.bias, o) : 0.f;
+    bias = mt_bias<DT_F32>(a, o);
 #pragma unroll
     for (int kk = 0; kk < IT * 4; ++kk) {
       const int i = 4 * kk + g;
-      wf[kk] = o < a.O && i < a.I ? mt_load1<DT_F32>(a.A, (size_t)o * a.I + i) : 0.f;
+      wf[kk] = mt_weight(a, o, i);
     }
   }
   const int t0 = blockIdx.x * a.per, t1 = min(a.tiles, t0 + a.per);
@@ -180,11 +187,11 @@ __global__ __launch_bounds__((MtGeom<OT, IT>::THREADS)) void fno_mix_bwd(MixTrai
   {
     const int o = 16 * (ow) + n;
     gb = 0.f;
-    bias = a.bias && o < a.O ? mt_load1<DT_F32>(a.bias, o) : 0.f;
+    bias = mt_bias<DT_F32>(a, o);
 #pragma unroll
     for (int kk = 0; kk < IT * 4; ++kk) {
       const int i = 4 * kk + g;
-      wf[kk] = o < a.O && i < a.I ? mt_load1<DT_F32>(a.A, (size_t)o * a.I + i) : 0.f;
+      wf[kk] = mt_weight(a, o, i);
     }
 #pragma unroll
     for (int it = 0; it < IT; ++it) ga[it] = v4f{0.f, 0.f, 0.f, 0.f};
@@ -194,7 +201,7 @@ __global__ __launch_bounds__((MtGeom<OT, IT>::THREADS)) void fno_mix_bwd(MixTrai
 #pragma unroll
     for (int kk = 0; kk < OT * 4; ++kk) {
       const int o = 4 * kk + g, i = 16 * (iw + G::WI * m) + n;
-      wt[m][kk] = o < a.O && i < a.I ? mt_load1<DT_F32>(a.A, (size_t)o * a.I + i) : 0.f;
+      wt[m][kk] = mt_weight(a, o, i);
     }
   const int t0 = blockIdx.x * a.per, t1 = min(a.tiles, t0 + a.per);
   Code16 xc[G::NU], nac;

@@ -50,6 +50,13 @@ __device__ __forceinline__ float mt_load1(const void *p, size_t i) {
   else return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(p)[i] << 16);
 }
 
+// bias of channel o, 0 where there is none; loaded without a branch
+template <int DT>
+__device__ __forceinline__ float mt_bias(const MixTrainArgs &a, int o) {
+  const float v = mt_load1<DT>(a.bias ? a.bias : a.A, a.bias ? min(o, a.O - 1) : 0);
+  return a.bias && o < a.O ? v : 0.f;
+}
+
 // 16 codes of a row's piece at pixel p (zeros past the row's blocks) and their exponent
 struct Code16 {
   ck_u32x4 q;

@@ -88,19 +88,22 @@ __device__ __forceinline__ void mh_write16(uint16_t *p, const ck_u32x4 &v) {
 }
 
 // Weights as an operand: lane's column is `col`, the summed index the 32 of step k;
-// at(col, s) addresses A
+// at(col, s) addresses A. The addresses are clamped and the values selected: with a
+// branch around each load, each is waited for before the next (5 us of a small call).
 template <typename F>
 __device__ __forceinline__ ck_u32x4 mh_weights(const uint16_t *A, int col, int ncol, int ns, int k, int lane, F at) {
+  uint32_t h[8];
+  const int c = min(col, ncol - 1);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const int s = 32 * k + mh_slot(lane >> 4, q >> 2) + (q & 3);
+    h[q] = A[at(c, min(s, ns - 1))];
+  }
   ck_u32x4 r;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    uint32_t h[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int s = 32 * k + mh_slot(lane >> 4, q >> 1) + 2 * (q & 1) + i;
-      h[i] = col < ncol && s < ns ? A[at(col, s)] : 0u;
-    }
-    r[q] = h[0] | h[1] << 16;
+    const int s = 32 * k + mh_slot(lane >> 4, q >> 1) + 2 * (q & 1);
+    r[q] = (col < ncol && s < ns ? h[2 * q] : 0u) | (col < ncol && s + 1 < ns ? h[2 * q + 1] << 16 : 0u);
   }
   return r;
 }
@@ -167,7 +170,7 @@ __global__ __launch_bounds__((MhGeom<OT, IT, true>::THREADS)) void fno_mix_save_
   float bias;
   {
     const int o = 16 * (ow) + n;
-    bias = a.bias && o < a.O ? mt_load1<DT>(a.bias, o) : 0.f;
+    bias = mt_bias<DT>(a, o);
 #pragma unroll
     for (int k = 0; k < G::KI; ++k)
       wf[k] = mh_weights(A, o, a.O, a.I, k, lane, [&](int c, int s) { return c * a.I + s; });
@@ -283,7 +286,7 @@ __global__ __launch_bounds__((MhGeom<OT, IT, false>::THREADS))
   {
     const int o = 16 * (ow) + n;
     gb = 0.f;
-    bias = a.bias && o < a.O ? mt_load1<DT>(a.bias, o) : 0.f;
+    bias = mt_bias<DT>(a, o);
 #pragma unroll
     for (int k = 0; k < G::KI; ++k)
       wf[k] = mh_weights(A, o, a.O, a.I, k, lane, [&](int c, int s) { return c * a.I + s; });

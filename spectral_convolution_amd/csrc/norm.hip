@@ -59,12 +59,16 @@ __global__ __launch_bounds__(1024) void fno_norm_params(NormArgs a, int S) {
   __shared__ float4 joint[16];
   const int c = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int share = a.B < 16 ? 16 / a.B : 1, slots = 16 / share, part = wave % share;
-  const float w = param(a.w_post, DT, c, 1.f), bp = param(a.b_post, DT, c, 0.f), sc = param(a.scale, DT, c, 1.f);
+  const uint32_t wb = param_bits<DT>(a.w_post, a.gy, c), bb = param_bits<DT>(a.b_post, a.gy, c),
+                 sb = param_bits<DT>(a.scale, a.gy, c);
   const size_t kstep = (size_t)a.C * a.B * S;
+  const float w = param_value<DT>(a.w_post, wb, 1.f), bp = param_value<DT>(a.b_post, bb, 0.f),
+              sc = param_value<DT>(a.scale, sb, 1.f);
   float t[5] = {0.f, 0.f, 0.f, 0.f, 0.f};  // sums over b of gate T, gate G, U, V and gate (w_post T + b_post G)
   for (int b0 = 0; b0 < a.B; b0 += slots) {  // once where waves share a sample
     const int b = b0 + wave / share;
     const bool ok = b < a.B;
+    const uint32_t gb = param_bits<DT>(a.gate, a.gy, (size_t)min(b, a.B - 1) * a.C + c);
     float v[4] = {0.f, 0.f, 0.f, 0.f};
     if (ok) {
       const float *src = a.part + ((size_t)c * a.B + b) * S;
@@ -93,7 +97,7 @@ __global__ __launch_bounds__(1024) void fno_norm_params(NormArgs a, int S) {
       }
     }
     if (!ok) break;
-    const float g = param(a.gate, DT, (size_t)b * a.C + c, 1.f), n = fmaf(w, v[0], bp * v[1]);
+    const float g = param_value<DT>(a.gate, gb, 1.f), n = fmaf(w, v[0], bp * v[1]);
     if (lane == 0) put<DT>(a.g_gate, (size_t)b * a.C + c, sc * n);
     t[0] = fmaf(g, v[0], t[0]);
     t[1] = fmaf(g, v[1], t[1]);

@@ -23,6 +23,23 @@ __device__ __forceinline__ float param(const void *p, int dtype, size_t i, float
   return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(p)[i] << 16);
 }
 
+// The storage bits of p[i], of any[i] where there is no p: several of these follow
+// each other without a wait, which a branch around each load would bring (param()).
+template <int DT>
+__device__ __forceinline__ uint32_t param_bits(const void *p, const void *any, size_t i) {
+  const void *q = p ? p : any;
+  if constexpr (DT == DT_F32) return reinterpret_cast<const uint32_t *>(q)[i];
+  else return reinterpret_cast<const uint16_t *>(q)[i];
+}
+template <int DT>
+__device__ __forceinline__ float param_value(const void *p, uint32_t bits, float none) {
+  float v;
+  if constexpr (DT == DT_F32) v = __uint_as_float(bits);
+  else if constexpr (DT == DT_F16) v = (float)__builtin_bit_cast(_Float16, (uint16_t)bits);
+  else v = __uint_as_float(bits << 16);
+  return p ? v : none;
+}
+
 template <int DT>
 __device__ __forceinline__ void put(void *p, size_t i, float v) {
   if (!p) return;

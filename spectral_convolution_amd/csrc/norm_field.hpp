@@ -9,14 +9,16 @@ namespace fno {
 // {scale gate w_post, scale gate b_post, w_pre, b_pre} of the channels of sample b
 template <int DT>
 __device__ __forceinline__ void norm_table(const NormArgs &a, int b, int n, float4 *tab) {
+  const void *any = a.gy ? a.gy : a.x;  // a field: at least a sample's channels long
   for (int c = threadIdx.x; c < n; c += blockDim.x) {
-    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (c < a.C) {
-      const float sg = param(a.scale, DT, c, 1.f) * param(a.gate, DT, (size_t)b * a.C + c, 1.f);
-      t = make_float4(sg * param(a.w_post, DT, c, 1.f), sg * param(a.b_post, DT, c, 0.f), param(a.w_pre, DT, c, 1.f),
-                      param(a.b_pre, DT, c, 0.f));
-    }
-    tab[c] = t;
+    const int i = min(c, a.C - 1);
+    const uint32_t sc = param_bits<DT>(a.scale, any, i), g = param_bits<DT>(a.gate, any, (size_t)b * a.C + i),
+                   w = param_bits<DT>(a.w_post, any, i), bp = param_bits<DT>(a.b_post, any, i),
+                   wu = param_bits<DT>(a.w_pre, any, i), bu = param_bits<DT>(a.b_pre, any, i);
+    const float sg = param_value<DT>(a.scale, sc, 1.f) * param_value<DT>(a.gate, g, 1.f);
+    const float4 t = make_float4(sg * param_value<DT>(a.w_post, w, 1.f), sg * param_value<DT>(a.b_post, bp, 0.f),
+                                 param_value<DT>(a.w_pre, wu, 1.f), param_value<DT>(a.b_pre, bu, 0.f));
+    tab[c] = c < a.C ? t : make_float4(0.f, 0.f, 0.f, 0.f);
   }
 }
 
