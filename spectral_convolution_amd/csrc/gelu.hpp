@@ -32,8 +32,31 @@ __device__ __forceinline__ float gelu_half(float v) {
   return fmaf(-0.5f * fabsf(v), r, fmaxf(v, 0.0f));
 }
 
+// GELU and its derivative for the fp32 training kernels, both from the normal
+// distribution's upper tail q = 1 - Phi(|v|) = exp(-v^2 / 2) t P(t), t = 1 / (1 + 0.39 |v|),
+// P of degree 5 fitted here by weighted least squares to 1e-8 of q (1.2e-7 with
+// everything in fp32; erff and expf give 6e-8, in five times the operations: a step
+// on 16 x 32 x 32 channels, 128^2 took 82 us with them). |v| is cut off at 100 where
+// it multiplies a vanished tail: infinities stay what they are.
+__device__ __forceinline__ float normal_tail(float a, float e) {
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.39f, a, 1.0f));
+  float p = fmaf(0.053847310403341085f, t, -0.2582449235385277f);
+  p = fmaf(p, t, 0.3751703021987614f);
+  p = fmaf(p, t, -0.016637008264066055f);
+  p = fmaf(p, t, 0.19443737777823863f);
+  p = fmaf(p, t, 0.1514269511269713f);
+  return p * t * e;
+}
+__device__ __forceinline__ float normal_bell(float v) {  // exp(-v^2 / 2)
+  return __builtin_amdgcn_exp2f(v * v * -0.72134752044448170f);
+}
+__device__ __forceinline__ float gelu_train(float v) {
+  const float a = fabsf(v), q = normal_tail(a, normal_bell(v));
+  return fmaf(-fminf(a, 100.0f), q, fmaxf(v, 0.0f));
+}
 __device__ __forceinline__ float gelu_slope(float v) {
-  return 0.5f * (1.0f + erff(v * 0.70710678118654752f)) + v * expf(-0.5f * v * v) * 0.39894228040143268f;
+  const float e = normal_bell(v), q = normal_tail(fabsf(v), e);
+  return fmaf(__builtin_amdgcn_fmed3f(v, -100.0f, 100.0f) * 0.39894228040143268f, e, v >= 0.0f ? 1.0f - q : q);
 }
 
 // The derivative for the half-precision kernels. It needs exp(-v^2 / 2) anyway,
