@@ -12,20 +12,26 @@ from ._lib import DTYPES, NORM_KINDS, NormGradsStruct, NormParamsStruct, check, 
 
 _NORM_NAMES = ("w_post", "b_post", "gate", "scale", "w_pre", "b_pre")
 
-# A call on a small field takes a few microseconds on the GPU, so the checks on
-# the way there are kept to a handful of attribute reads a tensor: _ptr() says yes
-# or hands over to _refuse(), which finds out what is wrong and says so.
+# A call on a small field takes a few microseconds on the GPU, so the checks on the
+# way there are few: the extension (csrc/binding.cpp) looks at all of a call's tensors at
+# once, and where one does not fit _ptr() or _buffer() find out what is wrong and say so.
 _torch = None
 _names = None
+_native = None
+_functions = {}
 
 
 def _t():
-    """torch, imported on first use (importing the binding does not import it)."""
-    global _torch, _names
+    """torch, imported on first use (importing the binding does not import it), and with it the extension."""
+    global _torch, _names, _native
     if _torch is None:
         import torch
-        _torch = torch
+        try:
+            from . import _native as native
+        except ImportError as e:
+            raise RuntimeError("_native.so not built (run python -m spectral_convolution_amd.build)") from e
         _names = {torch.float32: "f32", torch.float16: "f16", torch.bfloat16: "bf16"}
+        _native, _torch = native, torch
     return _torch
 
 
@@ -53,8 +59,24 @@ def _ptr(name, t, shape, dtype, dev, optional=False):
     _refuse(name, t, shape, dtype, dev, optional)
 
 
-def _buffer(name, t, need, align, dev):
-    """Address of a buffer of at least `need` bytes at a multiple of `align`."""
+def _ptrs(names, need, td, dev, ref, *pairs):
+    """Addresses of the tensors in pairs (tensor, shape, tensor, shape, ...), of ref's
+    dtype td and device dev; the first `need` of them may not be None."""
+    got = _native.addresses(ref, *pairs)
+    if got is None or 0 in got[:need]:
+        got = tuple(_ptr(n, t, s, td, dev, i >= need)
+                    for i, (n, t, s) in enumerate(zip(names, pairs[::2], pairs[1::2])))
+    return got
+
+
+def _buffer(name, t, need, align, ref):
+    """Address of a buffer of at least `need` bytes at a multiple of `align`, on ref's device."""
+    try:
+        p = _native.buffer(ref, t, need, align)
+    except OverflowError:
+        p = None
+    if p is not None:
+        return p
     if not isinstance(t, _t().Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     have = t.numel() * t.element_size()
@@ -63,8 +85,8 @@ def _buffer(name, t, need, align, dev):
     p = t.data_ptr()
     if p % align:
         raise ValueError(f"{name} must be {align}-byte aligned")
-    if t.get_device() != dev or not t.is_contiguous():
-        _refuse(name, t, t.shape, t.dtype, dev, False)
+    if t.get_device() != ref.get_device() or not t.is_contiguous():
+        _refuse(name, t, t.shape, t.dtype, ref.get_device(), False)
     return p
 
 
@@ -101,7 +123,10 @@ def _call(fn, dev, stream, *args):
         stream = torch._C._cuda_getCurrentRawStream(dev)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    st = getattr(lib(), fn)(*args, stream)
+    f = _functions.get(fn)
+    if f is None:
+        f = _functions[fn] = getattr(lib(), fn)
+    st = f(*args, stream)
     if st:
         check(st, fn)
 
@@ -143,19 +168,25 @@ def fno_checkpoint_pack(x, saved, stream=None):
     """Keep x in 8 bits (blocks of 32 along its last axis) in `saved`."""
     dt, td, dev, shape = _field(x, "x")
     rows, n = _rows(shape)
-    s = _buffer("saved", saved, fno_checkpoint_bytes(rows, n), 256, dev)
-    _call("fno_checkpoint_pack", dev, stream, _ptr("x", x, shape, td, dev), s, rows, n, DTYPES[dt])
+    s = _buffer("saved", saved, fno_checkpoint_bytes(rows, n), 256, x)
+    (p,) = _ptrs(("x",), 1, td, dev, x, x, shape)
+    _call("fno_checkpoint_pack", dev, stream, p, s, rows, n, DTYPES[dt])
 
 
 def fno_checkpoint_unpack(saved, y, stream=None):
     """Read the values kept in `saved` back into y (shape and dtype as packed)."""
     dt, td, dev, shape = _field(y, "y")
     rows, n = _rows(shape)
-    s = _buffer("saved", saved, fno_checkpoint_bytes(rows, n), 256, dev)
-    _call("fno_checkpoint_unpack", dev, stream, s, _ptr("y", y, shape, td, dev), rows, n, DTYPES[dt])
+    s = _buffer("saved", saved, fno_checkpoint_bytes(rows, n), 256, y)
+    (p,) = _ptrs(("y",), 1, td, dev, y, y, shape)
+    _call("fno_checkpoint_unpack", dev, stream, s, p, rows, n, DTYPES[dt])
 
 
 # --------------------------------------------------------------- channel mix
+
+_MIX_FORWARD = ("x", "A", "y", "bias", "add")
+_MIX_BACKWARD = ("A", "gy", "bias", "gx", "gA", "gbias", "gadd")
+
 
 def fno_channel_mix_saved_bytes(batch, c_in, c_out, pixels, act=0, has_add=False):
     """Bytes of what fno_channel_mix_save keeps."""
@@ -186,10 +217,9 @@ def fno_channel_mix_save(x, A, bias, add, y, saved, act=0, stream=None):
     B, I, P = _split(shape, "x")
     O = _split(_field(y, "y")[3], "y")[1]
     out = (B, O) + shape[2:]
-    args = (_ptr("x", x, shape, td, dev), _ptr("A", A, (O, I), td, dev), _ptr("bias", bias, (O,), td, dev, True),
-            _ptr("add", add, out, td, dev, True), _ptr("y", y, out, td, dev),
-            _buffer("saved", saved, fno_channel_mix_saved_bytes(B, I, O, P, act, add is not None), 256, dev))
-    _call("fno_channel_mix_save", dev, stream, *args, B, I, O, P, act, DTYPES[dt])
+    px, pA, py, pbias, padd = _ptrs(_MIX_FORWARD, 3, td, dev, x, x, shape, A, (O, I), y, out, bias, (O,), add, out)
+    ps = _buffer("saved", saved, fno_channel_mix_saved_bytes(B, I, O, P, act, add is not None), 256, x)
+    _call("fno_channel_mix_save", dev, stream, px, pA, pbias, padd, py, ps, B, I, O, P, act, DTYPES[dt])
 
 
 def fno_channel_mix_backward_saved(saved, A, bias, gy, gx, gA, gbias, gadd, workspace, act=0, has_add=False,
@@ -203,13 +233,14 @@ def fno_channel_mix_backward_saved(saved, A, bias, gy, gx, gA, gbias, gadd, work
     if A.dim() != 2 or A.shape[0] != O:
         raise ValueError(f"A shape {tuple(A.shape)} does not map to gy's {O} channels")
     I = A.shape[1]
-    args = [_buffer("saved", saved, fno_channel_mix_saved_bytes(B, I, O, P, act, has_add), 256, dev),
-            _ptr("A", A, (O, I), td, dev), _ptr("bias", bias, (O,), td, dev, True), _ptr("gy", gy, shape, td, dev),
-            _ptr("gx", gx, (B, I) + shape[2:], td, dev, True), _ptr("gA", gA, (O, I), td, dev, True),
-            _ptr("gbias", gbias, (O,), td, dev, True), _ptr("gadd", gadd, shape, td, dev, True), None]
+    ps = _buffer("saved", saved, fno_channel_mix_saved_bytes(B, I, O, P, act, has_add), 256, gy)
+    pA, pgy, pbias, pgx, pgA, pgbias, pgadd = _ptrs(_MIX_BACKWARD, 2, td, dev, gy, A, (O, I), gy, shape, bias, (O,), gx,
+                                                    (B, I) + shape[2:], gA, (O, I), gbias, (O,), gadd, shape)
+    ws = None
     if gA is not None or gbias is not None:
-        args[8] = _buffer("workspace", workspace, fno_channel_mix_workspace_bytes(B, I, O, P, dt), 16, dev)
-    _call("fno_channel_mix_backward_saved", dev, stream, *args, B, I, O, P, act, int(has_add), DTYPES[dt])
+        ws = _buffer("workspace", workspace, fno_channel_mix_workspace_bytes(B, I, O, P, dt), 16, gy)
+    _call("fno_channel_mix_backward_saved", dev, stream, ps, pA, pbias, pgy, pgx, pgA, pgbias, pgadd, ws, B, I, O, P,
+          act, int(has_add), DTYPES[dt])
 
 
 # --------------------------------------------------------------------- norms
@@ -228,13 +259,12 @@ class NormParams:
         self.w_post, self.b_post, self.gate, self.scale = w_post, b_post, gate, scale
         self.w_pre, self.b_pre = w_pre, b_pre
 
-    def _struct(self, B, C, td, dev):
+    def _pairs(self, B, C):
         c = (C,)
-        return NormParamsStruct(
-            NORM_KINDS[self.kind], self.eps, _ptr("w_post", self.w_post, c, td, dev, True),
-            _ptr("b_post", self.b_post, c, td, dev, True), _ptr("gate", self.gate, (B, C), td, dev, True),
-            _ptr("scale", self.scale, c, td, dev, True), _ptr("w_pre", self.w_pre, c, td, dev, True),
-            _ptr("b_pre", self.b_pre, c, td, dev, True))
+        return self.w_post, c, self.b_post, c, self.gate, (B, C), self.scale, c, self.w_pre, c, self.b_pre, c
+
+    def _struct(self, addresses):
+        return NormParamsStruct(NORM_KINDS[self.kind], self.eps, *addresses)
 
 
 class NormGrads:
@@ -246,16 +276,7 @@ class NormGrads:
         self.w_post, self.b_post, self.gate, self.scale = w_post, b_post, gate, scale
         self.w_pre, self.b_pre = w_pre, b_pre
 
-    def _struct(self, B, C, td, dev):
-        """(the C struct, whether any gradient is wanted)"""
-        c = (C,)
-        p = (_ptr("gradient of w_post", self.w_post, c, td, dev, True),
-             _ptr("gradient of b_post", self.b_post, c, td, dev, True),
-             _ptr("gradient of gate", self.gate, (B, C), td, dev, True),
-             _ptr("gradient of scale", self.scale, c, td, dev, True),
-             _ptr("gradient of w_pre", self.w_pre, c, td, dev, True),
-             _ptr("gradient of b_pre", self.b_pre, c, td, dev, True))
-        return NormGradsStruct(*p), p != (None,) * 6
+    _pairs = NormParams._pairs
 
 
 def fno_norm_residual_saved_bytes(batch, channels, pixels):
@@ -279,14 +300,19 @@ def fno_norm_residual_workspace_empty(x):
     return _empty(fno_norm_residual_workspace_bytes(*_split(shape, "x"), dt), x)
 
 
+_NORM_FORWARD = ("x", "v", "y", "u") + _NORM_NAMES
+_NORM_BACKWARD = (("gy", "x", "v", "gu", "gx", "gv") + _NORM_NAMES + tuple("gradient of " + n for n in _NORM_NAMES))
+_NORM_BACKWARD_SAVED = _NORM_BACKWARD[:1] + _NORM_BACKWARD[3:]
+
+
 def _norm_forward(fn, prm, x, v, y, u, saved, stream):
     dt, td, dev, shape = _field(x, "x")
     B, C, P = _split(shape, "x")
-    args = [_ptr("x", x, shape, td, dev), _ptr("v", v, shape, td, dev), _ptr("y", y, shape, td, dev),
-            _ptr("u", u, shape, td, dev, True)]
+    p = _ptrs(_NORM_FORWARD, 3, td, dev, x, x, shape, v, shape, y, shape, u, shape, *prm._pairs(B, C))
+    args = p[:4]
     if saved is not False:
-        args.append(_buffer("saved", saved, fno_norm_residual_saved_bytes(B, C, P), 256, dev))
-    _call(fn, dev, stream, prm._struct(B, C, td, dev), *args, B, C, P, DTYPES[dt])
+        args += (_buffer("saved", saved, fno_norm_residual_saved_bytes(B, C, P), 256, x),)
+    _call(fn, dev, stream, prm._struct(p[4:]), *args, B, C, P, DTYPES[dt])
 
 
 def fno_norm_residual(params, x, v, y, u, stream=None):
@@ -303,16 +329,20 @@ def fno_norm_residual_save(params, x, v, y, u, saved, stream=None):
 def _norm_backward(fn, prm, x, v, saved, gy, gu, gx, gv, grads, workspace, stream):
     dt, td, dev, shape = _field(gy, "gy")
     B, C, P = _split(shape, "gy")
-    args = [_ptr("gy", gy, shape, td, dev)] + [_ptr(n, t, shape, td, dev, True)
-                                               for n, t in (("gu", gu), ("gx", gx), ("gv", gv))]
+    tail = (gu, shape, gx, shape, gv, shape) + prm._pairs(B, C)
+    if grads is not None:
+        tail += grads._pairs(B, C)
     if saved is False:
-        args = [_ptr("x", x, shape, td, dev), _ptr("v", v, shape, td, dev)] + args
+        p = _ptrs(_NORM_BACKWARD, 3, td, dev, gy, gy, shape, x, shape, v, shape, *tail)
+        first, p = p[1:3], p[:1] + p[3:]
     else:
-        args.insert(0, _buffer("saved", saved, fno_norm_residual_saved_bytes(B, C, P), 256, dev))
-    st = prm._struct(B, C, td, dev)
-    gr, any_ = (NormGradsStruct(), False) if grads is None else grads._struct(B, C, td, dev)
-    ws = _buffer("workspace", workspace, fno_norm_residual_workspace_bytes(B, C, P, dt), 16, dev) if any_ else None
-    _call(fn, dev, stream, st, *args, gr, ws, B, C, P, DTYPES[dt])
+        p = _ptrs(_NORM_BACKWARD_SAVED, 1, td, dev, gy, gy, shape, *tail)
+        first = (_buffer("saved", saved, fno_norm_residual_saved_bytes(B, C, P), 256, gy),)
+    wanted = p[10:]
+    ws = None
+    if any(wanted):
+        ws = _buffer("workspace", workspace, fno_norm_residual_workspace_bytes(B, C, P, dt), 16, gy)
+    _call(fn, dev, stream, prm._struct(p[4:10]), *first, *p[:4], NormGradsStruct(*wanted), ws, B, C, P, DTYPES[dt])
 
 
 def fno_norm_residual_backward(params, x, v, gy, gu, gx, gv, grads, workspace, stream=None):

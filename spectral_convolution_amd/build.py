@@ -17,6 +17,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfno.so")
+NATIVE = os.path.join(HERE, "_native.so")
 
 SOURCES = ["plane_kernels.hip", "plane_mfma.hip", "axis_kernels.hip", "contract.hip", "contract_mx.hip", "backward.hip", "weights.hip", "pointwise.hip", "fused.hip", "fno_api.cpp",
            "fno_model.cpp", "checkpoint.hip", "norm.hip", "norm_f32.hip", "norm_f16.hip", "norm_bf16.hip", "mix_train.hip", "mix_train_f16.hip", "mix_train_bf16.hip",
@@ -50,11 +51,32 @@ def _compile(src, verbose):
     return obj
 
 
+def _native(verbose):
+    """Compile the binding's own extension (host code against torch's headers)."""
+    import importlib.util
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    import sysconfig
+    tmp = NATIVE + ".tmp"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           "-I", os.path.join(torch, "include"), "-I", sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L", os.path.join(torch, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, NATIVE)
+
+
 def build(verbose: bool = False, jobs: int = 8) -> str:
-    """Compile every source and link libfno.so; returns the library path."""
+    """Compile every source, link libfno.so and build the binding's extension;
+    returns the library path."""
     os.makedirs(BUILD, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
+        native = ex.submit(_native, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
+        native.result()
     tmp = LIB + ".tmp"
     cmd = [_hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
     if verbose:
