@@ -115,7 +115,8 @@ __global__ __launch_bounds__((MtGeom<OT, IT>::THREADS)) void fno_mix_save(MixTra
       const int o = 16 * ow + n;
       const long p = p0 + pb + 16 * g;
       const size_t row = (size_t)b * a.O + min(o, a.O - 1);
-      nadd.load(a.add, row * P + p, p0 + G::PT <= P ? 16 : o < a.O ? P - p : 0);
+      if (p0 + G::PT <= P) nadd.load64(a.add, row * P + p0 + pb, lane);
+      else nadd.load(a.add, row * P + p, o < a.O ? P - p : 0);
     }
   };
   if (G::AHEAD && t0 < t1) fetch(t0);
@@ -143,7 +144,8 @@ __global__ __launch_bounds__((MtGeom<OT, IT>::THREADS)) void fno_mix_save(MixTra
 #pragma unroll
       for (int q = 0; q < 4; ++q) reinterpret_cast<ck_u32x4 *>(d)[q] = xv[k].r[q];
     }
-    const Px16<DT_F32> ad = nadd;
+    Px16<DT_F32> ad = nadd;
+    if (whole) mt_exchange(ad.r);
     __syncthreads();
     if (G::AHEAD && t + 1 < t1) fetch(t + 1);
     v4f z[4];
@@ -168,7 +170,10 @@ __global__ __launch_bounds__((MtGeom<OT, IT>::THREADS)) void fno_mix_save(MixTra
         const float v = z[e & 3][e >> 2] + bias + ad.get(e);
         y[e] = a.act ? mt_gelu<DT_F32>(v) : v;
       }
-      if (ok) store16<DT_F32>(a.y, row * P + p, whole ? 16 : P - p, y);
+      if (ok) {
+        if (whole) store64(a.y, row * P + p0 + pb, lane, y);
+        else store16<DT_F32>(a.y, row * P + p, P - p, y);
+      }
     }
     if (!G::AHEAD) __syncthreads();
   }
@@ -218,7 +223,7 @@ __global__ __launch_bounds__((MtGeom<OT, IT>::THREADS)) void fno_mix_bwd(MixTrai
     const int o = 16 * ow + n;
     const size_t row = (size_t)b * a.O + min(o, a.O - 1);
     if (p0 + G::PT <= P) {
-      ngy.load(a.gy, row * P + p, 16);
+      ngy.load64(a.gy, row * P + p0 + pb, lane);
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         if (o >= a.O) ngy.r[q] = ck_u32x4{0u, 0u, 0u, 0u};
@@ -233,7 +238,8 @@ __global__ __launch_bounds__((MtGeom<OT, IT>::THREADS)) void fno_mix_bwd(MixTrai
     const long p0 = (long)(t - b * a.tpb) * G::PT;
     const bool whole = p0 + G::PT <= P;
     if (!G::AHEAD) fetch(t);
-    const Px16<DT_F32> gy = ngy;
+    Px16<DT_F32> gy = ngy;
+    if (whole) mt_exchange(gy.r);
     const Code16 ac = nac;
 #pragma unroll
     for (int k = 0; k < G::NU; ++k) {
@@ -264,7 +270,11 @@ __global__ __launch_bounds__((MtGeom<OT, IT>::THREADS)) void fno_mix_bwd(MixTrai
 #pragma unroll
         for (int e = 0; e < 16; ++e) gz[e] *= mt_slope<DT_F32>(z[e & 3][e >> 2] + bias + ac.get(e, s));
       }
-      if (a.gadd && ok) store16<DT_F32>(a.gadd, row * P + p, whole ? 16 : P - p, gz);
+      if (a.gadd && ok) {
+        const size_t at = row * P + p0 + pb;
+        if (whole) store64(a.gadd, at, lane, gz);
+        else store16<DT_F32>(a.gadd, at + 16 * g, P - p, gz);
+      }
       float *d = gs + (16 * (ow) + n) * G::PITCH + pb + 16 * g;
 #pragma unroll
       for (int q = 0; q < 4; ++q)
@@ -303,7 +313,11 @@ __global__ __launch_bounds__((MtGeom<OT, IT>::THREADS)) void fno_mix_bwd(MixTrai
 #pragma unroll
           for (int e = 0; e < 16; ++e) v[e] = acc[e & 3][e >> 2];
           const long q = p0 + sb + 16 * g;
-          if (i < a.I) store16<DT_F32>(a.gx, ((size_t)b * a.I + i) * P + q, whole ? 16 : P - q, v);
+          if (i < a.I) {
+            const size_t at = ((size_t)b * a.I + i) * P + p0 + sb;
+            if (whole) store64(a.gx, at, lane, v);
+            else store16<DT_F32>(a.gx, at + 16 * g, P - q, v);
+          }
         }
       }
     }
