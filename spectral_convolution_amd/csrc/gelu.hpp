@@ -16,7 +16,8 @@ __device__ __forceinline__ float gelu(float v) { return 0.5f * v * (1.0f + erff(
 // GELU(v) = max(v, 0) - |v| r / 2. One reciprocal on the transcendental
 // unit; formula 7.1.26 needs an exponential as well, which made the
 // projection (128 hidden GELUs per pixel) 21 us slower at B = 20, 256^2.
-__device__ __forceinline__ float gelu_half(float v) {
+// `a` is |v|, or |v| cut off where r is 0 (normal_tail() below says why).
+__device__ __forceinline__ float gelu_half_at(float v, float a) {
   const float x = fabsf(v) * 0.70710678118654752f;
   float p = fmaf(0.0000430638f, x, 0.0002765672f);
   p = fmaf(p, x, 0.0001520143f);
@@ -29,8 +30,10 @@ __device__ __forceinline__ float gelu_half(float v) {
   p = p * p;
   p = p * p;
   const float r = __builtin_amdgcn_rcpf(p);
-  return fmaf(-0.5f * fabsf(v), r, fmaxf(v, 0.0f));
+  return fmaf(-0.5f * a, r, fmaxf(v, 0.0f));
 }
+__device__ __forceinline__ float gelu_half(float v) { return gelu_half_at(v, fabsf(v)); }
+__device__ __forceinline__ float gelu_half_train(float v) { return gelu_half_at(v, fminf(fabsf(v), 100.0f)); }
 
 // GELU and its derivative for the fp32 training kernels, both from the normal
 // distribution's upper tail q = 1 - Phi(|v|) = exp(-v^2 / 2) t P(t), t = 1 / (1 + 0.39 |v|),

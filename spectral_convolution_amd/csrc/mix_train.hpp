@@ -114,7 +114,7 @@ struct Code16 {
 };
 
 template <int DT>
-__device__ __forceinline__ float mt_gelu(float z) { return DT == DT_F32 ? gelu_train(z) : gelu_half(z); }
+__device__ __forceinline__ float mt_gelu(float z) { return DT == DT_F32 ? gelu_train(z) : gelu_half_train(z); }
 template <int DT>
 __device__ __forceinline__ float mt_slope(float z) { return DT == DT_F32 ? gelu_slope(z) : gelu_slope_half(z); }
 

@@ -397,3 +397,22 @@ def test_mix_at_the_ends_of_fp16(scale_x, scale_gy):
     assert max(abs(gx).max(), abs(gA).max()) < 65504
     close("gx", out["gx"], gx, "f16", extra=ACT["f16"], size=np.einsum("oi,bop->bip", abs(v["A"]), gzs))
     close("gA", out["gA"], gA, "f16", extra=ACT["f16"], size=np.einsum("bop,bip->oi", gzs, abs(xk)))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_mix_of_infinities(dtype):
+    """GELU of plus infinity is infinite, of minus infinity its limit, 0; the block that held
+    one reads back as NaN, so the gradients through its pixels are NaN and others are as before."""
+    c = _mix_case(dtype, 1, 5, 6, 100, True, seed=14)
+    clean = _mix_run(c, 1)
+    a = c["add"][0].clone()
+    a[0, 1, 40], a[0, 2, 41] = float("inf"), -float("inf")
+    y, out = _mix_run({**c, "add": (a, None)}, 1)
+    assert y[0, 1, 40] == float("inf") and y[0, 2, 41] == 0
+    same = torch.ones_like(y, dtype=torch.bool)
+    same[0, 1, 40] = same[0, 2, 41] = False
+    assert torch.equal(y[same], clean[0][same])
+    hit = torch.zeros(100, dtype=torch.bool, device=DEV)
+    hit[32:64] = True
+    assert torch.isnan(out["gadd"][0, 1:3, hit]).all() and torch.equal(out["gx"][0][:, ~hit], clean[1]["gx"][0][:, ~hit])
+    assert torch.equal(out["gadd"][0, 3:], clean[1]["gadd"][0, 3:])
