@@ -471,7 +471,8 @@ fno_status_t fno_channel_mix_save(const void *x, const void *A,
  * gz = gy act'(z):
  *   gx = A^T gz [batch][c_in][pixels],  gadd = gz [batch][c_out][pixels],
  *   gA = sum gz x^^T [c_out][c_in],  gbias = sum gz [c_out]
- * (sums over samples and pixels, in fp32). Each may be NULL, not all; bias as
+ * (sums over samples and pixels, in fp32). What an infinite gz reaches is not
+ * finite, NaN where fp32 would give an infinity. Each may be NULL, not all; bias as
  * in the forward; has_add: whether the forward had an add input (gadd must be
  * NULL otherwise). workspace: fno_channel_mix_workspace_bytes bytes, 16-byte
  * aligned, needed for gA or gbias; its contents do not matter. */
