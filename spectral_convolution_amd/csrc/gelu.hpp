@@ -35,7 +35,7 @@ __device__ __forceinline__ float gelu_half_at(float v, float a) {
 __device__ __forceinline__ float gelu_half(float v) { return gelu_half_at(v, fabsf(v)); }
 __device__ __forceinline__ float gelu_half_train(float v) { return gelu_half_at(v, fminf(fabsf(v), 100.0f)); }
 
-// GELU and its derivative for the fp32 training kernels, both from the normal
+// GELU for the fp32 training kernels and its derivative for all of them, both from the normal
 // distribution's upper tail q = 1 - Phi(|v|) = exp(-v^2 / 2) t P(t), t = 1 / (1 + 0.39 |v|),
 // P of degree 5 fitted here by weighted least squares to 1e-8 of q (1.2e-7 with
 // everything in fp32; erff and expf give 6e-8, in five times the operations: a step
@@ -60,22 +60,6 @@ __device__ __forceinline__ float gelu_train(float v) {
 __device__ __forceinline__ float gelu_slope(float v) {
   const float e = normal_bell(v), q = normal_tail(fabsf(v), e);
   return fmaf(__builtin_amdgcn_fmed3f(v, -100.0f, 100.0f) * 0.39894228040143268f, e, v >= 0.0f ? 1.0f - q : q);
-}
-
-// The derivative for the half-precision kernels. It needs exp(-v^2 / 2) anyway,
-// so erf is taken from Abramowitz & Stegun, formula 7.1.26, which uses the
-// same exponential: erfc(x) = t (a1 + ... + a5 t^4) exp(-x^2), t = 1 / (1 + p x),
-// x >= 0 (absolute error below 1.5e-7; below 1e-6 for the whole derivative in
-// fp32), odd symmetry of erf for v < 0.
-__device__ __forceinline__ float gelu_slope_half(float v) {
-  const float e = __builtin_amdgcn_exp2f(v * v * -0.72134752044448170f);  // exp(-v^2 / 2)
-  const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f * 0.70710678118654752f, fabsf(v), 1.0f));
-  float p = fmaf(0.5f * 1.061405429f, t, 0.5f * -1.453152027f);
-  p = fmaf(p, t, 0.5f * 1.421413741f);
-  p = fmaf(p, t, 0.5f * -0.284496736f);
-  p = fmaf(p, t, 0.5f * 0.254829592f);
-  const float q = p * t * e;  // 1 - Phi(|v|)
-  return fmaf(v * 0.39894228040143268f, e, v >= 0.0f ? 1.0f - q : q);
 }
 
 }  // namespace fno

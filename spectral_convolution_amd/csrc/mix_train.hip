@@ -273,7 +273,7 @@ __global__ __launch_bounds__((MtGeom<OT, IT>::THREADS)) void fno_mix_bwd(MixTrai
       if (a.act) {
         const float s = ck_step(ac.e);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) gz[e] *= mt_slope<DT_F32>(z[e & 3][e >> 2] + bias + ac.get(e, s));
+        for (int e = 0; e < 16; ++e) gz[e] *= gelu_slope(z[e & 3][e >> 2] + bias + ac.get(e, s));
       }
       if (a.gadd && ok) {
         const size_t at = row * P + p0 + pb;

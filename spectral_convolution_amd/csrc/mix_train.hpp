@@ -115,8 +115,6 @@ struct Code16 {
 
 template <int DT>
 __device__ __forceinline__ float mt_gelu(float z) { return DT == DT_F32 ? gelu_train(z) : gelu_half_train(z); }
-template <int DT>
-__device__ __forceinline__ float mt_slope(float z) { return DT == DT_F32 ? gelu_slope(z) : gelu_slope_half(z); }
 
 // The workgroup's sums of gA (ga[it]: rows 16 ow + 4 (lane / 16) + j, columns
 // 16 it + lane % 16, ow = wave % OT) and gbias (gb, a lane's share of row

@@ -372,7 +372,7 @@ __global__ __launch_bounds__((MhGeom<OT, IT, false>::THREADS))
         const float s = ck_step(ac.e);
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          gz[e] *= mt_slope<DT>(fmaf((float)(int8_t)(ac.q[e >> 2] >> (8 * (e & 3))), s, z[e >> 2][e & 3]));
+          gz[e] *= gelu_slope(fmaf((float)(int8_t)(ac.q[e >> 2] >> (8 * (e & 3))), s, z[e >> 2][e & 3]));
       }
       if (a.gadd && o < a.O) store16<DT>(a.gadd, ((size_t)b * a.O + o) * P + p, whole ? 16 : P - p, gz);
       uint32_t hi[8], lo[8];
