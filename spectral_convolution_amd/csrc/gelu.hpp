@@ -16,8 +16,7 @@ __device__ __forceinline__ float gelu(float v) { return 0.5f * v * (1.0f + erff(
 // GELU(v) = max(v, 0) - |v| r / 2. One reciprocal on the transcendental
 // unit; formula 7.1.26 needs an exponential as well, which made the
 // projection (128 hidden GELUs per pixel) 21 us slower at B = 20, 256^2.
-// `a` is |v|, or |v| cut off where r is 0 (normal_tail() below says why).
-__device__ __forceinline__ float gelu_half_at(float v, float a) {
+__device__ __forceinline__ float gelu_half(float v) {
   const float x = fabsf(v) * 0.70710678118654752f;
   float p = fmaf(0.0000430638f, x, 0.0002765672f);
   p = fmaf(p, x, 0.0001520143f);
@@ -30,17 +29,18 @@ __device__ __forceinline__ float gelu_half_at(float v, float a) {
   p = p * p;
   p = p * p;
   const float r = __builtin_amdgcn_rcpf(p);
-  return fmaf(-0.5f * a, r, fmaxf(v, 0.0f));
+  return fmaf(-0.5f * fabsf(v), r, fmaxf(v, 0.0f));
 }
-__device__ __forceinline__ float gelu_half(float v) { return gelu_half_at(v, fabsf(v)); }
-__device__ __forceinline__ float gelu_half_train(float v) { return gelu_half_at(v, fminf(fabsf(v), 100.0f)); }
 
-// GELU for the fp32 training kernels and its derivative for all of them, both from the normal
+// GELU and its derivative for the training kernels of all types, both from the normal
 // distribution's upper tail q = 1 - Phi(|v|) = exp(-v^2 / 2) t P(t), t = 1 / (1 + 0.39 |v|),
-// P of degree 5 fitted here by weighted least squares to 1e-8 of q (1.2e-7 with
-// everything in fp32; erff and expf give 6e-8, in five times the operations: a step
-// on 16 x 32 x 32 channels, 128^2 took 82 us with them). |v| is cut off at 100 where
-// it multiplies a vanished tail: infinities stay what they are.
+// P of degree 5 fitted here by weighted least squares. Absolute errors of q: the fit below 1e-8,
+// with everything in fp32 1.4e-7 (erff and expf: 6e-8, in five times the operations: a step
+// on 16 x 32 x 32 channels, 128^2, fp32 took 82 us with them and 76 without). Relative to q the
+// fit is off by 6e-8 up to |v| = 1, 3e-6 up to 3, 2e-4 up to 5 and 4e-4 up to 6, which no
+// fp16 result shows; gelu_half() above (1e-6 of absolute error) is off by several fp16 steps from
+// -3 on and no faster in a training step (32 x 64 x 64 channels, 256^2: within 1 us of 535).
+// |v| is cut off at 100 where it multiplies a vanished tail: infinities stay what they are.
 __device__ __forceinline__ float normal_tail(float a, float e) {
   const float t = __builtin_amdgcn_rcpf(fmaf(0.39f, a, 1.0f));
   float p = fmaf(0.053847310403341085f, t, -0.2582449235385277f);

@@ -173,7 +173,7 @@ __global__ __launch_bounds__((MtGeom<OT, IT>::THREADS)) void fno_mix_save(MixTra
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
         const float v = z[e & 3][e >> 2] + bias + ad.get(e);
-        y[e] = a.act ? mt_gelu<DT_F32>(v) : v;
+        y[e] = a.act ? gelu_train(v) : v;
       }
       if (ok) {
         if (whole) store64(a.y, row * P + p0 + pb, lane, y);

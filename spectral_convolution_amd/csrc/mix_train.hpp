@@ -113,9 +113,6 @@ struct Code16 {
   __device__ __forceinline__ float get(int k, float step) const { return ck_value(q[k >> 2], k & 3, step); }
 };
 
-template <int DT>
-__device__ __forceinline__ float mt_gelu(float z) { return DT == DT_F32 ? gelu_train(z) : gelu_half_train(z); }
-
 // The workgroup's sums of gA (ga[it]: rows 16 ow + 4 (lane / 16) + j, columns
 // 16 it + lane % 16, ow = wave % OT) and gbias (gb, a lane's share of row
 // 16 ow + lane % 16) to the workspace, the WP pixel parts added through LDS

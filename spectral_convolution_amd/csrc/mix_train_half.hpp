@@ -262,7 +262,7 @@ __global__ __launch_bounds__((MhGeom<OT, IT, true>::THREADS)) void fno_mix_save_
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
         const float v = z[e >> 2][e & 3] + ad.get(e);
-        y[e] = a.act ? mt_gelu<DT>(v) : v;
+        y[e] = a.act ? gelu_train(v) : v;
       }
       if (ok) store16<DT>(a.y, row * P + p, whole ? 16 : P - p, y);
     }

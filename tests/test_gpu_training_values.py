@@ -49,3 +49,24 @@ def test_mix_slope_of_infinite_z(dtype, channels):
     assert (y[:, 0] == float("inf")).all() and (y[:, 1] == 0).all()
     assert torch.equal(gadd[:, 0], gy[:, 0]) and (gadd[:, 1] == 0).all()
     assert torch.isfinite(gx).all() and torch.isfinite(gbias).all()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_mix_gelu_of_every_storage_value(dtype):
+    """GELU of all storage values in [-8, 8] (z = add). The normal tail q is off by at most 1e-8 (its fit)
+    and about ten roundings, and v^2 / 2 carries two more into the exponential: |v| times that, and the
+    rounding of the result, bound the error, so a small GELU far out on the left keeps its digits."""
+    z = torch.arange(1 << 16, dtype=torch.int32).to(torch.int16).view(DT[dtype])
+    z = z[torch.isfinite(z) & (z.abs() <= 8)]
+    n = z.numel()
+    z64 = z.double()
+    ref = z64 * torch.special.ndtr(z64)
+    add = z.view(1, 1, n).to(DEV)
+    one = torch.zeros(1, 1, n, dtype=DT[dtype], device=DEV)
+    y, *_ = _run(one, torch.zeros(1, 1, dtype=DT[dtype], device=DEV), torch.zeros(1, dtype=DT[dtype], device=DEV), add,
+                 add.clone())
+    q = torch.special.ndtr(-z64.abs())
+    step = torch.finfo(DT[dtype]).eps / 2 * ref.abs() + (2.0 ** -25 if dtype == "f16" else 2.0 ** -134)
+    bound = step * (1 + 2.0 ** -10) + z64.abs() * (1e-8 + (10 + z64 ** 2) * 2.0 ** -24 * q) + 2.0 ** -24 * ref.abs()
+    off = (y.view(-1).cpu().double() - ref).abs()
+    assert (off <= bound).all(), f"over by {float((off / bound).max()):.3g} at {float(z64[(off / bound).argmax()])}"
