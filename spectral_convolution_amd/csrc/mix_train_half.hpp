@@ -2,12 +2,14 @@
 // (mix_train.hip has the operator and the shape of a tile). The three products
 // run on v_mfma_f32_16x16x32_{f16,bf16}: values read back from 8 bits are
 // exact in either type, weights and the forward's x are used as stored, and
-// gz = gy act'(z), an fp32 value, enters its two products as two 16-bit numbers,
-// the value and the remainder of its rounding, so gx and gA are as good as
-// from fp32 operands: one rounding of gz would show as large as that of the
-// results. fp16 has too little range for that as it stands: gz / 2 is taken
-// (|act'| < 1.13 would pass the type's largest) and the remainder times 2^11,
-// whose products have accumulators of their own, so a gz far below the smallest
+// gz = gy act'(z), an fp32 value, enters its two products as 16-bit pieces: gx and gA
+// are small where the gz of several channels or pixels cancel, and one rounding of gz would
+// show there. bf16: three pieces of 8 bits, which are all 24 (two left gx off by
+// 2^-17 of its terms; the backward of 32 x 64 x 64 channels, 256^2, takes 309 us with three,
+// 293 with two). They lie one after the other as further channels of the summed index.
+// fp16: two pieces, 22 bits. It has too little range for that as it stands: gz / 2 is
+// taken (|act'| < 1.13 would pass the type's largest) and the remainder of its rounding times
+// 2^11, whose products have accumulators of their own, so a gz far below the smallest
 // normal number keeps its digits (without it, gy around 2^-12 left gA off by 2^-13).
 //
 // LDS holds [channel][pixel] halves. A product that sums over channels reads
@@ -34,7 +36,13 @@ typedef __bf16 mt_b8 __attribute__((ext_vector_type(8)));
 template <int OT>
 constexpr int mh_waves(bool fwd) { return OT == 8 || (fwd && OT == 4) ? 8 : 4; }
 
-template <int OT, int IT, bool FWD>
+// pieces of gz, and the accumulators of a product with them
+template <int DT>
+constexpr int mh_pieces() { return DT == DT_F16 ? 2 : 3; }
+template <int DT>
+constexpr int mh_sums() { return DT == DT_F16 ? 2 : 1; }
+
+template <int DT, int OT, int IT, bool FWD>
 struct MhGeom {
   static constexpr int WAVES = mh_waves<OT>(FWD), THREADS = 64 * WAVES;
   static constexpr int PER_EU = OT * IT <= 16 && IT <= 2 * OT ? 3 : 2;
@@ -42,10 +50,12 @@ struct MhGeom {
   static constexpr int WI = IT < WAVES ? IT : WAVES, ITW = IT / WI;    // gx: waves over c_in; tiles of a wave
   static constexpr int KI = (IT + 1) / 2, KO = (OT + 1) / 2;              // 32-channel steps
   static constexpr int PT = 64 * WP, PITCH = PT + 4;                      // pixels of a tile; halves of an LDS row
-  static constexpr int XS = KI * 32 * PITCH * 2, GS = KO * 32 * PITCH * 2;
+  // gz in LDS: pieces, the rows of one and the 32-row steps of all (fp16's pieces share no step)
+  static constexpr int NP = mh_pieces<DT>(), ROWS = DT == DT_F16 ? KO * 32 : OT * 16, KS = (NP * ROWS + 31) / 32;
+  static constexpr int XS = KI * 32 * PITCH * 2, GS = KS * 32 * PITCH * 2;
   static constexpr int UNITS = IT * 16 * (PT / 16), NU = (UNITS + THREADS - 1) / THREADS;
   static constexpr int SUMS = WP > 1 ? WP * OT * 16 * (IT * 16 + 1) * 4 : 0;
-  static constexpr int LDS_FWD = 2 * XS, LDS_BWD = XS + 2 * GS > SUMS ? XS + 2 * GS : SUMS;
+  static constexpr int LDS_FWD = 2 * XS, LDS_BWD = XS + GS > SUMS ? XS + GS : SUMS;
 };
 
 template <int DT>
@@ -87,22 +97,22 @@ __device__ __forceinline__ void mh_write16(uint16_t *p, const ck_u32x4 &v) {
   reinterpret_cast<uint2 *>(p)[1] = make_uint2(v[2], v[3]);
 }
 
-// Weights as an operand: lane's column is `col`, the summed index the 32 of step k;
-// at(col, s) addresses A. The addresses are clamped and the values selected: with a
+// Weights as an operand: lane's column is `col`, the summed index the 32 of step k (DUP:
+// 16, twice); at(col, s) addresses A. The addresses are clamped and the values selected: with a
 // branch around each load, each is waited for before the next (5 us of a small call).
-template <typename F>
+template <bool DUP = false, typename F>
 __device__ __forceinline__ ck_u32x4 mh_weights(const uint16_t *A, int col, int ncol, int ns, int k, int lane, F at) {
   uint32_t h[8];
-  const int c = min(col, ncol - 1);
+  const int c = min(col, ncol - 1), last = DUP ? 15 : ~0;
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
-    const int s = 32 * k + mh_slot(lane >> 4, q >> 2) + (q & 3);
+    const int s = 32 * k + ((mh_slot(lane >> 4, q >> 2) + (q & 3)) & last);
     h[q] = A[at(c, min(s, ns - 1))];
   }
   ck_u32x4 r;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    const int s = 32 * k + mh_slot(lane >> 4, q >> 1) + 2 * (q & 1);
+    const int s = 32 * k + ((mh_slot(lane >> 4, q >> 1) + 2 * (q & 1)) & last);
     r[q] = (col < ncol && s < ns ? h[2 * q] : 0u) | (col < ncol && s + 1 < ns ? h[2 * q + 1] << 16 : 0u);
   }
   return r;
@@ -128,29 +138,30 @@ __device__ __forceinline__ uint2 mh_decode4(uint32_t q, float step) {
   }
 }
 
-// Two values as value and remainder; mh_join puts the products' sums together
+// Two values in pieces; mh_join puts the products' sums together
 template <int DT>
-constexpr int mh_sums() { return DT == DT_F16 ? 2 : 1; }
-
-template <int DT>
-__device__ __forceinline__ void mh_split(float a, float b, uint32_t &hi, uint32_t &lo) {
+__device__ __forceinline__ void mh_split(float a, float b, int e, uint32_t (&w)[mh_pieces<DT>()][8]) {
   if constexpr (DT == DT_F16) {
     half2_t h;
     h.x = (_Float16)(0.5f * a);
     h.y = (_Float16)(0.5f * b);
-    hi = __builtin_bit_cast(uint32_t, h);
-    lo = ck_pair<DT>(fmaf((float)h.x, -2048.f, 1024.f * a), fmaf((float)h.y, -2048.f, 1024.f * b));
+    w[0][e] = __builtin_bit_cast(uint32_t, h);
+    w[1][e] = ck_pair<DT>(fmaf((float)h.x, -2048.f, 1024.f * a), fmaf((float)h.y, -2048.f, 1024.f * b));
   } else {
-    const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
-    hi = __builtin_amdgcn_perm(ub, ua, 0x07060302u);
-    lo = ck_pair<DT>(a - __uint_as_float(ua & 0xffff0000u), b - __uint_as_float(ub & 0xffff0000u));
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {  // each the upper 8 bits of what is left, the last all of it
+      const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+      w[q][e] = __builtin_amdgcn_perm(ub, ua, 0x07060302u);
+      a -= __uint_as_float(ua & 0xffff0000u);
+      b -= __uint_as_float(ub & 0xffff0000u);
+    }
   }
 }
 
 template <int DT>
 __device__ __forceinline__ float mh_join(float hi, float lo) { return DT == DT_F16 ? fmaf(lo, 0x1p-10f, hi + hi) : hi; }
 
-// zero the LDS rows past the channels' tiles (half of a 32-channel step): never written again
+// zero the LDS rows past T tiles of 16 (half of the last of K 32-row steps): never written again
 template <int T, int K, int PITCH, int THREADS>
 __device__ __forceinline__ void mh_clear(uint16_t *s) {
   if constexpr (16 * T < 32 * K)
@@ -158,8 +169,8 @@ __device__ __forceinline__ void mh_clear(uint16_t *s) {
 }
 
 template <int DT, int OT, int IT>
-__global__ __launch_bounds__((MhGeom<OT, IT, true>::THREADS)) void fno_mix_save_half(MixTrainArgs a) {
-  using G = MhGeom<OT, IT, true>;
+__global__ __launch_bounds__((MhGeom<DT, OT, IT, true>::THREADS)) void fno_mix_save_half(MixTrainArgs a) {
+  using G = MhGeom<DT, OT, IT, true>;
   extern __shared__ float4 lds4[];
   uint16_t *xs0 = reinterpret_cast<uint16_t *>(lds4);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4, n = lane & 15;
@@ -270,18 +281,18 @@ __global__ __launch_bounds__((MhGeom<OT, IT, true>::THREADS)) void fno_mix_save_
 }
 
 template <int DT, int OT, int IT>
-__global__ __launch_bounds__((MhGeom<OT, IT, false>::THREADS))
-    __attribute__((amdgpu_waves_per_eu(MhGeom<OT, IT, false>::PER_EU))) void fno_mix_bwd_half(MixTrainArgs a) {
-  using G = MhGeom<OT, IT, false>;
+__global__ __launch_bounds__((MhGeom<DT, OT, IT, false>::THREADS))
+    __attribute__((amdgpu_waves_per_eu(MhGeom<DT, OT, IT, false>::PER_EU))) void fno_mix_bwd_half(MixTrainArgs a) {
+  using G = MhGeom<DT, OT, IT, false>;
   extern __shared__ float4 lds4[];
-  uint16_t *xs = reinterpret_cast<uint16_t *>(lds4), *gh = xs + G::XS / 2, *gl = gh + G::GS / 2;
+  uint16_t *xs = reinterpret_cast<uint16_t *>(lds4), *gs = xs + G::XS / 2;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4, n = lane & 15;
   const int ow = wave % G::WO, pb = 64 * (wave / G::WO), iw = wave % G::WI;
   const long P = a.P, nb = (P + kCkBlock - 1) / kCkBlock;
   const uint16_t *A = reinterpret_cast<const uint16_t *>(a.A);
   ck_u32x4 wf[G::KI], wt[G::ITW][G::KO];
   float bias, gb;
-  constexpr int NS = mh_sums<DT>();
+  constexpr int NP = G::NP, NS = mh_sums<DT>();
   v4f ga[NS][IT];
   {
     const int o = 16 * (ow) + n;
@@ -297,10 +308,14 @@ __global__ __launch_bounds__((MhGeom<OT, IT, false>::THREADS))
   for (int m = 0; m < G::ITW; ++m)
 #pragma unroll
     for (int k = 0; k < G::KO; ++k)
-      wt[m][k] = mh_weights(A, 16 * (iw + G::WI * m) + n, a.I, a.O, k, lane, [&](int c, int s) { return s * a.I + c; });
+      wt[m][k] = mh_weights<DT == DT_BF16 && OT == 1>(A, 16 * (iw + G::WI * m) + n, a.I, a.O, k, lane, [&](int c, int s) { return s * a.I + c; });
   mh_clear<IT, G::KI, G::PITCH, G::THREADS>(xs);
-  mh_clear<OT, G::KO, G::PITCH, G::THREADS>(gh);
-  mh_clear<OT, G::KO, G::PITCH, G::THREADS>(gl);
+  if constexpr (DT == DT_F16) {
+#pragma unroll
+    for (int q = 0; q < NP; ++q) mh_clear<OT, G::KO, G::PITCH, G::THREADS>(gs + q * G::ROWS * G::PITCH);
+  } else {
+    mh_clear<NP * OT, G::KS, G::PITCH, G::THREADS>(gs);
+  }
   const int t0 = blockIdx.x * a.per, t1 = min(a.tiles, t0 + a.per);
   // the next tile's codes of x and add and its gy, in flight over a whole tile's work
   Code16 xc[G::NU], nac;
@@ -375,27 +390,28 @@ __global__ __launch_bounds__((MhGeom<OT, IT, false>::THREADS))
           gz[e] *= gelu_slope(fmaf((float)(int8_t)(ac.q[e >> 2] >> (8 * (e & 3))), s, z[e >> 2][e & 3]));
       }
       if (a.gadd && o < a.O) store16<DT>(a.gadd, ((size_t)b * a.O + o) * P + p, whole ? 16 : P - p, gz);
-      uint32_t hi[8], lo[8];
+      uint32_t w[NP][8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) mh_split<DT>(gz[2 * e], gz[2 * e + 1], hi[e], lo[e]);
+      for (int e = 0; e < 8; ++e) mh_split<DT>(gz[2 * e], gz[2 * e + 1], e, w);
       const int at = (16 * (ow) + n) * G::PITCH + pb + 16 * g;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        reinterpret_cast<uint2 *>(gh + at)[q] = make_uint2(hi[2 * q], hi[2 * q + 1]);
-        reinterpret_cast<uint2 *>(gl + at)[q] = make_uint2(lo[2 * q], lo[2 * q + 1]);
-      }
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int c = 0; c < NP; ++c)
+          reinterpret_cast<uint2 *>(gs + c * G::ROWS * G::PITCH + at)[q] = make_uint2(w[c][2 * q], w[c][2 * q + 1]);
       if (a.part) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) gb += gz[e];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const ck_u32x4 h{hi[4 * k], hi[4 * k + 1], hi[4 * k + 2], hi[4 * k + 3]};
-          const ck_u32x4 l{lo[4 * k], lo[4 * k + 1], lo[4 * k + 2], lo[4 * k + 3]};
+          ck_u32x4 h[NP];
+#pragma unroll
+          for (int c = 0; c < NP; ++c) h[c] = ck_u32x4{w[c][4 * k], w[c][4 * k + 1], w[c][4 * k + 2], w[c][4 * k + 3]};
 #pragma unroll
           for (int it = 0; it < IT; ++it) {
             const ck_u32x4 xv = mh_read16(xs + (16 * it + n) * G::PITCH + pb + 16 * g + 8 * k);
-            ga[0][it] = mh_mma<DT>(h, xv, ga[0][it]);
-            ga[NS - 1][it] = mh_mma<DT>(l, xv, ga[NS - 1][it]);
+#pragma unroll
+            for (int c = 0; c < NP; ++c) ga[c % NS][it] = mh_mma<DT>(h[c], xv, ga[c % NS][it]);
           }
         }
       }
@@ -414,10 +430,11 @@ __global__ __launch_bounds__((MhGeom<OT, IT, false>::THREADS))
 #pragma unroll
           for (int k = 0; k < G::KO; ++k)
 #pragma unroll
-            for (int pt = 0; pt < 4; ++pt) {
-              acc[0][pt] = mh_mma<DT>(mh_pixels<G::PITCH>(gh, k, sb, pt, lane), wt[m][k], acc[0][pt]);
-              acc[NS - 1][pt] = mh_mma<DT>(mh_pixels<G::PITCH>(gl, k, sb, pt, lane), wt[m][k], acc[NS - 1][pt]);
-            }
+            for (int pt = 0; pt < 4; ++pt)
+#pragma unroll
+              for (int c = 0; c < G::KS / G::KO; ++c)  // the channels once more: the next piece of their gz
+                acc[c % NS][pt] = mh_mma<DT>(mh_pixels<G::PITCH>(gs + c * G::KO * 32 * G::PITCH, k, sb, pt, lane), wt[m][k],
+                                             acc[c % NS][pt]);
           float v[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) v[e] = mh_join<DT>(acc[0][e >> 2][e & 3], acc[NS - 1][e >> 2][e & 3]);
@@ -427,7 +444,7 @@ __global__ __launch_bounds__((MhGeom<OT, IT, false>::THREADS))
       }
     }
     // the next tile's channels overwrite xs, last read before the barrier above;
-    // its gz overwrite gh and gl only after the next barrier
+    // its gz overwrite gs only after the next barrier
   }
   if (!a.part) return;
 #pragma unroll
@@ -439,8 +456,8 @@ __global__ __launch_bounds__((MhGeom<OT, IT, false>::THREADS))
 
 template <int DT, int OT, int IT>
 MtPick mh_pick3() {
-  using F = MhGeom<OT, IT, true>;
-  using G = MhGeom<OT, IT, false>;
+  using F = MhGeom<DT, OT, IT, true>;
+  using G = MhGeom<DT, OT, IT, false>;
   constexpr int by_lds = 160 * 1024 / G::LDS_BWD, by_regs = 4 * G::PER_EU / G::WAVES;
   return {(const void *)fno_mix_save_half<DT, OT, IT>,
           (const void *)fno_mix_bwd_half<DT, OT, IT>,

@@ -70,3 +70,42 @@ def test_mix_gelu_of_every_storage_value(dtype):
     bound = step * (1 + 2.0 ** -10) + z64.abs() * (1e-8 + (10 + z64 ** 2) * 2.0 ** -24 * q) + 2.0 ** -24 * ref.abs()
     off = (y.view(-1).cpu().double() - ref).abs()
     assert (off <= bound).all(), f"over by {float((off / bound).max()):.3g} at {float(z64[(off / bound).argmax()])}"
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("channels", [2, 16, 24, 64, 100])
+def test_mix_gradients_that_cancel(dtype, channels):
+    """Pairs of output channels with opposite weights and nearly equal z: gx and gA are small differences of
+    gz, an fp32 value whatever the fields' type. Bounds: z is off by 2 2^-24 max(|z|, 1) and the derivative, of slope
+    at most 0.8, by 12 2^-24 more; a sum of c_out (or of all pixels') products adds a rounding of its
+    partial sums, at most the sizes' sum, for each of its steps in a row, fewer than 8; sizes at most |gy| 1.13."""
+    rng = np.random.default_rng(channels)
+    P, half = 192, channels // 2
+    t = lambda *s: torch.from_numpy(rng.standard_normal(s)).to(DT[dtype])  # noqa: E731
+    # add in steps of 2^-5, which 8 bits keep as every block's largest is 2; the partner's is a step off
+    add1 = (t(1, half, P).double() * 0.5).to(DT[dtype])
+    add1 = (torch.round(add1.double() * 32) / 32).to(DT[dtype])
+    add1[..., ::32] = 2.0
+    add1 = add1.clamp(-2, 2)
+    add2 = (add1.double() + 2.0 ** -5).clamp(-2, 2).to(DT[dtype])
+    add = torch.cat([add1, add2], 1)
+    A = torch.cat([torch.ones(half, 1), -torch.ones(half, 1)]).to(DT[dtype])
+    bias = torch.cat([torch.zeros(half), 2 * torch.ones(half)]).to(DT[dtype])  # with x = 1, z = 1 + add for both
+    gy = t(1, half, P)
+    gy = torch.cat([gy, gy], 1)
+    x = torch.ones(1, 1, P, dtype=DT[dtype])
+    _, gx, gA, gbias, gadd = _run(*(s.to(DEV) for s in (x, A, bias, add, gy)))
+    z = add.double() + 1
+    slope = torch.special.ndtr(z) + z * torch.exp(-z * z / 2) / np.sqrt(2 * np.pi)
+    gz = gy.double() * slope
+    want = (A.double()[None] * gz).sum(1, keepdim=True)
+    size = gy.double().abs()
+    assert float(want.abs().mean() / size.sum(1).mean()) < 0.05  # they do cancel
+    tol = ((0.8 * 2 * 3 + 12) * 2.0 ** -24 * size + 8 * 2.0 ** -24 * 1.13 * size).sum(1, keepdim=True)
+    half_step = torch.finfo(DT[dtype]).eps / 2
+    off = (gx.cpu().double() - want).abs() - half_step * (1 + 2.0 ** -10) * want.abs() - tol
+    assert (off <= 0).all(), f"gx over by {float(off.max()):.3g}, tolerance {float(tol.max()):.3g}"
+    sums = gz.sum(2)[0]
+    tol = ((0.8 * 2 * 3 + 12) * 2.0 ** -24 * size + 8 * 2.0 ** -24 * 1.13 * size).sum(2)[0]
+    off = (gA.cpu().double()[:, 0] - sums).abs() - half_step * (1 + 2.0 ** -10) * sums.abs() - tol
+    assert (off <= 0).all(), f"gA over by {float(off.max()):.3g}, tolerance {float(tol.max()):.3g}"
