@@ -8,13 +8,14 @@ check and marshal arguments, every value is computed in the library's kernels.
 import ctypes
 import functools
 
-from ._lib import DTYPES, NORM_KINDS, NormGradsStruct, NormParamsStruct, check, lib
+from ._lib import DTYPES, NORM_KINDS, SIGNATURES, NormGradsStruct, NormParamsStruct, check, lib
 
 _NORM_NAMES = ("w_post", "b_post", "gate", "scale", "w_pre", "b_pre")
 
 # A call on a small field takes a few microseconds on the GPU, so the checks on the
 # way there are few: the extension (csrc/binding.cpp) looks at all of a call's tensors at
 # once, and where one does not fit _ptr() or _buffer() find out what is wrong and say so.
+_INT_MAX = (1 << 31) - 1
 _torch = None
 _names = None
 _native = None
@@ -108,6 +109,8 @@ def _split(shape, name):
     P = 1
     for s in shape[2:]:
         P *= s
+    if shape[0] > _INT_MAX or shape[1] > _INT_MAX:  # ctypes would pass on the low 32 bits
+        raise ValueError(f"{name} shape {shape}: batch and channels must be below 2^31")
     return shape[0], shape[1], P
 
 
@@ -134,6 +137,9 @@ def _call(fn, dev, stream, *args):
 @functools.lru_cache(maxsize=1024)
 def _bytes(fn, *args):
     """A size that the library computes from a shape (a call asks for the same ones every time)."""
+    for v, t in zip(args, SIGNATURES[fn][1]):  # ctypes would pass on the low bits
+        if t(v).value != v:
+            raise ValueError(f"{fn}: {v} is out of the library's range")
     n = ctypes.c_size_t()
     check(getattr(lib(), fn)(*args, ctypes.byref(n)), fn)
     return n.value
