@@ -29,8 +29,8 @@ def _t():
         import torch
         try:
             from . import _native as native
-        except ImportError as e:
-            raise RuntimeError("_native.so not built (run python -m spectral_convolution_amd.build)") from e
+        except ImportError as e:  # not there, or built against another torch
+            raise RuntimeError(f"_native.so does not load: {e} (run python -m spectral_convolution_amd.build)") from e
         _names = {torch.float32: "f32", torch.float16: "f16", torch.bfloat16: "bf16"}
         _native, _torch = native, torch
     return _torch

@@ -7,10 +7,12 @@ Every HIP translation unit is compiled with packed-fp32 instructions disabled.
 """
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -52,10 +54,13 @@ def _compile(src, verbose):
 
 
 def _native(verbose):
-    """Compile the binding's own extension (host code against torch's headers)."""
-    import importlib.util
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
-    import sysconfig
+    """Compile the binding's own extension (host code against torch's headers).
+    Where torch is not installed the binding has no use either, and libfno.so needs neither."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        print("torch is not installed: _native.so, the extension of the Python binding, is not built", file=sys.stderr)
+        return
+    torch = os.path.dirname(spec.origin)
     tmp = NATIVE + ".tmp"
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
            "-I", os.path.join(torch, "include"), "-I", sysconfig.get_paths()["include"],
@@ -76,7 +81,6 @@ def build(verbose: bool = False, jobs: int = 8) -> str:
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
         native = ex.submit(_native, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
-        native.result()
     tmp = LIB + ".tmp"
     cmd = [_hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
     if verbose:
@@ -85,6 +89,7 @@ def build(verbose: bool = False, jobs: int = 8) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    native.result()  # its failure is reported once the library is there
     return LIB
 
 
