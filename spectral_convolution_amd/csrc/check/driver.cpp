@@ -18,6 +18,7 @@
 
 long check_launches();
 long check_reports();
+void *check_reserve(size_t n);
 
 namespace {
 
@@ -142,6 +143,15 @@ void run_checkpoint(long rows, long n, fno_dtype_t dt) {
   EXPECT(fno_checkpoint_unpack(s.p, x.p, rows, n, dt, nullptr) == FNO_OK);
 }
 
+// more values than the host could hold: nothing behind the buffers
+void run_checkpoint_far(long rows, long n, fno_dtype_t dt) {
+  size_t bytes = 0;
+  EXPECT(fno_checkpoint_bytes(rows, n, &bytes) == FNO_OK);
+  void *x = check_reserve((size_t)rows * n * es_of(dt)), *s = check_reserve(bytes);
+  EXPECT(fno_checkpoint_pack(x, s, rows, n, dt, nullptr) == FNO_OK);
+  EXPECT(fno_checkpoint_unpack(s, x, rows, n, dt, nullptr) == FNO_OK);
+}
+
 void run_norm(int B, int C, long P, int kind, bool params, fno_dtype_t dt) {
   const size_t es = es_of(dt), n = (size_t)B * C * P * es, nc = C * es;
   size_t sb = 0, wb = 0;
@@ -207,6 +217,9 @@ int main() {
   const long ck[][2] = {{1, 1}, {7, 31}, {96, 3721}, {5, 32}, {1280, 1000}, {3, 40000}};
   for (const auto &c : ck)
     for (fno_dtype_t dt : dts) run_checkpoint(c[0], c[1], dt);
+  const long far[][2] = {{1L << 33, 1}, {(1L << 32) + 7, 31}, {512, 1L << 31}, {1L << 40, 1}, {1L << 35, 32}};
+  for (const auto &c : far)
+    for (fno_dtype_t dt : dts) run_checkpoint_far(c[0], c[1], dt);
   struct N { int B, C; long P; };
   const N nn[] = {{2, 4, 256}, {1, 1, 2}, {3, 7, 33}, {1, 16, 1000}, {20, 64, 4096}, {3, 48, 3721}, {2, 65, 100},
                   {2, 130, 64}, {1, 256, 777}, {1, 512, 65}, {300, 8, 5}, {1, 1, 1}, {5, 64, 1}, {9, 257, 1},

@@ -46,6 +46,16 @@ void report(const char *launch, const char *what) {
 }  // namespace bounds
 }  // namespace fno
 
+// an allocation of that many bytes with no memory behind it, for buffers that only kernels would touch
+void *check_reserve(size_t n) {
+  static uintptr_t next = (uintptr_t)1 << 50;  // above every address of the process
+  std::lock_guard<std::mutex> g(mu);
+  void *p = reinterpret_cast<void *>(next);
+  live[next] = n;
+  next += (n + 511) / 256 * 256;
+  return p;
+}
+
 long check_launches() { return n_launch; }
 long check_reports() { return n_report; }
 
@@ -130,6 +140,8 @@ hipError_t hipGetSymbolAddress(void **ptr, const void *symbol) {
 hipError_t hipLaunchKernel(const void *, dim3 grid, dim3 block, void **, size_t lds, hipStream_t) {
   if (grid.x < 1 || grid.y < 1 || grid.z < 1 || block.x < 1 || block.x > 1024) return hipErrorInvalidConfiguration;
   if (lds > 160 * 1024) return hipErrorInvalidValue;
+  // the runtime takes fewer than 2^32 threads in a dimension, and 65536 workgroups in y and z
+  if ((uint64_t)grid.x * block.x >> 32 || grid.y > 65536 || grid.z > 65536) return hipErrorInvalidConfiguration;
   std::lock_guard<std::mutex> g(mu);
   ++n_launch;
   return hipSuccess;

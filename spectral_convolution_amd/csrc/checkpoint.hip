@@ -7,6 +7,8 @@
 // Bound by memory: the field plus 1 1/32 bytes a value, each moved once (84 M bf16
 // values: pack 50 us, unpack 38 us, 5.1 and 6.7 TB/s).
 
+#include <algorithm>
+
 #include "checkpoint.hpp"
 
 namespace fno {
@@ -14,6 +16,7 @@ namespace fno {
 namespace {
 constexpr int kCkThreads = 256;
 constexpr int kCkRuns = 4;  // runs of 256 units a workgroup handles
+constexpr long kCkRow = 1L << 22;  // workgroups in the grid's first dimension, which takes fewer than 2^32 threads
 }  // namespace
 
 // (row, unit in row) of unit base + local, base's row and remainder known
@@ -28,7 +31,7 @@ __device__ __forceinline__ void ck_place(long row0, uint32_t rem0, uint32_t upr,
 template <int DT, bool PACK>
 __global__ __launch_bounds__(kCkThreads) void fno_checkpoint(CkArgs a) {
   const uint32_t upr = (uint32_t)(4 * a.nb);  // units per row
-  const long base = (long)blockIdx.x * (kCkThreads * kCkRuns), total = a.rows * (long)upr;
+  const long base = ((long)blockIdx.y * kCkRow + blockIdx.x) * (kCkThreads * kCkRuns), total = a.rows * (long)upr;
   const long row0 = base / upr;
   const uint32_t rem0 = (uint32_t)(base - row0 * upr);
 #pragma unroll
@@ -76,7 +79,8 @@ __global__ __launch_bounds__(kCkThreads) void fno_checkpoint(CkArgs a) {
 hipError_t launch_checkpoint(const CkArgs &a, bool pack, int dtype, hipStream_t s) {
   FNO_BOUNDS(check_checkpoint(a, pack, dtype);)
   const long total = a.rows * 4 * a.nb, per = kCkThreads * kCkRuns;
-  const dim3 grid((unsigned)((total + per - 1) / per));
+  const long groups = (total + per - 1) / per;
+  const dim3 grid((unsigned)std::min(groups, kCkRow), (unsigned)((groups + kCkRow - 1) / kCkRow));
   CkArgs arg = a;
   void *args[] = {(void *)&arg};
   const void *k;
