@@ -360,9 +360,10 @@ __global__ __launch_bounds__(tok_threads<NT>()) __attribute__((amdgpu_waves_per_
       float gg[V], gv[V];
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float vh = (ck_get<DT>(vr[j], e) - m) * r, gs = y[j][e] * ck_get<DT>(sc, e), wv = ck_get<DT>(w, e);
-        gg[e] = gs * fmaf(vh, wv, ck_get<DT>(bp, e));
-        float g = fmaf(-vh, hv, gs * (ck_get<DT>(gr[j], e) * wv));
+        const float vh = (ck_get<DT>(vr[j], e) - m) * r, s = ck_get<DT>(sc, e), wv = ck_get<DT>(w, e);
+        gg[e] = y[j][e] * s * fmaf(vh, wv, ck_get<DT>(bp, e));
+        // h rounded as in its mean above: over one channel the two are then equal and gv is 0
+        float g = fmaf(-vh, hv, y[j][e] * (s * ck_get<DT>(gr[j], e) * wv));
         if (KIND == kLayer) g -= mh;
         gv[e] = r * g;
       }
