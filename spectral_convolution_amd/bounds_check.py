@@ -63,10 +63,11 @@ def build(jobs: int = 4) -> str:
     return prog
 
 
-def run(prog: str, timeout: float = 600.0) -> subprocess.CompletedProcess:
+def run(prog: str, timeout: float = 600.0, args=(), calls: str = "") -> subprocess.CompletedProcess:
+    """Run the program; args and calls (its standard input) as csrc/check/driver.cpp says."""
     env = dict(os.environ, ASAN_OPTIONS="detect_leaks=0:allocator_may_return_null=1",
                UBSAN_OPTIONS="print_stacktrace=1")
-    return subprocess.run([prog], capture_output=True, text=True, timeout=timeout, env=env)
+    return subprocess.run([prog, *args], input=calls, capture_output=True, text=True, timeout=timeout, env=env)
 
 
 if __name__ == "__main__":

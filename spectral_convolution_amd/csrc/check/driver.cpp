@@ -5,7 +5,11 @@
 // allocation-free entry, the FNO block, the full FNO2d network and the
 // training operators around a block). Each launch is checked by its launcher's
 // bounds hook against the recording runtime's allocations; the program exits
-// non-zero if any span or assumption was broken. Host code only.
+// non-zero if any span or assumption was broken. With the argument `kernels` it
+// prints the kernels of the library, with `trace` the launches (kernel | grid x, y, workgroup) of the training
+// operators' calls that standard input lists, a line each:
+//   norm DTYPE KIND BATCH CHANNELS PIXELS  |  mix DTYPE BATCH C_IN C_OUT PIXELS ACT ADD  |  checkpoint DTYPE ROWS N
+// Host code only.
 
 #include <hip/hip_runtime.h>
 
@@ -19,6 +23,8 @@
 long check_launches();
 long check_reports();
 void *check_reserve(size_t n);
+void check_trace(bool on);
+void check_list_kernels();
 
 namespace {
 
@@ -188,9 +194,60 @@ void run_mix(int B, int I, int O, long P, int act, bool add, fno_dtype_t dt) {
                                         P, act, add, dt, nullptr) == FNO_OK);
 }
 
+void trace_calls() {
+  char op[16];
+  int dt, B;
+  check_trace(true);
+  while (std::scanf("%15s %d %d", op, &dt, &B) == 3) {
+    const auto d = (fno_dtype_t)dt;
+    const size_t es = es_of(d);
+    size_t sb = 0, wb = 0;
+    auto far = [](size_t n) { return check_reserve(n); };
+    if (!std::strcmp(op, "norm")) {
+      const int kind = B;
+      int C;
+      long P;
+      EXPECT(std::scanf("%d %d %ld", &B, &C, &P) == 3);
+      EXPECT(fno_norm_residual_saved_bytes(B, C, P, &sb) == FNO_OK);
+      EXPECT(fno_norm_residual_workspace_bytes(B, C, P, d, &wb) == FNO_OK);
+      const size_t n = (size_t)B * C * P * es;
+      fno_norm_params_t p{kind, 1e-5f, far(C * es), far(C * es), far((size_t)B * C * es), far(C * es), far(C * es), far(C * es)};
+      fno_norm_grads_t g{far(C * es), far(C * es), far((size_t)B * C * es), far(C * es), far(C * es), far(C * es)};
+      void *saved = far(sb);
+      EXPECT(fno_norm_residual_save(&p, far(n), far(n), far(n), far(n), saved, B, C, P, d, nullptr) == FNO_OK);
+      EXPECT(fno_norm_residual_backward_saved(&p, saved, far(n), far(n), far(n), far(n), &g, far(wb), B, C, P, d, nullptr) ==
+             FNO_OK);
+    } else if (!std::strcmp(op, "mix")) {
+      int I, O, act, add;
+      long P;
+      EXPECT(std::scanf("%d %d %ld %d %d", &I, &O, &P, &act, &add) == 5);
+      EXPECT(fno_channel_mix_saved_bytes(B, I, O, P, act, add, &sb) == FNO_OK);
+      EXPECT(fno_channel_mix_workspace_bytes(B, I, O, P, d, &wb) == FNO_OK);
+      const size_t nx = (size_t)B * I * P * es, ny = (size_t)B * O * P * es, na = (size_t)O * I * es;
+      void *saved = far(sb), *A = far(na), *bias = far(O * es);
+      EXPECT(fno_channel_mix_save(far(nx), A, bias, add ? far(ny) : nullptr, far(ny), saved, B, I, O, P, act, d, nullptr) ==
+             FNO_OK);
+      EXPECT(fno_channel_mix_backward_saved(saved, A, bias, far(ny), far(nx), far(na), far(O * es), add ? far(ny) : nullptr,
+                                            far(wb), B, I, O, P, act, add, d, nullptr) == FNO_OK);
+    } else {
+      long n;
+      EXPECT(std::scanf("%ld", &n) == 1);
+      run_checkpoint_far(B, n, d);
+    }
+  }
+}
+
 }  // namespace
 
-int main() {
+int main(int argc, char **argv) {
+  if (argc > 1 && !std::strcmp(argv[1], "kernels")) {
+    check_list_kernels();
+    return 0;
+  }
+  if (argc > 1 && !std::strcmp(argv[1], "trace")) {
+    trace_calls();
+    return check_reports() == 0 && n_fail == 0 ? 0 : 1;
+  }
   const fno_dtype_t dts[3] = {FNO_F32, FNO_F16, FNO_BF16};
   // 2D: matrix-core planes (64 .. 256) and the VALU planes (small and
   // non-power-of-two grids), ragged and maximal modes, small and large batches

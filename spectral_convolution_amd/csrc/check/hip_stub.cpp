@@ -7,11 +7,14 @@
 
 #include <hip/hip_runtime.h>
 
+#include <cxxabi.h>
+
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
 #include <map>
 #include <mutex>
+#include <string>
 
 #include "../../../include/fno.h"
 #include "../common.hpp"
@@ -21,6 +24,20 @@ namespace {
 std::mutex mu;
 std::map<uintptr_t, size_t> live;  // base -> bytes
 long n_launch = 0, n_report = 0;
+bool trace = false;  // print each launch's kernel, grid and workgroup
+
+// host stub -> kernel name; filled by the objects' constructors, so made on first use
+std::map<const void *, std::string> &kernels() {
+  static std::map<const void *, std::string> m;
+  return m;
+}
+std::string plain(const std::string &name) {
+  int st = 0;
+  char *d = abi::__cxa_demangle(name.c_str(), nullptr, nullptr, &st);
+  const std::string r = st == 0 && d ? d : name;
+  std::free(d);
+  return r;
+}
 
 }  // namespace
 
@@ -56,6 +73,10 @@ void *check_reserve(size_t n) {
   return p;
 }
 
+void check_trace(bool on) { trace = on; }
+void check_list_kernels() {
+  for (const auto &k : kernels()) std::printf("%s\n", plain(k.second).c_str());
+}
 long check_launches() { return n_launch; }
 long check_reports() { return n_report; }
 
@@ -137,13 +158,14 @@ hipError_t hipGetSymbolAddress(void **ptr, const void *symbol) {
   return hipSuccess;
 }
 
-hipError_t hipLaunchKernel(const void *, dim3 grid, dim3 block, void **, size_t lds, hipStream_t) {
+hipError_t hipLaunchKernel(const void *f, dim3 grid, dim3 block, void **, size_t lds, hipStream_t) {
   if (grid.x < 1 || grid.y < 1 || grid.z < 1 || block.x < 1 || block.x > 1024) return hipErrorInvalidConfiguration;
   if (lds > 160 * 1024) return hipErrorInvalidValue;
   // the runtime takes fewer than 2^32 threads in a dimension, and 65536 workgroups in y and z
   if ((uint64_t)grid.x * block.x >> 32 || grid.y > 65536 || grid.z > 65536) return hipErrorInvalidConfiguration;
   std::lock_guard<std::mutex> g(mu);
   ++n_launch;
+  if (trace) std::printf("%s | %u %u %u\n", plain(kernels()[f]).c_str(), grid.x, grid.y, block.x);
   return hipSuccess;
 }
 
@@ -185,8 +207,10 @@ void **__hipRegisterFatBinary(const void *) {
   return &h;
 }
 void __hipUnregisterFatBinary(void **) {}
-void __hipRegisterFunction(void **, const void *, char *, const char *, unsigned int, void *, void *, void *, void *,
-                           int *) {}
+void __hipRegisterFunction(void **, const void *host, char *, const char *name, unsigned int, void *, void *, void *,
+                           void *, int *) {
+  kernels()[host] = name;
+}
 void __hipRegisterVar(void **, void *, char *, const char *, int, size_t, int, int) {}
 
 // the <<<...>>> configuration, handed from the push to the generated stub's pop
