@@ -59,8 +59,8 @@ void check_lift_fold(const void *P, const void *p, const void *w, const void *Wb
 void check_block_rows(const void *zg, const void *zexp, const void *tb, const void *x, const void *wb,
                       const void *bias, const void *y, int B, int Ci, int Co, int H, int W, int NN, int dtype);
 void check_checkpoint(const CkArgs &a, bool pack, int dtype);
-void check_mix_train(const MixTrainArgs &a, bool fwd, int S, size_t lds, int dtype);
-void check_norm(const NormArgs &a, bool fwd, int S, int dtype);
+void check_mix_train(const MixTrainArgs &a, bool fwd, int S, size_t lds, int dtype, int pt, int threads);
+void check_norm(const NormArgs &a, bool fwd, int S, int dtype, int threads, int rpg, size_t lds, int wide, int deep);
 
 }  // namespace fno
 

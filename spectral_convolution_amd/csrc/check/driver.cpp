@@ -15,6 +15,7 @@
 
 #include <cstdio>
 #include <cstring>
+#include <string>
 #include <vector>
 
 #include "../../../include/fno.h"
@@ -194,46 +195,47 @@ void run_mix(int B, int I, int O, long P, int act, bool add, fno_dtype_t dt) {
                                         P, act, add, dt, nullptr) == FNO_OK);
 }
 
+// one call of a training operator, forward and backward, with nothing behind its buffers
+void trace_call(const std::string &op, int dt, const std::vector<long> &v) {
+  const auto d = (fno_dtype_t)dt;
+  const size_t es = es_of(d);
+  size_t sb = 0, wb = 0;
+  auto far = [](size_t n) { return check_reserve(n); };
+  if (op == "norm") {
+    const int kind = (int)v[0], B = (int)v[1], C = (int)v[2];
+    const long P = v[3];
+    EXPECT(fno_norm_residual_saved_bytes(B, C, P, &sb) == FNO_OK);
+    EXPECT(fno_norm_residual_workspace_bytes(B, C, P, d, &wb) == FNO_OK);
+    const size_t n = (size_t)B * C * P * es, nc = C * es, ng = (size_t)B * nc;
+    const fno_norm_params_t p{kind, 1e-5f, far(nc), far(nc), far(ng), far(nc), far(nc), far(nc)};
+    const fno_norm_grads_t g{far(nc), far(nc), far(ng), far(nc), far(nc), far(nc)};
+    void *saved = far(sb);
+    EXPECT(fno_norm_residual_save(&p, far(n), far(n), far(n), far(n), saved, B, C, P, d, nullptr) == FNO_OK);
+    EXPECT(fno_norm_residual_backward_saved(&p, saved, far(n), far(n), far(n), far(n), &g, far(wb), B, C, P, d, nullptr) == FNO_OK);
+  } else if (op == "mix") {
+    const int B = (int)v[0], I = (int)v[1], O = (int)v[2], act = (int)v[4], add = (int)v[5];
+    const long P = v[3];
+    EXPECT(fno_channel_mix_saved_bytes(B, I, O, P, act, add, &sb) == FNO_OK);
+    EXPECT(fno_channel_mix_workspace_bytes(B, I, O, P, d, &wb) == FNO_OK);
+    const size_t nx = (size_t)B * I * P * es, ny = (size_t)B * O * P * es, na = (size_t)O * I * es;
+    void *saved = far(sb), *A = far(na), *bias = far(O * es);
+    EXPECT(fno_channel_mix_save(far(nx), A, bias, add ? far(ny) : nullptr, far(ny), saved, B, I, O, P, act, d, nullptr) == FNO_OK);
+    EXPECT(fno_channel_mix_backward_saved(saved, A, bias, far(ny), far(nx), far(na), far(O * es), add ? far(ny) : nullptr,
+                                          far(wb), B, I, O, P, act, add, d, nullptr) == FNO_OK);
+  } else {
+    run_checkpoint_far(v[0], v[1], d);
+  }
+}
+
 void trace_calls() {
-  char op[16];
-  int dt, B;
   check_trace(true);
-  while (std::scanf("%15s %d %d", op, &dt, &B) == 3) {
-    const auto d = (fno_dtype_t)dt;
-    const size_t es = es_of(d);
-    size_t sb = 0, wb = 0;
-    auto far = [](size_t n) { return check_reserve(n); };
-    if (!std::strcmp(op, "norm")) {
-      const int kind = B;
-      int C;
-      long P;
-      EXPECT(std::scanf("%d %d %ld", &B, &C, &P) == 3);
-      EXPECT(fno_norm_residual_saved_bytes(B, C, P, &sb) == FNO_OK);
-      EXPECT(fno_norm_residual_workspace_bytes(B, C, P, d, &wb) == FNO_OK);
-      const size_t n = (size_t)B * C * P * es;
-      fno_norm_params_t p{kind, 1e-5f, far(C * es), far(C * es), far((size_t)B * C * es), far(C * es), far(C * es), far(C * es)};
-      fno_norm_grads_t g{far(C * es), far(C * es), far((size_t)B * C * es), far(C * es), far(C * es), far(C * es)};
-      void *saved = far(sb);
-      EXPECT(fno_norm_residual_save(&p, far(n), far(n), far(n), far(n), saved, B, C, P, d, nullptr) == FNO_OK);
-      EXPECT(fno_norm_residual_backward_saved(&p, saved, far(n), far(n), far(n), far(n), &g, far(wb), B, C, P, d, nullptr) ==
-             FNO_OK);
-    } else if (!std::strcmp(op, "mix")) {
-      int I, O, act, add;
-      long P;
-      EXPECT(std::scanf("%d %d %ld %d %d", &I, &O, &P, &act, &add) == 5);
-      EXPECT(fno_channel_mix_saved_bytes(B, I, O, P, act, add, &sb) == FNO_OK);
-      EXPECT(fno_channel_mix_workspace_bytes(B, I, O, P, d, &wb) == FNO_OK);
-      const size_t nx = (size_t)B * I * P * es, ny = (size_t)B * O * P * es, na = (size_t)O * I * es;
-      void *saved = far(sb), *A = far(na), *bias = far(O * es);
-      EXPECT(fno_channel_mix_save(far(nx), A, bias, add ? far(ny) : nullptr, far(ny), saved, B, I, O, P, act, d, nullptr) ==
-             FNO_OK);
-      EXPECT(fno_channel_mix_backward_saved(saved, A, bias, far(ny), far(nx), far(na), far(O * es), add ? far(ny) : nullptr,
-                                            far(wb), B, I, O, P, act, add, d, nullptr) == FNO_OK);
-    } else {
-      long n;
-      EXPECT(std::scanf("%ld", &n) == 1);
-      run_checkpoint_far(B, n, d);
-    }
+  char op[16];
+  int dt;
+  while (std::scanf("%15s %d", op, &dt) == 2) {
+    const std::string name = op;
+    std::vector<long> v(name == "norm" ? 4 : name == "mix" ? 6 : 2);
+    for (long &x : v) EXPECT(std::scanf("%ld", &x) == 1);
+    trace_call(name, dt, v);
   }
 }
 
@@ -284,12 +286,23 @@ int main(int argc, char **argv) {
   for (const N &c : nn)
     for (fno_dtype_t dt : dts)
       for (int kind = 0; kind < 2; ++kind) run_norm(c.B, c.C, c.P, kind, kind == 0 || c.C != 64, dt);
+  // the largest rows and batches the header allows: nothing behind the buffers
+  const N nf[] = {{1, 512, fno::kNormMaxPixels}, {65535, 100, 70}, {65535, 512, 31}, {4, 64, fno::kNormMaxPixels - 5}, {3, 9, (1L << 27) - 31},
+                  {2000000000, 64, 1}, {134217728, 8192, 1}, {65535, 256, 65536}};
+  for (const N &c : nf)
+    for (int dt = 0; dt < 3; ++dt)
+      for (int kind = 0; kind < 2; ++kind) trace_call("norm", dt, {kind, c.B, c.C, c.P});
   struct M { int B, I, O; long P; };
   const M mm[] = {{2, 4, 4, 256}, {1, 1, 1, 1}, {3, 5, 70, 33}, {2, 40, 72, 1001}, {1, 64, 64, 4096}, {1, 128, 128, 300},
                   {2, 128, 3, 100}, {1, 17, 33, 7}, {4, 32, 32, 1024}, {70, 8, 16, 500}};
   for (const M &c : mm)
     for (fno_dtype_t dt : dts)
       for (int k = 0; k < 4; ++k) run_mix(c.B, c.I, c.O, c.P, k & 1, (k & 2) != 0, dt);
+  const M mf[] = {{1, 128, 128, fno::kMixTrainPixels}, {1024, 128, 128, fno::kMixTrainPixels}, {1 << 30, 3, 5, 64}, {1 << 29, 128, 128, 65},
+                  {7, 33, 20, fno::kMixTrainPixels - 3}};
+  for (const M &c : mf)
+    for (int dt = 0; dt < 3; ++dt)
+      for (int k = 0; k < 4; ++k) trace_call("mix", dt, {c.B, c.I, c.O, c.P, k & 1, k >> 1});
   const long reports = check_reports();
   // the checker itself: spans past the end of a buffer must be reported
   {
@@ -302,6 +315,30 @@ int main(int argc, char **argv) {
     EXPECT(check_reports() == before + 1);
     fno::check_channel_mix(x.p, A.p, nullptr, nullptr, y.p, 1, 1, 5, 16, fno::DT_F16);  // A and y a row short
     EXPECT(check_reports() == before + 3);
+  }
+  {
+    std::fprintf(stderr, "self-test: a norm's planted mistakes follow\n");
+    const size_t n = (size_t)2 * 20 * 100 * 4;
+    fno::NormArgs a{};
+    a.eps = 1e-5f, a.B = 2, a.C = 20, a.P = 100, a.per = 4;
+    a.x = check_reserve(n), a.v = check_reserve(n), a.y = check_reserve(n);
+    long before = check_reports();
+    auto more = [&](long k) {
+      const bool hit = check_reports() - before >= (k ? 1 : 0) && (k || check_reports() == before);
+      before = check_reports();
+      return hit;
+    };
+    fno::check_norm(a, true, 1, fno::DT_F32, 256, 4, 0, 1, 3);  // as launched
+    EXPECT(more(0));
+    fno::check_norm(a, true, 1, fno::DT_F32, 256, 4, 0, 1, 2);  // a group of channels short
+    EXPECT(more(1));
+    fno::check_norm(a, true, 1, fno::DT_F32, 256, 4, 0, 1, 4);  // a group that has no channel
+    EXPECT(more(1));
+    fno::check_norm(a, true, 1, fno::DT_F16, 256, 4, 0, 2, 2);  // waves that are not there
+    EXPECT(more(1));
+    a.per = 2;
+    fno::check_norm(a, true, 1, fno::DT_F32, 256, 4, 0, 1, 3);  // tiles left out
+    EXPECT(more(1));
   }
   std::printf("launches checked: %ld, bounds reports: %ld, driver failures: %d\n", check_launches(), reports,
               n_fail);

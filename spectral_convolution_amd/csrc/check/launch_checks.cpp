@@ -5,6 +5,7 @@
 
 #include "../plane_mfma.hpp"
 
+#include <algorithm>
 #include <cstdio>
 
 namespace fno {
@@ -342,9 +343,71 @@ void check_checkpoint(const CkArgs &a, bool pack, int dtype) {
   c.need("blocks cover the row", a.nb == (a.n + 31) / 32);
   c.need("codes 8-byte aligned", ((uintptr_t)a.codes & 7) == 0);
   c.need("units of a row in 32 bits", 4 * a.nb + 1024 < (1L << 32));
+  // the units of the first and last workgroups, placed as ck_place() does
+  const long upr = 4 * a.nb, total = a.rows * upr, groups = (total + 1023) / 1024;
+  for (long g : {0L, 1L, groups / 2, groups - 2, groups - 1}) {
+    if (g < 0 || g >= groups) continue;
+    const long base = g * 1024, row0 = base / upr;
+    const uint32_t rem0 = (uint32_t)(base - row0 * upr);
+    for (uint32_t local : {0u, 3u, 255u, 256u, 1020u, 1023u}) {
+      if (base + local >= total) continue;
+      const uint32_t v = rem0 + local, d = upr > 1024 ? (v >= upr ? 1u : 0u) : v / (uint32_t)upr;
+      const long row = row0 + d, u = v - (uint32_t)(d * upr);
+      c.need("unit in its row", row < a.rows && u < upr && row * upr + u == base + local);
+    }
+  }
 }
 
-void check_norm(const NormArgs &a, bool fwd, int S, int dtype) {
+namespace {
+
+// The accesses of a norm on a field, as FieldTile forms them: uniform offsets of a wave's first and last groups and a
+// 32-bit offset a lane; the last tile's loads shifted back to end with the row.
+void norm_field_tiles(const Ctx &c, const NormArgs &a, int dtype, int W, int CPT) {
+  const long V = dtype == DT_F32 ? 4 : 8, ES = dtype == DT_F32 ? 4 : 2, PX = 8 * V, P = a.P, nb = (P + 31) / 32;
+  const long nt = (P + PX - 1) / PX;
+  bool in_row = true, wide = true, ends = true, codes = true, exists = true;
+  for (long b : {0L, (long)a.B - 1})
+    for (int w = 0; w < W; ++w)
+      for (int lane = 0; lane < 64; ++lane) {
+        const int cl = lane >> 3, pl = lane & 7, g = (CPT - 1) * W + w, last = std::min(g, (a.C - 1) / 8);
+        const int clast = std::min(cl, a.C - 1 - 8 * last);
+        const uint32_t off = (uint32_t)cl * (uint32_t)P * ES + 16u * pl, off_last = (uint32_t)clast * (uint32_t)P * ES + 16u * pl;
+        const uint32_t code = (uint32_t)cl * (uint32_t)nb * 32 + (uint32_t)V * pl;
+        const uint32_t code_last = (uint32_t)clast * (uint32_t)nb * 32 + (uint32_t)V * pl;
+        wide = wide && off == cl * P * ES + 16 * pl && code == cl * nb * 32 + V * pl && (uint64_t)off + 32 < 1ull << 32;
+        for (int k = 0; k < CPT; ++k) {
+          const bool inner = k < CPT - 1;
+          const long row = b * a.C + (inner ? 8 * (w + k * W) + cl : 8 * last + clast);  // where the access belongs
+          exists = exists && row < (b + 1) * a.C;
+          const long base = inner ? b * a.C + 8 * w + 8L * k * W : b * a.C + 8 * last;
+          for (long t : {0L, nt - 2, nt - 1}) {
+            if (t < 0) continue;
+            const long f = (base * P + t * PX) * ES + (inner ? off : off_last), n = P - (t * PX + pl * V);
+            if ((t + 1) * PX <= P) {
+              in_row = in_row && f >= row * P * ES && f + 16 <= (row + 1) * P * ES;
+            } else if (P < V) {  // by the element
+              ends = ends && (n <= 0 || (f >= row * P * ES && f + std::min(n, V) * ES <= (row + 1) * P * ES));
+            } else {
+              const long at = f - std::max(0L, V - n) * ES;
+              ends = ends && at >= row * P * ES && at + 16 <= (row + 1) * P * ES;
+            }
+            if (t * PX + pl * V < nb * 32) {
+              const long q = base * nb * 32 + t * PX + (inner ? code : code_last);
+              codes = codes && q >= row * nb * 32 && q + V <= (row + 1) * nb * 32;
+            }
+          }
+        }
+      }
+  c.need("channels of a wave's groups exist", exists);
+  c.need("lane offsets in 32 bits", wide);
+  c.need("whole tiles inside their rows", in_row);
+  c.need("last tile's accesses inside their rows", ends);
+  c.need("codes inside their rows", codes);
+}
+
+}  // namespace
+
+void check_norm(const NormArgs &a, bool fwd, int S, int dtype, int threads, int rpg, size_t lds, int wide, int deep) {
   const Ctx c{fwd ? "fno_norm_fwd" : "fno_norm_bwd"};
   const size_t es = es_of(dtype), n = (size_t)a.B * a.C * a.P * es, nc = (size_t)a.C * es, ng = (size_t)a.B * nc;
   auto opt = [&](const char *what, const void *p, size_t bytes) {
@@ -385,9 +448,23 @@ void check_norm(const NormArgs &a, bool fwd, int S, int dtype) {
     opt("runs' sums", a.part, (size_t)4 * a.C * S * (a.P == 1 ? 1 : a.B) * 4);
   }
   c.need("channels held by a workgroup", a.C >= 1 && a.C <= (a.P == 1 ? kNormMaxToken : kNormMaxField));
+  const long V = dtype == DT_F32 ? 4 : 8;
+  if (a.P == 1) {
+    c.need("a row's threads and pieces hold its channels", (long)wide * deep * V >= a.C);
+    c.need("whole rows a workgroup", threads == wide * rpg && (wide == 64 || rpg == 1));
+    c.need("parameters' LDS", lds == (fwd ? 0 : (size_t)4 * 16 * deep * wide) && lds <= kLdsMax);
+    c.need("every workgroup has a row", S >= 1 && (long)(S - 1) * rpg < a.B);
+  } else {
+    const long nt = (a.P + 8 * V - 1) / (8 * V);
+    c.need("groups of channels: only a wave's last may be empty", 8 * wide * deep >= a.C && 8 * wide * (deep - 1) < a.C);
+    c.need("waves of a workgroup", threads == 64 * wide * rpg && (wide == 1 ? rpg == 4 : rpg == 1));
+    c.need("runs cover the tiles", a.per >= 1 && a.per % rpg == 0 && (long)S * a.per >= nt && (long)(S - 1) * a.per < nt);
+    c.need("rows short enough for lane offsets, samples for the grid", a.P <= kNormMaxPixels && a.B <= 65535);
+    norm_field_tiles(c, a, dtype, wide, deep);
+  }
 }
 
-void check_mix_train(const MixTrainArgs &a, bool fwd, int S, size_t lds, int dtype) {
+void check_mix_train(const MixTrainArgs &a, bool fwd, int S, size_t lds, int dtype, int pt, int threads) {
   const Ctx c{fwd ? "fno_mix_save" : "fno_mix_bwd"};
   const size_t es = es_of(dtype), nx = (size_t)a.B * a.I * a.P * es, ny = (size_t)a.B * a.O * a.P * es;
   const size_t nb = (a.P + 31) / 32, na = (size_t)a.O * a.I;
@@ -416,6 +493,27 @@ void check_mix_train(const MixTrainArgs &a, bool fwd, int S, size_t lds, int dty
   }
   c.need("1 <= channels <= 128", a.I >= 1 && a.I <= kMixTrainMax && a.O >= 1 && a.O <= kMixTrainMax);
   c.need("LDS at most 160 KiB", lds <= kLdsMax);
+  // tiles of 64 pixels for each wave beside those of the output channels
+  auto pow2 = [](int ch) { return ch <= 16 ? 1 : ch <= 32 ? 2 : ch <= 64 ? 4 : 8; };
+  const int OT = pow2(a.O), IT = pow2(a.I);
+  c.need("waves over channels and pixels", threads % (64 * OT) == 0 && pt == threads / OT);
+  c.need("tiles counted in 32 bits", (long)a.B * ((a.P + pt - 1) / pt) == a.tiles && a.tpb == (a.P + pt - 1) / pt);
+  c.need("runs cover the tiles", a.per >= 1 && (long)S * a.per >= a.tiles && (long)(S - 1) * a.per < a.tiles);
+  // LDS: a row of a tile for each channel of x; in the backward also gz's, and at the end the sums
+  const size_t px = dtype == DT_F32 ? 4 : 2, pitch = pt + 4, xs = 16 * IT * pitch * px, gz = 16 * OT * pitch * px;
+  const size_t pieces = dtype == DT_F32 ? 1 : dtype == DT_F16 ? 2 : 3;
+  c.need("LDS of a tile", lds >= (fwd ? xs : xs + pieces * gz));
+  if (!fwd && pt > 64) c.need("LDS of the sums", lds >= (size_t)pt / 64 * 16 * OT * (16 * IT + 1) * 4);
+  // a lane's 16 pixels of the first and last tiles: whole ones inside the row, others cut off at its end
+  bool fields = true, codes = true;
+  for (long t : {0L, (long)a.tpb - 2, (long)a.tpb - 1})
+    for (int p = 0; t >= 0 && p < pt; p += 16) {
+      const long p0 = t * pt, at = p0 + p;
+      fields = fields && (p0 + pt <= a.P ? at + 16 <= a.P : at >= 0);
+      codes = codes && (at >= (long)nb * 32 || at + 16 <= (long)nb * 32);
+    }
+  c.need("a whole tile's pixels inside the row", fields);
+  c.need("16 codes inside the row's blocks", codes);
 }
 
 }  // namespace fno

@@ -402,18 +402,19 @@ size_t mix_train_workspace_bytes(int B, int I, int O, long P, int dtype) {
 
 hipError_t launch_mix_save(const MixTrainArgs &a, int dtype, hipStream_t s) {
   const MtPick k = mt_pick(a.O, a.I, dtype);
-  FNO_BOUNDS(check_mix_train(a, true, 0, k.lds_fwd, dtype);)
-  if (hipError_t e = raise_lds_cap(k.fwd, k.lds_fwd); e != hipSuccess) return e;
   MixTrainArgs arg = a;
+  const int S = mt_runs(arg, k.pt_fwd, kMtForward);
+  FNO_BOUNDS(check_mix_train(arg, true, S, k.lds_fwd, dtype, k.pt_fwd, k.threads_fwd);)
+  if (hipError_t e = raise_lds_cap(k.fwd, k.lds_fwd); e != hipSuccess) return e;
   void *args[] = {(void *)&arg};
-  return hipLaunchKernel(k.fwd, dim3((unsigned)mt_runs(arg, k.pt_fwd, kMtForward)), dim3((unsigned)k.threads_fwd), args, k.lds_fwd, s);
+  return hipLaunchKernel(k.fwd, dim3((unsigned)S), dim3((unsigned)k.threads_fwd), args, k.lds_fwd, s);
 }
 
 hipError_t launch_mix_bwd(const MixTrainArgs &a, int dtype, hipStream_t s) {
   const MtPick k = mt_pick(a.O, a.I, dtype);
   MixTrainArgs arg = a;
   int S = mt_runs(arg, k.pt_bwd, k.resident);
-  FNO_BOUNDS(check_mix_train(a, false, S, k.lds_bwd, dtype);)
+  FNO_BOUNDS(check_mix_train(arg, false, S, k.lds_bwd, dtype, k.pt_bwd, k.threads_bwd);)
   if (hipError_t e = raise_lds_cap(k.bwd, k.lds_bwd); e != hipSuccess) return e;
   void *args[] = {(void *)&arg};
   hipError_t e = hipLaunchKernel(k.bwd, dim3((unsigned)S), dim3((unsigned)k.threads_bwd), args, k.lds_bwd, s);

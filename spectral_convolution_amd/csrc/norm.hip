@@ -202,10 +202,10 @@ size_t norm_workspace_bytes(int B, int C, long P, int dtype) {
 }
 
 hipError_t launch_norm_fwd(const NormArgs &a, int dtype, hipStream_t s) {
-  FNO_BOUNDS(check_norm(a, true, 0, dtype);)
   const NormPick k = pick(a, true, dtype);
   NormArgs arg = a;
   const long S = norm_runs(a, dtype, k, kFieldRuns, &arg.per);
+  FNO_BOUNDS(check_norm(arg, true, (int)S, dtype, k.threads, k.rpg, k.lds, k.wide, k.deep);)
   const dim3 grid((unsigned)S, a.P == 1 ? 1u : (unsigned)a.B);
   void *args[] = {(void *)&arg};
   return hipLaunchKernel(k.kernel, grid, dim3((unsigned)k.threads), args, k.lds, s);
@@ -215,7 +215,7 @@ hipError_t launch_norm_bwd(const NormArgs &a, int dtype, hipStream_t s) {
   const NormPick k = pick(a, false, dtype);
   NormArgs arg = a;
   int S = (int)norm_runs(a, dtype, k, a.P == 1 ? kTokenRuns : kFieldRuns, &arg.per);
-  FNO_BOUNDS(check_norm(a, false, S, dtype);)
+  FNO_BOUNDS(check_norm(arg, false, S, dtype, k.threads, k.rpg, k.lds, k.wide, k.deep);)
   const bool tok = a.P == 1;
   const dim3 grid((unsigned)S, tok ? 1u : (unsigned)a.B);
   void *args[] = {(void *)&arg};

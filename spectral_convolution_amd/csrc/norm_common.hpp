@@ -5,12 +5,14 @@
 
 namespace fno {
 
-// a call's kernel, its threads, the tiles (rows) a workgroup has at a time and
-// the LDS it is launched with
+// a call's kernel, its threads, the tiles (rows) a workgroup has at a time, the LDS it is
+// launched with, and how a tile (row) is split: waves and groups of 8 channels a wave (threads
+// and 16-byte pieces a thread)
 struct NormPick {
   const void *kernel;
   int threads, rpg;
   size_t lds;
+  int wide, deep;
 };
 
 constexpr int kRms = 0;

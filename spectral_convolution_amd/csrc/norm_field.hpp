@@ -2,6 +2,8 @@
 // (norm.hip has the mathematics and the design).
 #pragma once
 
+#include <algorithm>
+
 #include "norm_common.hpp"
 
 namespace fno {
@@ -536,7 +538,7 @@ NormPick field_kernel(int C, int w) {
                   : w == 2 ? field_pick<DT, KIND, 2, FWD>(cpt)
                   : w == 4 ? field_pick<DT, KIND, 4, FWD>(cpt)
                            : field_pick<DT, KIND, 8, FWD>(cpt);
-  return {k, w == 1 ? 256 : 64 * w, w == 1 ? 4 : 1, 0};
+  return {k, w == 1 ? 256 : 64 * w, w == 1 ? 4 : 1, 0, w, w == 1 || w == 4 ? cpt : std::max(cpt, 5)};
 }
 
 template <int DT, int KIND>

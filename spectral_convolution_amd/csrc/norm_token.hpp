@@ -402,8 +402,8 @@ __global__ __launch_bounds__(tok_threads<NT>()) __attribute__((amdgpu_waves_per_
 
 template <int DT, int KIND, bool FWD, int NT, int CH>
 NormPick tok_pick() {
-  if constexpr (FWD) return {(const void *)fno_norm_tok_fwd<DT, NT, CH, KIND>, tok_threads<NT>(), tok_threads<NT>() / NT, 0};
-  else return {(const void *)fno_norm_tok_bwd<DT, NT, CH, KIND>, tok_threads<NT>(), tok_threads<NT>() / NT, (size_t)64 * CH * NT};
+  if constexpr (FWD) return {(const void *)fno_norm_tok_fwd<DT, NT, CH, KIND>, tok_threads<NT>(), tok_threads<NT>() / NT, 0, NT, CH};
+  else return {(const void *)fno_norm_tok_bwd<DT, NT, CH, KIND>, tok_threads<NT>(), tok_threads<NT>() / NT, (size_t)64 * CH * NT, NT, CH};
 }
 
 template <int DT, int KIND>
