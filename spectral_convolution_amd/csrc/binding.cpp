@@ -15,6 +15,8 @@
 
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <memory>
+
 namespace {
 
 bool fits(const at::Tensor &t, PyObject *shape, const at::Tensor &ref) {
@@ -31,29 +33,27 @@ bool fits(const at::Tensor &t, PyObject *shape, const at::Tensor &ref) {
   return t.is_contiguous();
 }
 
+struct Release {
+  void operator()(PyObject *o) const { Py_XDECREF(o); }
+};
+
 PyObject *addresses(PyObject *, PyObject *const *args, Py_ssize_t n) {
   try {
     if (n < 1 || n % 2 == 0 || !THPVariable_Check(args[0])) Py_RETURN_NONE;
     const at::Tensor &ref = THPVariable_Unpack(args[0]);
-    PyObject *out = PyTuple_New(n / 2);
+    std::unique_ptr<PyObject, Release> out(PyTuple_New(n / 2));  // released on every way out but the last
     if (!out) return nullptr;
     for (Py_ssize_t i = 1; i < n; i += 2) {
       void *p = nullptr;
       if (args[i] != Py_None) {
-        if (!THPVariable_Check(args[i]) || !fits(THPVariable_Unpack(args[i]), args[i + 1], ref)) {
-          Py_DECREF(out);
-          Py_RETURN_NONE;
-        }
+        if (!THPVariable_Check(args[i]) || !fits(THPVariable_Unpack(args[i]), args[i + 1], ref)) Py_RETURN_NONE;
         p = THPVariable_Unpack(args[i]).data_ptr();
       }
       PyObject *v = PyLong_FromVoidPtr(p);
-      if (!v) {
-        Py_DECREF(out);
-        return nullptr;
-      }
-      PyTuple_SET_ITEM(out, i / 2, v);
+      if (!v) return nullptr;
+      PyTuple_SET_ITEM(out.get(), i / 2, v);
     }
-    return out;
+    return out.release();
   } catch (const std::exception &e) {  // a tensor without storage, say: no address
     PyErr_Clear();
     Py_RETURN_NONE;
