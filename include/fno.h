@@ -438,12 +438,15 @@ fno_status_t fno_model2d_destroy(fno_model2d_t model);
  * exponent is e = max(floor(log2 M) - 6, low), low = -24 for FNO_F16, else
  * -126 (e = low where M = 0), and a value x is kept as
  *   q = rint(x 2^-e) (ties to even), clamped to [-127, 127],
- * so it reads back as q 2^e, off by at most M / 64 (half of 2^e unless the
- * clamp acts), exactly representable in the storage type. A block holding an
+ * so it reads back as q 2^e, exactly representable in the storage type, off by
+ * at most half of 2^e, and by 2^e where the clamp acts (at most M / 64, or 2^-127
+ * in FNO_F32 and FNO_BF16 blocks below 2^-120). A block holding an
  * infinity or a NaN has e = 127 and reads back as NaN throughout.
  * Layout: int8 codes [rows][32 nb], nb = ceil(n / 32), zero past n; then, from
  * the next multiple of 256 bytes, int8 exponents [rows][nb]; the whole rounded
- * up to 256 bytes (fno_checkpoint_bytes: n + n / 32 bytes a row, roughly).
+ * up to 256 bytes (fno_checkpoint_bytes). A row takes 33 nb bytes: 1 1/32 a value
+ * where n is long or a multiple of 32, but 33 for a single one, which is more than
+ * the field itself.
  * saved is 256-byte aligned. n <= 2^31, rows * n <= 2^40, else UNSUPPORTED. */
 fno_status_t fno_checkpoint_bytes(long rows, long n, size_t *bytes);
 fno_status_t fno_checkpoint_pack(const void *x, void *saved, long rows, long n,
@@ -454,8 +457,10 @@ fno_status_t fno_checkpoint_unpack(const void *saved, void *y, long rows,
 /* Channel mix of a training step, fno_channel_mix that also keeps what its
  * backward needs in 8 bits: the checkpoint of x (rows [batch * c_in][pixels])
  * and, with GELU and an add input, that of add (rows [batch * c_out][pixels])
- * behind it, in `saved` (fno_channel_mix_saved_bytes, 256-byte aligned). y is
- * that of x and add as given. act 0 or 1, bias and add may be NULL.
+ * behind it, in `saved` (fno_channel_mix_saved_bytes, 256-byte aligned). Rows lie
+ * along the pixels, so fields of fewer than 9 (FNO_F32) or 17 pixels are kept in
+ * more bytes than they have. y is that of x and add as given. act 0 or 1, bias and
+ * add may be NULL.
  * c_in, c_out <= 128, pixels <= 2^26 and batch * pixels <= 2^36, else
  * UNSUPPORTED. */
 fno_status_t fno_channel_mix_saved_bytes(int batch, int c_in, int c_out,
@@ -471,8 +476,10 @@ fno_status_t fno_channel_mix_save(const void *x, const void *A,
  * gz = gy act'(z):
  *   gx = A^T gz [batch][c_in][pixels],  gadd = gz [batch][c_out][pixels],
  *   gA = sum gz x^^T [c_out][c_in],  gbias = sum gz [c_out]
- * (sums over samples and pixels, in fp32). What an infinite gz reaches is not
- * finite, NaN where fp32 would give an infinity. Each may be NULL, not all; bias as
+ * (sums over samples and pixels, in fp32; gz enters the products of FNO_F16 with 22
+ * bits, of the other types with 24). GELU's derivative is 1 at z = infinity and 0
+ * at -infinity. What an infinite gz or weight reaches is not finite, NaN
+ * where fp32 would give an infinity. Each may be NULL, not all; bias as
  * in the forward; has_add: whether the forward had an add input (gadd must be
  * NULL otherwise). workspace: fno_channel_mix_workspace_bytes bytes, 16-byte
  * aligned, needed for gA or gbias; its contents do not matter. */

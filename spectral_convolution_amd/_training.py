@@ -368,9 +368,10 @@ def fno_norm_residual_backward_saved(params, saved, gy, gu, gx, gv, grads, works
 
 def channel_mix(x, A, bias=None, add=None, act=0):
     """y = act(A x + bias + add), differentiable in all four; x (and, with
-    GELU, add) is kept for the backward in 8 bits. Without gradients the same kernel runs and
-    what it kept is dropped: y is the same either way, and fno_channel_mix, which keeps
-    nothing, is no faster but for fields of 64 channels or fewer and 16 bits (228 us instead of 245 at best)."""
+    GELU, add) is kept for the backward in 8 bits, rows along the pixels (33
+    bytes for each 32 of them: fields of a few pixels take more than they have).
+    Without gradients the same kernel runs and what it kept is dropped: y is the
+    same either way, and fno_channel_mix, which keeps nothing, is mostly slower, and at best 0.8 of it (16-bit fields of up to 64 channels)."""
     from ._training_autograd import ChannelMixFunction
     if not isinstance(A, _t().Tensor) or A.dim() != 2:
         raise ValueError("A must be a [c_out][c_in] tensor")

@@ -4,8 +4,8 @@
 // A field is seen as rows of n contiguous values, each row as blocks of 32
 // (the last one may be short). With M the largest magnitude of a block, its
 // exponent is e = max(floor(log2 M) - 6, low) (low for M = 0) and a value is
-// kept as q = rint(x 2^-e), clamped to [-127, 127]: 64 <= M 2^-e < 128, so a
-// value is off by at most half of 2^e, and by 2^e where the clamp acts. low
+// kept as q = rint(x 2^-e), clamped to [-127, 127]: M 2^-e < 128 (and 64 or more but where e is
+// low), so a value is off by at most half of 2^e, and by 2^e where the clamp acts. low
 // is -24 for fp16 (every value is a multiple of 2^-24, so tiny blocks are
 // kept exactly) and -126 for fp32 / bf16 (2^e and 2^-e stay normal numbers).
 // A block that holds an infinity or a NaN has e = 127, which reads back as

@@ -23,10 +23,12 @@
 // gA and gbias stay in registers over a workgroup's run of tiles, go to the
 // workspace once and are added in a fixed order by fno_mix_params.
 //
-// Measured (MI355X; forward + backward): 32 x 64 x 64 channels, 256^2, fp16 533 us, 4.1
-// TB/s against 5.1 of a copy (vector instructions 65 % of the issue slots in the backward,
-// half of them GELU's derivative and the split of gz); 16 x 32 x 32, 128^2, fp32 62 to 70
-// us, 3.8 TB/s; at 128 x 128 fp32 channels the fp32 matrix rate is the bound.
+// Measured (MI355X; forward + backward, a pass among others): 32 x 64 x 64 channels, 256^2, fp16 545
+// us, 4.0 TB/s against 5.1 of a copy (vector instructions 67 % of the issue slots in the
+// backward, half of them GELU's derivative and the split of gz), bf16 559 us; 16 x 32 x 32,
+// 128^2, fp32 70 us, 3.4 TB/s; 16 x 128 x 128, 128^2, fp32 502 us: 206 us forward, 1.9 TB/s and 27 %
+// of the fp32 matrix rate (154 TFLOP/s of a library product), backward 297 us, 57 % of it: two
+// waves a SIMD that wait at the same barriers, nothing loaded ahead.
 
 #include <algorithm>
 
@@ -380,7 +382,10 @@ MtPick mt_pick(int O, int I, int dtype) {
 
 // Workgroups of a call, each a contiguous run of tiles; fills the tiling in. The
 // backward takes as many as the chip holds at once: with a few more, the last
-// ones run alone (1024 of 768: 382 us against 300 at 32 x 64 x 64 channels, 256^2).
+// ones run alone (1024 of 768: 382 us against 300 at 32 x 64 x 64 channels, 256^2, fp16).
+// fp32: two workgroups of four waves a CU, one of eight. Where registers or LDS hold one of the
+// former only (eight tiles of c_in, or four and one of c_out) these are two full rounds, and one round is no
+// better on the whole (16 x 128^2 pixels: 128 x 16 channels 84 us, 88 in one; 128 x 64 174, 167 in one).
 int mt_runs(MixTrainArgs &a, int pt, long most) {
   a.tpb = (int)((a.P + pt - 1) / pt);
   a.tiles = a.B * a.tpb;

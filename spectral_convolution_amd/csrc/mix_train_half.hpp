@@ -31,8 +31,10 @@ typedef __bf16 mt_b8 __attribute__((ext_vector_type(8)));
 // WAVES in a workgroup. Backward: four, or eight for eight tiles of c_out, so that
 // a wave has one of them; its registers (a row of gA, a tile's inputs ahead)
 // fit three waves a SIMD up to 16 tiles of gA, where few waves do not stage many
-// rows of x. Forward: eight from four tiles of c_out on, tiles of 128 pixels: with
-// 64, a row's piece of the codes is half a line, and evicted as such.
+// rows of x (five variants spill: 16 to 44 bytes a lane, bf16 with one tile of c_out and eight of
+// c_in 424: 16 x 128 x 16 channels, 128^2, 101 us where fp16 takes 55). Forward: eight
+// from four tiles of c_out on, tiles of 128 pixels: with 64, a row's piece of the codes
+// is half a line, and evicted as such.
 template <int OT>
 constexpr int mh_waves(bool fwd) { return OT == 8 || (fwd && OT == 4) ? 8 : 4; }
 

@@ -45,8 +45,10 @@
 //
 // Measured (MI355X; a 1 GiB copy runs at 5.1 TB/s): forward of 32 x 64 x 256^2 fp16
 // 199 us, 5.4 TB/s; backward of 4 x 32 x 64^3 fp32 161 us (5.0 TB/s) in a loop of its own,
-// 179 among others; forward with checkpoints and backward from them of 20 x 64 x
-// 256^2 fp16 144 + 165 us, 5.4 TB/s; forward of 8192 x 1024 bf16 tokens 19 us.
+// 176 among others; forward with checkpoints and backward from them of 20 x 64 x
+// 256^2 fp16 144 + 164 us, 5.4 TB/s (layer norm: 368 for both, its backward spills 44 bytes a lane).
+// 8192 x 1024 bf16 tokens, their fields (67 MB) from memory: forward 23 us (24 in a kernel trace;
+// 18 to 19 with up to three sets of fields in turn, which the 256 MB cache partly holds), backward 43 (38 in a trace).
 
 #include <algorithm>
 

@@ -95,7 +95,7 @@ __device__ __forceinline__ void tok_fix(ck_u32x4 (&r)[CH], int t, int C) {
 
 // NT threads hold a row, CH 16-byte pieces each. Parameters are loaded where they
 // are used: held from the start they cost more in waves than their latency does (8192
-// x 1024 bf16: 29.4 us instead of 26.3).
+// x 1024 bf16, the forward as it was then: 29.4 us instead of 26.3).
 template <int DT, int NT, int CH, int KIND>
 __global__ __launch_bounds__(tok_threads<NT>()) void fno_norm_tok_fwd(NormArgs a) {
   constexpr int V = ck_vec<DT>(), RPG = tok_threads<NT>() / NT;
@@ -409,9 +409,10 @@ NormPick tok_pick() {
 template <int DT, int KIND>
 NormPick tok_kernel(bool fwd, int C) {
   // Forward: one piece a thread, so that many waves have loads in flight (8192 x 1024
-  // bf16: 23.3 us with one, 27.8 with two). Backward: two where that needs no more
-  // threads than 512, as each workgroup leaves sums to add (1024 x 8192 fp16: 72 us
-  // with 512 threads, 105 with 1024); four spill.
+  // bf16 in a kernel trace: 23.3 us with one, 27.8 with two). Backward: two where that needs no more
+  // threads than 512, as each workgroup leaves sums to add (1024 x 8192 fp16: 71 us
+  // with 512 threads, 105 with 1024); four, in fp32 above 4096 channels, spill 350 bytes a lane
+  // (1024 x 8192 fp32: 116 us, 2.3 TB/s).
   if constexpr (DT == DT_F32) {
     if (C <= 256) return fwd ? tok_pick<DT, KIND, true, 64, 1>() : tok_pick<DT, KIND, false, 64, 1>();
     if (C <= 512) return fwd ? tok_pick<DT, KIND, true, 128, 1>() : tok_pick<DT, KIND, false, 128, 1>();
