@@ -19,7 +19,7 @@
 #include <vector>
 
 #include "../../../include/fno.h"
-#include "../common.hpp"
+#include "../train.hpp"
 
 long check_launches();
 long check_reports();

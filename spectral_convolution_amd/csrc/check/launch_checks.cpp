@@ -4,6 +4,7 @@
 // kernel's structural assumptions. Host code only.
 
 #include "../plane_mfma.hpp"
+#include "../train.hpp"
 
 #include <algorithm>
 #include <cstdio>

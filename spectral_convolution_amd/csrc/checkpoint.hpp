@@ -17,7 +17,7 @@
 // int8 [rows][nb]; each part starts on a multiple of 256 bytes.
 #pragma once
 
-#include "common.hpp"
+#include "train.hpp"
 
 namespace fno {
 
