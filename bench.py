@@ -10,7 +10,8 @@ for --settle-ms (default 300 ms): after an idle period the device's power
 management first runs kernels fast for about a millisecond and then slows
 every kernel in steps by up to ~25 % for a few milliseconds before settling,
 so a short timed region that starts from idle measures that transient instead
-of the sustained rate. Prints one JSON line:
+of the sustained rate. Prints one JSON line (--full: with the kernels, launch shapes
+and distributions of every workload, not of the headline alone):
 
 * value: layers/s on the headline workload (default: the 256x256 fp16 layer,
   B=32, Cin=Cout=64, modes 32x32), GB/s and the fraction of the 8 TB/s HBM
@@ -651,6 +652,38 @@ def _summary(r):
             f"= {rf['achieved']:.0f} GB/s algorithmic ({100 * rf['frac']:.1f} %)")
 
 
+def _digits(o):
+    """o with its floats to six significant digits."""
+    if isinstance(o, float):
+        return float(f"{o:.6g}")
+    if isinstance(o, dict):
+        return {k: _digits(v) for k, v in o.items()}
+    return [_digits(v) for v in o] if isinstance(o, list) else o
+
+
+def short_line(out):
+    """The record as printed: everything of the headline workload, of the others their
+    rates, roofline and baseline. Whoever keeps the last few thousand characters of the output has
+    the whole line (the full record is three times as long: --full)."""
+    def of(d, *keys):
+        return {k: d[k] for k in keys if k in d} if d is not None else None
+
+    def workload(r):
+        w = of(r, "workload", "dtype", "ms_per_layer", "layers_per_s", "gbps", "hbm_frac", "launch_shape", "steps")
+        w["roofline"] = of(r["roofline"], "kernel", "achieved", "frac", "traffic")
+        if "cpu_baseline" in r:
+            w["cpu_baseline"] = of(r["cpu_baseline"], "value", "unit", "cores", "kind")
+        return w
+
+    line = {k: v if k in ("value", "ms_per_step") else _digits(v) for k, v in out.items()}
+    for k in ("metric_configs", "configs"):
+        line[k] = [_digits(workload(r)) for r in out[k]]
+    if "latency" in out:
+        stat = lambda r: {k: of(v, "mean") if isinstance(v, dict) else v for k, v in r.items()}  # noqa: E731
+        line["latency"] = _digits({**out["latency"], "sweep": [stat(r) for r in out["latency"]["sweep"]]})
+    return line
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -675,6 +708,7 @@ def main():
     ap.add_argument("--cache-probe", action="store_true",
                     help="only time each launch of --config/--dtype right after its producer and with the "
                          "Infinity Cache evicted in between (where the exchanged spectra are read from)")
+    ap.add_argument("--full", action="store_true", help="print every workload's kernels, launch shapes and distributions")
     ap.add_argument("--copy-only", type=int, default=0, metavar="BYTES",
                     help="only time a device-to-device copy of BYTES (counter calibration)")
     args = ap.parse_args()
@@ -778,7 +812,7 @@ def main():
             f"graph {r['graph_us']['mean']:.1f}±{r['graph_us']['std']:.1f} us"
             for r in out["latency"]["sweep"]), file=sys.stderr, flush=True)
     out["copy_1gib"] = copy_bandwidth(1 << 30)
-    print(json.dumps(out), flush=True)
+    print(json.dumps(out) if args.full else json.dumps(short_line(out), separators=(",", ":")), flush=True)
 
 
 if __name__ == "__main__":
