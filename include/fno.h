@@ -52,6 +52,7 @@
 #define FNO_H
 
 #include <stddef.h>
+#include <stdint.h>
 
 #ifdef __cplusplus
 extern "C" {
@@ -560,6 +561,86 @@ fno_status_t fno_norm_residual_backward_saved(
     const void *gu, void *gx, void *gv, const fno_norm_grads_t *grads,
     void *workspace, int batch, int channels, long pixels, fno_dtype_t dtype,
     void *stream);
+
+/* ---- operators of a regularised block --------------------------------------
+ * Group norm with an activation and dropout, and dropout into a residual stream,
+ * forward and backward. Fields are [batch][channels][pixels], or with
+ * channels_last 1 [batch][pixels][channels]; one pixel: tokens, either way.
+ * Fields are 16-byte aligned, parameters to their element; outputs share memory with
+ * nothing. Sums and statistics are fp32, results repeat bit for bit, calls
+ * can be captured into a graph.
+ *
+ * Dropout. What is dropped is a unit: a value, a channel of a sample or a sample,
+ * numbered in memory order (value i, b * channels + c, b). Unit u is dropped where its
+ * 16 random bits are below t = rint(65536 p) and multiplied by 65536 / (65536 - t)
+ * otherwise (t = 0: nothing is dropped; t = 65536: everything, to 0); a dropped value is 0
+ * whatever it was. The mask is computed where it is needed and never stored: the bits
+ * of u are half u % 2 (0: low) of word (u % 8) / 2 of block u / 8 of the generator Philox
+ * 4x32-10 (Salmon, Moraes, Dror, Shaw, SC 2011) with the seed as its key and
+ * (block, offset) as its counter, each 64 bits, low words first. The same seed, offset and
+ * shape give the same mask, in the backward above all; a program moves the offset
+ * on with every call. step, if not NULL, is device memory whose value is added to the
+ * offset when the call runs: a captured graph's replays draw masks of
+ * their own if the program moves it on between them (and not between a forward
+ * and its backward). */
+typedef enum {
+  FNO_DROP_ELEMENT = 0,
+  FNO_DROP_CHANNEL = 1,
+  FNO_DROP_SAMPLE = 2
+} fno_drop_unit_t;
+typedef struct {
+  float p; /* in [0, 1] */
+  int unit; /* fno_drop_unit_t */
+  uint64_t seed, offset;
+  const uint64_t *step; /* device memory, 8-byte aligned, or NULL */
+} fno_dropout_t;
+
+/* y = x + D(v); x may be NULL: y = D(v). Gradients: dL/dv = D(dL/dy), which is
+ * this call with x NULL on dL/dy, and dL/dx = dL/dy. pixels <= 2^31, 2^40 values,
+ * else UNSUPPORTED. */
+fno_status_t fno_dropout_residual(const fno_dropout_t *drop, const void *x,
+                                  const void *v, void *y, int batch,
+                                  int channels, long pixels, int channels_last,
+                                  fno_dtype_t dtype, void *stream);
+
+/* Group norm: with m the mean and s2 the mean squared deviation of a group, the
+ * channels / groups neighbouring channels of a sample over all its pixels,
+ *   y = D(act((x - m) / sqrt(s2 + eps) weight[c] + bias[c])),
+ * act 0: none, 1: GELU (the erf form), 2: SiLU, z / (1 + exp(-z)). */
+typedef struct {
+  int groups; /* divides the channels */
+  int act;
+  int channels_last;
+  float eps;          /* a positive normal number */
+  const void *weight; /* [channels]; NULL: 1 */
+  const void *bias;   /* [channels]; NULL: 0 */
+} fno_group_norm_params_t;
+
+/* stats [batch][groups][2] (fp32, 8-byte aligned) takes each group's m and
+ * 1 / sqrt(s2 + eps), which the backward needs; NULL: not wanted. drop NULL: none.
+ * workspace: fno_group_norm_workspace_bytes bytes, 16-byte aligned, for either call; its
+ * contents do not matter before or after. channels <= 8192, pixels <= 2^27,
+ * batch * groups < 2^31, 2^40 values, else UNSUPPORTED. */
+fno_status_t fno_group_norm_workspace_bytes(int batch, int channels,
+                                            long pixels, int groups,
+                                            int channels_last,
+                                            fno_dtype_t dtype, size_t *bytes);
+fno_status_t fno_group_norm(const fno_group_norm_params_t *params,
+                            const fno_dropout_t *drop, const void *x, void *y,
+                            float *stats, void *workspace, int batch,
+                            int channels, long pixels, fno_dtype_t dtype,
+                            void *stream);
+
+/* Gradients at gy = dL/dy with the x, stats and drop of the forward: gx, gw
+ * and gb (of weight and bias), each NULL where not wanted, not all. INVALID_ARG where
+ * a gradient is wanted of a parameter that is NULL. */
+fno_status_t fno_group_norm_backward(const fno_group_norm_params_t *params,
+                                     const fno_dropout_t *drop, const void *x,
+                                     const float *stats, const void *gy,
+                                     void *gx, void *gw, void *gb,
+                                     void *workspace, int batch, int channels,
+                                     long pixels, fno_dtype_t dtype,
+                                     void *stream);
 
 #ifdef __cplusplus
 }

@@ -8,6 +8,9 @@ if libfno.so is missing, importing a function that needs it raises.
 
 import ctypes
 
+from ._block_ops import (  # noqa: F401
+    Dropout, GroupNormParams, dropout_residual, fno_dropout_residual, fno_group_norm, fno_group_norm_backward,
+    fno_group_norm_stats_empty, fno_group_norm_workspace_bytes, fno_group_norm_workspace_empty, group_norm)
 from ._lib import DTYPES, FnoError, check, lib  # noqa: F401
 from ._training import (  # noqa: F401
     NormGrads, NormParams, channel_mix, fno_channel_mix_backward_saved, fno_channel_mix_save,
@@ -33,6 +36,9 @@ __all__ = [
     "NormParams", "NormGrads", "fno_norm_residual", "fno_norm_residual_save", "fno_norm_residual_backward",
     "fno_norm_residual_backward_saved", "fno_norm_residual_saved_bytes", "fno_norm_residual_saved_empty",
     "fno_norm_residual_workspace_bytes", "fno_norm_residual_workspace_empty", "channel_mix", "norm_residual",
+    "Dropout", "fno_dropout_residual", "dropout_residual", "GroupNormParams", "fno_group_norm",
+    "fno_group_norm_backward", "fno_group_norm_stats_empty", "fno_group_norm_workspace_bytes",
+    "fno_group_norm_workspace_empty", "group_norm",
 ]
 
 

@@ -11,6 +11,7 @@ STATUS_NAMES = {0: "FNO_OK", 1: "FNO_ERR_INVALID_ARG", 2: "FNO_ERR_UNSUPPORTED",
                 3: "FNO_ERR_OUT_OF_MEMORY", 4: "FNO_ERR_DEVICE"}
 DTYPES = {"f32": 0, "f16": 1, "bf16": 2}
 NORM_KINDS = {"rms": 0, "layer": 1}
+DROP_UNITS = {"element": 0, "channel": 1, "sample": 2}
 NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024  # FNO_NOALLOC_SCRATCH_BYTES
 
 # every symbol include/fno.h declares, with its ctypes signature
@@ -30,6 +31,19 @@ class NormGradsStruct(ctypes.Structure):
     _fields_ = [(n, _c_void_p) for n in ("w_post", "b_post", "gate", "scale", "w_pre", "b_pre")]
 
 
+class DropoutStruct(ctypes.Structure):
+    """fno_dropout_t"""
+    _fields_ = [("p", ctypes.c_float), ("unit", _c_int), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64),
+                ("step", _c_void_p)]
+
+
+class GroupNormParamsStruct(ctypes.Structure):
+    """fno_group_norm_params_t"""
+    _fields_ = [("groups", _c_int), ("act", _c_int), ("channels_last", _c_int), ("eps", ctypes.c_float),
+                ("weight", _c_void_p), ("bias", _c_void_p)]
+
+
+_DropP, _GnP = ctypes.POINTER(DropoutStruct), ctypes.POINTER(GroupNormParamsStruct)
 _NormP, _NormG = ctypes.POINTER(NormParamsStruct), ctypes.POINTER(NormGradsStruct)
 _BCP = [_c_int, _c_int, _c_long, _c_int, _c_void_p]  # batch, channels, pixels, dtype, stream
 SIGNATURES = {
@@ -83,6 +97,10 @@ SIGNATURES = {
     "fno_norm_residual_workspace_bytes": (_c_int, [_c_int, _c_int, _c_long, _c_int, _SizeP]),
     "fno_norm_residual_backward": (_c_int, [_NormP] + [_c_void_p] * 6 + [_NormG, _c_void_p] + _BCP),
     "fno_norm_residual_backward_saved": (_c_int, [_NormP] + [_c_void_p] * 5 + [_NormG, _c_void_p] + _BCP),
+    "fno_dropout_residual": (_c_int, [_DropP] + [_c_void_p] * 3 + [_c_int, _c_int, _c_long, _c_int, _c_int, _c_void_p]),
+    "fno_group_norm_workspace_bytes": (_c_int, [_c_int, _c_int, _c_long, _c_int, _c_int, _c_int, _SizeP]),
+    "fno_group_norm": (_c_int, [_GnP, _DropP] + [_c_void_p] * 4 + _BCP),
+    "fno_group_norm_backward": (_c_int, [_GnP, _DropP] + [_c_void_p] * 7 + _BCP),
 }
 
 _lib = None

@@ -20,7 +20,7 @@ import sys
 from .build import CSRC, HERE, ROOT, SOURCES, _hipcc
 
 OUT = os.path.join(HERE, "_build_check")
-CHECK_SOURCES = ["check/hip_stub.cpp", "check/launch_checks.cpp", "check/driver.cpp"]
+CHECK_SOURCES = ["check/hip_stub.cpp", "check/launch_checks.cpp", "check/block_checks.cpp", "check/driver.cpp"]
 FLAGS = [
     "-x", "hip", "--cuda-host-only", "-O1", "-g", "-std=c++17", "-fPIC", "-DFNO_BOUNDS_CHECK",
     "-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",

@@ -12,8 +12,17 @@
 //
 // The address of t, contiguous memory of that many bytes at a multiple of align on
 // ref's device, else None.
+//
+//   elsewhere(t, t, ...)
+//
+// Whether one of the tensors (or None) is a leaf whose gradient accumulator lives, in an autograd graph made
+// before, and belongs to another stream than the device's current one. A backward captured into a
+// graph would wait for that stream, which is not captured, and the end of the capture ends the process.
 
+#include <c10/core/impl/VirtualGuardImpl.h>
+#include <torch/csrc/autograd/function.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/autograd/variable.h>
 
 #include <memory>
 
@@ -76,7 +85,26 @@ PyObject *buffer(PyObject *, PyObject *const *args, Py_ssize_t n) {
   }
 }
 
-PyMethodDef methods[] = {{"buffer", (PyCFunction)(void *)buffer, METH_FASTCALL, nullptr},
+PyObject *elsewhere(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  try {
+    for (Py_ssize_t i = 0; i < n; ++i) {
+      if (!THPVariable_Check(args[i])) continue;
+      const at::Tensor &t = THPVariable_Unpack(args[i]);
+      if (!t.requires_grad() || !t.is_leaf()) continue;
+      const auto node = torch::autograd::impl::try_get_grad_accumulator(t);
+      if (!node) continue;
+      const auto its = node->stream();
+      if (its && *its != c10::impl::VirtualGuardImpl(t.device().type()).getStream(t.device())) Py_RETURN_TRUE;
+    }
+    Py_RETURN_FALSE;
+  } catch (const std::exception &e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+    return nullptr;
+  }
+}
+
+PyMethodDef methods[] = {{"elsewhere", (PyCFunction)(void *)elsewhere, METH_FASTCALL, nullptr},
+                         {"buffer", (PyCFunction)(void *)buffer, METH_FASTCALL, nullptr},
                          {"addresses", (PyCFunction)(void *)addresses, METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -31,6 +31,8 @@ struct FusedShape;
 struct CkArgs;
 struct NormArgs;
 struct MixTrainArgs;
+struct DropArgs;
+struct GnArgs;
 
 namespace bounds {
 // [p, p + n) inside one live allocation of the recording runtime (n = 0: true)
@@ -61,6 +63,12 @@ void check_block_rows(const void *zg, const void *zexp, const void *tb, const vo
 void check_checkpoint(const CkArgs &a, bool pack, int dtype);
 void check_mix_train(const MixTrainArgs &a, bool fwd, int S, size_t lds, int dtype, int pt, int threads);
 void check_norm(const NormArgs &a, bool fwd, int S, int dtype, int threads, int rpg, size_t lds, int wide, int deep);
+void check_drop(const DropArgs &a, int mode, int dtype);
+void check_gnorm_small(const GnArgs &a, bool last, bool bwd, int T, int NC, int dtype);
+void check_gnorm_rows(const GnArgs &a, bool bwd, bool out, int T, int dtype);
+void check_gnorm_cols(const GnArgs &a, bool bwd, bool out, bool runs, int dtype);
+void check_gnorm_join(const GnArgs &a, bool bwd, int dtype);
+void check_gnorm_params(const GnArgs &a, int samples, int dtype);
 
 }  // namespace fno
 

@@ -1,0 +1,144 @@
+// block_checks.cpp - the bounds-check build's model of the block operators' launches
+// (gnorm_kernels.hpp, drop.hip), as launch_checks.cpp has those of the others. Host code only.
+
+#include <algorithm>
+
+#include "../gnorm.hpp"
+
+namespace fno {
+
+namespace {
+
+size_t es_of(int dtype) { return dtype == DT_F32 ? 4 : 2; }
+
+struct Ctx {
+  const char *name;
+  void span(const char *what, const void *p, size_t n) const {
+    if (n && (!p || !bounds::inside(p, n))) bounds::report(name, what);
+  }
+  void opt(const char *what, const void *p, size_t n) const {
+    if (p) span(what, p, n);
+  }
+  void need(const char *what, bool ok) const {
+    if (!ok) bounds::report(name, what);
+  }
+};
+
+size_t values(const GnArgs &a) { return (size_t)a.B * a.C * a.P; }
+
+void gn_spans(const Ctx &c, const GnArgs &a, bool bwd, bool out, int dtype) {
+  const size_t es = es_of(dtype), n = values(a) * es, groups = (size_t)a.B * a.G;
+  c.span("x", a.x, n);
+  if (bwd) c.span("gy", a.gy, n);
+  if (out) c.span(bwd ? "gx" : "y", bwd ? a.gx : a.y, n);
+  c.opt("weight", a.w, a.C * es);
+  c.opt("bias", a.b, a.C * es);
+  c.opt("step", a.drop.step, 8);
+  if (bwd || out) c.opt("stats", a.stats, groups * 8);
+  c.need("groups of whole channels", a.G >= 1 && a.Cg * a.G == a.C);
+  c.need("threshold", a.drop.thr <= 65536);
+}
+
+}  // namespace
+
+void check_drop(const DropArgs &a, int mode, int dtype) {
+  const Ctx c{"fno_drop"};
+  const size_t es = es_of(dtype), n = (size_t)a.B * a.C * a.P * es;
+  const long V = dtype == DT_F32 ? 4 : 8, span = 1024, cpr = (a.n + V - 1) / V, total = a.rows * cpr;
+  c.opt("x", a.x, n);
+  c.span("v", a.v, n);
+  c.span("y", a.y, n);
+  c.opt("step", a.drop.step, 8);
+  c.need("rows are the field", a.rows >= 1 && a.n >= 1 && a.rows * a.n == (long)a.B * a.C * a.P);
+  // the chunks of the first and last workgroups, placed as the kernel does
+  const long groups = (total + span - 1) / span;
+  for (long g : {0L, 1L, groups / 2, groups - 2, groups - 1}) {
+    if (g < 0 || g >= groups) continue;
+    const long base = g * span, row0 = mode == 0 ? 0 : base / cpr, rem0 = base - row0 * cpr;
+    const bool whole = mode == 0 ? (base + span) * V <= a.n : base + span <= total && a.n % V == 0;
+    if (whole) {
+      c.need("whole chunks inside the field", (base + span) * V <= a.rows * a.n);
+      if (mode != 0) c.need("whole chunks where a flat field has them", base * V == row0 * a.n + rem0 * V);
+    }
+    for (long local : {0L, 1L, 255L, 256L, 1022L, 1023L}) {
+      if (base + local >= total) continue;
+      const long v = rem0 + local, d = mode == 0 ? 0 : cpr > span ? (v >= cpr ? 1 : 0) : (uint32_t)v / (uint32_t)cpr;
+      const long row = row0 + d, k = v - d * cpr;
+      c.need("chunk in its row", row < a.rows && k >= 0 && k < cpr && row * cpr + k == base + local);
+      if (mode == 2) {
+        const long b0 = row0 / a.P, prem = row0 - b0 * a.P;
+        c.need("sample of a row", prem + d < 1L << 32 && b0 + (prem + d) / a.P == row / a.P);
+      }
+    }
+  }
+}
+
+void check_gnorm_small(const GnArgs &a, bool last, bool bwd, int T, int NC, int dtype) {
+  const Ctx c{bwd ? "fno_gnorm_small backward" : "fno_gnorm_small"};
+  gn_spans(c, a, bwd, true, dtype);
+  const long V = dtype == DT_F32 ? 4 : 8, len = last ? a.Cg : a.P, rows = last ? a.P : a.Cg;
+  const long cpr = (len + V - 1) / V, chunks = rows * cpr, groups = (long)a.B * a.G, n = (long)values(a);
+  c.need("a team holds a group", chunks <= (long)T * NC);
+  c.need("groups in 31 bits", groups < 1L << 31);
+  c.need("one pixel: channels last", last || a.P > 1);
+  bool in = true, params = true;
+  for (long id : {0L, groups / 2, groups - 1}) {
+    const long b = id / a.G, c0 = (id - b * a.G) * a.Cg, pitch = last ? a.C : a.P;
+    const long first = last ? b * a.P * a.C + c0 : (b * a.C + c0) * a.P;
+    for (long q = 0; q < (long)T * NC; ++q) {
+      const long qc = std::min(q, chunks - 1), row = qc / cpr, k = (qc - row * cpr) * V;
+      const long nv = q < chunks ? std::min(len - k, V) : 0, at = first + row * pitch + k;
+      in = in && at >= 0 && at + (len % V == 0 ? V : nv) <= n;
+      params = params && (last ? c0 + k + std::min(len - k, V) <= a.C : c0 + row < a.C);
+    }
+  }
+  c.need("chunks inside the field", in);
+  c.need("parameters of existing channels", params);
+}
+
+void check_gnorm_rows(const GnArgs &a, bool bwd, bool out, int T, int dtype) {
+  const Ctx c{bwd ? "fno_gnorm_rows backward" : "fno_gnorm_rows"};
+  gn_spans(c, a, bwd, out, dtype);
+  const long V = dtype == DT_F32 ? 4 : 8, cpr = (a.P + V - 1) / V, rows = (long)a.B * a.C;
+  c.need("pieces cover the row", a.S >= 1 && a.per >= 1 && a.S * a.per >= cpr && (a.S - 1) * a.per < cpr);
+  c.need("a row of lanes or a workgroup", T == 8 || T == 64 || T == 256);
+  c.need("offsets of a row in 32 bits", cpr * V + 4L * T * V < 1L << 32);
+  if (!out) c.span("sums", a.part, (size_t)rows * a.S * 8);
+  if (bwd && out) c.span("group sums", a.gsum, (size_t)a.B * a.G * 8);
+  c.need("strides of the sums", a.sb == (long)a.C * a.S && a.sc == a.S && a.ss == 1);
+}
+
+void check_gnorm_cols(const GnArgs &a, bool bwd, bool out, bool runs, int dtype) {
+  const Ctx c{bwd ? "fno_gnorm_cols backward" : "fno_gnorm_cols"};
+  gn_spans(c, a, bwd, out, dtype);
+  const long V = dtype == DT_F32 ? 4 : 8, cpr = (a.C + V - 1) / V, rows = runs ? a.B * a.P : a.P;
+  c.need("pieces cover the rows", a.S >= 1 && a.per >= 1 && a.S * a.per >= rows && (a.S - 1) * a.per < rows);
+  for (long kb = 0; kb < cpr; kb += 256) {
+    const long kn = std::min(256L, cpr - kb), PL = 256 / kn;
+    c.need("lanes of a row", PL >= 1 && ((PL - 1) * V + V - 1) * kn + kn - 1 < 256 * V && (kb + kn - 1) * V < a.C);
+  }
+  if (!out) c.span("sums", a.part, (size_t)(runs ? 1 : a.B) * a.S * a.C * 8);
+  if (bwd && out) c.span("group sums", a.gsum, (size_t)a.B * a.G * 8);
+  c.need("strides of the sums", a.sb == (runs ? 0 : (long)a.C * a.S) && a.sc == 1 && a.ss == a.C);
+}
+
+void check_gnorm_join(const GnArgs &a, bool bwd, int dtype) {
+  const Ctx c{bwd ? "fno_gnorm_join backward" : "fno_gnorm_join"};
+  const size_t groups = (size_t)a.B * a.G;
+  c.span("sums", a.part, (size_t)a.B * a.C * a.S * 8);
+  c.span(bwd ? "group sums" : "stats", bwd ? a.gsum : a.stats, groups * 8);
+  c.need("last sum of a sample", (a.C - 1) * a.sc + (a.S - 1) * a.ss < a.sb && a.sb == (long)a.C * a.S);
+  const long piece = a.last ? a.per : a.per * (dtype == DT_F32 ? 4 : 8);
+  c.need("no empty piece", (a.S - 1) * piece < a.P);
+}
+
+void check_gnorm_params(const GnArgs &a, int samples, int dtype) {
+  const Ctx c{"fno_gnorm_params"};
+  const size_t es = es_of(dtype);
+  c.opt("gw", a.gw, a.C * es);
+  c.opt("gb", a.gb, a.C * es);
+  c.span("sums", a.part, (size_t)samples * a.S * a.C * 8);
+  c.need("last sum", (samples - 1) * a.sb + (a.C - 1) * a.sc + (a.S - 1) * a.ss < (long)samples * a.S * a.C);
+}
+
+}  // namespace fno

@@ -19,6 +19,7 @@
 #include <vector>
 
 #include "../../../include/fno.h"
+#include "../block_ops.hpp"
 #include "../train.hpp"
 
 long check_launches();
@@ -195,6 +196,34 @@ void run_mix(int B, int I, int O, long P, int act, bool add, fno_dtype_t dt) {
                                         P, act, add, dt, nullptr) == FNO_OK);
 }
 
+// dropout alone and into a residual, in every unit; nothing behind the buffers
+void run_drop(int B, int C, long P, fno_dtype_t dt) {
+  const size_t n = (size_t)B * C * P * es_of(dt);
+  void *x = check_reserve(n), *v = check_reserve(n), *y = check_reserve(n), *step = check_reserve(8);
+  for (int unit = 0; unit < 3; ++unit)
+    for (int last = 0; last < 2; ++last) {
+      const fno_dropout_t d{0.25f, unit, 1, 2, last ? static_cast<uint64_t *>(step) : nullptr};
+      EXPECT(fno_dropout_residual(&d, last ? x : nullptr, v, y, B, C, P, last, dt, nullptr) == FNO_OK);
+    }
+}
+
+// group norm, forward and backward, with every gradient and with one; nothing behind the buffers
+void run_gnorm(int B, int C, long P, int G, int last, fno_dtype_t dt) {
+  const size_t es = es_of(dt), n = (size_t)B * C * P * es, nc = C * es;
+  size_t wb = 0;
+  EXPECT(fno_group_norm_workspace_bytes(B, C, P, G, last, dt, &wb) == FNO_OK);
+  auto far = [](size_t k) { return check_reserve(k); };
+  void *x = far(n), *y = far(n), *ws = far(wb), *gy = far(n), *gx = far(n);
+  float *stats = static_cast<float *>(far((size_t)B * G * 8));
+  const fno_dropout_t d{0.25f, FNO_DROP_ELEMENT, 1, 2, nullptr};
+  const fno_group_norm_params_t p{G, 1, last, 1e-5f, far(nc), far(nc)}, q{G, 2, last, 1e-5f, nullptr, nullptr};
+  EXPECT(fno_group_norm(&p, &d, x, y, stats, ws, B, C, P, dt, nullptr) == FNO_OK);
+  EXPECT(fno_group_norm(&q, nullptr, x, y, nullptr, ws, B, C, P, dt, nullptr) == FNO_OK);
+  EXPECT(fno_group_norm_backward(&p, &d, x, stats, gy, gx, far(nc), far(nc), ws, B, C, P, dt, nullptr) == FNO_OK);
+  EXPECT(fno_group_norm_backward(&p, &d, x, stats, gy, nullptr, far(nc), nullptr, ws, B, C, P, dt, nullptr) == FNO_OK);
+  EXPECT(fno_group_norm_backward(&q, nullptr, x, stats, gy, gx, nullptr, nullptr, ws, B, C, P, dt, nullptr) == FNO_OK);
+}
+
 // one call of a training operator, forward and backward, with nothing behind its buffers
 void trace_call(const std::string &op, int dt, const std::vector<long> &v) {
   const auto d = (fno_dtype_t)dt;
@@ -303,6 +332,20 @@ int main(int argc, char **argv) {
   for (const M &c : mf)
     for (int dt = 0; dt < 3; ++dt)
       for (int k = 0; k < 4; ++k) trace_call("mix", dt, {c.B, c.I, c.O, c.P, k & 1, k >> 1});
+  struct D { int B, C; long P; };
+  const D dd[] = {{1, 1, 1}, {2, 4, 256}, {3, 7, 33}, {5, 1001, 1}, {32, 64, 65536}, {4, 3, 3721}, {7, 130, 9}, {1, 1, 1L << 31},
+                  {1 << 30, 1, 1024}, {2, 8192, 1L << 26}, {65536, 4096, 4096}, {2000000000, 3, 5}};
+  for (const D &c : dd)
+    for (fno_dtype_t dt : dts) run_drop(c.B, c.C, c.P, dt);
+  struct G { int B, C; long P; int G; };
+  const G gg[] = {{2, 4, 256, 2}, {1, 1, 1, 1}, {1, 1, 2, 1}, {5, 64, 1, 8}, {3, 6, 2, 3}, {2, 48, 33, 3}, {1, 61, 97, 1},
+                  {1, 96, 1000, 3}, {2, 48, 3721, 3}, {1, 3, 70000, 1}, {2, 512, 300, 1}, {1, 4096, 20, 2}, {300, 40, 1, 5},
+                  {1, 8192, 1, 1}, {2, 8192, 9, 4}, {20, 64, 65536, 8}, {16, 128, 16384, 32}, {8192, 1024, 1, 16},
+                  {1, 8192, fno::kGnMaxPixels, 1}, {3, 5, fno::kGnMaxPixels - 3, 5}, {1 << 30, 4, 3, 1}, {1 << 28, 8, 511, 4},
+                  {2, 8191, 65537, 1}, {1000000, 100, 70, 100}, {134217728, 8192, 1, 8}};
+  for (const G &c : gg)
+    for (fno_dtype_t dt : dts)
+      for (int last = 0; last < 2; ++last) run_gnorm(c.B, c.C, c.P, c.G, last, dt);
   const long reports = check_reports();
   // the checker itself: spans past the end of a buffer must be reported
   {

@@ -1,0 +1,78 @@
+// gnorm.hip - group norm with an activation and dropout behind it, forward and backward, on
+// fields with the channels first ([B][C][P]) or last ([B][P][C]).
+//
+// Over a group g of C / G channels and all pixels of a sample, n values:
+//   m = mean(x),  r = 1 / sqrt(mean((x - m)^2) + eps),  x^ = (x - m) r
+//   y = D(act(w[c] x^ + b[c]))            D: dropout (drop.hpp); act: none, GELU or SiLU
+// Backward at gy = dL/dy, z = w x^ + b, gz = D(gy) act'(z), with the sums over a channel's pixels
+//   s1[b][c] = sum gz,  s2[b][c] = sum gz x^:
+//   gb = sum_b s1,  gw = sum_b s2,
+//   gx = r (w gz - M1 - x^ M2),  M1 = sum_c w s1 / n,  M2 = sum_c w s2 / n.
+// The mask of D is computed again. Statistics and sums are fp32: squares are summed about a value
+// from among those summed, and partial moments joined by Chan's formula, so that neither a large mean nor
+// an outlier costs digits. No atomics: results repeat bit for bit.
+//
+// A group that fits a workgroup's registers is read once (fno_gnorm_small). Of larger ones a first
+// kernel leaves the moments (forward) or s1, s2 (backward) of every channel's pieces, a small one joins
+// them, a third reads the field again. A backward of small groups still needs s1, s2 for the
+// parameters, summed over runs of whole rows. Bound by memory.
+
+#include <algorithm>
+
+#include "gnorm.hpp"
+
+namespace fno {
+
+namespace {
+constexpr long kUnits = 2048;         // workgroups that fill the chip
+constexpr long kParts = 1L << 22;     // sums that pieces beyond one a sample may take
+}  // namespace
+
+GnPlan gn_plan(const GnArgs &a, int dtype) {
+  GnPlan p{};
+  const long V = gn_vec(dtype);
+  p.last = a.last || a.P == 1;
+  const long len = p.last ? a.Cg : a.P, rows = p.last ? a.P : a.Cg, chunks = up(len, V) * rows;
+  p.team = chunks <= 64 ? 16 : chunks <= 256 ? 64 : chunks <= 1024 ? 256 : chunks <= 4096 ? 1024 : 0;
+  p.bteam = chunks <= 2048 ? p.team : 0;
+  const long bc = (long)a.B * a.C;
+  if (!p.last) {
+    const long cpr = up(a.P, V);
+    p.T = cpr <= 16 ? 8 : cpr <= 256 ? 64 : 256;
+    p.S = 1, p.per = cpr;
+    if (p.T == 256) {  // at least two chunks a lane, at most 64
+      const long want = std::max(std::min(up(kUnits, bc), up(cpr, 512)), up(cpr, 64 * 256));
+      p.per = up(up(cpr, want), 256) * 256;
+      p.S = (int)up(cpr, p.per);
+    }
+    p.parts = (size_t)bc * p.S;
+    return p;
+  }
+  const long cpr = up(a.C, V), lanes = std::max(1L, (long)kThreads / std::min(cpr, (long)kThreads));
+  const long blocks = up(cpr, kThreads), most = std::max(1L, kParts / bc);
+  const long S = std::min({up(kUnits, a.B * blocks), up(a.P, 4 * lanes), most});
+  p.per = up(a.P, S);
+  p.S = (int)up(a.P, p.per);
+  const long all = a.B * a.P;
+  const long R = std::min({up(kUnits, 2 * blocks), up(all, 4 * lanes), std::max(1L, kParts / a.C)});
+  p.per_run = up(all, R);
+  p.runs = (int)up(all, p.per_run);
+  p.parts = std::max(p.bteam ? 0 : (size_t)bc * p.S, (size_t)a.C * p.runs);
+  return p;
+}
+
+size_t gnorm_workspace_bytes(const GnArgs &a, int dtype) {
+  const GnPlan p = gn_plan(a, dtype);
+  return (p.parts + (p.bteam ? 0 : (size_t)a.B * a.G)) * sizeof(float2);
+}
+
+hipError_t gnorm_f32(const GnArgs &a, bool fwd, void *workspace, hipStream_t s);
+hipError_t gnorm_f16(const GnArgs &a, bool fwd, void *workspace, hipStream_t s);
+hipError_t gnorm_bf16(const GnArgs &a, bool fwd, void *workspace, hipStream_t s);
+
+hipError_t launch_gnorm(const GnArgs &a, bool fwd, void *workspace, int dtype, hipStream_t s) {
+  if (dtype == DT_F32) return gnorm_f32(a, fwd, workspace, s);
+  return dtype == DT_F16 ? gnorm_f16(a, fwd, workspace, s) : gnorm_bf16(a, fwd, workspace, s);
+}
+
+}  // namespace fno

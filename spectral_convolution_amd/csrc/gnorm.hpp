@@ -1,0 +1,107 @@
+// gnorm.hpp - group norm with an activation and dropout: what its kernels share (gnorm.hip
+// has the mathematics and the design).
+#pragma once
+
+#include "checkpoint.hpp"
+#include "drop.hpp"
+#include "gelu.hpp"
+#include "norm_common.hpp"
+
+namespace fno {
+
+constexpr int kThreads = 256;
+constexpr long kMaxGrid = 1L << 22;  // workgroups of a launch: the kernels loop past it
+
+inline int gn_vec(int dtype) { return dtype == DT_F32 ? 4 : 8; }
+inline long up(long a, long b) { return (a + b - 1) / b; }
+
+// How a shape runs. team 0: the groups are too large for a workgroup's registers.
+struct GnPlan {
+  bool last;       // rows are a pixel's channels (one pixel: either order)
+  int team, bteam; // threads that hold a group, forward and backward
+  int T;           // lanes of a row (channels first)
+  int S, runs;     // pieces of a row or sample; channels last, small groups: runs of the parameters' sums
+  long per, per_run;
+  size_t parts;    // sums in the workspace
+};
+
+GnPlan gn_plan(const GnArgs &a, int dtype);
+
+enum : int { kActNone = 0, kActGelu = 1, kActSilu = 2 };
+
+// z / (1 + exp(-z)) and its derivative s (1 + z (1 - s)), s = 1 / (1 + exp(-z)); |z| is cut off
+// where it multiplies a vanished term, so infinities have their limits
+__device__ __forceinline__ float sigmoid(float z) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.4426950408889634f));
+}
+__device__ __forceinline__ float act_of(float z, int act) {
+  if (act == kActGelu) return gelu_train(z);
+  if (act == kActSilu) return fmaxf(z, -126.f) * sigmoid(z);
+  return z;
+}
+__device__ __forceinline__ float act_slope(float z, int act) {
+  if (act == kActGelu) return gelu_slope(z);
+  if (act == kActSilu) {
+    const float s = sigmoid(z);
+    return s * fmaf(__builtin_amdgcn_fmed3f(z, -126.f, 126.f), 1.f - s, 1.f);
+  }
+  return 1.f;
+}
+
+// (mean, sum of squared deviations) of na and nb values joined (Chan, Golub, LeVeque: Updating
+// formulae and a pairwise algorithm for computing sample variances, 1979)
+__device__ __forceinline__ void join_moments(float &n, float &mean, float &m2, float nb, float meanb, float m2b) {
+  const float t = n + nb;
+  if (nb == 0.f) return;
+  const float f = nb / t, d = meanb - mean;
+  mean = n == 0.f ? meanb : fmaf(d, f, mean);
+  m2 = n == 0.f ? m2b : m2 + m2b + d * d * n * f;
+  n = t;
+}
+
+template <int W>
+__device__ __forceinline__ float lane_sum(float v) {  // over aligned groups of W lanes
+#pragma unroll
+  for (int o = W / 2; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+
+// sum over the T threads of a group, in every one of them; red: a float a wave
+template <int T>
+__device__ __forceinline__ float team_sum(float v, float *red) {
+  if constexpr (T <= 64) {
+    return lane_sum<T>(v);
+  } else {
+    v = lane_sum<64>(v);
+    const int wave = threadIdx.x >> 6;
+    __syncthreads();  // whoever still reads the last sum
+    if ((threadIdx.x & 63) == 0) red[wave] = v;
+    __syncthreads();
+    v = 0.f;
+#pragma unroll
+    for (int i = 0; i < T / 64; ++i) v += red[i];
+    return v;
+  }
+}
+
+// V consecutive parameters p[i] .. as fp32, `none` where there is no p or i + e >= n
+template <int DT>
+__device__ __forceinline__ void param_piece(const void *p, size_t i, long n, float none, float *o) {
+  constexpr int V = ck_vec<DT>();
+  ck_u32x4 r{0u, 0u, 0u, 0u};
+  if (p) r = ck_load<DT>(p, i, n);
+#pragma unroll
+  for (int e = 0; e < V; ++e) o[e] = p ? ck_get<DT>(r, e) : none;
+}
+
+// kept bits of a chunk: its first value is value `i` of the field in memory order, of channel c and sample b
+template <int V, bool LAST>
+__device__ __forceinline__ uint32_t chunk_keep(const GnArgs &a, const DropKey &key, uint64_t i, long b, int c) {
+  if (a.drop.thr == 0) return 0xffu;
+  if (a.drop.unit == kDropElement) return drop_units(key, a.drop.thr, i, V);
+  if (a.drop.unit == kDropSample) return drop_one(key, a.drop.thr, (uint64_t)b);
+  const uint64_t u = (uint64_t)b * a.C + c;
+  return LAST ? drop_units(key, a.drop.thr, u, V) : drop_one(key, a.drop.thr, u);
+}
+
+}  // namespace fno

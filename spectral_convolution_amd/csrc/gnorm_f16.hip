@@ -1,0 +1,11 @@
+// gnorm_f16.hip - the group norm kernels of f16 fields (gnorm.hip).
+
+#include "gnorm_kernels.hpp"
+
+namespace fno {
+
+hipError_t gnorm_f16(const GnArgs &a, bool fwd, void *workspace, hipStream_t s) {
+  return fwd ? gn_forward<DT_F16>(a, workspace, s) : gn_backward<DT_F16>(a, workspace, s);
+}
+
+}  // namespace fno
