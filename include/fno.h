@@ -642,6 +642,41 @@ fno_status_t fno_group_norm_backward(const fno_group_norm_params_t *params,
                                      long pixels, fno_dtype_t dtype,
                                      void *stream);
 
+/* Microscaled 4-bit floats (the E2M1 elements and E8M0 scales of the OCP
+ * Microscaling Formats specification, MX 1.0) along the channels, the axis that a
+ * channel mix sums over: the field [batch][channels][pixels] is kept as
+ * batch * pixels rows of its channels' values, each row cut into blocks of 32 (the
+ * last may be short). A weight [c_out][c_in] is packed as batch = c_out, channels = c_in,
+ * pixels = 1. With M a block's largest magnitude its power of two is 2^e, e =
+ * max(floor(log2 M) - 2, -127) (-127 where M = 0), and a value x is kept as the nearest of
+ * 0, 1/2, 1, 3/2, 2, 3, 4, 6 to |x| 2^-e, ties to the even code, 6 past it, with x's
+ * sign: off by at most 2^e up to 6 2^e, and by less than 2 2^e past it, so by less than
+ * M / 4 (2^-128 in blocks below 2^-125). A block holding an infinity
+ * or a NaN reads back as NaN throughout, and so does what it is multiplied into.
+ * Layout: codes [rows][16 nb] bytes, nb = ceil(channels / 32), value 2 i of a block in the
+ * low half of its byte i, code = sign * 8 + the index in the list above, 0 past the
+ * channels; then, from the next multiple of 256 bytes, the bytes e + 127 (255: a
+ * NaN block) [rows][nb]; the whole rounded up to 256 bytes (fno_mx4_bytes). packed is
+ * 256-byte aligned, x and y 16. channels <= 65536, batch * pixels <= 2^31, 2^40
+ * values, else UNSUPPORTED. */
+fno_status_t fno_mx4_bytes(int batch, int channels, long pixels, size_t *bytes);
+fno_status_t fno_mx4_pack(const void *x, void *packed, int batch, int channels,
+                          long pixels, fno_dtype_t dtype, void *stream);
+fno_status_t fno_mx4_unpack(const void *packed, void *y, int batch,
+                            int channels, long pixels, fno_dtype_t dtype,
+                            void *stream);
+
+/* The channel mix of two packed operands, xq of a field [batch][c_in][pixels] and Aq
+ * of a weight [c_out][c_in]:
+ *   y[b][o][p] = act(sum_i A[o][i] x[b][i][p] + bias[o] + add[b][o][p]),
+ * products exact, sums in fp32, y rounded once to dtype, which bias and add have
+ * too (either may be NULL); act 0: none, 1: GELU. Sizes as above for either operand
+ * and for y, else UNSUPPORTED. */
+fno_status_t fno_channel_mix_mx4(const void *xq, const void *Aq,
+                                 const void *bias, const void *add, void *y,
+                                 int batch, int c_in, int c_out, long pixels,
+                                 int act, fno_dtype_t dtype, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -116,3 +116,60 @@ def group_norm_backward(x, groups, eps, w, b, kind, last, gy, factor=1.0):
     gx = (r * (q - m1 - h * m2)).reshape(x.shape)
     gxs = (r * (qs + s1 + hs * s2 + hs * abs(m2))).reshape(x.shape)
     return ((gx, (gz * hx).sum(over), gz.sum(over)), (gxs, (gzs * hsx).sum(over), gzs.sum(over)))
+
+
+# -------------------------------------------------------------- 4-bit floats
+
+MX4_VALUES = np.array([0, 0.5, 1, 1.5, 2, 3, 4, 6])
+
+
+def mx4(rows):
+    """(codes [n][nb][32], scale bytes [n][nb]) of rows [n][C]."""
+    n, C = rows.shape
+    nb = -(-C // 32)
+    b = np.zeros((n, nb * 32))
+    b[:, :C] = rows
+    b = b.reshape(n, nb, 32)
+    codes, scales = np.zeros(b.shape, np.uint8), np.zeros((n, nb), np.uint8)
+    for i in range(n):
+        for k in range(nb):
+            big = np.max(np.abs(b[i, k]))
+            if not np.isfinite(big):
+                scales[i, k] = 255
+                continue
+            e = -127 if big == 0 else max(math.frexp(big)[1] - 3, -127)
+            scales[i, k] = e + 127
+            v = np.abs(b[i, k]) * 2.0 ** -float(e)
+            near = np.abs(v[:, None] - MX4_VALUES[None, :])
+            # the nearest, of two as near the one with the even index
+            best = np.where(near == near.min(1, keepdims=True), np.arange(8) % 2, 2).argmin(1)
+            codes[i, k] = best + 8 * np.signbit(b[i, k])
+    return codes, scales
+
+
+def mx4_values(codes, scales, C):
+    v = MX4_VALUES[codes & 7] * np.where(codes >= 8, -1.0, 1.0)
+    step = np.where(scales == 255, np.nan, 2.0 ** (scales.astype(np.float64) - 127))
+    return (v * step[..., None]).reshape(len(codes), -1)[:, :C]
+
+
+def mx4_rows(x):
+    """The rows (b, p) of channels of a field [B][C][P] or tokens [B][C]."""
+    return x if x.ndim == 2 else np.moveaxis(x, 1, 2).reshape(-1, x.shape[1])
+
+
+def mx4_trip(x):
+    """What a field [B][C][P] or tokens [B][C] keep in 4-bit floats."""
+    rows = mx4_rows(x)
+    v = mx4_values(*mx4(rows), rows.shape[1])
+    return v if x.ndim == 2 else np.moveaxis(v.reshape(x.shape[0], x.shape[2], x.shape[1]), 2, 1)
+
+
+def mx4_mix(x, A, bias, add, kind):
+    """(y, sizes of its terms) of fields [B][C][P] at the values given (kept or not)."""
+    z = np.einsum("oi,bip->bop", A, x)
+    size = np.einsum("oi,bip->bop", abs(A), abs(x))
+    for t in (None if bias is None else bias[None, :, None], add):
+        if t is not None:
+            z, size = z + t, size + abs(t)
+    return (act(z, 1) if kind else z), size

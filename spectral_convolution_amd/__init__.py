@@ -9,8 +9,9 @@ if libfno.so is missing, importing a function that needs it raises.
 import ctypes
 
 from ._block_ops import (  # noqa: F401
-    Dropout, GroupNormParams, dropout_residual, fno_dropout_residual, fno_group_norm, fno_group_norm_backward,
-    fno_group_norm_stats_empty, fno_group_norm_workspace_bytes, fno_group_norm_workspace_empty, group_norm)
+    Dropout, GroupNormParams, Mx4Weight, channel_mix_mx4, dropout_residual, fno_channel_mix_mx4, fno_dropout_residual,
+    fno_group_norm, fno_group_norm_backward, fno_group_norm_stats_empty, fno_group_norm_workspace_bytes,
+    fno_group_norm_workspace_empty, fno_mx4_bytes, fno_mx4_empty, fno_mx4_pack, fno_mx4_unpack, group_norm)
 from ._lib import DTYPES, FnoError, check, lib  # noqa: F401
 from ._training import (  # noqa: F401
     NormGrads, NormParams, channel_mix, fno_channel_mix_backward_saved, fno_channel_mix_save,
@@ -38,7 +39,8 @@ __all__ = [
     "fno_norm_residual_workspace_bytes", "fno_norm_residual_workspace_empty", "channel_mix", "norm_residual",
     "Dropout", "fno_dropout_residual", "dropout_residual", "GroupNormParams", "fno_group_norm",
     "fno_group_norm_backward", "fno_group_norm_stats_empty", "fno_group_norm_workspace_bytes",
-    "fno_group_norm_workspace_empty", "group_norm",
+    "fno_group_norm_workspace_empty", "group_norm", "fno_mx4_bytes", "fno_mx4_empty", "fno_mx4_pack", "fno_mx4_unpack",
+    "fno_channel_mix_mx4", "Mx4Weight", "channel_mix_mx4",
 ]
 
 

@@ -14,7 +14,7 @@ def _check_capture(*inputs):
     """Refuse a call that is captured into a graph while an autograd graph made before, on another stream, still
     holds one of its leaves: the captured backward would wait for that stream, and the capture's end would
     end the process."""
-    if torch.cuda.is_current_stream_capturing() and torch.is_grad_enabled():
+    if inputs[0].is_cuda and torch.is_grad_enabled() and torch.cuda.is_current_stream_capturing():
         ops.base._t()
         if ops.base._native.elsewhere(*inputs):
             raise RuntimeError("a leaf of this call belongs to an autograd graph that lives on another stream: drop "

@@ -1,5 +1,6 @@
 """Binding of the operators of a regularised block (include/fno.h): group norm
-with an activation and dropout, and dropout into a residual stream. The names are
+with an activation and dropout, dropout into a residual stream, and the block's channel
+mix on microscaled 4-bit floats, for serving. The names are
 re-exported by the package; these functions check and marshal arguments, every
 value is computed in the library's kernels.
 """
@@ -148,6 +149,85 @@ def fno_group_norm_backward(params, x, stats, gy, gx, gw, gb, workspace, dropout
     ps = _stats(stats, B, G, dev, False)
     base._call("fno_group_norm_backward", dev, stream, params._struct(pw, pb), _drop(dropout, x), px, ps, pgy, pgx, pgw,
                pgb, ws, B, C, P, DTYPES[dt])
+
+
+# -------------------------------------------------------------- 4-bit floats
+
+def fno_mx4_bytes(batch, channels, pixels=1):
+    """Bytes of a [batch][channels][pixels] field (a weight: [c_out][c_in]) in 4-bit floats."""
+    return base._bytes("fno_mx4_bytes", batch, channels, pixels)
+
+
+def fno_mx4_empty(x):
+    """A device buffer (uint8 tensor) for x, [B][C](...), in 4-bit floats."""
+    return base._empty(fno_mx4_bytes(*base._split(tuple(x.shape), "x")), x)
+
+
+def fno_mx4_pack(x, packed, stream=None):
+    """Keep x, [B][C](...), in 4-bit floats in `packed`: blocks of 32 along the channels."""
+    dt, td, dev, shape = base._field(x, "x")
+    B, C, P = base._split(shape, "x")
+    s = base._buffer("packed", packed, fno_mx4_bytes(B, C, P), 256, x)
+    (p,) = base._ptrs(("x",), 1, td, dev, x, x, shape)
+    base._call("fno_mx4_pack", dev, stream, p, s, B, C, P, DTYPES[dt])
+
+
+def fno_mx4_unpack(packed, y, stream=None):
+    """Read the values kept in `packed` back into y (shape as packed)."""
+    dt, td, dev, shape = base._field(y, "y")
+    B, C, P = base._split(shape, "y")
+    s = base._buffer("packed", packed, fno_mx4_bytes(B, C, P), 256, y)
+    (p,) = base._ptrs(("y",), 1, td, dev, y, y, shape)
+    base._call("fno_mx4_unpack", dev, stream, s, p, B, C, P, DTYPES[dt])
+
+
+def fno_channel_mix_mx4(xq, Aq, bias, add, y, c_in, act=0, stream=None):
+    """y = act(A x + bias + add) of a packed field (or tokens) of c_in channels and a packed weight; y
+    [B][c_out](...), bias and add (either may be None) have the storage type."""
+    dt, td, dev, shape = base._field(y, "y")
+    B, O, P = base._split(shape, "y")
+    py, pbias, padd = base._ptrs(("y", "bias", "add"), 1, td, dev, y, y, shape, bias, (O,), add, shape)
+    px = base._buffer("xq", xq, fno_mx4_bytes(B, c_in, P), 256, y)
+    pA = base._buffer("Aq", Aq, fno_mx4_bytes(O, c_in), 256, y)
+    base._call("fno_channel_mix_mx4", dev, stream, px, pA, pbias, padd, py, B, c_in, O, P, act, DTYPES[dt])
+
+
+class Mx4Weight:
+    """A weight [c_out][c_in] kept in 4-bit floats for channel_mix_mx4: 17 bytes for each 32 values that
+    a row begins."""
+
+    __slots__ = ("c_out", "c_in", "packed")
+
+    def __init__(self, A):
+        torch = base._t()
+        if not isinstance(A, torch.Tensor) or A.dim() != 2:
+            raise ValueError("A must be a [c_out][c_in] tensor")
+        A = A.detach().contiguous()
+        if A.data_ptr() % 16:
+            A = A.clone()
+        self.c_out, self.c_in = A.shape
+        self.packed = fno_mx4_empty(A)
+        fno_mx4_pack(A, self.packed)
+
+
+def channel_mix_mx4(x, weight, bias=None, add=None, act=0):
+    """act(A x + bias + add) with A an Mx4Weight and x, [B][C](...), packed to 4-bit floats on the
+    way. For serving: it has no gradient, and refuses inputs that want one."""
+    torch = base._t()
+    if not isinstance(weight, Mx4Weight):
+        raise TypeError("weight must be an Mx4Weight")
+    if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in (x, bias, add)):
+        raise ValueError("channel_mix_mx4 has no gradient: call it under torch.no_grad()")
+    from ._training_autograd import _dense
+    x, add = _dense(x), _dense(add)
+    shape = tuple(x.shape)
+    if len(shape) < 2 or shape[1] != weight.c_in:
+        raise ValueError(f"x shape {shape} does not have the weight's {weight.c_in} channels")
+    packed = fno_mx4_empty(x)
+    fno_mx4_pack(x, packed)
+    y = torch.empty((shape[0], weight.c_out) + shape[2:], dtype=x.dtype, device=x.device)
+    fno_channel_mix_mx4(packed, weight.packed, None if bias is None else bias.contiguous(), add, y, weight.c_in, act)
+    return y
 
 
 # ------------------------------------------------- differentiable functions

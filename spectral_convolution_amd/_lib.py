@@ -98,6 +98,10 @@ SIGNATURES = {
     "fno_norm_residual_backward": (_c_int, [_NormP] + [_c_void_p] * 6 + [_NormG, _c_void_p] + _BCP),
     "fno_norm_residual_backward_saved": (_c_int, [_NormP] + [_c_void_p] * 5 + [_NormG, _c_void_p] + _BCP),
     "fno_dropout_residual": (_c_int, [_DropP] + [_c_void_p] * 3 + [_c_int, _c_int, _c_long, _c_int, _c_int, _c_void_p]),
+    "fno_mx4_bytes": (_c_int, [_c_int, _c_int, _c_long, _SizeP]),
+    "fno_mx4_pack": (_c_int, [_c_void_p, _c_void_p] + _BCP),
+    "fno_mx4_unpack": (_c_int, [_c_void_p, _c_void_p] + _BCP),
+    "fno_channel_mix_mx4": (_c_int, [_c_void_p] * 5 + [_c_int, _c_int, _c_int, _c_long, _c_int, _c_int, _c_void_p]),
     "fno_group_norm_workspace_bytes": (_c_int, [_c_int, _c_int, _c_long, _c_int, _c_int, _c_int, _SizeP]),
     "fno_group_norm": (_c_int, [_GnP, _DropP] + [_c_void_p] * 4 + _BCP),
     "fno_group_norm_backward": (_c_int, [_GnP, _DropP] + [_c_void_p] * 7 + _BCP),

@@ -23,8 +23,8 @@ NATIVE = os.path.join(HERE, "_native.so")
 
 SOURCES = ["plane_kernels.hip", "plane_mfma.hip", "axis_kernels.hip", "contract.hip", "contract_mx.hip", "backward.hip", "weights.hip", "pointwise.hip", "fused.hip", "fno_api.cpp",
            "fno_model.cpp", "checkpoint.hip", "norm.hip", "norm_f32.hip", "norm_f16.hip", "norm_bf16.hip", "mix_train.hip", "mix_train_f16.hip", "mix_train_bf16.hip",
-           "fno_train.cpp", "drop.hip", "gnorm.hip", "gnorm_f32.hip", "gnorm_f16.hip", "gnorm_bf16.hip", "fno_block_ops.cpp"]
-HEADERS = ["common.hpp", "fft_reg.hpp", "plane_common.hpp", "plane_valu.hpp", "plane_mfma.hpp", "contract.hpp", "train.hpp", "checkpoint.hpp", "gelu.hpp", "mix_train.hpp", "mix_train_half.hpp", "norm_common.hpp", "norm_field.hpp", "norm_token.hpp", "call_check.hpp", "block_ops.hpp", "drop.hpp", "gnorm.hpp", "gnorm_kernels.hpp"]
+           "fno_train.cpp", "drop.hip", "gnorm.hip", "gnorm_f32.hip", "gnorm_f16.hip", "gnorm_bf16.hip", "mx4.hip", "mx4_mix.hip", "fno_block_ops.cpp"]
+HEADERS = ["common.hpp", "fft_reg.hpp", "plane_common.hpp", "plane_valu.hpp", "plane_mfma.hpp", "contract.hpp", "train.hpp", "checkpoint.hpp", "gelu.hpp", "mix_train.hpp", "mix_train_half.hpp", "norm_common.hpp", "norm_field.hpp", "norm_token.hpp", "call_check.hpp", "block_ops.hpp", "drop.hpp", "gnorm.hpp", "gnorm_kernels.hpp", "mx4.hpp"]
 
 ARCH = "gfx950"
 CFLAGS = [

@@ -54,6 +54,8 @@ constexpr long kGnMaxPixels = 1L << 27;
 size_t gnorm_workspace_bytes(const GnArgs &a, int dtype);  // of the shape: B, C, G, Cg, P, last
 hipError_t launch_gnorm(const GnArgs &a, bool fwd, void *workspace, int dtype, hipStream_t s);
 
+constexpr int kMx4MaxChannels = 65536;
+constexpr long kMx4MaxRows = 1L << 31;
 // microscaled 4-bit floats (mx4.hpp): rows (b, p) of C values along the channels
 struct Mx4Args {
   const void *x;   // pack reads [B][C][P]

@@ -33,6 +33,8 @@ struct NormArgs;
 struct MixTrainArgs;
 struct DropArgs;
 struct GnArgs;
+struct Mx4Args;
+struct Mx4MixArgs;
 
 namespace bounds {
 // [p, p + n) inside one live allocation of the recording runtime (n = 0: true)
@@ -69,6 +71,8 @@ void check_gnorm_rows(const GnArgs &a, bool bwd, bool out, int T, int dtype);
 void check_gnorm_cols(const GnArgs &a, bool bwd, bool out, bool runs, int dtype);
 void check_gnorm_join(const GnArgs &a, bool bwd, int dtype);
 void check_gnorm_params(const GnArgs &a, int samples, int dtype);
+void check_mx4(const Mx4Args &a, bool pack, int dtype);
+void check_mx4_mix(const Mx4MixArgs &a, int dtype);
 
 }  // namespace fno
 

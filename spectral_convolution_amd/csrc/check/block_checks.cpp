@@ -1,9 +1,10 @@
 // block_checks.cpp - the bounds-check build's model of the block operators' launches
-// (gnorm_kernels.hpp, drop.hip), as launch_checks.cpp has those of the others. Host code only.
+// (gnorm_kernels.hpp, drop.hip, mx4.hip, mx4_mix.hip), as launch_checks.cpp has those of the others. Host code only.
 
 #include <algorithm>
 
 #include "../gnorm.hpp"
+#include "../mx4.hpp"
 
 namespace fno {
 
@@ -139,6 +140,39 @@ void check_gnorm_params(const GnArgs &a, int samples, int dtype) {
   c.opt("gb", a.gb, a.C * es);
   c.span("sums", a.part, (size_t)samples * a.S * a.C * 8);
   c.need("last sum", (samples - 1) * a.sb + (a.C - 1) * a.sc + (a.S - 1) * a.ss < (long)samples * a.S * a.C);
+}
+
+void check_mx4(const Mx4Args &a, bool pack, int dtype) {
+  const Ctx c{pack ? "fno_mx4_pack" : "fno_mx4_unpack"};
+  const long rows = a.B * a.P;
+  c.span("field", pack ? a.x : a.y, (size_t)a.B * a.C * a.P * es_of(dtype));
+  c.span("codes", a.codes, (size_t)rows * a.nb * 16);
+  c.span("scales", a.exps, (size_t)rows * a.nb);
+  c.need("blocks cover the row", a.nb == (a.C + 31) / 32);
+  c.need("codes 16-byte aligned", ((uintptr_t)a.codes & 15) == 0);
+  c.need("units of a row in 32 bits, rows in 31", 4 * a.nb + 1024 < 1L << 31 && rows <= 1L << 31);
+  if (a.P > 1) {  // the lanes of the first and last workgroups, placed as the kernel does
+    const long np = dtype == DT_F32 ? 2 : 4, ppr = (a.P + np - 1) / np, total = a.B * ppr;
+    for (long q : {0L, ppr - 1, total - 1}) {
+      const long b = q / ppr, p = (q - b * ppr) * np, n = std::min(np, a.P - p);
+      c.need("pixels of a lane", b < a.B && p >= 0 && n >= 1 && p + n <= a.P);
+    }
+    c.need("lanes for the grid", total + 256 < 1L << 32);
+  }
+}
+
+void check_mx4_mix(const Mx4MixArgs &a, int dtype) {
+  const Ctx c{"fno_mx4_mix"};
+  const size_t es = es_of(dtype), n = (size_t)a.B * a.O * a.P * es, rows = (size_t)a.B * a.P;
+  c.span("codes of x", a.xq, rows * a.nb * 16);
+  c.span("scales of x", a.xe, rows * a.nb);
+  c.span("codes of A", a.aq, (size_t)a.O * a.nb * 16);
+  c.span("scales of A", a.ae, (size_t)a.O * a.nb);
+  c.opt("bias", a.bias, a.O * es);
+  c.opt("add", a.add, n);
+  c.span("y", a.y, n);
+  c.need("blocks cover the row", a.nb == (a.I + 31) / 32);
+  c.need("codes 16-byte aligned", (((uintptr_t)a.xq | (uintptr_t)a.aq) & 15) == 0);
 }
 
 }  // namespace fno

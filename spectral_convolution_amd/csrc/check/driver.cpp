@@ -224,6 +224,20 @@ void run_gnorm(int B, int C, long P, int G, int last, fno_dtype_t dt) {
   EXPECT(fno_group_norm_backward(&q, nullptr, x, stats, gy, gx, nullptr, nullptr, ws, B, C, P, dt, nullptr) == FNO_OK);
 }
 
+// a field to 4-bit floats and back, and a channel mix of it; nothing behind the buffers
+void run_mx4(int B, int I, int O, long P, fno_dtype_t dt) {
+  size_t xb = 0, ab = 0;
+  EXPECT(fno_mx4_bytes(B, I, P, &xb) == FNO_OK);
+  EXPECT(fno_mx4_bytes(O, I, 1, &ab) == FNO_OK);
+  const size_t es = es_of(dt), nx = (size_t)B * I * P * es, ny = (size_t)B * O * P * es;
+  void *x = check_reserve(nx), *xq = check_reserve(xb), *aq = check_reserve(ab), *y = check_reserve(ny), *add = check_reserve(ny),
+       *bias = check_reserve(O * es);
+  EXPECT(fno_mx4_pack(x, xq, B, I, P, dt, nullptr) == FNO_OK);
+  EXPECT(fno_mx4_unpack(xq, x, B, I, P, dt, nullptr) == FNO_OK);
+  EXPECT(fno_channel_mix_mx4(xq, aq, bias, add, y, B, I, O, P, 1, dt, nullptr) == FNO_OK);
+  EXPECT(fno_channel_mix_mx4(xq, aq, nullptr, nullptr, y, B, I, O, P, 0, dt, nullptr) == FNO_OK);
+}
+
 // one call of a training operator, forward and backward, with nothing behind its buffers
 void trace_call(const std::string &op, int dt, const std::vector<long> &v) {
   const auto d = (fno_dtype_t)dt;
@@ -346,6 +360,12 @@ int main(int argc, char **argv) {
   for (const G &c : gg)
     for (fno_dtype_t dt : dts)
       for (int last = 0; last < 2; ++last) run_gnorm(c.B, c.C, c.P, c.G, last, dt);
+  struct X { int B, I, O; long P; };
+  const X xx[] = {{1, 1, 1, 1}, {2, 4, 4, 256}, {3, 33, 70, 7}, {5, 200, 72, 1001}, {8192, 4096, 4096, 1}, {1, 8192, 8192, 1},
+                  {32, 64, 64, 65536}, {16, 65536, 3, 1}, {2, 31, 129, 2}, {700, 96, 40, 1}, {1, 64, 512, 1L << 31},
+                  {2147483647, 32, 64, 1}, {1 << 20, 17, 5, 2047}};
+  for (const X &c : xx)
+    for (fno_dtype_t dt : dts) run_mx4(c.B, c.I, c.O, c.P, dt);
   const long reports = check_reports();
   // the checker itself: spans past the end of a buffer must be reported
   {

@@ -11,6 +11,7 @@
 
 #include "block_ops.hpp"
 #include "call_check.hpp"
+#include "mx4.hpp"
 
 using namespace fno;
 
@@ -62,9 +63,77 @@ fno_status_t gn_params(const fno_group_norm_params_t *p, const fno_dropout_t *dr
   return FNO_OK;
 }
 
+// ---- 4-bit floats
+
+fno_status_t mx4_shape(int batch, int channels, long pixels, fno_dtype_t dtype) {
+  if (batch < 1 || channels < 1 || pixels < 1 || !valid_dtype(dtype)) return FNO_ERR_INVALID_ARG;
+  if (channels > kMx4MaxChannels || pixels > kMx4MaxRows / batch || !values_in_range(batch, channels, pixels))
+    return FNO_ERR_UNSUPPORTED;
+  return FNO_OK;
+}
+
+fno_status_t run_mx4(const void *x, void *y, const void *packed, bool pack, int batch, int channels, long pixels,
+                     fno_dtype_t dtype, void *stream) {
+  if (!packed || !(pack ? x : y)) return FNO_ERR_INVALID_ARG;
+  const fno_status_t st = mx4_shape(batch, channels, pixels, dtype);
+  if (st != FNO_OK) return st;
+  const Mx4Layout l = mx4_layout(batch * pixels, channels);
+  const size_t bytes = (size_t)batch * channels * pixels * esize(dtype);
+  Spans s;
+  if (pack) {
+    s.in(x, bytes, 16);
+    s.out(packed, l.bytes, 256);
+  } else {
+    s.in(packed, l.bytes, 256);
+    s.out(y, bytes, 16);
+  }
+  if (!s.ok()) return FNO_ERR_INVALID_ARG;
+  uint8_t *base = static_cast<uint8_t *>(const_cast<void *>(packed));
+  const Mx4Args a{x, y, base, base + l.exps, batch, channels, pixels, l.nb};
+  return status_of(launch_mx4(a, pack, (int)dtype, (hipStream_t)stream));
+}
+
 }  // namespace
 
 extern "C" {
+
+fno_status_t fno_mx4_bytes(int batch, int channels, long pixels, size_t *bytes) {
+  if (!bytes) return FNO_ERR_INVALID_ARG;
+  const fno_status_t st = mx4_shape(batch, channels, pixels, FNO_F32);
+  if (st == FNO_OK) *bytes = mx4_layout(batch * pixels, channels).bytes;
+  return st;
+}
+
+fno_status_t fno_mx4_pack(const void *x, void *packed, int batch, int channels, long pixels, fno_dtype_t dtype,
+                          void *stream) {
+  return run_mx4(x, nullptr, packed, true, batch, channels, pixels, dtype, stream);
+}
+
+fno_status_t fno_mx4_unpack(const void *packed, void *y, int batch, int channels, long pixels, fno_dtype_t dtype,
+                            void *stream) {
+  return run_mx4(nullptr, y, packed, false, batch, channels, pixels, dtype, stream);
+}
+
+fno_status_t fno_channel_mix_mx4(const void *xq, const void *Aq, const void *bias, const void *add, void *y, int batch,
+                                 int c_in, int c_out, long pixels, int act, fno_dtype_t dtype, void *stream) {
+  if (!xq || !Aq || !y || (act != 0 && act != 1)) return FNO_ERR_INVALID_ARG;
+  for (int c : {c_in, c_out}) {
+    const fno_status_t st = mx4_shape(batch, c, pixels, dtype);
+    if (st != FNO_OK) return st;
+  }
+  const Mx4Layout lx = mx4_layout(batch * pixels, c_in), la = mx4_layout(c_out, c_in);
+  const size_t es = esize(dtype), n = (size_t)batch * c_out * pixels * es;
+  Spans s;
+  s.in(xq, lx.bytes, 256);
+  s.in(Aq, la.bytes, 256);
+  s.in(bias, c_out * es, es);
+  s.in(add, n, 16);
+  s.out(y, n, 16);
+  if (!s.ok()) return FNO_ERR_INVALID_ARG;
+  const uint8_t *x = static_cast<const uint8_t *>(xq), *A = static_cast<const uint8_t *>(Aq);
+  const Mx4MixArgs a{x, x + lx.exps, A, A + la.exps, bias, add, y, batch, c_in, c_out, pixels, lx.nb, act};
+  return status_of(launch_mx4_mix(a, (int)dtype, (hipStream_t)stream));
+}
 
 fno_status_t fno_dropout_residual(const fno_dropout_t *drop, const void *x, const void *v, void *y, int batch,
                                   int channels, long pixels, int channels_last, fno_dtype_t dtype, void *stream) {

@@ -178,7 +178,57 @@ def test_binding_refuses():
         fno.fno_group_norm_workspace_empty(x[0, 0], 2)
 
 
+def test_mx4_definition():
+    """Exact values keep, ties go to the even code, the cut is at 6, the error is as documented."""
+    v = np.array([[0, 0.5, 1, 1.5, 2, 3, 4, 6, 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5, 7.99, -0.0, -5.1] + [0.0] * 14])
+    q, s = ref.mx4(v)
+    assert s[0, 0] == 127
+    assert list(q[0, 0, :18]) == [0, 1, 2, 3, 4, 5, 6, 7, 0, 2, 2, 4, 4, 6, 6, 7, 8, 15]
+    rng = np.random.default_rng(0)
+    x = rng.standard_normal((50, 96)) * np.exp(2 * rng.standard_normal((50, 96)))
+    got = ref.mx4_trip(x)
+    M = abs(x).reshape(50, 3, 32).max(-1).repeat(32, -1).reshape(50, 96)
+    assert (abs(got - x) <= M / 4).all()
+    unit = 2.0 ** (np.floor(np.log2(M)) - 2)  # half the widest step between values below the cut
+    assert (abs(got - x) <= unit)[abs(x) <= 6 * unit].all()
+    assert np.array_equal(ref.mx4_trip(got), got)
+
+
+def test_mx4_refuses(L):
+    n = ctypes.c_size_t()
+    m, o, z = _mem(), _mem(), _mem()
+    for B, C, P, st in ((0, 4, 4, INVALID), (2, 0, 4, INVALID), (2, 4, 0, INVALID), (2, 65537, 1, UNSUPPORTED),
+                        (2, 32, (1 << 30) + 1, UNSUPPORTED), (1 << 20, 65536, 1 << 6, UNSUPPORTED)):
+        assert L.fno_mx4_bytes(B, C, P, ctypes.byref(n)) == st
+        assert L.fno_mx4_pack(m, o, B, C, P, 0, None) == st
+        assert L.fno_mx4_unpack(m, o, B, C, P, 0, None) == st
+        assert L.fno_channel_mix_mx4(m, o, None, None, z, B, C, 4, P, 0, 0, None) == st
+        assert L.fno_channel_mix_mx4(m, o, None, None, z, B, 4, C, P, 0, 0, None) == st
+    assert L.fno_mx4_bytes(2, 4, 4, None) == INVALID
+    for f in (L.fno_mx4_pack, L.fno_mx4_unpack):
+        assert f(None, o, 2, 4, 4, 0, None) == INVALID
+        assert f(m, None, 2, 4, 4, 0, None) == INVALID
+        assert f(m, m, 2, 4, 4, 0, None) == INVALID
+        assert f(m, o, 2, 4, 4, 7, None) == INVALID
+        assert f(m + 8, o, 2, 4, 4, 0, None) == INVALID
+        assert f(m, o + 8, 2, 4, 4, 0, None) == INVALID
+    assert L.fno_mx4_pack(m, o + 16, 2, 4, 4, 0, None) == INVALID  # packed: 256 bytes
+    f = L.fno_channel_mix_mx4
+    assert f(None, o, None, None, z, 2, 4, 4, 4, 0, 0, None) == INVALID
+    assert f(m, None, None, None, z, 2, 4, 4, 4, 0, 0, None) == INVALID
+    assert f(m, o, None, None, None, 2, 4, 4, 4, 0, 0, None) == INVALID
+    assert f(m, o, None, None, z, 2, 4, 4, 4, 2, 0, None) == INVALID
+    assert f(m, o, None, None, z, 2, 4, 4, 4, 0, 3, None) == INVALID
+    assert f(m + 16, o, None, None, z, 2, 4, 4, 4, 0, 0, None) == INVALID
+    assert f(m, o, z, None, z, 2, 4, 4, 4, 0, 0, None) == INVALID
+    assert f(m, o, None, z, z, 2, 4, 4, 4, 0, 0, None) == INVALID
+    assert f(m, o, None, None, m, 2, 4, 4, 4, 0, 0, None) == INVALID
+    assert f(m, o, z + 2, None, _mem(), 2, 4, 4, 4, 0, 0, None) == INVALID
+
+
 @pytest.mark.parametrize("call", [
+    lambda: fno.fno_mx4_bytes((1 << 32) + 2, 4), lambda: fno.fno_mx4_bytes(2, (1 << 32) + 4),
+    lambda: fno.fno_mx4_bytes(2, 4, (1 << 64) + 4),
     lambda: fno.fno_group_norm_workspace_bytes((1 << 32) + 2, 4, 16, 2),
     lambda: fno.fno_group_norm_workspace_bytes(2, (1 << 32) + 4, 16, 2),
     lambda: fno.fno_group_norm_workspace_bytes(2, 4, (1 << 64) + 16, 2),

@@ -1,0 +1,209 @@
+"""GPU parity of the 4-bit floats: codes and scales have to be equal to their definition's
+(oracle/block.py), the channel mix of packed operands within its roundings."""
+
+import numpy as np
+import pytest
+import torch
+
+import spectral_convolution_amd as fno
+from oracle import block as ref
+from training_util import DT, close, f64, stored
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+DTYPES = ["f32", "f16", "bf16"]
+
+
+def parts(packed, rows, C):
+    nb = -(-C // 32)
+    b = packed.cpu().numpy()
+    q = b[:rows * nb * 16].reshape(rows, nb, 16)
+    at = -(-rows * nb * 16 // 256) * 256
+    return np.stack([q & 15, q >> 4], -1).reshape(rows, nb, 32), b[at:at + rows * nb].reshape(rows, nb)
+
+
+def pack(x):
+    packed = torch.full((fno.fno_mx4_bytes(x.shape[0], x.shape[1], x[0, 0].numel()),), 77, dtype=torch.uint8, device=DEV)
+    fno.fno_mx4_pack(x.to(DEV), packed)
+    return packed
+
+
+def check_kept(x, x64):
+    """Codes, scales and the values read back are the definition's."""
+    packed = pack(x)
+    rows = ref.mx4_rows(x64)
+    q, s = ref.mx4(rows)
+    gq, gs = parts(packed, len(rows), rows.shape[1])
+    assert (gs == s).all() and (gq == q).all()
+    y = torch.full_like(x.to(DEV), 3.0)
+    fno.fno_mx4_unpack(packed, y)
+    assert np.array_equal(f64(y), ref.mx4_trip(x64), equal_nan=True)
+    return packed
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", [(1, 1), (3, 31), (2, 32), (5, 33), (300, 40), (7, 1000), (2, 8192), (1, 65536), (1, 1, 2),
+                                   (2, 4, 256), (3, 33, 7), (1, 64, 1001), (2, 130, 3), (5, 7, 5), (2, 96, 65), (70, 40, 33)],
+                         ids=str)
+def test_kept_values(dtype, shape):
+    x, x64 = stored(np.random.default_rng(sum(shape)), shape, dtype, spread=True)
+    check_kept(x, x64)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("field", [False, True])
+def test_ties_and_ends(dtype, field):
+    """Every border between codes, from both sides, at scales from the type's lowest to its highest."""
+    fi = torch.finfo(DT[dtype])
+    least = {"f32": -149, "f16": -24, "bf16": -133}[dtype]
+    most = int(np.log2(fi.max))
+    rows = []
+    borders = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5, 6, 7, 7.5])
+    near = np.concatenate([borders, borders * (1 + float(fi.eps)), borders * (1 - float(fi.eps))])
+    for e in (least, least + 1, least + 3, -126, -127, -125, -14, 0, 5, most - 2):
+        if e < least:
+            continue
+        rows.append(np.concatenate([near, [4.0, -0.0]]) * 2.0 ** e)
+        rows.append(-np.concatenate([near[:15], [7.9375] * 17]) * 2.0 ** e)
+    rows += [np.zeros(32), -np.zeros(32), np.full(32, float(fi.max)), np.full(32, 2.0 ** least), np.full(32, float(fi.tiny))]
+    x = torch.tensor(np.array(rows)).to(DT[dtype])
+    if field:
+        x = x.t().reshape(1, 32, -1).contiguous()
+    check_kept(x, x.double().numpy())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("field", [False, True])
+def test_poisoned_blocks(dtype, field):
+    x = torch.ones(5, 100)
+    x[0, 5], x[1, 40], x[2, 99], x[3, 63] = float("nan"), float("inf"), -float("inf"), -float("nan")
+    x = x.to(DT[dtype])
+    if field:
+        x = x.t().reshape(1, 100, 5).contiguous()
+    check_kept(x, x.double().numpy())
+
+
+# ------------------------------------------------------------------ products
+
+def mix(dtype, B, I, O, P, act, add, bias, seed=0, poison=None):
+    rng = np.random.default_rng(seed)
+    shape = (B, I) if P == 1 else (B, I, P)
+    x, x64 = stored(rng, shape, dtype, spread=True)
+    A, A64 = stored(rng, (O, I), dtype, I ** -0.5)
+    b, b64 = stored(rng, (O,), dtype, 0.3) if bias else (None, None)
+    out = (B, O) if P == 1 else (B, O, P)
+    d, d64 = stored(rng, out, dtype) if add else (None, None)
+    y = torch.full(out, 7.0, dtype=DT[dtype], device=DEV)
+    dev = lambda t: None if t is None else t.to(DEV)  # noqa: E731
+    fno.fno_channel_mix_mx4(pack(x), pack(A), dev(b), dev(d), y, I, act=act)
+    x3 = ref.mx4_trip(x64).reshape(B, I, P)
+    want, size = ref.mx4_mix(x3, ref.mx4_trip(A64), b64, None if d64 is None else d64.reshape(B, O, P), act)
+    return y, want.reshape(out), size.reshape(out)
+
+
+# (B, I, O, P): one value, block and step ends, tile ends in rows and columns, tokens and fields, few and many rows
+MIXES = [(1, 1, 1, 1), (1, 33, 5, 1), (2, 128, 64, 1), (17, 129, 70, 1), (300, 200, 257, 1), (1, 4096, 96, 1), (3, 1000, 33, 1),
+         (16, 512, 512, 1), (33, 512, 130, 1), (260, 544, 513, 1), (1, 32, 1, 2), (2, 4, 4, 256), (3, 31, 7, 5), (2, 64, 64, 300),
+         (1, 200, 72, 1001), (4, 96, 130, 17), (5, 40, 3, 63), (1, 512, 300, 515)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", MIXES, ids=str)
+def test_mix(dtype, shape):
+    i = MIXES.index(shape)
+    for act, add, bias in ((0, False, False), (1, True, True), (i % 2, i % 3 == 0, True)):
+        y, want, size = mix(dtype, *shape, act, add, bias, seed=i)
+        close("y", y, want, dtype, size=size)
+
+
+def test_poisoned_block_poisons_its_products():
+    for P in (1, 40):
+        x = torch.ones((4, 100) if P == 1 else (4, 100, P), device=DEV)
+        A = torch.ones(20, 100, device=DEV)
+        x[2, 50] = float("nan")
+        A[7, 99] = float("inf")
+        y = torch.empty((4, 20) if P == 1 else (4, 20, P), device=DEV)
+        fno.fno_channel_mix_mx4(pack(x), pack(A), None, None, y, 100)
+        bad = torch.zeros_like(y, dtype=torch.bool)
+        bad[2], bad[:, 7] = True, True
+        assert torch.isnan(y[bad]).all() and (y[~bad] == 100).all()
+
+
+def test_wide_scales():
+    """Operands whose scales lie at opposite ends multiply to ordinary values."""
+    x, A = torch.randn(40, 256, device=DEV), torch.randn(30, 256, device=DEV)
+    y, big = torch.empty(40, 30, device=DEV), torch.empty(40, 30, device=DEV)
+    fno.fno_channel_mix_mx4(pack(x), pack(A), None, None, y, 256)
+    fno.fno_channel_mix_mx4(pack(x * 2.0 ** 110), pack(A * 2.0 ** -110), None, None, big, 256)
+    assert torch.equal(y, big)
+
+
+def test_repeats_bit_for_bit_on_streams_and_in_a_graph():
+    for shape in ((1, 2048, 300), (200, 600, 300)):
+        B, I, O = shape
+        x, A = torch.randn(B, I, device=DEV), torch.randn(O, I, device=DEV)
+        xq, Aq = fno.fno_mx4_empty(x), pack(A)
+        y, want = torch.empty(B, O, device=DEV), torch.empty(B, O, device=DEV)
+
+        def step(out):
+            fno.fno_mx4_pack(x, xq)
+            fno.fno_channel_mix_mx4(xq, Aq, None, None, out, I, act=1)
+
+        step(want)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(torch.cuda.Stream()):
+            step(y)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step(y)
+        for _ in range(3):
+            y.zero_()
+            x.mul_(1.5)
+            step(want)
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(3, 40, 21, 1), (2, 40, 21, 35), (1, 600, 513, 1), (300, 512, 260, 1)], ids=str)
+def test_guards(dtype, shape):
+    """Nothing is written beside the outputs."""
+    B, I, O, P = shape
+    x = torch.randn((B, I) if P == 1 else (B, I, P), device=DEV).to(DT[dtype])
+    A = torch.randn(O, I, device=DEV)
+    size = fno.fno_mx4_bytes(B, I, P)
+    buf = torch.full((size + 512,), 99, dtype=torch.uint8, device=DEV)
+    fno.fno_mx4_pack(x, buf[256:256 + size])
+    assert (buf[:256] == 99).all() and (buf[256 + size:] == 99).all()
+    n = B * O * P
+    out = torch.full((n + 128,), 3.0, dtype=DT[dtype], device=DEV)
+    y = out[64:64 + n].view((B, O) if P == 1 else (B, O, P)).fill_(float("nan"))
+    fno.fno_channel_mix_mx4(buf[256:256 + size], pack(A), None, None, y, I)
+    assert (out[:64] == 3).all() and (out[64 + n:] == 3).all() and torch.isfinite(y).all()
+    n = x.numel()
+    out = torch.full((n + 128,), 3.0, dtype=DT[dtype], device=DEV)
+    fno.fno_mx4_unpack(buf[256:256 + size], out[64:64 + n].view(x.shape))
+    assert (out[:64] == 3).all() and (out[64 + n:] == 3).all()
+
+
+@pytest.mark.parametrize("grid", [(), (5, 7), (3, 4, 5)], ids=str)
+def test_serving_call(grid):
+    x = torch.randn(2, 70, *grid, device=DEV)
+    A, b, add = torch.randn(33, 70, device=DEV), torch.randn(33, device=DEV), torch.randn(2, 33, *grid, device=DEV)
+    w = fno.Mx4Weight(A)
+    y = fno.channel_mix_mx4(x, w, b, add, act=1)
+    P = x[0, 0].numel()
+    x3 = ref.mx4_trip(f64(x).reshape(2, 70, P))
+    want, size = ref.mx4_mix(x3, ref.mx4_trip(f64(A)), f64(b), f64(add).reshape(2, 33, P), 1)
+    close("y", y.reshape(2, 33, P), want, "f32", size=size)
+    strided = torch.randn(70, 2, *grid, device=DEV).transpose(0, 1)
+    assert torch.equal(fno.channel_mix_mx4(strided, w), fno.channel_mix_mx4(strided.contiguous(), w))
+    with pytest.raises(ValueError, match="gradient"):
+        fno.channel_mix_mx4(x.requires_grad_(), w)
+    with torch.no_grad():
+        assert torch.equal(fno.channel_mix_mx4(x, w, b, add, act=1), y)
+    with pytest.raises(ValueError, match="channels"):
+        fno.channel_mix_mx4(x.detach()[:, :69].contiguous(), w)
