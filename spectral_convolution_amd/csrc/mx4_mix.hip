@@ -164,6 +164,293 @@ __global__ __launch_bounds__(kThreads) void fno_mx4_mix(Gemm g) {
   }
 }
 
+// Few second rows (one token, a handful): a workgroup has 16 f and all 16 NS s, its eight waves an
+// eighth of the steps each, joined through LDS. Every load of a wave's next U steps is in flight at a time: bound by
+// the first operand's bytes. WHOLE: rows of whole steps (nb % 4 == 0), scales four at a time.
+template <int DT, int NS, bool WHOLE>
+__global__ __launch_bounds__(512) void fno_mx4_mix_few(Gemm g) {
+  constexpr int W = 8, U = NS == 1 ? 8 : 4;
+  __shared__ v4f red[W][NS][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, quad = lane >> 4;
+  const long ft = (g.nf + 15) / 16, tiles = ft * g.batches, steps = (g.nb + 3) / 4, per = (steps + W - 1) / W;
+  const long k0 = wave * per, k1 = min(steps, k0 + per);
+  size_t sr[NS];
+#pragma unroll
+  for (int j = 0; j < NS; ++j) sr[j] = (size_t)min(16L * j + l16, g.ns - 1) * g.nb;
+  for (long t = blockIdx.x; t < tiles; t += gridDim.x) {
+    const long b = t / ft, f0 = (t - b * ft) * 16;
+    const size_t fr = (size_t)(b * g.nf + min(f0 + l16, g.nf - 1)) * g.nb;
+    v4f acc[NS];
+#pragma unroll
+    for (int j = 0; j < NS; ++j) acc[j] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (long k = k0; k < k1; k += U) {
+      ck_u32x4 fc[U], sc[NS][U];
+      uint32_t fx[U], sx[NS][U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const long step = min(k + u, k1 - 1);
+        const long kb = 4 * step + quad, kc = WHOLE ? kb : min(kb, g.nb - 1);
+        fc[u] = *reinterpret_cast<const ck_u32x4 *>(g.fq + (fr + kc) * 16);
+        fx[u] = WHOLE ? *reinterpret_cast<const uint32_t *>(g.fe + fr + 4 * step) : g.fe[fr + kc];
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+          sc[j][u] = *reinterpret_cast<const ck_u32x4 *>(g.sq + (sr[j] + kc) * 16);
+          sx[j][u] = WHOLE ? *reinterpret_cast<const uint32_t *>(g.se + sr[j] + 4 * step) : g.se[sr[j] + kc];
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);  // all loads first
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        // no such step or block: codes of 0 on one side, scales that make 0 of them on both
+        const bool none = k + u >= k1 || (!WHOLE && 4 * (k + u) + quad >= g.nb);
+        fc[u] = none ? ck_u32x4{0u, 0u, 0u, 0u} : fc[u];
+        fx[u] = none ? 127u : WHOLE ? fx[u] >> 8 * quad : fx[u];
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+          sx[j][u] = none ? 127u : WHOLE ? sx[j][u] >> 8 * quad : sx[j][u];
+          acc[j] = mx4_product(fc[u], fx[u], sc[j][u], sx[j][u], acc[j]);
+        }
+      }
+    }
+    __syncthreads();  // the last tile's sums have been read
+#pragma unroll
+    for (int j = 0; j < NS; ++j) red[wave][j][lane] = acc[j];
+    __syncthreads();
+    if (wave < NS) {
+      v4f v = red[0][wave][lane];
+#pragma unroll
+      for (int w = 1; w < W; ++w) v += red[w][wave][lane];
+      const long s = 16 * wave + l16, f = f0 + 4 * quad;
+      if (s < g.ns && f < g.nf) {
+        float bias[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) bias[r] = g.bias_f ? bias_at<DT>(g, f + r, g.nf) : bias_at<DT>(g, s, g.ns);
+        mx4_finish<DT>(g, v, bias, (size_t)(b * g.ybatch + s * g.ys + f), (int)min(4L, g.nf - f));
+      }
+    }
+  }
+}
+
+namespace {
+
+typedef float v16f __attribute__((ext_vector_type(16)));
+
+// SIZE bytes a lane from p to LDS at `to` + SIZE lane
+template <int SIZE>
+__device__ __forceinline__ void mx4_to_lds(const uint8_t *p, uint8_t *to) {
+  const auto from = (const __attribute__((address_space(1))) void *)p;
+  const auto at = (__attribute__((address_space(3))) void *)to;
+  static_assert(SIZE == 16 || SIZE == 4, "the builtin takes a literal");
+  if constexpr (SIZE == 16) __builtin_amdgcn_global_load_lds(from, at, 16, 0, 0);
+  else __builtin_amdgcn_global_load_lds(from, at, 4, 0, 0);
+}
+
+// the unit of row r that lies at place l % 8 of its 128 bytes, and the other way round
+__device__ __forceinline__ int mx4_unit(int r, int l) { return (l & 7) ^ ((r >> 1 & 3) | (r >> 4 & 1) << 2); }
+
+// A barrier that also waits for the wave's loads to LDS, whose end only the count of loads tells
+__device__ __forceinline__ void mx4_barrier() {
+  __builtin_amdgcn_s_waitcnt(0);
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
+}
+
+// Workgroups go round the eight XCDs, each with an L2 of its own: an XCD gets neighbouring tiles.
+__device__ __forceinline__ long mx4_tile(long group, long tiles) {
+  const long xcd = group % 8, whole = tiles / 8, rest = tiles % 8;
+  return xcd * whole + min(xcd, rest) + group / 8;
+}
+
+}  // namespace
+
+// Large products: a workgroup has a tile of 64 W x 64 W, its four waves a quarter each on
+// v_mfma_scale_f32_32x32x64_f8f6f4 (lane l: row l % 32, block l / 32 of two). Codes of 256 of the sum's values go from
+// memory straight to LDS, the next ones while these are multiplied: rows of 128 bytes, whose 16-byte units are
+// swapped by row so that a fragment's reads meet no bank twice (a pass serves rows r .. r + 7 and r + 16 .. r + 23).
+// Fragments are read a step of 64 values ahead; the barrier between two buffers stands before the last step's
+// products, which cover the first reads from the new one. Rows of whole 128 values (nb % 4 == 0).
+template <int DT, int W>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(W == 4 ? 1 : 2, W == 4 ? 1 : 2)))
+void fno_mx4_mix_tiles(Gemm g) {
+  constexpr int T = 64 * W, ROWS = 2 * T, NL = ROWS / 32, NX = ROWS / 64;  // loads of a wave: codes of a stage, scales of two
+  __shared__ __attribute__((aligned(128))) uint8_t buf0[ROWS * 128], buf1[ROWS * 128], sx0[ROWS * 16], sx1[ROWS * 16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l32 = lane & 31, half = lane >> 5;
+  const int wf = wave & 1, ws = wave >> 1;
+  const long ft = (g.nf + T - 1) / T, st = (g.ns + T - 1) / T, tiles = ft * st * g.batches;
+  const int stages = (int)((g.nb + 7) / 8), pairs = (stages + 1) / 2;
+  const long t = mx4_tile(blockIdx.x, tiles);
+  const long si = t % st, fb = t / st, b = fb / ft, f0 = (fb - b * ft) * T, s0 = si * T;
+  // waves 0, 1 fetch the first operand's rows, 2 and 3 the second's
+  const bool first = wave < 2;
+  const long row0 = first ? b * g.nf + f0 : s0;
+  const int rows = (int)min((long)T, (first ? g.nf - f0 : g.ns - s0)), mine = (wave & 1) * (T / 2);
+  const uint8_t *codes = (first ? g.fq : g.sq) + (size_t)row0 * g.nb * 16, *scales = (first ? g.fe : g.se) + (size_t)row0 * g.nb;
+  uint32_t off[NL], xoff[NX];
+#pragma unroll
+  for (int n = 0; n < NL; ++n) {
+    const int r = mine + 8 * n + (lane >> 3), unit = mx4_unit(r, lane);
+    off[n] = (uint32_t)(min(r, rows - 1) * (int)g.nb + unit) * 16;
+  }
+#pragma unroll
+  for (int n = 0; n < NX; ++n) xoff[n] = (uint32_t)(min(mine + 16 * n + (lane >> 2), rows - 1) * (int)g.nb);
+  const int at = (wave >> 1) * T + mine;  // the wave's first row in LDS
+
+  auto fetch = [&](uint8_t *to, int stage) {
+    if (stage >= stages) return;
+    const uint8_t *p = codes + (size_t)stage * 128;
+    const bool part = 8 * stage + 8 > g.nb;  // four blocks are there: the other four again, nobody multiplies them
+#pragma unroll
+    for (int n = 0; n < NL; ++n) {
+      uint32_t o = off[n];
+      if (part) o -= mx4_unit(mine + 8 * n + (lane >> 3), lane) & 4 ? 64u : 0u;
+      mx4_to_lds<16>(p + o, to + (at + 8 * n) * 128);
+    }
+  };
+  auto fetch_scales = [&](uint8_t *to, int pair) {
+    if (pair >= pairs) return;
+    const uint32_t x = (uint32_t)min(16 * pair + 4 * (lane & 3), (int)g.nb - 4);
+#pragma unroll
+    for (int n = 0; n < NX; ++n) mx4_to_lds<4>(scales + (xoff[n] + x), to + (at + 16 * n) * 16);
+  };
+
+  v16f acc[W][W];
+#pragma unroll
+  for (int i = 0; i < W; ++i)
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  // a lane's row within 32, and its unit's place: rows of a fragment differ by multiples of 32, which the swap ignores
+  const int swap = mx4_unit(l32, 0);
+  const int frow = wf * (T / 2) + l32, srow = T + ws * (T / 2) + l32;
+  ck_u32x4 fc[2][W], sc[2][W];
+  uint2 fx[W], sx[W];  // a stage's scales, the lane's own at bytes 0, 2 of either word
+  auto read = [&](const uint8_t *from, int step, int slot) {
+    const int u = ((2 * step + half) ^ swap) * 16;
+#pragma unroll
+    for (int i = 0; i < W; ++i) fc[slot][i] = *reinterpret_cast<const ck_u32x4 *>(from + (frow + 32 * i) * 128 + u);
+#pragma unroll
+    for (int j = 0; j < W; ++j) sc[slot][j] = *reinterpret_cast<const ck_u32x4 *>(from + (srow + 32 * j) * 128 + u);
+  };
+  auto read_scales = [&](const uint8_t *from, int odd) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const uint2 v = *reinterpret_cast<const uint2 *>(from + (frow + 32 * i) * 16 + 8 * odd);
+      fx[i] = make_uint2(v.x >> 8 * half, v.y >> 8 * half);
+    }
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      const uint2 v = *reinterpret_cast<const uint2 *>(from + (srow + 32 * j) * 16 + 8 * odd);
+      sx[j] = make_uint2(v.x >> 8 * half, v.y >> 8 * half);
+    }
+  };
+  auto multiply = [&](auto step, int slot) {
+    constexpr int STEP = decltype(step)::value, SEL = STEP & 1 ? 2 : 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        const v8i x{(int)fc[slot][i][0], (int)fc[slot][i][1], (int)fc[slot][i][2], (int)fc[slot][i][3], 0, 0, 0, 0};
+        const v8i y{(int)sc[slot][j][0], (int)sc[slot][j][1], (int)sc[slot][j][2], (int)sc[slot][j][3], 0, 0, 0, 0};
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, acc[i][j], 4, 4, SEL, (int)(STEP & 2 ? fx[i].y : fx[i].x),
+                                                                    SEL, (int)(STEP & 2 ? sx[j].y : sx[j].x));
+      }
+  };
+  auto stage = [&](const uint8_t *now, const uint8_t *next, uint8_t *freed, const uint8_t *xnext, int odd_next, int s) {
+    const bool whole = 8 * s + 8 <= g.nb;
+    read(now, 1, 1);
+    multiply(std::integral_constant<int, 0>{}, 0);
+    read(now, 2, 0);
+    multiply(std::integral_constant<int, 1>{}, 1);
+    if (whole) {
+      read(now, 3, 1);
+      multiply(std::integral_constant<int, 2>{}, 0);
+    }
+    mx4_barrier();  // what is fetched has landed, and this stage's fragments have been read
+    if (s + 1 < stages) read(next, 0, 0);
+    fetch(freed, s + 2);
+    if (whole) multiply(std::integral_constant<int, 3>{}, 1);
+    if (s + 1 < stages) read_scales(xnext, odd_next);
+  };
+
+  fetch_scales(sx0, 0);
+  fetch(buf0, 0);
+  mx4_barrier();
+  fetch(buf1, 1);
+  fetch_scales(sx1, 1);
+  read(buf0, 0, 0);
+  read_scales(sx0, 0);
+  for (int p = 0; p < pairs; p += 2) {
+    stage(buf0, buf1, buf0, sx0, 1, 2 * p);
+    if (2 * p + 1 >= stages) break;
+    stage(buf1, buf0, buf1, sx1, 0, 2 * p + 1);
+    if (2 * p + 2 >= stages) break;
+    fetch_scales(sx0, p + 2);
+    stage(buf0, buf1, buf0, sx1, 1, 2 * p + 2);
+    if (2 * p + 3 >= stages) break;
+    stage(buf1, buf0, buf1, sx0, 0, 2 * p + 3);
+    fetch_scales(sx1, p + 3);
+  }
+  // A lane has rows f = 8 q + 4 half .. + 3 of a fragment (q = 0 .. 3) in column s. 32 columns at a time go through
+  // LDS, so that lanes finish and store whole 16 bytes of neighbours, 128 W bytes a column (16 bits).
+  mx4_barrier();
+  constexpr int N = ck_vec<DT>(), FW = 32 * W, PITCH = FW + 4, LANES = FW / N;  // lanes of a column
+  float *mine_f = reinterpret_cast<float *>(wave & 2 ? buf1 : buf0) + (wave & 1) * 32 * PITCH;
+  static_assert(2 * 32 * PITCH * 4 <= sizeof(buf0), "two waves' columns fit a buffer");
+  const long fl = f0 + wf * (T / 2) + lane % LANES * N;
+  const int there = (int)max(0L, min((long)N, g.nf - fl));
+  float bf[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) bf[e] = g.bias_f && there > 0 ? bias_at<DT>(g, fl + e, g.nf) : 0.f;
+#pragma unroll
+  for (int j = 0; j < W; ++j) {
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<v4f *>(mine_f + l32 * PITCH + 32 * i + 8 * q + 4 * half) =
+            v4f{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll 2
+    for (int c = lane / LANES; c < 32; c += 64 / LANES) {
+      const long s = s0 + ws * (T / 2) + 32 * j + c;
+      if (s >= g.ns || there == 0) continue;
+      const float bs = g.bias_f ? 0.f : bias_at<DT>(g, s, g.ns);
+      float o[N];
+#pragma unroll
+      for (int e = 0; e < N; e += 4) {
+        const v4f v = *reinterpret_cast<const v4f *>(mine_f + c * PITCH + lane % LANES * N + e);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) o[e + r] = v[r] + (bf[e + r] + bs);
+      }
+      const size_t y = (size_t)(b * g.ybatch + s * g.ys + fl);
+      if (g.add) {
+        const ck_u32x4 d = ck_load<DT>(g.add, y, there);
+#pragma unroll
+        for (int e = 0; e < N; ++e) o[e] += ck_get<DT>(d, e);
+      }
+      if (g.act)
+#pragma unroll
+        for (int e = 0; e < N; ++e) o[e] = gelu_train(o[e]);
+      ck_store<DT>(g.y, y, there, ck_raw<DT>(o));
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+namespace {
+
+template <int DT>
+const void *few_kernel(const Gemm &g) {
+  const bool whole = g.nb % 4 == 0;
+  if (g.ns <= 16) return whole ? (const void *)fno_mx4_mix_few<DT, 1, true> : (const void *)fno_mx4_mix_few<DT, 1, false>;
+  if (g.ns <= 32) return whole ? (const void *)fno_mx4_mix_few<DT, 2, true> : (const void *)fno_mx4_mix_few<DT, 2, false>;
+  return whole ? (const void *)fno_mx4_mix_few<DT, 4, true> : (const void *)fno_mx4_mix_few<DT, 4, false>;
+}
+
+}  // namespace
+
 hipError_t launch_mx4_mix(const Mx4MixArgs &a, int dtype, hipStream_t s) {
   Gemm g{};
   g.bias = a.bias, g.add = a.add, g.y = a.y, g.nb = a.nb, g.act = a.act;
@@ -175,11 +462,23 @@ hipError_t launch_mx4_mix(const Mx4MixArgs &a, int dtype, hipStream_t s) {
     g.nf = a.P, g.ns = a.O, g.batches = a.B, g.ybatch = a.O * a.P, g.ys = a.P, g.bias_f = 0;
   }
   FNO_BOUNDS(check_mx4_mix(a, dtype);)
-  const long tiles = (g.nf + 255) / 256 * ((g.ns + 63) / 64) * g.batches;
   void *args[] = {(void *)&g};
+  if (g.ns <= 64 && g.nb >= 32) {
+    const void *k = dtype == DT_F32 ? few_kernel<DT_F32>(g) : dtype == DT_F16 ? few_kernel<DT_F16>(g) : few_kernel<DT_BF16>(g);
+    return hipLaunchKernel(k, dim3((unsigned)std::min((g.nf + 15) / 16 * g.batches, kMaxGrid)), dim3(512), args, 0, s);
+  }
+  auto tiles = [&](long T) { return (g.nf + T - 1) / T * ((g.ns + T - 1) / T) * g.batches; };
+  if (g.nb % 4 == 0 && g.nb >= 16 && g.ns > 64 && tiles(128) <= kMaxGrid) {
+    const bool wide = tiles(256) >= 128;
+    const void *k = dtype == DT_F32 ? (wide ? (const void *)fno_mx4_mix_tiles<DT_F32, 4> : (const void *)fno_mx4_mix_tiles<DT_F32, 2>)
+                    : dtype == DT_F16 ? (wide ? (const void *)fno_mx4_mix_tiles<DT_F16, 4> : (const void *)fno_mx4_mix_tiles<DT_F16, 2>)
+                                      : (wide ? (const void *)fno_mx4_mix_tiles<DT_BF16, 4> : (const void *)fno_mx4_mix_tiles<DT_BF16, 2>);
+    return hipLaunchKernel(k, dim3((unsigned)tiles(wide ? 256 : 128)), dim3(kThreads), args, 0, s);
+  }
+  const long all = (g.nf + 255) / 256 * ((g.ns + 63) / 64) * g.batches;
   const void *k = dtype == DT_F32 ? (const void *)fno_mx4_mix<DT_F32>
                   : dtype == DT_F16 ? (const void *)fno_mx4_mix<DT_F16> : (const void *)fno_mx4_mix<DT_BF16>;
-  return hipLaunchKernel(k, dim3((unsigned)std::min(tiles, kMaxGrid)), dim3(kThreads), args, 0, s);
+  return hipLaunchKernel(k, dim3((unsigned)std::min(all, kMaxGrid)), dim3(kThreads), args, 0, s);
 }
 
 }  // namespace fno

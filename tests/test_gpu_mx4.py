@@ -7,7 +7,7 @@ import torch
 
 import spectral_convolution_amd as fno
 from oracle import block as ref
-from training_util import DT, close, f64, stored
+from training_util import CHAIN, DT, close, f64, stored
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -114,6 +114,63 @@ def test_mix(dtype, shape):
     for act, add, bias in ((0, False, False), (1, True, True), (i % 2, i % 3 == 0, True)):
         y, want, size = mix(dtype, *shape, act, add, bias, seed=i)
         close("y", y, want, dtype, size=size)
+
+
+def random_packed(gen, rows, C):
+    """(packed, values in float64 [rows][C]): any codes, scales around 1."""
+    nb = -(-C // 32)
+    code = torch.randint(0, 16, (rows, nb, 32), generator=gen, device=DEV, dtype=torch.uint8)
+    code.view(rows, -1)[:, C:] = 0
+    scale = torch.randint(120, 135, (rows, nb), generator=gen, device=DEV, dtype=torch.uint8)
+    at = -(-rows * nb * 16 // 256) * 256
+    packed = torch.zeros(fno.fno_mx4_bytes(rows, C), dtype=torch.uint8, device=DEV)
+    packed[:rows * nb * 16] = (code[..., ::2] | code[..., 1::2] << 4).view(-1)
+    packed[at:at + rows * nb] = scale.view(-1)
+    v = torch.from_numpy(np.concatenate([ref.MX4_VALUES, -ref.MX4_VALUES])).to(DEV)[code.long()]
+    v = v * torch.exp2(scale.double() - 127)[..., None]
+    return packed, v.view(rows, -1)[:, :C]
+
+
+# rows of either operand and the sum's length: tiles of 128 and 256 whole and cut, sums that end in the
+# first and second half of a stage of 256, one to many stages, and the kernels beside
+@pytest.mark.parametrize("shape", [(65, 128, 512), (128, 256, 640), (129, 127, 768), (300, 200, 896), (257, 700, 1024),
+                                   (96, 1000, 1152), (400, 300, 4096), (3000, 3100, 512), (2900, 3300, 1920), (4096, 2304, 640),
+                                   (130, 140, 500), (300, 300, 600), (70, 66, 992), (64, 4096, 4096), (40, 3000, 1100)], ids=str)
+def test_large_products(shape):
+    B, O, I = shape
+    gen = torch.Generator(device=DEV).manual_seed(B)
+    (xq, x), (aq, a) = random_packed(gen, B, I), random_packed(gen, O, I)
+    z, size = x @ a.t(), x.abs() @ a.t().abs()
+    for dtype, act in (("f32", 0), ("bf16", 1), ("f16", 0)):
+        bias = torch.randn(O, generator=gen, device=DEV).to(DT[dtype])
+        add = torch.randn(B, O, generator=gen, device=DEV).to(DT[dtype]) if act == 0 else None
+        scale = 2.0 ** -9 if dtype == "f16" else 1.0  # sums of up to some thousands stay in range
+        y = torch.full((B, O), float("nan"), dtype=DT[dtype], device=DEV)
+        q = xq.clone()
+        if dtype == "f16":
+            at = -(-B * -(-I // 32) * 16 // 256) * 256
+            q[at:at + B * -(-I // 32)] -= 9
+        fno.fno_channel_mix_mx4(q, aq, bias, add, y, I, act=act)
+        want = z * scale + bias.double() + (0 if add is None else add.double())
+        terms = size * scale + bias.double().abs() + (0 if add is None else add.double().abs())
+        want = want * torch.special.ndtr(want) if act else want
+        bound = float(torch.finfo(DT[dtype]).eps) / 2 * want.abs() * 1.001 + CHAIN * terms + 2.0 ** -25
+        assert ((y.double() - want).abs() <= bound).all(), (dtype, act)
+
+
+@pytest.mark.parametrize("shape", [(2, 512, 100, 300), (3, 640, 300, 129), (1, 1024, 70, 1000), (9, 512, 513, 700)], ids=str)
+def test_large_products_of_fields(shape):
+    B, I, O, P = shape
+    gen = torch.Generator(device=DEV).manual_seed(P)
+    (xq, x), (aq, a) = random_packed(gen, B * P, I), random_packed(gen, O, I)
+    fold = lambda t: t.view(B, P, O).transpose(1, 2)  # noqa: E731
+    bias = torch.randn(O, generator=gen, device=DEV)
+    add = torch.randn(B, O, P, generator=gen, device=DEV)
+    y = torch.full((B, O, P), float("nan"), device=DEV)
+    fno.fno_channel_mix_mx4(xq, aq, bias, add, y, I)
+    want = fold(x @ a.t()) + bias.double().view(1, O, 1) + add.double()
+    terms = fold(x.abs() @ a.t().abs()) + bias.double().abs().view(1, O, 1) + add.double().abs()
+    assert ((y.double() - want).abs() <= 2.0 ** -24 * want.abs() + CHAIN * terms).all()
 
 
 def test_poisoned_block_poisons_its_products():
