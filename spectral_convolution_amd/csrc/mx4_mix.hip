@@ -256,35 +256,51 @@ __device__ __forceinline__ void mx4_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
 }
 
-// Workgroups go round the eight XCDs, each with an L2 of its own: an XCD gets neighbouring tiles.
-__device__ __forceinline__ long mx4_tile(long group, long tiles) {
-  const long xcd = group % 8, whole = tiles / 8, rest = tiles % 8;
-  return xcd * whole + min(xcd, rest) + group / 8;
+// The scheduler's order for a step: M products with R reads of LDS (MASK 0x100) or loads from memory (0x10) between them
+template <int MASK, int R, int M>
+__device__ __forceinline__ void mx4_interleave() {
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(MASK, (R + M - 1) / M, 0);
+  }
+}
+
+// Workgroups go round the eight XCDs, each with an L2 of its own: an XCD gets neighbouring tiles, eight rows of them
+// at a time, so that its 32 workgroups share operands' rows on both sides.
+struct Mx4Tile {
+  int b, f, s;
+};
+__device__ __forceinline__ Mx4Tile mx4_tile(uint32_t group, uint32_t ft, uint32_t st, uint32_t tiles) {
+  const uint32_t xcd = group % 8, t = xcd * (tiles / 8) + min(xcd, tiles % 8) + group / 8, per = ft * st, b = t / per, r = t - b * per;
+  const uint32_t band = r / (8 * st), high = min(8u, ft - 8 * band), in = r - band * 8 * st, s = in / high;
+  return Mx4Tile{(int)b, (int)(8 * band + in - s * high), (int)s};
 }
 
 }  // namespace
 
-// Large products: a workgroup has a tile of 64 W x 64 W, its four waves a quarter each on
+// Large products: a workgroup has a tile of 64 WF x 64 WF, its waves 32 WF x 32 WS each on
 // v_mfma_scale_f32_32x32x64_f8f6f4 (lane l: row l % 32, block l / 32 of two). Codes of 256 of the sum's values go from
 // memory straight to LDS, the next ones while these are multiplied: rows of 128 bytes, whose 16-byte units are
 // swapped by row so that a fragment's reads meet no bank twice (a pass serves rows r .. r + 7 and r + 16 .. r + 23).
 // Fragments are read a step of 64 values ahead; the barrier between two buffers stands before the last step's
 // products, which cover the first reads from the new one. Rows of whole 128 values (nb % 4 == 0).
-template <int DT, int W>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(W == 4 ? 1 : 2, W == 4 ? 1 : 2)))
+template <int DT, int WF, int WS>
+__global__ __launch_bounds__(256 * WF / WS) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void fno_mx4_mix_tiles(Gemm g) {
-  constexpr int T = 64 * W, ROWS = 2 * T, NL = ROWS / 32, NX = ROWS / 64;  // loads of a wave: codes of a stage, scales of two
+  constexpr int T = 64 * WF, ROWS = 2 * T, NW = 4 * WF / WS;   // waves: two along f, the others along s
+  constexpr int NL = ROWS / 8 / NW, NX = ROWS / 16 / NW;       // loads of a wave: codes of a stage, scales of two
   __shared__ __attribute__((aligned(128))) uint8_t buf0[ROWS * 128], buf1[ROWS * 128], sx0[ROWS * 16], sx1[ROWS * 16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l32 = lane & 31, half = lane >> 5;
   const int wf = wave & 1, ws = wave >> 1;
-  const long ft = (g.nf + T - 1) / T, st = (g.ns + T - 1) / T, tiles = ft * st * g.batches;
+  const uint32_t ft = (uint32_t)((g.nf + T - 1) / T), st = (uint32_t)((g.ns + T - 1) / T), tiles = ft * st * (uint32_t)g.batches;
   const int stages = (int)((g.nb + 7) / 8), pairs = (stages + 1) / 2;
-  const long t = mx4_tile(blockIdx.x, tiles);
-  const long si = t % st, fb = t / st, b = fb / ft, f0 = (fb - b * ft) * T, s0 = si * T;
-  // waves 0, 1 fetch the first operand's rows, 2 and 3 the second's
-  const bool first = wave < 2;
+  const Mx4Tile tile = mx4_tile(blockIdx.x, ft, st, tiles);
+  const long b = tile.b, f0 = (long)tile.f * T, s0 = (long)tile.s * T;
+  // the first half of the waves fetches the first operand's rows, the others the second's
+  const bool first = wave < NW / 2;
   const long row0 = first ? b * g.nf + f0 : s0;
-  const int rows = (int)min((long)T, (first ? g.nf - f0 : g.ns - s0)), mine = (wave & 1) * (T / 2);
+  const int rows = (int)min((long)T, (first ? g.nf - f0 : g.ns - s0)), mine = wave % (NW / 2) * (2 * T / NW);
   const uint8_t *codes = (first ? g.fq : g.sq) + (size_t)row0 * g.nb * 16, *scales = (first ? g.fe : g.se) + (size_t)row0 * g.nb;
   uint32_t off[NL], xoff[NX];
 #pragma unroll
@@ -294,85 +310,97 @@ void fno_mx4_mix_tiles(Gemm g) {
   }
 #pragma unroll
   for (int n = 0; n < NX; ++n) xoff[n] = (uint32_t)(min(mine + 16 * n + (lane >> 2), rows - 1) * (int)g.nb);
-  const int at = (wave >> 1) * T + mine;  // the wave's first row in LDS
+  const int at = (first ? 0 : T) + mine;  // the wave's first row in LDS
 
-  auto fetch = [&](uint8_t *to, int stage) {
-    if (stage >= stages) return;
-    const uint8_t *p = codes + (size_t)stage * 128;
-    const bool part = 8 * stage + 8 > g.nb;  // four blocks are there: the other four again, nobody multiplies them
+  // A row that ends in half a stage is fetched 64 bytes past its end, at the last row into the scales behind the
+  // codes: nobody multiplies them. Past the last stage it is fetched again, so that a stage has no branch.
+  auto fetch = [&](uint8_t *to, int stage) __attribute__((always_inline)) {
+    const uint8_t *p = codes + (size_t)min(stage, stages - 1) * 128;
 #pragma unroll
     for (int n = 0; n < NL; ++n) {
       uint32_t o = off[n];
-      if (part) o -= mx4_unit(mine + 8 * n + (lane >> 3), lane) & 4 ? 64u : 0u;
+      asm volatile("" : "+v"(o));  // one base in scalar registers and 32 bits a lane, not an address for each load
       mx4_to_lds<16>(p + o, to + (at + 8 * n) * 128);
     }
   };
-  auto fetch_scales = [&](uint8_t *to, int pair) {
-    if (pair >= pairs) return;
-    const uint32_t x = (uint32_t)min(16 * pair + 4 * (lane & 3), (int)g.nb - 4);
+  auto fetch_scales = [&](uint8_t *to, int pair) __attribute__((always_inline)) {
+    const uint32_t x = (uint32_t)min(16 * min(pair, pairs - 1) + 4 * (lane & 3), (int)g.nb - 4);
 #pragma unroll
     for (int n = 0; n < NX; ++n) mx4_to_lds<4>(scales + (xoff[n] + x), to + (at + 16 * n) * 16);
   };
 
-  v16f acc[W][W];
+  v16f acc[WF][WS];
 #pragma unroll
-  for (int i = 0; i < W; ++i)
+  for (int i = 0; i < WF; ++i)
 #pragma unroll
-    for (int j = 0; j < W; ++j)
+    for (int j = 0; j < WS; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
   // a lane's row within 32, and its unit's place: rows of a fragment differ by multiples of 32, which the swap ignores
   const int swap = mx4_unit(l32, 0);
-  const int frow = wf * (T / 2) + l32, srow = T + ws * (T / 2) + l32;
-  ck_u32x4 fc[2][W], sc[2][W];
-  uint2 fx[W], sx[W];  // a stage's scales, the lane's own at bytes 0, 2 of either word
-  auto read = [&](const uint8_t *from, int step, int slot) {
+  const int frow = wf * (32 * WF) + l32, srow = T + ws * (32 * WS) + l32;
+  ck_u32x4 fc[2][WF], sc[2][WS];
+  uint2 fx[2][WF], sx[2][WS];  // scales of this stage and the next, the lane's own at bytes 0, 2 of either word
+  auto read = [&](const uint8_t *from, int step, int slot) __attribute__((always_inline)) {
     const int u = ((2 * step + half) ^ swap) * 16;
 #pragma unroll
-    for (int i = 0; i < W; ++i) fc[slot][i] = *reinterpret_cast<const ck_u32x4 *>(from + (frow + 32 * i) * 128 + u);
+    for (int i = 0; i < WF; ++i) fc[slot][i] = *reinterpret_cast<const ck_u32x4 *>(from + (frow + 32 * i) * 128 + u);
 #pragma unroll
-    for (int j = 0; j < W; ++j) sc[slot][j] = *reinterpret_cast<const ck_u32x4 *>(from + (srow + 32 * j) * 128 + u);
+    for (int j = 0; j < WS; ++j) sc[slot][j] = *reinterpret_cast<const ck_u32x4 *>(from + (srow + 32 * j) * 128 + u);
   };
-  auto read_scales = [&](const uint8_t *from, int odd) {
+  auto read_scales = [&](const uint8_t *from, int odd, int slot) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-      const uint2 v = *reinterpret_cast<const uint2 *>(from + (frow + 32 * i) * 16 + 8 * odd);
-      fx[i] = make_uint2(v.x >> 8 * half, v.y >> 8 * half);
-    }
+    for (int i = 0; i < WF; ++i) fx[slot][i] = *reinterpret_cast<const uint2 *>(from + (frow + 32 * i) * 16 + 8 * odd);
 #pragma unroll
-    for (int j = 0; j < W; ++j) {
-      const uint2 v = *reinterpret_cast<const uint2 *>(from + (srow + 32 * j) * 16 + 8 * odd);
-      sx[j] = make_uint2(v.x >> 8 * half, v.y >> 8 * half);
-    }
+    for (int j = 0; j < WS; ++j) sx[slot][j] = *reinterpret_cast<const uint2 *>(from + (srow + 32 * j) * 16 + 8 * odd);
   };
-  auto multiply = [&](auto step, int slot) {
+  auto own_scales = [&](int slot) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < WF; ++i) fx[slot][i] = make_uint2(fx[slot][i].x >> 8 * half, fx[slot][i].y >> 8 * half);
+#pragma unroll
+    for (int j = 0; j < WS; ++j) sx[slot][j] = make_uint2(sx[slot][j].x >> 8 * half, sx[slot][j].y >> 8 * half);
+  };
+  auto multiply = [&](auto step, int slot, int xslot) __attribute__((always_inline)) {
     constexpr int STEP = decltype(step)::value, SEL = STEP & 1 ? 2 : 0;
 #pragma unroll
-    for (int i = 0; i < W; ++i)
+    for (int i = 0; i < WF; ++i)
 #pragma unroll
-      for (int j = 0; j < W; ++j) {
+      for (int j = 0; j < WS; ++j) {
         const v8i x{(int)fc[slot][i][0], (int)fc[slot][i][1], (int)fc[slot][i][2], (int)fc[slot][i][3], 0, 0, 0, 0};
         const v8i y{(int)sc[slot][j][0], (int)sc[slot][j][1], (int)sc[slot][j][2], (int)sc[slot][j][3], 0, 0, 0, 0};
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, acc[i][j], 4, 4, SEL, (int)(STEP & 2 ? fx[i].y : fx[i].x),
-                                                                    SEL, (int)(STEP & 2 ? sx[j].y : sx[j].x));
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, acc[i][j], 4, 4, SEL, (int)(STEP & 2 ? fx[xslot][i].y : fx[xslot][i].x),
+                                                                    SEL, (int)(STEP & 2 ? sx[xslot][j].y : sx[xslot][j].x));
       }
   };
-  auto stage = [&](const uint8_t *now, const uint8_t *next, uint8_t *freed, const uint8_t *xnext, int odd_next, int s) {
-    const bool whole = 8 * s + 8 <= g.nb;
+  // A stage that another follows: every step's products go on while the next step's fragments are read. X: the
+  // scales' registers of this stage.
+  auto stage = [&](auto xslot, const uint8_t *now, const uint8_t *next, uint8_t *freed, const uint8_t *xnext, int odd_next,
+                   int s) __attribute__((always_inline)) {
+    constexpr int X = decltype(xslot)::value;
     read(now, 1, 1);
-    multiply(std::integral_constant<int, 0>{}, 0);
+    multiply(std::integral_constant<int, 0>{}, 0, X);
+    mx4_interleave<0x100, WF + WS, WF * WS>();
+    __builtin_amdgcn_sched_barrier(0);
     read(now, 2, 0);
-    multiply(std::integral_constant<int, 1>{}, 1);
-    if (whole) {
-      read(now, 3, 1);
-      multiply(std::integral_constant<int, 2>{}, 0);
-    }
+    multiply(std::integral_constant<int, 1>{}, 1, X);
+    mx4_interleave<0x100, WF + WS, WF * WS>();
+    __builtin_amdgcn_sched_barrier(0);
+    read(now, 3, 1);
+    multiply(std::integral_constant<int, 2>{}, 0, X);
+    mx4_interleave<0x100, WF + WS, WF * WS>();
+    __builtin_amdgcn_sched_barrier(0);
     mx4_barrier();  // what is fetched has landed, and this stage's fragments have been read
-    if (s + 1 < stages) read(next, 0, 0);
+    read(next, 0, 0);
+    read_scales(xnext, odd_next, 1 - X);
     fetch(freed, s + 2);
-    if (whole) multiply(std::integral_constant<int, 3>{}, 1);
-    if (s + 1 < stages) read_scales(xnext, odd_next);
+    multiply(std::integral_constant<int, 3>{}, 1, X);
+    mx4_interleave<0x100, 2 * (WF + WS), (WF * WS + 1) / 2>();  // reads of LDS stay in front of loads to it
+    mx4_interleave<0x010, NL, (WF * WS + 1) / 2>();
+    __builtin_amdgcn_sched_barrier(0);
+    own_scales(1 - X);
   };
+  constexpr std::integral_constant<int, 0> X0{};
+  constexpr std::integral_constant<int, 1> X1{};
 
   fetch_scales(sx0, 0);
   fetch(buf0, 0);
@@ -380,62 +408,88 @@ void fno_mx4_mix_tiles(Gemm g) {
   fetch(buf1, 1);
   fetch_scales(sx1, 1);
   read(buf0, 0, 0);
-  read_scales(sx0, 0);
-  for (int p = 0; p < pairs; p += 2) {
-    stage(buf0, buf1, buf0, sx0, 1, 2 * p);
-    if (2 * p + 1 >= stages) break;
-    stage(buf1, buf0, buf1, sx1, 0, 2 * p + 1);
-    if (2 * p + 2 >= stages) break;
-    fetch_scales(sx0, p + 2);
-    stage(buf0, buf1, buf0, sx1, 1, 2 * p + 2);
-    if (2 * p + 3 >= stages) break;
-    stage(buf1, buf0, buf1, sx0, 0, 2 * p + 3);
-    fetch_scales(sx1, p + 3);
+  read_scales(sx0, 0, 0);
+  own_scales(0);
+  const int whole = (int)(g.nb / 8);
+  // The pair's scales and the next one's change places; reads of them stand right behind a barrier, where no fetch is
+  // under way that the compiler would wait for, not knowing which of the two they come from.
+  uint8_t *xnow = sx0, *xnext = sx1;
+  int s = 0;
+  for (; s + 2 <= whole; s += 2) {
+    stage(X0, buf0, buf1, buf0, xnow, 1, s);
+    stage(X1, buf1, buf0, buf1, xnext, 0, s + 1);
+    fetch_scales(xnow, s / 2 + 2);
+    uint8_t *const x = xnow;
+    xnow = xnext, xnext = x;
   }
-  // A lane has rows f = 8 q + 4 half .. + 3 of a fragment (q = 0 .. 3) in column s. 32 columns at a time go through
-  // LDS, so that lanes finish and store whole 16 bytes of neighbours, 128 W bytes a column (16 bits).
-  mx4_barrier();
-  constexpr int N = ck_vec<DT>(), FW = 32 * W, PITCH = FW + 4, LANES = FW / N;  // lanes of a column
-  float *mine_f = reinterpret_cast<float *>(wave & 2 ? buf1 : buf0) + (wave & 1) * 32 * PITCH;
-  static_assert(2 * 32 * PITCH * 4 <= sizeof(buf0), "two waves' columns fit a buffer");
-  const long fl = f0 + wf * (T / 2) + lane % LANES * N;
-  const int there = (int)max(0L, min((long)N, g.nf - fl));
-  float bf[N];
+#pragma unroll 1
+  for (long k = 8 * s + half; k < g.nb; k += 2) {  // up to 12 blocks more: straight from memory, two at a time
 #pragma unroll
-  for (int e = 0; e < N; ++e) bf[e] = g.bias_f && there > 0 ? bias_at<DT>(g, fl + e, g.nf) : 0.f;
-#pragma unroll
-  for (int j = 0; j < W; ++j) {
-#pragma unroll
-    for (int i = 0; i < W; ++i)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<v4f *>(mine_f + l32 * PITCH + 32 * i + 8 * q + 4 * half) =
-            v4f{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-    __builtin_amdgcn_wave_barrier();
-#pragma unroll 2
-    for (int c = lane / LANES; c < 32; c += 64 / LANES) {
-      const long s = s0 + ws * (T / 2) + 32 * j + c;
-      if (s >= g.ns || there == 0) continue;
-      const float bs = g.bias_f ? 0.f : bias_at<DT>(g, s, g.ns);
-      float o[N];
-#pragma unroll
-      for (int e = 0; e < N; e += 4) {
-        const v4f v = *reinterpret_cast<const v4f *>(mine_f + c * PITCH + lane % LANES * N + e);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) o[e + r] = v[r] + (bf[e + r] + bs);
-      }
-      const size_t y = (size_t)(b * g.ybatch + s * g.ys + fl);
-      if (g.add) {
-        const ck_u32x4 d = ck_load<DT>(g.add, y, there);
-#pragma unroll
-        for (int e = 0; e < N; ++e) o[e] += ck_get<DT>(d, e);
-      }
-      if (g.act)
-#pragma unroll
-        for (int e = 0; e < N; ++e) o[e] = gelu_train(o[e]);
-      ck_store<DT>(g.y, y, there, ck_raw<DT>(o));
+    for (int i = 0; i < WF; ++i) {
+      const size_t at = (size_t)(b * g.nf + min(f0 + frow + 32 * i, g.nf - 1)) * g.nb + k;
+      fc[0][i] = *reinterpret_cast<const ck_u32x4 *>(g.fq + at * 16);
+      fx[0][i].x = g.fe[at];
     }
-    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int j = 0; j < WS; ++j) {
+      const size_t at = (size_t)min(s0 + srow - T + 32 * j, g.ns - 1) * g.nb + k;
+      sc[0][j] = *reinterpret_cast<const ck_u32x4 *>(g.sq + at * 16);
+      sx[0][j].x = g.se[at];
+    }
+    multiply(std::integral_constant<int, 0>{}, 0, 0);
+  }
+  // A lane has rows f = 8 q + 4 half .. + 3 of a fragment (q = 0 .. 3) in column s. Up to 64 rows of 32 columns at a time
+  // go through LDS, so that lanes finish and store whole 16 bytes of neighbours, 128 bytes a column (16 bits).
+  mx4_barrier();
+  constexpr int PI = WF >= 2 ? 2 : 1, N = ck_vec<DT>(), PITCH = 32 * PI + 4, LANES = 32 * PI / N;  // lanes of a column
+  float *part = reinterpret_cast<float *>(first ? buf0 : buf1) + wave % (NW / 2) * 32 * PITCH;
+  static_assert(NW / 2 * 32 * PITCH * 4 <= (int)sizeof(buf0), "half of the waves' parts fit a buffer");
+#pragma unroll 1
+  for (int h = 0; h < WF / PI; ++h) {
+    const long fl = f0 + wf * (32 * WF) + 32 * PI * h + lane % LANES * N;
+    const int there = (int)max(0L, min((long)N, g.nf - fl));
+    float bf[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) bf[e] = g.bias_f && there > 0 ? bias_at<DT>(g, fl + e, g.nf) : 0.f;
+#pragma unroll 1
+    for (int j = 0; j < WS; ++j) {  // one copy of what follows: straight-line code of all parts costs more than it does
+#pragma unroll
+      for (int k = 0; k < WF / PI * WS; ++k)
+        if (k == h * WS + j)
+#pragma unroll
+          for (int i = 0; i < PI; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const v16f &c = acc[PI * (k / WS) + i][k % WS];
+              *reinterpret_cast<v4f *>(part + l32 * PITCH + 32 * i + 8 * q + 4 * half) =
+                  v4f{c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
+            }
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll 2
+      for (int c = lane / LANES; c < 32; c += 64 / LANES) {
+        const long s = s0 + ws * (32 * WS) + 32 * j + c;
+        if (s >= g.ns || there == 0) continue;
+        const float bs = g.bias_f ? 0.f : bias_at<DT>(g, s, g.ns);
+        float o[N];
+#pragma unroll
+        for (int e = 0; e < N; e += 4) {
+          const v4f v = *reinterpret_cast<const v4f *>(part + c * PITCH + lane % LANES * N + e);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) o[e + r] = v[r] + (bf[e + r] + bs);
+        }
+        const size_t y = (size_t)(b * g.ybatch + s * g.ys + fl);
+        if (g.add) {
+          const ck_u32x4 d = ck_load<DT>(g.add, y, there);
+#pragma unroll
+          for (int e = 0; e < N; ++e) o[e] += ck_get<DT>(d, e);
+        }
+        if (g.act)
+#pragma unroll
+          for (int e = 0; e < N; ++e) o[e] = gelu_train(o[e]);
+        ck_store<DT>(g.y, y, there, ck_raw<DT>(o));
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
   }
 }
 
@@ -447,6 +501,12 @@ const void *few_kernel(const Gemm &g) {
   if (g.ns <= 16) return whole ? (const void *)fno_mx4_mix_few<DT, 1, true> : (const void *)fno_mx4_mix_few<DT, 1, false>;
   if (g.ns <= 32) return whole ? (const void *)fno_mx4_mix_few<DT, 2, true> : (const void *)fno_mx4_mix_few<DT, 2, false>;
   return whole ? (const void *)fno_mx4_mix_few<DT, 4, true> : (const void *)fno_mx4_mix_few<DT, 4, false>;
+}
+
+template <int DT>
+const void *tiles_kernel(int w) {
+  return w == 4 ? (const void *)fno_mx4_mix_tiles<DT, 4, 2>
+         : w == 2 ? (const void *)fno_mx4_mix_tiles<DT, 2, 2> : (const void *)fno_mx4_mix_tiles<DT, 1, 1>;
 }
 
 }  // namespace
@@ -463,17 +523,18 @@ hipError_t launch_mx4_mix(const Mx4MixArgs &a, int dtype, hipStream_t s) {
   }
   FNO_BOUNDS(check_mx4_mix(a, dtype);)
   void *args[] = {(void *)&g};
+  // few rows: 1 x 8192 x 8192 97 us as below, 13 so
   if (g.ns <= 64 && g.nb >= 32) {
     const void *k = dtype == DT_F32 ? few_kernel<DT_F32>(g) : dtype == DT_F16 ? few_kernel<DT_F16>(g) : few_kernel<DT_BF16>(g);
     return hipLaunchKernel(k, dim3((unsigned)std::min((g.nf + 15) / 16 * g.batches, kMaxGrid)), dim3(512), args, 0, s);
   }
   auto tiles = [&](long T) { return (g.nf + T - 1) / T * ((g.ns + T - 1) / T) * g.batches; };
-  if (g.nb % 4 == 0 && g.nb >= 16 && g.ns > 64 && tiles(128) <= kMaxGrid) {
-    const bool wide = tiles(256) >= 128;
-    const void *k = dtype == DT_F32 ? (wide ? (const void *)fno_mx4_mix_tiles<DT_F32, 4> : (const void *)fno_mx4_mix_tiles<DT_F32, 2>)
-                    : dtype == DT_F16 ? (wide ? (const void *)fno_mx4_mix_tiles<DT_F16, 4> : (const void *)fno_mx4_mix_tiles<DT_F16, 2>)
-                                      : (wide ? (const void *)fno_mx4_mix_tiles<DT_BF16, 4> : (const void *)fno_mx4_mix_tiles<DT_BF16, 2>);
-    return hipLaunchKernel(k, dim3((unsigned)tiles(wide ? 256 : 128)), dim3(kThreads), args, 0, s);
+  if (g.nb % 4 == 0 && g.nb >= 16 && g.ns > 64 && tiles(64) <= kMaxGrid) {
+    // The largest tiles that still give three quarters of the 256 compute units one (bf16, random codes; tiles of
+    // 256 / 128 / 64): 4096^3 59 / 68 / 106 us, 2048 x 4096 x 4096 44 / 34 / 56, 512 x 4096 x 4096 39 / 19 / 14.
+    const int w = tiles(256) >= 192 ? 4 : tiles(128) >= 192 ? 2 : 1;
+    const void *k = dtype == DT_F32 ? tiles_kernel<DT_F32>(w) : dtype == DT_F16 ? tiles_kernel<DT_F16>(w) : tiles_kernel<DT_BF16>(w);
+    return hipLaunchKernel(k, dim3((unsigned)tiles(64 * w)), dim3(w == 4 ? 512 : 256), args, 0, s);
   }
   const long all = (g.nf + 255) / 256 * ((g.ns + 63) / 64) * g.batches;
   const void *k = dtype == DT_F32 ? (const void *)fno_mx4_mix<DT_F32>
