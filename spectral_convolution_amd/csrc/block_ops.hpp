@@ -64,6 +64,7 @@ struct Mx4Args {
   uint8_t *exps;   // [B P][nb], 2^(exp - 127)
   int B, C;
   long P, nb;
+  int step;        // fields: blocks that a workgroup packs at a time (set by the launcher)
 };
 hipError_t launch_mx4(const Mx4Args &a, bool pack, int dtype, hipStream_t s);
 

@@ -69,8 +69,7 @@ void check_drop(const DropArgs &a, int mode, int dtype);
 void check_gnorm_small(const GnArgs &a, bool last, bool bwd, int T, int NC, int dtype);
 void check_gnorm_rows(const GnArgs &a, bool bwd, bool out, int T, int dtype);
 void check_gnorm_cols(const GnArgs &a, bool bwd, bool out, bool runs, int dtype);
-void check_gnorm_join(const GnArgs &a, bool bwd, int dtype);
-void check_gnorm_params(const GnArgs &a, int samples, int dtype);
+void check_gnorm_join(const GnArgs &a, bool bwd, bool group, int samples, int dtype);
 void check_mx4(const Mx4Args &a, bool pack, int dtype);
 void check_mx4_mix(const Mx4MixArgs &a, int dtype);
 

@@ -79,7 +79,7 @@ void check_gnorm_small(const GnArgs &a, bool last, bool bwd, int T, int NC, int 
   gn_spans(c, a, bwd, true, dtype);
   const long V = dtype == DT_F32 ? 4 : 8, len = last ? a.Cg : a.P, rows = last ? a.P : a.Cg;
   const long cpr = (len + V - 1) / V, chunks = rows * cpr, groups = (long)a.B * a.G, n = (long)values(a);
-  c.need("a team holds a group", chunks <= (long)T * NC);
+  c.need("a team holds a group", chunks <= (long)T * NC && T <= 1024);
   c.need("groups in 31 bits", groups < 1L << 31);
   c.need("one pixel: channels last", last || a.P > 1);
   bool in = true, params = true;
@@ -123,23 +123,25 @@ void check_gnorm_cols(const GnArgs &a, bool bwd, bool out, bool runs, int dtype)
   c.need("strides of the sums", a.sb == (runs ? 0 : (long)a.C * a.S) && a.sc == 1 && a.ss == a.C);
 }
 
-void check_gnorm_join(const GnArgs &a, bool bwd, int dtype) {
+void check_gnorm_join(const GnArgs &a, bool bwd, bool group, int samples, int dtype) {
   const Ctx c{bwd ? "fno_gnorm_join backward" : "fno_gnorm_join"};
-  const size_t groups = (size_t)a.B * a.G;
-  c.span("sums", a.part, (size_t)a.B * a.C * a.S * 8);
-  c.span(bwd ? "group sums" : "stats", bwd ? a.gsum : a.stats, groups * 8);
-  c.need("last sum of a sample", (a.C - 1) * a.sc + (a.S - 1) * a.ss < a.sb && a.sb == (long)a.C * a.S);
-  const long piece = a.last ? a.per : a.per * (dtype == DT_F32 ? 4 : 8);
-  c.need("no empty piece", (a.S - 1) * piece < a.P);
-}
-
-void check_gnorm_params(const GnArgs &a, int samples, int dtype) {
-  const Ctx c{"fno_gnorm_params"};
-  const size_t es = es_of(dtype);
-  c.opt("gw", a.gw, a.C * es);
-  c.opt("gb", a.gb, a.C * es);
-  c.span("sums", a.part, (size_t)samples * a.S * a.C * 8);
-  c.need("last sum", (samples - 1) * a.sb + (a.C - 1) * a.sc + (a.S - 1) * a.ss < (long)samples * a.S * a.C);
+  const size_t groups = (size_t)a.B * a.G, es = es_of(dtype);
+  c.need("something to join", group || samples);
+  if (group) {
+    c.span("sums", a.part, (size_t)a.B * a.C * a.S * 8);
+    c.span(bwd ? "group sums" : "stats", bwd ? a.gsum : a.stats, groups * 8);
+    c.need("last sum of a sample", (a.C - 1) * a.sc + (a.S - 1) * a.ss < a.sb && a.sb == (long)a.C * a.S);
+    const long piece = a.last ? a.per : a.per * (dtype == DT_F32 ? 4 : 8);
+    c.need("no empty piece", (a.S - 1) * piece < a.P);
+    c.need("a group's sums in 32 bits", (long)a.Cg * a.S + 4096 < 1L << 32);
+  }
+  if (samples) {
+    c.opt("gw", a.gw, a.C * es);
+    c.opt("gb", a.gb, a.C * es);
+    c.span("sums", a.part, (size_t)samples * a.S * a.C * 8);
+    c.need("last sum", (samples - 1) * a.sb + (a.C - 1) * a.sc + (a.S - 1) * a.ss < (long)samples * a.S * a.C);
+    c.need("a channel's sums in 32 bits", (long)samples * a.S + 512 < 1L << 32);
+  }
 }
 
 void check_mx4(const Mx4Args &a, bool pack, int dtype) {

@@ -89,7 +89,7 @@ fno_status_t run_mx4(const void *x, void *y, const void *packed, bool pack, int 
   }
   if (!s.ok()) return FNO_ERR_INVALID_ARG;
   uint8_t *base = static_cast<uint8_t *>(const_cast<void *>(packed));
-  const Mx4Args a{x, y, base, base + l.exps, batch, channels, pixels, l.nb};
+  const Mx4Args a{x, y, base, base + l.exps, batch, channels, pixels, l.nb, 1};
   return status_of(launch_mx4(a, pack, (int)dtype, (hipStream_t)stream));
 }
 

@@ -18,7 +18,7 @@ inline long up(long a, long b) { return (a + b - 1) / b; }
 // How a shape runs. team 0: the groups are too large for a workgroup's registers.
 struct GnPlan {
   bool last;       // rows are a pixel's channels (one pixel: either order)
-  int team, bteam; // threads that hold a group, forward and backward
+  int team, bteam; // threads that hold a group, forward and backward; 2048: 1024 with twice the chunks each
   int T;           // lanes of a row (channels first)
   int S, runs;     // pieces of a row or sample; channels last, small groups: runs of the parameters' sums
   long per, per_run;
@@ -34,18 +34,39 @@ enum : int { kActNone = 0, kActGelu = 1, kActSilu = 2 };
 __device__ __forceinline__ float sigmoid(float z) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.4426950408889634f));
 }
-__device__ __forceinline__ float act_of(float z, int act) {
-  if (act == kActGelu) return gelu_train(z);
-  if (act == kActSilu) return fmaxf(z, -126.f) * sigmoid(z);
+template <int ACT>
+__device__ __forceinline__ float act_of(float z) {
+  if constexpr (ACT == kActGelu) return gelu_train(z);
+  if constexpr (ACT == kActSilu) return fmaxf(z, -126.f) * sigmoid(z);
   return z;
 }
-__device__ __forceinline__ float act_slope(float z, int act) {
-  if (act == kActGelu) return gelu_slope(z);
-  if (act == kActSilu) {
+// GELU's derivative is gelu_slope() with a step fewer: with q the upper tail at |z| and bell the density,
+// g = |z| bell - q is even in z, and the derivative 1 + g above 0, -g below.
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z) {
+  if constexpr (ACT == kActGelu) {
+    const float a = fabsf(z);
+    const float x = fmaf(fminf(a, 100.f), 0.39894228040143268f, -normal_tail(a, 1.f));
+    return 0.5f + copysignf(fmaf(normal_bell(z), x, 0.5f), z);
+  }
+  if constexpr (ACT == kActSilu) {
     const float s = sigmoid(z);
     return s * fmaf(__builtin_amdgcn_fmed3f(z, -126.f, 126.f), 1.f - s, 1.f);
   }
   return 1.f;
+}
+// f(activation, dropout or not) as integral constants: a branch a chunk, not one a value. The kernels are as near to
+// the vector units' rate as to memory's (20 x 64 x 256^2 fp16, GELU, backward sums: 100 us with branches and
+// selects at every value).
+template <typename F>
+__device__ __forceinline__ void with_act(const GnArgs &a, F f) {
+  auto act = [&](auto drop) __attribute__((always_inline)) {
+    if (a.act == kActGelu) f(std::integral_constant<int, kActGelu>{}, drop);
+    else if (a.act == kActSilu) f(std::integral_constant<int, kActSilu>{}, drop);
+    else f(std::integral_constant<int, kActNone>{}, drop);
+  };
+  if (a.drop.thr) act(std::true_type{});
+  else act(std::false_type{});
 }
 
 // (mean, sum of squared deviations) of na and nb values joined (Chan, Golub, LeVeque: Updating
@@ -57,6 +78,19 @@ __device__ __forceinline__ void join_moments(float &n, float &mean, float &m2, f
   mean = n == 0.f ? meanb : fmaf(d, f, mean);
   m2 = n == 0.f ? m2b : m2 + m2b + d * d * n * f;
   n = t;
+}
+
+// A whole chunk loaded for the last time, or stored: past the caches, which keep what is still to be read
+template <int DT>
+__device__ __forceinline__ ck_u32x4 load_last(const void *p, size_t i) {
+  using E = typename std::conditional<DT == DT_F32, float, uint16_t>::type;
+  return __builtin_nontemporal_load(reinterpret_cast<const ck_u32x4_any *>(reinterpret_cast<const E *>(p) + i));
+}
+template <int DT>
+__device__ __forceinline__ void store_chunk(void *p, size_t i, int n, const ck_u32x4 &r) {
+  using E = typename std::conditional<DT == DT_F32, float, uint16_t>::type;
+  if (n == ck_vec<DT>()) __builtin_nontemporal_store((ck_u32x4_any)r, reinterpret_cast<ck_u32x4_any *>(reinterpret_cast<E *>(p) + i));
+  else ck_store<DT>(p, i, n, r);
 }
 
 template <int W>
@@ -97,7 +131,6 @@ __device__ __forceinline__ void param_piece(const void *p, size_t i, long n, flo
 // kept bits of a chunk: its first value is value `i` of the field in memory order, of channel c and sample b
 template <int V, bool LAST>
 __device__ __forceinline__ uint32_t chunk_keep(const GnArgs &a, const DropKey &key, uint64_t i, long b, int c) {
-  if (a.drop.thr == 0) return 0xffu;
   if (a.drop.unit == kDropElement) return drop_units(key, a.drop.thr, i, V);
   if (a.drop.unit == kDropSample) return drop_one(key, a.drop.thr, (uint64_t)b);
   const uint64_t u = (uint64_t)b * a.C + c;

@@ -31,105 +31,154 @@ __global__ __launch_bounds__(T > kThreads ? T : kThreads) void fno_gnorm_small(G
     const size_t first = LAST ? (size_t)b * a.P * a.C + c0 : ((size_t)b * a.C + c0) * a.P;
     const size_t pitch = LAST ? a.C : a.P;
     ck_u32x4 rx[NC], rg[BWD ? NC : 1];
-    uint32_t row[NC], k[NC];
-    int nv[NC];  // values of the chunk, 0 where there is none
-#pragma unroll
-    for (int i = 0; i < NC; ++i) {
-      const uint32_t q = t + i * T, qc = min(q, chunks - 1);
-      row[i] = qc / cpr;
-      k[i] = (qc - row[i] * cpr) * V;
-      nv[i] = q < chunks ? (int)min(len - k[i], (uint32_t)V) : 0;
-    }
+    // Where chunk i of a thread lies; each phase works it out again, since the registers go to the values.
+    struct Place {
+      uint32_t row, k;
+      int n;  // values of the chunk, 0 where there is none
+      size_t at;
+    };
+    uint32_t mine = t;
+    auto place = [&](int i) __attribute__((always_inline)) {
+      const uint32_t q = mine + i * T, qc = min(q, chunks - 1);
+      Place p;
+      p.row = qc / cpr;
+      p.k = (qc - p.row * cpr) * V;
+      p.n = q < chunks ? (int)min(len - p.k, (uint32_t)V) : 0;
+      p.at = first + p.row * pitch + p.k;
+      return p;
+    };
+    auto again = [&]() __attribute__((always_inline)) { asm volatile("" : "+v"(mine)); };
     if (whole) {
 #pragma unroll
-      for (int i = 0; i < NC; ++i) rx[i] = ck_load<DT>(a.x, first + row[i] * pitch + k[i], V);
+      for (int i = 0; i < NC; ++i) rx[i] = ck_load<DT>(a.x, place(i).at, V);
       if constexpr (BWD)
 #pragma unroll
-        for (int i = 0; i < NC; ++i) rg[i] = ck_load<DT>(a.gy, first + row[i] * pitch + k[i], V);
+        for (int i = 0; i < NC; ++i) rg[i] = ck_load<DT>(a.gy, place(i).at, V);
+    } else if (len >= V) {  // a row's last chunk as the 16 bytes that end with the row: no load waits for another
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const Place p = place(i);
+        rx[i] = ck_load<DT>(a.x, p.at - (V - p.n) % V, V);
+        if constexpr (BWD) rg[i] = ck_load<DT>(a.gy, p.at - (V - p.n) % V, V);
+      }
+      again();
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int gone = (V - place(i).n) % V * (16 / V);
+        rx[i] = ck_shift(rx[i], gone);
+        if constexpr (BWD) rg[i] = ck_shift(rg[i], gone);
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
-        rx[i] = ck_load<DT>(a.x, first + row[i] * pitch + k[i], nv[i]);
-        if constexpr (BWD) rg[i] = ck_load<DT>(a.gy, first + row[i] * pitch + k[i], nv[i]);
+        const Place p = place(i);
+        rx[i] = ck_load<DT>(a.x, p.at, p.n);
+        if constexpr (BWD) rg[i] = ck_load<DT>(a.gy, p.at, p.n);
       }
     }
     float mean, r;
     if constexpr (!BWD) {
       float s = 0.f;
+      again();
 #pragma unroll
-      for (int i = 0; i < NC; ++i)
+      for (int i = 0; i < NC; ++i) {
+        const int nv = place(i).n;
 #pragma unroll
-        for (int e = 0; e < V; ++e) s += e < nv[i] ? ck_get<DT>(rx[i], e) : 0.f;
+        for (int e = 0; e < V; ++e) s += e < nv ? ck_get<DT>(rx[i], e) : 0.f;
+        channel_done();
+      }
       mean = team_sum<T>(s, red[0]) / n;
+      fresh<DT>(rx);
+      again();
       s = 0.f;
 #pragma unroll
-      for (int i = 0; i < NC; ++i)
+      for (int i = 0; i < NC; ++i) {
+        const int nv = place(i).n;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           const float d = ck_get<DT>(rx[i], e) - mean;
-          s = e < nv[i] ? fmaf(d, d, s) : s;
+          s = e < nv ? fmaf(d, d, s) : s;
         }
+        channel_done();
+      }
       r = rsq(team_sum<T>(s, red[1]) / n + a.eps);
+      fresh<DT>(rx);
       if (a.stats && there && t == 0) a.stats[gid] = make_float2(mean, r);
     } else {
       const float2 st = a.stats[gid];
       mean = st.x, r = st.y;
     }
-    auto params = [&](int i, float *w, float *bb) {
+    const float scale = a.drop.scale;
+    // a chunk's w and b, and with DROP its kept bits
+    auto chunk = [&](auto drop, const Place &p, float *w, float *bb) __attribute__((always_inline)) {
       if constexpr (LAST) {
-        param_piece<DT>(a.w, c0 + k[i], nv[i] ? (long)len - k[i] : 0, 1.f, w);
-        param_piece<DT>(a.b, c0 + k[i], nv[i] ? (long)len - k[i] : 0, 0.f, bb);
+        param_piece<DT>(a.w, c0 + p.k, p.n ? (long)len - p.k : 0, 1.f, w);
+        param_piece<DT>(a.b, c0 + p.k, p.n ? (long)len - p.k : 0, 0.f, bb);
       } else {
-        const float w1 = param(a.w, DT, c0 + row[i], 1.f), b1 = param(a.b, DT, c0 + row[i], 0.f);
+        const float w1 = param(a.w, DT, c0 + p.row, 1.f), b1 = param(a.b, DT, c0 + p.row, 0.f);
 #pragma unroll
         for (int e = 0; e < V; ++e) w[e] = w1, bb[e] = b1;
       }
+      return decltype(drop)::value ? chunk_keep<V, LAST>(a, key, p.at, b, (int)(LAST ? c0 + p.k : c0 + p.row)) : 0xffu;
     };
-    auto keep = [&](int i) {
-      const size_t at = first + row[i] * pitch + k[i];
-      return chunk_keep<V, LAST>(a, key, at, b, (int)(LAST ? c0 + k[i] : c0 + row[i]));
-    };
-    const float scale = a.drop.scale;
     if constexpr (!BWD) {
+      again();
+      with_act(a, [&](auto act, auto drop) __attribute__((always_inline)) {
+        constexpr int ACT = decltype(act)::value;
 #pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        if (i * T >= (int)chunks) break;
-        float w[V], bb[V], o[V];
-        params(i, w, bb);
-        const uint32_t m = keep(i);
+        for (int i = 0; i < NC; ++i) {
+          if (i * T >= (int)chunks) break;
+          const Place p = place(i);
+          float w[V], bb[V], o[V];
+          const uint32_t m = chunk(drop, p, w, bb);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float z = fmaf((ck_get<DT>(rx[i], e) - mean) * r, w[e], bb[e]);
-          o[e] = m >> e & 1 ? act_of(z, a.act) * scale : 0.f;
+          for (int e = 0; e < V; ++e) {
+            const float z = fmaf((ck_get<DT>(rx[i], e) - mean) * r, w[e], bb[e]);
+            o[e] = m >> e & 1 ? act_of<ACT>(z) * scale : 0.f;
+          }
+          if (there && p.n) store_chunk<DT>(a.y, p.at, p.n, ck_raw<DT>(o));
+          channel_done();
         }
-        if (there && nv[i]) ck_store<DT>(a.y, first + row[i] * pitch + k[i], nv[i], ck_raw<DT>(o));
-      }
+      });
     } else {
-      float g1[NC][V], h[NC][V], s1 = 0.f, s2 = 0.f;  // w gz and x^
+      // Twice over the values in registers, whose 16-bit forms take half the room of w gz and x^: the second time
+      // with the sums of the first.
+      float s1 = 0.f, s2 = 0.f;
+      auto each = [&](auto out) __attribute__((always_inline)) {
+        constexpr bool OUT = decltype(out)::value;
+        again();
+        with_act(a, [&](auto act, auto drop) __attribute__((always_inline)) {
+          constexpr int ACT = decltype(act)::value;
 #pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        float w[V], bb[V];
-        params(i, w, bb);
-        const uint32_t m = keep(i);
+          for (int i = 0; i < NC; ++i) {
+            if (i * T >= (int)chunks) break;
+            const Place p = place(i);
+            float w[V], bb[V], o[V];
+            const uint32_t m = chunk(drop, p, w, bb);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          h[i][e] = (ck_get<DT>(rx[i], e) - mean) * r;
-          const float z = fmaf(h[i][e], w[e], bb[e]);
-          const float gz = ck_get<DT>(rg[i], e) * scale * act_slope(z, a.act);
-          g1[i][e] = (m >> e & 1) && e < nv[i] ? gz * w[e] : 0.f;
-          s1 += g1[i][e];
-          s2 = e < nv[i] ? fmaf(g1[i][e], h[i][e], s2) : s2;
-        }
-      }
+            for (int e = 0; e < V; ++e) {
+              const float h = (ck_get<DT>(rx[i], e) - mean) * r, z = fmaf(h, w[e], bb[e]);
+              const float gz = ck_get<DT>(rg[i], e) * scale * act_slope<ACT>(z);
+              const float g = (m >> e & 1) && e < p.n ? gz * w[e] : 0.f;
+              if constexpr (OUT) {
+                o[e] = r * (g - s1 - h * s2);
+              } else {
+                s1 += g;
+                s2 = e < p.n ? fmaf(g, h, s2) : s2;
+              }
+            }
+            if constexpr (OUT)
+              if (there && p.n) store_chunk<DT>(a.gx, p.at, p.n, ck_raw<DT>(o));
+            channel_done();
+          }
+        });
+      };
+      each(std::false_type{});
       s1 = team_sum<T>(s1, red[0]) / n;
       s2 = team_sum<T>(s2, red[1]) / n;
-#pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        float o[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) o[e] = r * (g1[i][e] - s1 - h[i][e] * s2);
-        if (there && nv[i]) ck_store<DT>(a.gx, first + row[i] * pitch + k[i], nv[i], ck_raw<DT>(o));
-      }
+      fresh<DT>(rx);
+      fresh<DT>(rg);
+      each(std::true_type{});
     }
   }
 }
@@ -145,7 +194,7 @@ struct Row {
   long b;
   int c;
   size_t base;
-  float mean, r, w, bias, m1, m2;
+  float mean, r, rw, bias, c1, c2;  // z = (x - mean) rw + bias; gx = rw gz + c1 + (x - mean) c2
   float s1 = 0.f, s2 = 0.f, shift = 0.f, cnt = 0.f;
 
   __device__ __forceinline__ Row(const GnArgs &args, const DropKey &k, long row) : a(args), key(k) {
@@ -156,11 +205,11 @@ struct Row {
       const size_t g = (size_t)b * a.G + c / a.Cg;
       const float2 st = a.stats[g];
       mean = st.x, r = st.y;
-      w = param(a.w, DT, c, 1.f);
+      rw = r * param(a.w, DT, c, 1.f);
       bias = param(a.b, DT, c, 0.f);
       if constexpr (BWD && OUT) {
         const float2 m = a.gsum[g];
-        m1 = m.x, m2 = m.y;
+        c1 = -r * m.x, c2 = -r * r * m.y;
       }
     }
   }
@@ -183,25 +232,31 @@ struct Row {
       }
       return;
     }
-    const uint32_t m = chunk_keep<V, false>(a, key, base + p, b, c);
-    float o[V];
+    with_act(a, [&](auto act, auto drop) __attribute__((always_inline)) {
+      constexpr int ACT = decltype(act)::value;
+      constexpr bool DROP = decltype(drop)::value;
+      const uint32_t m = DROP ? chunk_keep<V, false>(a, key, base + p, b, c) : 0;
+      float o[V];
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const float h = (ck_get<DT>(x, e) - mean) * r, z = fmaf(h, w, bias);
-      const bool kept = m >> e & 1;
-      if constexpr (!BWD) {
-        o[e] = kept ? act_of(z, a.act) * a.drop.scale : 0.f;
-      } else {
-        const float gz = kept && e < n ? ck_get<DT>(gy, e) * a.drop.scale * act_slope(z, a.act) : 0.f;
-        if constexpr (OUT) {
-          o[e] = r * (w * gz - m1 - h * m2);
+      for (int e = 0; e < V; ++e) {
+        const float d = ck_get<DT>(x, e) - mean, z = fmaf(d, rw, bias);
+        if constexpr (!BWD) {
+          o[e] = act_of<ACT>(z);
+          if constexpr (DROP) o[e] = m >> e & 1 ? o[e] * a.drop.scale : 0.f;
         } else {
-          s1 += gz;
-          s2 = e < n ? fmaf(gz, h, s2) : s2;
+          float gz = ck_get<DT>(gy, e) * act_slope<ACT>(z);
+          if constexpr (DROP) gz = m >> e & 1 ? gz * a.drop.scale : 0.f;
+          if constexpr (OUT) {
+            o[e] = fmaf(rw, gz, fmaf(d, c2, c1));
+          } else {
+            gz = e < n ? gz : 0.f;
+            s1 += gz;
+            s2 = e < n ? fmaf(gz, d, s2) : s2;
+          }
         }
       }
-    }
-    if constexpr (OUT) ck_store<DT>(BWD ? a.gx : a.y, base + p, n, ck_raw<DT>(o));
+      if constexpr (OUT) store_chunk<DT>(BWD ? a.gx : a.y, base + p, n, ck_raw<DT>(o));
+    });
   }
 };
 
@@ -215,6 +270,7 @@ __global__ __launch_bounds__(kThreads) void fno_gnorm_rows(GnArgs a) {
   const long rows = (long)a.B * a.C, units = (rows + R - 1) / R * a.S;
   const uint32_t cpr = (uint32_t)((a.P + V - 1) / V), full = (uint32_t)(a.P / V);
   const ck_u32x4 none{0u, 0u, 0u, 0u};
+  auto load = [&](const void *p, size_t i) { return ck_load<DT>(p, i, V); };
   for (long u = blockIdx.x; u < units; u += gridDim.x) {
     const long rg = u / a.S;
     const int s = (int)(u - rg * a.S);
@@ -226,10 +282,9 @@ __global__ __launch_bounds__(kThreads) void fno_gnorm_rows(GnArgs a) {
       for (; k + (AHEAD - 1) * T < min(end, full); k += AHEAD * T) {
         ck_u32x4 x[AHEAD], g[AHEAD];
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) x[i] = ck_load<DT>(a.x, st.base + (size_t)(k + i * T) * V, V);
+        for (int i = 0; i < AHEAD; ++i) x[i] = load(a.x, st.base + (size_t)(k + i * T) * V);
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i)
-          g[i] = BWD ? ck_load<DT>(a.gy, st.base + (size_t)(k + i * T) * V, V) : none;
+        for (int i = 0; i < AHEAD; ++i) g[i] = BWD ? load(a.gy, st.base + (size_t)(k + i * T) * V) : none;
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) st.chunk(x[i], g[i], (k + i * T) * V, V);
       }
@@ -254,7 +309,7 @@ __global__ __launch_bounds__(kThreads) void fno_gnorm_rows(GnArgs a) {
         }
       } else {
         v0 = lane_sum<W>(v0);
-        v1 = lane_sum<W>(v1);
+        v1 = lane_sum<W>(v1 * st.r);
       }
       if constexpr (T > 64) {
         const int wave = threadIdx.x >> 6;
@@ -290,6 +345,7 @@ __global__ __launch_bounds__(kThreads) void fno_gnorm_cols(GnArgs a) {
   const DropKey key = drop_key(a.drop);
   const ck_u32x4 none{0u, 0u, 0u, 0u};
   const long units = RUNS ? a.S : (long)a.B * a.S, all = (long)a.B * a.P;
+  auto load = [&](const void *p, size_t i) { return ck_load<DT>(p, i, V); };
   float w[V], bias[V];
   int grp[V];
   if constexpr (BWD || OUT) {
@@ -306,21 +362,23 @@ __global__ __launch_bounds__(kThreads) void fno_gnorm_cols(GnArgs a) {
       const long p0 = (u - b * a.S) * a.per;
       r0 = b * a.P + p0, r1 = b * a.P + min(a.P, p0 + a.per);
     }
-    float mean[V], r[V], m1[V], m2[V], s1[V], s2[V], shift[V], count = 0.f;
+    // z = (x - mean) rw + bias; gx = rw gz + c1 + (x - mean) c2
+    float mean[V], r[V], rw[V], c1[V], c2[V], s1[V], s2[V], shift[V], count = 0.f;
     auto stats = [&](long sample) {
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         if (e > 0 && grp[e] == grp[e - 1]) {
           mean[e] = mean[e - 1], r[e] = r[e - 1];
-          if constexpr (BWD && OUT) m1[e] = m1[e - 1], m2[e] = m2[e - 1];
-          continue;
+          if constexpr (BWD && OUT) c1[e] = c1[e - 1], c2[e] = c2[e - 1];
+        } else {
+          const float2 st = a.stats[sample * a.G + grp[e]];
+          mean[e] = st.x, r[e] = st.y;
+          if constexpr (BWD && OUT) {
+            const float2 m = a.gsum[sample * a.G + grp[e]];
+            c1[e] = -r[e] * m.x, c2[e] = -r[e] * r[e] * m.y;
+          }
         }
-        const float2 st = a.stats[sample * a.G + grp[e]];
-        mean[e] = st.x, r[e] = st.y;
-        if constexpr (BWD && OUT) {
-          const float2 m = a.gsum[sample * a.G + grp[e]];
-          m1[e] = m.x, m2[e] = m.y;
-        }
+        rw[e] = r[e] * w[e];
       }
     };
 #pragma unroll
@@ -339,25 +397,30 @@ __global__ __launch_bounds__(kThreads) void fno_gnorm_cols(GnArgs a) {
         return;
       }
       const size_t at = (size_t)row * a.C + c0;
-      const uint32_t m = chunk_keep<V, true>(a, key, at, b, c0);
-      float o[V];
+      with_act(a, [&](auto act, auto drop) __attribute__((always_inline)) {
+        constexpr int ACT = decltype(act)::value;
+        constexpr bool DROP = decltype(drop)::value;
+        const uint32_t m = DROP ? chunk_keep<V, true>(a, key, at, b, c0) : 0;
+        float o[V];
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float h = (ck_get<DT>(x, e) - mean[e]) * r[e], z = fmaf(h, w[e], bias[e]);
-        const bool kept = m >> e & 1;
-        if constexpr (!BWD) {
-          o[e] = kept ? act_of(z, a.act) * a.drop.scale : 0.f;
-        } else {
-          const float gz = kept ? ck_get<DT>(gy, e) * a.drop.scale * act_slope(z, a.act) : 0.f;
-          if constexpr (OUT) {
-            o[e] = r[e] * (w[e] * gz - m1[e] - h * m2[e]);
+        for (int e = 0; e < V; ++e) {
+          const float d = ck_get<DT>(x, e) - mean[e], z = fmaf(d, rw[e], bias[e]);
+          if constexpr (!BWD) {
+            o[e] = act_of<ACT>(z);
+            if constexpr (DROP) o[e] = m >> e & 1 ? o[e] * a.drop.scale : 0.f;
           } else {
-            s1[e] += gz;
-            s2[e] = fmaf(gz, h, s2[e]);
+            float gz = ck_get<DT>(gy, e) * act_slope<ACT>(z);
+            if constexpr (DROP) gz = m >> e & 1 ? gz * a.drop.scale : 0.f;
+            if constexpr (OUT) {
+              o[e] = fmaf(rw[e], gz, fmaf(d, c2[e], c1[e]));
+            } else {
+              s1[e] += gz;
+              s2[e] = fmaf(gz, RUNS ? d * r[e] : d, s2[e]);  // a run's samples have an r each
+            }
           }
         }
-      }
-      if constexpr (OUT) ck_store<DT>(BWD ? a.gx : a.y, at, n, ck_raw<DT>(o));
+        if constexpr (OUT) store_chunk<DT>(BWD ? a.gx : a.y, at, n, ck_raw<DT>(o));
+      });
     };
     if (lane) {
       if constexpr ((BWD || OUT) && !RUNS) stats(b);
@@ -367,9 +430,9 @@ __global__ __launch_bounds__(kThreads) void fno_gnorm_cols(GnArgs a) {
         for (; row + (AHEAD - 1) * PL < r1; row += AHEAD * PL) {
           ck_u32x4 x[AHEAD], g[AHEAD];
 #pragma unroll
-          for (int i = 0; i < AHEAD; ++i) x[i] = ck_load<DT>(a.x, (size_t)(row + i * PL) * a.C + c0, V);
+          for (int i = 0; i < AHEAD; ++i) x[i] = load(a.x, (size_t)(row + i * PL) * a.C + c0);
 #pragma unroll
-          for (int i = 0; i < AHEAD; ++i) g[i] = BWD ? ck_load<DT>(a.gy, (size_t)(row + i * PL) * a.C + c0, V) : none;
+          for (int i = 0; i < AHEAD; ++i) g[i] = BWD ? load(a.gy, (size_t)(row + i * PL) * a.C + c0) : none;
 #pragma unroll
           for (int i = 0; i < AHEAD; ++i) {
             if constexpr (RUNS) {
@@ -403,6 +466,8 @@ __global__ __launch_bounds__(kThreads) void fno_gnorm_cols(GnArgs a) {
             const float d = count > 0.f ? v0 / count : 0.f;
             v1 = fmaxf(v1 - v0 * d, 0.f) + (v1 - v1);
             v0 = shift[e] + d;
+          } else if constexpr (!RUNS) {
+            v1 *= r[e];
           }
           red[(pl * V + e) * kn + kl] = make_float2(v0, v1);
         }
@@ -426,19 +491,59 @@ __global__ __launch_bounds__(kThreads) void fno_gnorm_cols(GnArgs a) {
 
 // ------------------------------------------------------------------- joins
 
-// A wave a group: its statistics (forward), or M1 and M2 (backward), from the pieces' sums.
-template <int DT, bool BWD>
-__global__ __launch_bounds__(64) void fno_gnorm_join(GnArgs a) {
-  const int lane = threadIdx.x;
-  const long piece = a.last ? a.per : a.per * ck_vec<DT>(), groups = (long)a.B * a.G;
-  for (long id = blockIdx.x; id < groups; id += gridDim.x) {
+constexpr int kJoin = 1024;
+
+// The sums of pieces joined. The first `groups` workgroups: a group's statistics (forward), or its M1 and M2
+// (backward), a wave a group or, WIDE, all waves; the others: gw and gb of 8 channels each, 128 slices of the
+// sums of `samples` samples (or runs).
+template <int DT, bool BWD, bool WIDE>
+__global__ __launch_bounds__(kJoin) void fno_gnorm_join(GnArgs a, int groups, int samples) {
+  __shared__ float red[16][3];
+  __shared__ float2 slice[128][9];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (BWD && (int)blockIdx.x >= groups) {
+    const int l = threadIdx.x & 7, sl = threadIdx.x >> 3, c = ((int)blockIdx.x - groups) * 8 + l;
+    float2 v = make_float2(0.f, 0.f);
+    const uint32_t all = (uint32_t)samples * (uint32_t)a.S;
+    if (c < a.C)
+#pragma unroll 4
+      for (uint32_t i = sl; i < all; i += 128) {
+        const uint32_t b = i / (uint32_t)a.S;
+        const float2 p = a.part[(long)b * a.sb + c * a.sc + (long)(i - b * a.S) * a.ss];
+        v.x += p.x, v.y += p.y;
+      }
+    slice[sl][l] = v;
+    __syncthreads();
+    if (sl < 16) {  // two waves
+#pragma unroll
+      for (int i = 1; i < 8; ++i) {
+        const float2 p = slice[sl + 16 * i][l];
+        v.x += p.x, v.y += p.y;
+      }
+      // eight slices a wave, 8 lanes each
+#pragma unroll
+      for (int o = 8; o < 64; o <<= 1) v.x += __shfl_xor(v.x, o, 64), v.y += __shfl_xor(v.y, o, 64);
+      if (lane < 8) red[wave * 8 + l][0] = v.x, red[wave * 8 + l][1] = v.y;
+    }
+    __syncthreads();
+    if (threadIdx.x < 8 && c < a.C) {
+      put<DT>(a.gb, c, red[l][0] + red[8 + l][0]);
+      put<DT>(a.gw, c, red[l][1] + red[8 + l][1]);
+    }
+    return;
+  }
+  const long piece = a.last ? a.per : a.per * ck_vec<DT>(), all = (long)a.B * a.G;
+  const int step = WIDE ? kJoin : 64, me = WIDE ? threadIdx.x : lane;
+  const uint32_t n_part = (uint32_t)a.Cg * (uint32_t)a.S, inner = a.last ? (uint32_t)a.Cg : (uint32_t)a.S;
+  for (long id = WIDE ? blockIdx.x : blockIdx.x * 16L + wave; id < all; id += WIDE ? groups : groups * 16L) {
     const long b = id / a.G;
     const int c0 = (int)(id - b * a.G) * a.Cg;
     float n = 0.f, v0 = 0.f, v1 = 0.f;
-    for (long i = lane; i < (long)a.Cg * a.S; i += 64) {
-      // neighbours in memory one after the other
-      const int c = c0 + (int)(a.last ? i % a.Cg : i / a.S);
-      const long s = a.last ? i / a.Cg : i % a.S;
+#pragma unroll 4
+    for (uint32_t i = me; i < n_part; i += step) {  // neighbours in memory one after the other
+      const uint32_t outer = i / inner, in = i - outer * inner;
+      const int c = c0 + (int)(a.last ? in : outer);
+      const long s = a.last ? outer : in;
       const float2 p = a.part[b * a.sb + c * a.sc + s * a.ss];
       if constexpr (BWD) {
         const float w = param(a.w, DT, c, 1.f);
@@ -451,38 +556,29 @@ __global__ __launch_bounds__(64) void fno_gnorm_join(GnArgs a) {
     if constexpr (BWD) {
       v0 = lane_sum<64>(v0);
       v1 = lane_sum<64>(v1);
-      const float size = (float)a.Cg * (float)a.P;
-      if (lane == 0) a.gsum[id] = make_float2(v0 / size, v1 / size);
     } else {
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {
         const float nb = __shfl_xor(n, o, 64), mb = __shfl_xor(v0, o, 64), qb = __shfl_xor(v1, o, 64);
         join_moments(n, v0, v1, nb, mb, qb);
       }
-      if (lane == 0) a.stats[id] = make_float2(v0, rsq(v1 / n + a.eps));
+    }
+    if constexpr (WIDE) {
+      __syncthreads();  // the last group's are read
+      if (lane == 0) red[wave][0] = n, red[wave][1] = v0, red[wave][2] = v1;
+      __syncthreads();
+      if (threadIdx.x == 0)
+        for (int i = 1; i < 16; ++i) {
+          if constexpr (BWD) v0 += red[i][1], v1 += red[i][2];
+          else join_moments(n, v0, v1, red[i][0], red[i][1], red[i][2]);
+        }
+    }
+    if (me == 0) {
+      const float size = (float)a.Cg * (float)a.P;
+      if constexpr (BWD) a.gsum[id] = make_float2(v0 / size, v1 / size);
+      else a.stats[id] = make_float2(v0, rsq(v1 / n + a.eps));
     }
   }
-}
-
-// gw and gb from `samples` x S pieces' sums: 32 channels a workgroup, 32 slices of the sums.
-template <int DT>
-__global__ __launch_bounds__(1024) void fno_gnorm_params(GnArgs a, int samples) {
-  __shared__ float2 red[32][33];
-  const int l = threadIdx.x & 31, sl = threadIdx.x >> 5, c = blockIdx.x * 32 + l;
-  float2 v = make_float2(0.f, 0.f);
-  if (c < a.C)
-    for (long i = sl; i < (long)samples * a.S; i += 32) {
-      const long b = i / a.S;
-      const float2 p = a.part[b * a.sb + c * a.sc + (i - b * a.S) * a.ss];
-      v.x += p.x, v.y += p.y;
-    }
-  red[sl][l] = v;
-  __syncthreads();
-  if (sl != 0 || c >= a.C) return;
-  v = red[0][l];
-  for (int i = 1; i < 32; ++i) v.x += red[i][l].x, v.y += red[i][l].y;
-  put<DT>(a.gb, c, v.x);
-  put<DT>(a.gw, c, v.y);
 }
 
 // ------------------------------------------------------------------ launch
@@ -511,10 +607,12 @@ hipError_t gn_small(const GnArgs &a, int team, hipStream_t s) {
   const void *k = team == 16 ? (const void *)fno_gnorm_small<DT, LAST, BWD, 16, 4>
                   : team == 64 ? (const void *)fno_gnorm_small<DT, LAST, BWD, 64, 4>
                   : team == 256 ? (const void *)fno_gnorm_small<DT, LAST, BWD, 256, 4>
-                                : (const void *)fno_gnorm_small<DT, LAST, BWD, 1024, BWD ? 2 : 4>;
-  const int threads = team > kThreads ? team : kThreads;
-  FNO_BOUNDS(check_gnorm_small(a, LAST, BWD, team, BWD && team == 1024 ? 2 : 4, DT);)
-  return gn_run(k, up((long)a.B * a.G, threads / team), 1, threads, args, s);
+                                : (const void *)fno_gnorm_small<DT, LAST, BWD, 1024, 4>;
+  if constexpr (!BWD)
+    if (team > 1024) k = (const void *)fno_gnorm_small<DT, LAST, BWD, 1024, 8>;
+  const int threads = std::max(kThreads, std::min(team, 1024));
+  FNO_BOUNDS(check_gnorm_small(a, LAST, BWD, std::min(team, 1024), team > 1024 ? 8 : 4, DT);)
+  return gn_run(k, up((long)a.B * a.G, std::max(1, threads / team)), 1, threads, args, s);
 }
 
 template <int DT, bool BWD, bool OUT>
@@ -537,20 +635,17 @@ hipError_t gn_cols(const GnArgs &a, hipStream_t s) {
              up(up(a.C, ck_vec<DT>()), kThreads), kThreads, args, s);
 }
 
+// samples 0: no parameters' gradients; group: the groups' sums are wanted
 template <int DT, bool BWD>
-hipError_t gn_join(const GnArgs &a, hipStream_t s) {
+hipError_t gn_join(const GnArgs &a, bool group, int samples, hipStream_t s) {
   GnArgs arg = a;
-  void *args[] = {(void *)&arg};
-  FNO_BOUNDS(check_gnorm_join(a, BWD, DT);)
-  return gn_run((const void *)fno_gnorm_join<DT, BWD>, (long)a.B * a.G, 1, 64, args, s);
-}
-
-template <int DT>
-hipError_t gn_params(const GnArgs &a, int samples, hipStream_t s) {
-  GnArgs arg = a;
-  void *args[] = {(void *)&arg, (void *)&samples};
-  FNO_BOUNDS(check_gnorm_params(a, samples, DT);)
-  return gn_run((const void *)fno_gnorm_params<DT>, up(a.C, 32), 1, 1024, args, s);
+  const bool wide = (long)a.Cg * a.S > 1024;
+  const long all = (long)a.B * a.G;
+  int groups = group ? (int)std::min(wide ? all : up(all, 16), kMaxGrid / 4) : 0;
+  void *args[] = {(void *)&arg, (void *)&groups, (void *)&samples};
+  FNO_BOUNDS(check_gnorm_join(a, BWD, group, samples, DT);)
+  const void *k = wide ? (const void *)fno_gnorm_join<DT, BWD, true> : (const void *)fno_gnorm_join<DT, BWD, false>;
+  return gn_run(k, groups + (samples ? up(a.C, 8) : 0), 1, kJoin, args, s);
 }
 
 template <int DT>
@@ -561,7 +656,7 @@ hipError_t gn_forward(GnArgs a, void *workspace, hipStream_t s) {
   gn_attach(a, p, workspace, false);
   if (!a.stats) a.stats = a.gsum;  // kept for nobody
   hipError_t e = p.last ? gn_cols<DT, false, false, false>(a, s) : gn_rows<DT, false, false>(a, p.T, s);
-  if (e == hipSuccess) e = gn_join<DT, false>(a, s);
+  if (e == hipSuccess) e = gn_join<DT, false>(a, true, 0, s);
   if (e == hipSuccess) e = p.last ? gn_cols<DT, false, true, false>(a, s) : gn_rows<DT, false, true>(a, p.T, s);
   return e;
 }
@@ -578,10 +673,9 @@ hipError_t gn_backward(GnArgs a, void *workspace, hipStream_t s) {
   gn_attach(a, p, workspace, runs);
   if (!p.last) e = gn_rows<DT, true, false>(a, p.T, s);
   else e = runs ? gn_cols<DT, true, false, true>(a, s) : gn_cols<DT, true, false, false>(a, s);
-  if (e == hipSuccess && sums) e = gn_params<DT>(a, runs ? 1 : a.B, s);
-  if (p.bteam || !a.gx) return e;
-  if (e == hipSuccess) e = gn_join<DT, true>(a, s);
-  if (e == hipSuccess) e = p.last ? gn_cols<DT, true, true, false>(a, s) : gn_rows<DT, true, true>(a, p.T, s);
+  const bool out = !p.bteam && a.gx;
+  if (e == hipSuccess) e = gn_join<DT, true>(a, out, !sums ? 0 : runs ? 1 : a.B, s);
+  if (e == hipSuccess && out) e = p.last ? gn_cols<DT, true, true, false>(a, s) : gn_rows<DT, true, true>(a, p.T, s);
   return e;
 }
 

@@ -96,84 +96,124 @@ __global__ __launch_bounds__(kMx4Threads) void fno_mx4_tokens(Mx4Args a) {
 
 // ------------------------------------------------------------------- fields
 
-// A lane has NP pixels of a sample: chunk q of them is chunk q % ppr of sample q / ppr.
+// A lane has NP pixels of a sample: chunk q of them is chunk q % ppr of sample q / ppr. Packing, two blocks of a
+// workgroup's pixels at a time go through LDS, so that neighbouring lanes store neighbouring 16 bytes: each
+// storing its own pixels' took twice as long (20 x 64 x 256^2 fp16 77 us).
 template <int DT, bool PACK>
 __global__ __launch_bounds__(kMx4Threads) void fno_mx4_field(Mx4Args a) {
-  constexpr int NP = DT == DT_F32 ? 2 : 4;
+  constexpr int NP = DT == DT_F32 ? 2 : 4, PIX = NP * kMx4Threads, KB = 2;
+  __shared__ ck_u32x4 stage[PACK ? PIX * KB : 1];
+  __shared__ uint8_t scales[PACK ? PIX * KB : 1];
   const long ppr = (a.P + NP - 1) / NP, total = a.B * ppr;
-  const long q = (long)blockIdx.x * kMx4Threads + threadIdx.x;
-  if (q >= total) return;
-  const long b = q / ppr, p = (q - b * ppr) * NP;
-  const int n = (int)min((long)NP, a.P - p);
+  const long q0 = (long)blockIdx.x * kMx4Threads, q = q0 + threadIdx.x, qc = min(q, total - 1);
+  if (!PACK && q >= total) return;
+  const long b = qc / ppr, p = (qc - b * ppr) * NP;
+  const int n = q < total ? (int)min((long)NP, a.P - p) : 0;
   using E = typename std::conditional<DT == DT_F32, uint32_t, uint16_t>::type;
-  for (long kb = blockIdx.y; kb < a.nb; kb += gridDim.y) {
-    const int c0 = (int)kb * kMx4Block, nc = min(kMx4Block, a.C - c0);
-    const size_t first = ((size_t)b * a.C + c0) * a.P + p, row = (size_t)b * a.P + p;
-    u32x2 r[kMx4Block];
+  // unit u of the stage, so placed that lanes 8 units apart meet other banks
+  auto at = [](int u) { return u ^ (u >> 3 & 7); };
+  // Where all lanes have whole chunks of pixels the workgroup's rows follow each other, over samples' ends too.
+  const bool whole = a.P % NP == 0 && q0 + kMx4Threads <= total;
+  const int step = PACK ? a.step : 1;  // blocks at a time
+  for (long kb0 = (long)blockIdx.y * step; kb0 < a.nb; kb0 += (long)gridDim.y * step) {
     if constexpr (PACK) {
-      const E *src = reinterpret_cast<const E *>(a.x) + first;
-      if (n == NP) {
+      const int kn = (int)min((long)step, a.nb - kb0);
+      for (int kk = 0; kk < kn; ++kk) {
+        const long kb = kb0 + kk;
+        const int c0 = (int)kb * kMx4Block, nc = min(kMx4Block, a.C - c0);
+        const E *src = reinterpret_cast<const E *>(a.x) + ((size_t)b * a.C + c0) * a.P + p;
+        u32x2 r[kMx4Block];
+        if (n == NP) {
 #pragma unroll
-        for (int i = 0; i < kMx4Block; ++i)
-          r[i] = *reinterpret_cast<const u32x2_any *>(src + (size_t)min(i, nc - 1) * a.P);
-      } else {
-#pragma unroll
-        for (int i = 0; i < kMx4Block; ++i) {
-          const E *s = src + (size_t)min(i, nc - 1) * a.P;
-          if constexpr (DT == DT_F32) {
-            r[i] = u32x2{s[0], 0u};
-          } else {
-            r[i] = u32x2{(uint32_t)s[0], 0u};
-            if (n > 1) r[i][0] |= (uint32_t)s[1] << 16;
-            if (n > 2) r[i][1] = s[2];
-          }
-        }
-      }
-      if (nc < kMx4Block)
-#pragma unroll
-        for (int i = 0; i < kMx4Block; ++i)
-          if (i >= nc) r[i] = u32x2{0u, 0u};
-#pragma unroll
-      for (int j = 0; j < NP; ++j) {
-        uint32_t key = 0;
-        ck_u32x4 code{0u, 0u, 0u, 0u};
-        if constexpr (DT == DT_F32) {
-#pragma unroll
-          for (int i = 0; i < kMx4Block; ++i) key = max(key, r[i][j] & 0x7fffffffu);
+          for (int i = 0; i < kMx4Block; ++i)
+            r[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x2_any *>(src + (size_t)min(i, nc - 1) * a.P));
         } else {
 #pragma unroll
-          for (int i = 0; i < kMx4Block; ++i) key = max(key, (j & 1 ? r[i][j / 2] >> 16 : r[i][j / 2]) & 0x7fffu);
-          if constexpr (DT == DT_F16) key = __float_as_uint((float)__builtin_bit_cast(_Float16, (uint16_t)key));
-          else key <<= 16;
-        }
-        const uint32_t s = mx4_scale(key);
-        const float f = mx4_factor(s);
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          uint32_t v = 0;
-          if constexpr (DT == DT_F32) {
-            auto at = [&](int i) { return __uint_as_float(r[8 * w + i][j]); };
-            v = mx4_pair<0>(v, at(0), at(1), f);
-            v = mx4_pair<1>(v, at(2), at(3), f);
-            v = mx4_pair<2>(v, at(4), at(5), f);
-            v = mx4_pair<3>(v, at(6), at(7), f);
-          } else {  // the halves of two channels' dwords side by side
-            auto at = [&](int i) {
-              return __builtin_amdgcn_perm(r[8 * w + i + 1][j / 2], r[8 * w + i][j / 2], j & 1 ? 0x07060302u : 0x05040100u);
-            };
-            v = mx4_pair<DT, 0>(v, at(0), f);
-            v = mx4_pair<DT, 1>(v, at(2), f);
-            v = mx4_pair<DT, 2>(v, at(4), f);
-            v = mx4_pair<DT, 3>(v, at(6), f);
+          for (int i = 0; i < kMx4Block; ++i) {
+            const E *s = src + (size_t)min(i, nc - 1) * a.P;
+            r[i] = u32x2{0u, 0u};
+            if (n > 0) r[i][0] = s[0];
+            if constexpr (DT != DT_F32) {
+              if (n > 1) r[i][0] |= (uint32_t)s[1] << 16;
+              if (n > 2) r[i][1] = s[2];
+            }
           }
-          code[w] = s == kMx4Bad ? 0u : v;
         }
-        if (j < n) {
-          *reinterpret_cast<ck_u32x4 *>(a.codes + ((row + j) * a.nb + kb) * 16) = code;
-          a.exps[(row + j) * a.nb + kb] = (uint8_t)s;
+        if (nc < kMx4Block)
+#pragma unroll
+          for (int i = 0; i < kMx4Block; ++i)
+            if (i >= nc) r[i] = u32x2{0u, 0u};
+        uint32_t key[NP];
+        if constexpr (DT == DT_F32) {
+          key[0] = key[1] = 0;
+#pragma unroll
+          for (int i = 0; i < kMx4Block; ++i)
+#pragma unroll
+            for (int j = 0; j < NP; ++j) key[j] = max(key[j], r[i][j] & 0x7fffffffu);
+        } else {  // two pixels a word
+          u16x2 m[2] = {u16x2{0, 0}, u16x2{0, 0}};
+#pragma unroll
+          for (int i = 0; i < kMx4Block; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              m[j] = __builtin_elementwise_max(m[j], __builtin_bit_cast(u16x2, r[i][j] & 0x7fff7fffu));
+#pragma unroll
+          for (int j = 0; j < NP; ++j) {
+            key[j] = m[j / 2][j & 1];
+            if constexpr (DT == DT_F16) key[j] = __float_as_uint((float)__builtin_bit_cast(_Float16, (uint16_t)key[j]));
+            else key[j] <<= 16;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < NP; ++j) {
+          ck_u32x4 code;
+          const uint32_t s = mx4_scale(key[j]);
+          const float f = mx4_factor(s);
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            uint32_t v = 0;
+            if constexpr (DT == DT_F32) {
+              auto val = [&](int i) { return __uint_as_float(r[8 * w + i][j]); };
+              v = mx4_pair<0>(v, val(0), val(1), f);
+              v = mx4_pair<1>(v, val(2), val(3), f);
+              v = mx4_pair<2>(v, val(4), val(5), f);
+              v = mx4_pair<3>(v, val(6), val(7), f);
+            } else {  // the halves of two channels' dwords side by side
+              auto val = [&](int i) {
+                return __builtin_amdgcn_perm(r[8 * w + i + 1][j / 2], r[8 * w + i][j / 2], j & 1 ? 0x07060302u : 0x05040100u);
+              };
+              v = mx4_pair<DT, 0>(v, val(0), f);
+              v = mx4_pair<DT, 1>(v, val(2), f);
+              v = mx4_pair<DT, 2>(v, val(4), f);
+              v = mx4_pair<DT, 3>(v, val(6), f);
+            }
+            code[w] = s == kMx4Bad ? 0u : v;
+          }
+          if (whole) {
+            const int u = (threadIdx.x * NP + j) * kn + kk;
+            stage[at(u)] = code;
+            scales[u] = (uint8_t)s;
+          } else if (j < n) {
+            const size_t block = ((size_t)b * a.P + p + j) * a.nb + kb;
+            *reinterpret_cast<ck_u32x4 *>(a.codes + block * 16) = code;
+            a.exps[block] = (uint8_t)s;
+          }
         }
       }
+      if (whole) {
+        __syncthreads();
+        const size_t first = (size_t)q0 * NP;
+        for (int u = threadIdx.x; u < PIX * kn; u += kMx4Threads) {
+          const int px = kn == KB ? u / KB : u, kk = u - px * kn;
+          *reinterpret_cast<ck_u32x4 *>(a.codes + ((first + px) * a.nb + kb0 + kk) * 16) = stage[at(u)];
+          a.exps[(first + px) * a.nb + kb0 + kk] = scales[u];
+        }
+        __syncthreads();
+      }
     } else {
+      const long kb = kb0;
+      const int c0 = (int)kb * kMx4Block, nc = min(kMx4Block, a.C - c0);
+      const size_t row = (size_t)b * a.P + p;
       ck_u32x4 code[NP];
       uint32_t s[NP];
 #pragma unroll
@@ -182,7 +222,7 @@ __global__ __launch_bounds__(kMx4Threads) void fno_mx4_field(Mx4Args a) {
         code[j] = *reinterpret_cast<const ck_u32x4 *>(a.codes + block * 16);
         s[j] = a.exps[block];
       }
-      E *dst = reinterpret_cast<E *>(a.y) + first;
+      E *dst = reinterpret_cast<E *>(a.y) + ((size_t)b * a.C + c0) * a.P + p;
       // two channels of all pixels at a time
       auto pair = [&](auto sel, int w) {
         constexpr int SEL = decltype(sel)::value;
@@ -202,7 +242,7 @@ __global__ __launch_bounds__(kMx4Threads) void fno_mx4_field(Mx4Args a) {
           else t = u32x2{ck_pair<DT>(o[0], o[1]), ck_pair<DT>(o[2], o[3])};
           E *d = dst + (size_t)c * a.P;
           if (n == NP) {
-            *reinterpret_cast<u32x2_any *>(d) = t;
+            __builtin_nontemporal_store((u32x2_any)t, reinterpret_cast<u32x2_any *>(d));
           } else {
             d[0] = (E)t[0];
             if constexpr (DT != DT_F32) {
@@ -239,8 +279,10 @@ hipError_t launch_mx4(const Mx4Args &a, bool pack, int dtype, hipStream_t s) {
         : dtype == DT_F16 ? FNO_PICK(DT_F16, fno_mx4_tokens) : FNO_PICK(DT_BF16, fno_mx4_tokens);
   } else {
     const long np = dtype == DT_F32 ? 2 : 4, groups = (a.B * ((a.P + np - 1) / np) + kMx4Threads - 1) / kMx4Threads;
-    // a workgroup has all of its pixels' blocks, so that rows are written whole, unless the chip would stay empty
-    grid = dim3((unsigned)groups, (unsigned)std::min(a.nb, std::max(1L, 1024 / groups)));
+    // a workgroup has all of its pixels' blocks, so that rows are written whole, unless the chip would stay empty;
+    // two at a time where they go through LDS and there are enough (5 x 200 x 1001 fp32, which has neither: 4.5 us, not 8.6)
+    arg.step = pack && a.P % np == 0 && groups * ((a.nb + 1) / 2) >= 512 ? 2 : 1;
+    grid = dim3((unsigned)groups, (unsigned)std::min((a.nb + arg.step - 1) / arg.step, std::max(1L, 1024 / groups)));
     k = dtype == DT_F32 ? FNO_PICK(DT_F32, fno_mx4_field)
         : dtype == DT_F16 ? FNO_PICK(DT_F16, fno_mx4_field) : FNO_PICK(DT_BF16, fno_mx4_field);
   }

@@ -264,3 +264,20 @@ def test_serving_call(grid):
         assert torch.equal(fno.channel_mix_mx4(x, w, b, add, act=1), y)
     with pytest.raises(ValueError, match="channels"):
         fno.channel_mix_mx4(x.detach()[:, :69].contiguous(), w)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", [(3, 40, 1024), (2, 70, 4096), (5, 96, 1020), (1, 33, 2052), (40, 64, 52), (2, 200, 514)], ids=str)
+def test_kept_values_of_whole_workgroups(dtype, shape):
+    """Pixels of a workgroup that follow each other over samples' ends, odd and even numbers of blocks."""
+    B, C, P = shape
+    gen = torch.Generator(device=DEV).manual_seed(C)
+    x = torch.randn(shape, generator=gen, device=DEV).mul_(torch.exp2(torch.randint(-4, 5, (B, C, 1), generator=gen, device=DEV)))
+    x = x.to(DT[dtype])
+    packed = pack(x)
+    rows = x.transpose(1, 2).reshape(B * P, C).contiguous()  # tokens, whose codes the other tests hold to the definition
+    want = pack(rows)
+    nb = -(-C // 32)
+    at = -(-B * P * nb * 16 // 256) * 256
+    assert torch.equal(packed[:B * P * nb * 16], want[:B * P * nb * 16])
+    assert torch.equal(packed[at:at + B * P * nb], want[at:at + B * P * nb])
