@@ -67,7 +67,7 @@ void check_mix_train(const MixTrainArgs &a, bool fwd, int S, size_t lds, int dty
 void check_norm(const NormArgs &a, bool fwd, int S, int dtype, int threads, int rpg, size_t lds, int wide, int deep);
 void check_drop(const DropArgs &a, int mode, int dtype);
 void check_gnorm_small(const GnArgs &a, bool last, bool bwd, int T, int NC, int dtype);
-void check_gnorm_rows(const GnArgs &a, bool bwd, bool out, int T, int dtype);
+void check_gnorm_rows(const GnArgs &a, bool bwd, bool out, bool fold, bool params, int T, int dtype);
 void check_gnorm_cols(const GnArgs &a, bool bwd, bool out, bool runs, int dtype);
 void check_gnorm_join(const GnArgs &a, bool bwd, bool group, int samples, int dtype);
 void check_mx4(const Mx4Args &a, bool pack, int dtype);

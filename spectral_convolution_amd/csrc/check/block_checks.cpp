@@ -31,7 +31,7 @@ void gn_spans(const Ctx &c, const GnArgs &a, bool bwd, bool out, int dtype) {
   const size_t es = es_of(dtype), n = values(a) * es, groups = (size_t)a.B * a.G;
   c.span("x", a.x, n);
   if (bwd) c.span("gy", a.gy, n);
-  if (out) c.span(bwd ? "gx" : "y", bwd ? a.gx : a.y, n);
+  if (out && !(bwd && !a.gx)) c.span(bwd ? "gx" : "y", bwd ? a.gx : a.y, n);
   c.opt("weight", a.w, a.C * es);
   c.opt("bias", a.b, a.C * es);
   c.opt("step", a.drop.step, 8);
@@ -97,16 +97,27 @@ void check_gnorm_small(const GnArgs &a, bool last, bool bwd, int T, int NC, int 
   c.need("parameters of existing channels", params);
 }
 
-void check_gnorm_rows(const GnArgs &a, bool bwd, bool out, int T, int dtype) {
+void check_gnorm_rows(const GnArgs &a, bool bwd, bool out, bool fold, bool params, int T, int dtype) {
   const Ctx c{bwd ? "fno_gnorm_rows backward" : "fno_gnorm_rows"};
   gn_spans(c, a, bwd, out, dtype);
   const long V = dtype == DT_F32 ? 4 : 8, cpr = (a.P + V - 1) / V, rows = (long)a.B * a.C;
   c.need("pieces cover the row", a.S >= 1 && a.per >= 1 && a.S * a.per >= cpr && (a.S - 1) * a.per < cpr);
   c.need("a row of lanes or a workgroup", T == 8 || T == 64 || T == 256);
   c.need("offsets of a row in 32 bits", cpr * V + 4L * T * V < 1L << 32);
-  if (!out) c.span("sums", a.part, (size_t)rows * a.S * 8);
-  if (bwd && out) c.span("group sums", a.gsum, (size_t)a.B * a.G * 8);
+  if (!out || fold) c.span("sums", a.part, (size_t)rows * a.S * 8);
+  if (bwd && out && !fold) c.span("group sums", a.gsum, (size_t)a.B * a.G * 8);
   c.need("strides of the sums", a.sb == (long)a.C * a.S && a.sc == a.S && a.ss == 1);
+  c.need("workgroups", a.main + (params ? 1 : 0) >= 1 && (long)a.main + (a.C + 7) / 8 < 1L << 24);
+  if (fold) {
+    c.need("no empty piece, a second pass", out && (a.S - 1) * a.per * V < a.P);
+    c.need("a group's sums in 31 bits", (long)a.Cg * a.S + 256 < 1L << 31);
+  }
+  if (params) {
+    c.need("behind a folded backward", fold && bwd);
+    c.opt("gw", a.gw, a.C * es_of(dtype));
+    c.opt("gb", a.gb, a.C * es_of(dtype));
+    c.need("a channel's sums in 32 bits", (long)a.B * a.S + 256 < 1L << 32);
+  }
 }
 
 void check_gnorm_cols(const GnArgs &a, bool bwd, bool out, bool runs, int dtype) {

@@ -201,17 +201,14 @@ struct Row {
     b = row / a.C;
     c = (int)(row - b * a.C);
     base = (size_t)row * a.P;
-    if constexpr (BWD || OUT) {
-      const size_t g = (size_t)b * a.G + c / a.Cg;
-      const float2 st = a.stats[g];
-      mean = st.x, r = st.y;
-      rw = r * param(a.w, DT, c, 1.f);
-      bias = param(a.b, DT, c, 0.f);
-      if constexpr (BWD && OUT) {
-        const float2 m = a.gsum[g];
-        c1 = -r * m.x, c2 = -r * r * m.y;
-      }
-    }
+  }
+  __device__ __forceinline__ size_t group() const { return (size_t)b * a.G + c / a.Cg; }
+  // st: the group's statistics; m: its M1 and M2
+  __device__ __forceinline__ void use(const float2 &st, const float2 &m) {
+    mean = st.x, r = st.y;
+    rw = r * param(a.w, DT, c, 1.f);
+    bias = param(a.b, DT, c, 0.f);
+    c1 = -r * m.x, c2 = -r * r * m.y;
   }
 
   // chunk at value p of the row, n of its values there
@@ -260,22 +257,102 @@ struct Row {
   }
 };
 
-// T lanes a row, S pieces a row. OUT: the second pass; else the sums of the pieces.
-template <int DT, bool BWD, bool OUT, int T>
+// A float2 each of T threads' (n, v0, v1) joined: moments, or with BWD sums. T threads a team; red: three floats a wave.
+template <bool BWD, int T>
+__device__ __forceinline__ void team_join(float &n, float &v0, float &v1, float (*red)[3]) {
+  constexpr int W = T < 64 ? T : 64;
+#pragma unroll
+  for (int o = 1; o < W; o <<= 1) {
+    const float nb = BWD ? 0.f : __shfl_xor(n, o, 64), mb = __shfl_xor(v0, o, 64), qb = __shfl_xor(v1, o, 64);
+    if constexpr (BWD) v0 += mb, v1 += qb;
+    else join_moments(n, v0, v1, nb, mb, qb);
+  }
+  if constexpr (T > 64) {
+    const int wave = threadIdx.x >> 6;
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) red[wave][0] = n, red[wave][1] = v0, red[wave][2] = v1;
+    __syncthreads();
+    n = red[0][0], v0 = red[0][1], v1 = red[0][2];
+#pragma unroll
+    for (int i = 1; i < T / 64; ++i) {
+      if constexpr (BWD) v0 += red[i][1], v1 += red[i][2];
+      else join_moments(n, v0, v1, red[i][0], red[i][1], red[i][2]);
+    }
+  }
+}
+
+// gw and gb of channels 8 block .. + 7 from the sums of the samples' pieces: 32 threads a channel
+template <int DT>
+__device__ __forceinline__ void params_block(const GnArgs &a, int block) {
+  __shared__ float2 slice[32][9];
+  const int l = threadIdx.x & 7, sl = threadIdx.x >> 3, c = block * 8 + l;
+  float2 v = make_float2(0.f, 0.f);
+  const uint32_t all = (uint32_t)a.B * (uint32_t)a.S;
+  if (c < a.C)
+#pragma unroll 4
+    for (uint32_t i = sl; i < all; i += 32) {
+      const uint32_t b = i / (uint32_t)a.S;
+      const float2 p = a.part[(long)b * a.sb + c * a.sc + (long)(i - b * a.S) * a.ss];
+      v.x += p.x, v.y += p.y;
+    }
+  slice[sl][l] = v;
+  __syncthreads();
+  if (sl > 0 || c >= a.C) return;
+  for (int i = 1; i < 32; ++i) v.x += slice[i][l].x, v.y += slice[i][l].y;
+  put<DT>(a.gb, c, v.x);
+  put<DT>(a.gw, c, v.y);
+}
+
+// T lanes a row, S pieces a row. OUT: the second pass; else the sums of the pieces. FOLD: the second pass joins
+// its group's pieces itself (a launch less), and workgroups behind the rows' (from a.main on) join the parameters'.
+template <int DT, bool BWD, bool OUT, bool FOLD, int T>
 __global__ __launch_bounds__(kThreads) void fno_gnorm_rows(GnArgs a) {
   constexpr int V = ck_vec<DT>(), R = kThreads / T, AHEAD = 4;
   __shared__ float red[4][3];
+  if constexpr (BWD && FOLD)
+    if ((int)blockIdx.x >= a.main) {
+      params_block<DT>(a, (int)blockIdx.x - a.main);
+      return;
+    }
   const int t = threadIdx.x % T;
   const DropKey key = drop_key(a.drop);
   const long rows = (long)a.B * a.C, units = (rows + R - 1) / R * a.S;
   const uint32_t cpr = (uint32_t)((a.P + V - 1) / V), full = (uint32_t)(a.P / V);
   const ck_u32x4 none{0u, 0u, 0u, 0u};
   auto load = [&](const void *p, size_t i) { return ck_load<DT>(p, i, V); };
-  for (long u = blockIdx.x; u < units; u += gridDim.x) {
+  for (long u = blockIdx.x; u < units; u += FOLD ? a.main : (int)gridDim.x) {
     const long rg = u / a.S;
     const int s = (int)(u - rg * a.S);
     const long rid = rg * R + threadIdx.x / T, row = min(rid, rows - 1);
     Row<DT, BWD, OUT> st(a, key, row);
+    if constexpr (FOLD) {
+      const int g = st.c / a.Cg, c0 = g * a.Cg;
+      const float2 *part = a.part + ((size_t)st.b * a.C + c0) * a.S;  // the group's Cg rows of S
+      float n = 0.f, v0 = 0.f, v1 = 0.f;
+      for (int i = t; i < a.Cg * a.S; i += T) {
+        const int ch = i / a.S;
+        const float2 p = part[i];
+        if constexpr (BWD) {
+          const float w = param(a.w, DT, c0 + ch, 1.f);
+          v0 = fmaf(w, p.x, v0), v1 = fmaf(w, p.y, v1);
+        } else {
+          const long at = (long)(i - ch * a.S) * a.per * V;
+          join_moments(n, v0, v1, (float)(min(a.P, at + a.per * V) - at), p.x, p.y);
+        }
+      }
+      team_join<BWD, T>(n, v0, v1, red);
+      if constexpr (BWD) {
+        const float size = (float)a.Cg * (float)a.P;
+        st.use(a.stats[st.group()], make_float2(v0 / size, v1 / size));
+      } else {
+        const float2 m = make_float2(v0, rsq(v1 / n + a.eps));
+        if (a.stats && t == 0 && s == 0 && st.c == c0 && rid < rows) a.stats[st.group()] = m;
+        st.use(m, make_float2(0.f, 0.f));
+      }
+    } else if constexpr (BWD || OUT) {
+      const size_t g = st.group();
+      st.use(a.stats[g], BWD && OUT ? a.gsum[g] : make_float2(0.f, 0.f));
+    }
     const uint32_t end = (uint32_t)min((long)cpr, (s + 1L) * a.per);
     uint32_t k = (uint32_t)(s * a.per) + t;
     if (!OUT || rid < rows) {
@@ -297,32 +374,14 @@ __global__ __launch_bounds__(kThreads) void fno_gnorm_rows(GnArgs a) {
     }
     if constexpr (!OUT) {
       float n = st.cnt, v0 = st.s1, v1 = st.s2;
-      constexpr int W = T < 64 ? T : 64;
       if constexpr (!BWD) {
         const float d = n > 0.f ? v0 / n : 0.f;
         v1 = fmaxf(v1 - v0 * d, 0.f) + (v1 - v1);  // not below 0, NaN where it is NaN
         v0 = st.shift + d;
-#pragma unroll
-        for (int o = 1; o < W; o <<= 1) {
-          const float nb = __shfl_xor(n, o, 64), mb = __shfl_xor(v0, o, 64), qb = __shfl_xor(v1, o, 64);
-          join_moments(n, v0, v1, nb, mb, qb);
-        }
       } else {
-        v0 = lane_sum<W>(v0);
-        v1 = lane_sum<W>(v1 * st.r);
+        v1 *= st.r;
       }
-      if constexpr (T > 64) {
-        const int wave = threadIdx.x >> 6;
-        __syncthreads();
-        if ((threadIdx.x & 63) == 0) red[wave][0] = n, red[wave][1] = v0, red[wave][2] = v1;
-        __syncthreads();
-        if (threadIdx.x == 0)
-#pragma unroll
-          for (int i = 1; i < 4; ++i) {
-            if constexpr (BWD) v0 += red[i][1], v1 += red[i][2];
-            else join_moments(n, v0, v1, red[i][0], red[i][1], red[i][2]);
-          }
-      }
+      team_join<BWD, T>(n, v0, v1, red);
       if (t == 0 && rid < rows) a.part[rid * a.S + s] = make_float2(v0, v1);
     }
   }
@@ -615,15 +674,18 @@ hipError_t gn_small(const GnArgs &a, int team, hipStream_t s) {
   return gn_run(k, up((long)a.B * a.G, std::max(1, threads / team)), 1, threads, args, s);
 }
 
-template <int DT, bool BWD, bool OUT>
-hipError_t gn_rows(const GnArgs &a, int T, hipStream_t s) {
+// fold: as in the kernel; params: its backward joins the parameters' sums too
+template <int DT, bool BWD, bool OUT, bool FOLD>
+hipError_t gn_rows(const GnArgs &a, int T, bool params, hipStream_t s) {
   GnArgs arg = a;
+  // no gx: the parameters' sums alone, in the order that they have beside it
+  arg.main = BWD && OUT && !a.gx ? 0 : (int)std::min(up((long)a.B * a.C, kThreads / T) * a.S, kMaxGrid);
   void *args[] = {(void *)&arg};
-  const void *k = T == 8 ? (const void *)fno_gnorm_rows<DT, BWD, OUT, 8>
-                  : T == 64 ? (const void *)fno_gnorm_rows<DT, BWD, OUT, 64>
-                            : (const void *)fno_gnorm_rows<DT, BWD, OUT, 256>;
-  FNO_BOUNDS(check_gnorm_rows(a, BWD, OUT, T, DT);)
-  return gn_run(k, up((long)a.B * a.C, kThreads / T) * a.S, 1, kThreads, args, s);
+  const void *k = T == 8 ? (const void *)fno_gnorm_rows<DT, BWD, OUT, FOLD, 8>
+                  : T == 64 ? (const void *)fno_gnorm_rows<DT, BWD, OUT, FOLD, 64>
+                            : (const void *)fno_gnorm_rows<DT, BWD, OUT, FOLD, 256>;
+  FNO_BOUNDS(check_gnorm_rows(arg, BWD, OUT, FOLD, params, T, DT);)
+  return hipLaunchKernel(k, dim3((unsigned)(arg.main + (params ? up(a.C, 8) : 0))), dim3(kThreads), args, 0, s);
 }
 
 template <int DT, bool BWD, bool OUT, bool RUNS>
@@ -648,17 +710,22 @@ hipError_t gn_join(const GnArgs &a, bool group, int samples, hipStream_t s) {
   return gn_run(k, groups + (samples ? up(a.C, 8) : 0), 1, kJoin, args, s);
 }
 
+// channels first: a group's pieces are few enough for each of its second pass's teams to join them
+inline bool gn_fold(const GnArgs &a, const GnPlan &p) { return !p.last && (long)a.Cg * a.S <= 4 * p.T; }
+
 template <int DT>
 hipError_t gn_forward(GnArgs a, void *workspace, hipStream_t s) {
   const GnPlan p = gn_plan(a, DT);
   a.last = p.last;
   if (p.team) return p.last ? gn_small<DT, true, false>(a, p.team, s) : gn_small<DT, false, false>(a, p.team, s);
   gn_attach(a, p, workspace, false);
+  hipError_t e = p.last ? gn_cols<DT, false, false, false>(a, s) : gn_rows<DT, false, false, false>(a, p.T, false, s);
+  if (e != hipSuccess) return e;
+  if (gn_fold(a, p)) return gn_rows<DT, false, true, true>(a, p.T, false, s);
   if (!a.stats) a.stats = a.gsum;  // kept for nobody
-  hipError_t e = p.last ? gn_cols<DT, false, false, false>(a, s) : gn_rows<DT, false, false>(a, p.T, s);
-  if (e == hipSuccess) e = gn_join<DT, false>(a, true, 0, s);
-  if (e == hipSuccess) e = p.last ? gn_cols<DT, false, true, false>(a, s) : gn_rows<DT, false, true>(a, p.T, s);
-  return e;
+  e = gn_join<DT, false>(a, true, 0, s);
+  if (e != hipSuccess) return e;
+  return p.last ? gn_cols<DT, false, true, false>(a, s) : gn_rows<DT, false, true, false>(a, p.T, false, s);
 }
 
 template <int DT>
@@ -669,14 +736,15 @@ hipError_t gn_backward(GnArgs a, void *workspace, hipStream_t s) {
   hipError_t e = hipSuccess;
   if (p.bteam && a.gx) e = p.last ? gn_small<DT, true, true>(a, p.bteam, s) : gn_small<DT, false, true>(a, p.bteam, s);
   if (e != hipSuccess || (p.bteam && !sums)) return e;
-  const bool runs = p.bteam && p.last;
+  const bool runs = p.bteam && p.last, out = !p.bteam && a.gx;
   gn_attach(a, p, workspace, runs);
-  if (!p.last) e = gn_rows<DT, true, false>(a, p.T, s);
+  if (!p.last) e = gn_rows<DT, true, false, false>(a, p.T, false, s);
   else e = runs ? gn_cols<DT, true, false, true>(a, s) : gn_cols<DT, true, false, false>(a, s);
-  const bool out = !p.bteam && a.gx;
-  if (e == hipSuccess) e = gn_join<DT, true>(a, out, !sums ? 0 : runs ? 1 : a.B, s);
-  if (e == hipSuccess && out) e = p.last ? gn_cols<DT, true, true, false>(a, s) : gn_rows<DT, true, true>(a, p.T, s);
-  return e;
+  if (e != hipSuccess) return e;
+  if (!p.bteam && gn_fold(a, p)) return gn_rows<DT, true, true, true>(a, p.T, sums, s);
+  e = gn_join<DT, true>(a, out, !sums ? 0 : runs ? 1 : a.B, s);
+  if (e != hipSuccess || !out) return e;
+  return p.last ? gn_cols<DT, true, true, false>(a, s) : gn_rows<DT, true, true, false>(a, p.T, false, s);
 }
 
 }  // namespace fno

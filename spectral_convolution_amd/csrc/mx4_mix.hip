@@ -164,11 +164,12 @@ __global__ __launch_bounds__(kThreads) void fno_mx4_mix(Gemm g) {
 }
 
 // Few second rows (one token, a handful): a workgroup has 16 f and all 16 NS s, its eight waves an
-// eighth of the steps each, joined through LDS. Every load of a wave's next U steps is in flight at a time: bound by
-// the first operand's bytes. WHOLE: rows of whole steps (nb % 4 == 0), scales four at a time.
+// eighth of the steps each, joined through LDS. Every load of a wave's next four steps is in flight at a time: bound by
+// the first operand's bytes (28672 x 8192: 125 MB). WHOLE: rows of whole steps (nb % 4 == 0), whose
+// scales of four steps are one load; a load of four bytes for each took a third more time.
 template <int DT, int NS, bool WHOLE>
 __global__ __launch_bounds__(512) void fno_mx4_mix_few(Gemm g) {
-  constexpr int W = 8, U = NS == 1 ? 8 : 4;
+  constexpr int W = 8, U = 4;
   __shared__ v4f red[W][NS][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, quad = lane >> 4;
   const long ft = (g.nf + 15) / 16, tiles = ft * g.batches, steps = (g.nb + 3) / 4, per = (steps + W - 1) / W;
@@ -176,6 +177,21 @@ __global__ __launch_bounds__(512) void fno_mx4_mix_few(Gemm g) {
   size_t sr[NS];
 #pragma unroll
   for (int j = 0; j < NS; ++j) sr[j] = (size_t)min(16L * j + l16, g.ns - 1) * g.nb;
+  // the scales of steps k .. k + 3 of the row at block `row`, a lane's own in the low byte of each later
+  auto scales = [&](const uint8_t *e, size_t row, long k, uint32_t *x) __attribute__((always_inline)) {
+    if (WHOLE && k + U <= steps) {
+      typedef unsigned u32x4_4 __attribute__((ext_vector_type(4), aligned(4)));
+      const u32x4_4 v = *reinterpret_cast<const u32x4_4 *>(e + row + 4 * k);
+#pragma unroll
+      for (int u = 0; u < U; ++u) x[u] = v[u];
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const long step = min(k + u, k1 - 1);
+        x[u] = WHOLE ? *reinterpret_cast<const uint32_t *>(e + row + 4 * step) : e[row + min(4 * step + quad, g.nb - 1)];
+      }
+    }
+  };
   for (long t = blockIdx.x; t < tiles; t += gridDim.x) {
     const long b = t / ft, f0 = (t - b * ft) * 16;
     const size_t fr = (size_t)(b * g.nf + min(f0 + l16, g.nf - 1)) * g.nb;
@@ -185,17 +201,15 @@ __global__ __launch_bounds__(512) void fno_mx4_mix_few(Gemm g) {
     for (long k = k0; k < k1; k += U) {
       ck_u32x4 fc[U], sc[NS][U];
       uint32_t fx[U], sx[NS][U];
+      scales(g.fe, fr, k, fx);
+#pragma unroll
+      for (int j = 0; j < NS; ++j) scales(g.se, sr[j], k, sx[j]);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const long step = min(k + u, k1 - 1);
-        const long kb = 4 * step + quad, kc = WHOLE ? kb : min(kb, g.nb - 1);
+        const long kb = 4 * min(k + u, k1 - 1) + quad, kc = WHOLE ? kb : min(kb, g.nb - 1);
         fc[u] = *reinterpret_cast<const ck_u32x4 *>(g.fq + (fr + kc) * 16);
-        fx[u] = WHOLE ? *reinterpret_cast<const uint32_t *>(g.fe + fr + 4 * step) : g.fe[fr + kc];
 #pragma unroll
-        for (int j = 0; j < NS; ++j) {
-          sc[j][u] = *reinterpret_cast<const ck_u32x4 *>(g.sq + (sr[j] + kc) * 16);
-          sx[j][u] = WHOLE ? *reinterpret_cast<const uint32_t *>(g.se + sr[j] + 4 * step) : g.se[sr[j] + kc];
-        }
+        for (int j = 0; j < NS; ++j) sc[j][u] = *reinterpret_cast<const ck_u32x4 *>(g.sq + (sr[j] + kc) * 16);
       }
       __builtin_amdgcn_sched_barrier(0);  // all loads first
 #pragma unroll
@@ -498,8 +512,8 @@ template <int DT>
 const void *few_kernel(const Gemm &g) {
   const bool whole = g.nb % 4 == 0;
   if (g.ns <= 16) return whole ? (const void *)fno_mx4_mix_few<DT, 1, true> : (const void *)fno_mx4_mix_few<DT, 1, false>;
-  if (g.ns <= 32) return whole ? (const void *)fno_mx4_mix_few<DT, 2, true> : (const void *)fno_mx4_mix_few<DT, 2, false>;
-  return whole ? (const void *)fno_mx4_mix_few<DT, 4, true> : (const void *)fno_mx4_mix_few<DT, 4, false>;
+  if (g.ns > 32) return (const void *)fno_mx4_mix_few<DT, 4, false>;
+  return whole ? (const void *)fno_mx4_mix_few<DT, 2, true> : (const void *)fno_mx4_mix_few<DT, 2, false>;
 }
 
 template <int DT>
@@ -522,13 +536,14 @@ hipError_t launch_mx4_mix(const Mx4MixArgs &a, int dtype, hipStream_t s) {
   }
   FNO_BOUNDS(check_mx4_mix(a, dtype);)
   void *args[] = {(void *)&g};
-  // few rows: 1 x 8192 x 8192 97 us as below, 13 so
-  if (g.ns <= 64 && g.nb >= 32) {
+  // few rows: 1 x 8192 x 8192 97 us as below, 11 so; from 33 on tiles are as fast where rows are whole steps
+  // (64 x 8192 x 8192: 42 us so, 27 in tiles)
+  if (g.nb >= 32 && g.ns <= (g.nb % 4 == 0 ? 32 : 64)) {
     const void *k = dtype == DT_F32 ? few_kernel<DT_F32>(g) : dtype == DT_F16 ? few_kernel<DT_F16>(g) : few_kernel<DT_BF16>(g);
     return hipLaunchKernel(k, dim3((unsigned)std::min((g.nf + 15) / 16 * g.batches, kMaxGrid)), dim3(512), args, 0, s);
   }
   auto tiles = [&](long T) { return (g.nf + T - 1) / T * ((g.ns + T - 1) / T) * g.batches; };
-  if (g.nb % 4 == 0 && g.nb >= 16 && g.ns > 64 && tiles(64) <= kMaxGrid) {
+  if (g.nb % 4 == 0 && g.nb >= 16 && g.ns > 32 && tiles(64) <= kMaxGrid) {
     // The largest tiles that still give three quarters of the 256 compute units one (bf16, random codes; tiles of
     // 256 / 128 / 64): 4096^3 59 / 68 / 106 us, 2048 x 4096 x 4096 44 / 34 / 56, 512 x 4096 x 4096 39 / 19 / 14.
     const int w = tiles(256) >= 192 ? 4 : tiles(128) >= 192 ? 2 : 1;
