@@ -47,6 +47,7 @@ struct GnArgs {
   int S;                 // pieces of a row (channels first) or of a sample (channels last), or runs
   long per;              // 16-byte chunks of such a piece (channels first), rows of it (channels last)
   long sb, sc, ss;       // strides of part: sample, channel, piece
+  int whole;             // channels last, forward: channels of a group whose sums are joined to one, else 0 (join: 1)
   int main;              // channels first: workgroups of the rows, in front of those of the parameters' sums
 };
 

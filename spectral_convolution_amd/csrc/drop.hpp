@@ -62,4 +62,9 @@ __device__ __forceinline__ uint32_t drop_one(const DropKey &key, uint32_t thr, u
   return (drop_block(key, thr, u >> 3) >> (u & 7)) & 1u ? 0xffu : 0u;
 }
 
+// v where bit e is set, else 0 (whatever v is, a NaN too), without a branch round what computes v
+__device__ __forceinline__ float drop_masked(uint32_t keep, int e, float v) {
+  return __uint_as_float(__float_as_uint(v) & (uint32_t)__builtin_amdgcn_sbfe((int)keep, e, 1));
+}
+
 }  // namespace fno

@@ -134,7 +134,7 @@ __global__ __launch_bounds__(T > kThreads ? T : kThreads) void fno_gnorm_small(G
 #pragma unroll
           for (int e = 0; e < V; ++e) {
             const float z = fmaf((ck_get<DT>(rx[i], e) - mean) * r, w[e], bb[e]);
-            o[e] = m >> e & 1 ? act_of<ACT>(z) * scale : 0.f;
+            o[e] = drop_masked(m, e, act_of<ACT>(z) * scale);
           }
           if (there && p.n) store_chunk<DT>(a.y, p.at, p.n, ck_raw<DT>(o));
           channel_done();
@@ -159,7 +159,7 @@ __global__ __launch_bounds__(T > kThreads ? T : kThreads) void fno_gnorm_small(G
             for (int e = 0; e < V; ++e) {
               const float h = (ck_get<DT>(rx[i], e) - mean) * r, z = fmaf(h, w[e], bb[e]);
               const float gz = ck_get<DT>(rg[i], e) * scale * act_slope<ACT>(z);
-              const float g = (m >> e & 1) && e < p.n ? gz * w[e] : 0.f;
+              const float g = drop_masked(m, e, e < p.n ? gz * w[e] : 0.f);
               if constexpr (OUT) {
                 o[e] = r * (g - s1 - h * s2);
               } else {
@@ -239,10 +239,10 @@ struct Row {
         const float d = ck_get<DT>(x, e) - mean, z = fmaf(d, rw, bias);
         if constexpr (!BWD) {
           o[e] = act_of<ACT>(z);
-          if constexpr (DROP) o[e] = m >> e & 1 ? o[e] * a.drop.scale : 0.f;
+          if constexpr (DROP) o[e] = drop_masked(m, e, o[e] * a.drop.scale);
         } else {
           float gz = ck_get<DT>(gy, e) * act_slope<ACT>(z);
-          if constexpr (DROP) gz = m >> e & 1 ? gz * a.drop.scale : 0.f;
+          if constexpr (DROP) gz = drop_masked(m, e, gz * a.drop.scale);
           if constexpr (OUT) {
             o[e] = fmaf(rw, gz, fmaf(d, c2, c1));
           } else {
@@ -394,7 +394,7 @@ __global__ __launch_bounds__(kThreads) void fno_gnorm_rows(GnArgs a) {
 // RUNS rows of any samples (the parameters' sums of small groups).
 template <int DT, bool BWD, bool OUT, bool RUNS>
 __global__ __launch_bounds__(kThreads) void fno_gnorm_cols(GnArgs a) {
-  constexpr int V = ck_vec<DT>(), AHEAD = 2;
+  constexpr int V = ck_vec<DT>(), AHEAD = BWD || OUT ? 2 : 4;
   __shared__ float2 red[OUT ? 1 : kThreads * V];
   __shared__ float cnt[OUT || BWD ? 1 : kThreads];
   const int cpr = (a.C + V - 1) / V, kb = blockIdx.y * kThreads, kn = min(kThreads, cpr - kb), PL = kThreads / kn;
@@ -466,10 +466,10 @@ __global__ __launch_bounds__(kThreads) void fno_gnorm_cols(GnArgs a) {
           const float d = ck_get<DT>(x, e) - mean[e], z = fmaf(d, rw[e], bias[e]);
           if constexpr (!BWD) {
             o[e] = act_of<ACT>(z);
-            if constexpr (DROP) o[e] = m >> e & 1 ? o[e] * a.drop.scale : 0.f;
+            if constexpr (DROP) o[e] = drop_masked(m, e, o[e] * a.drop.scale);
           } else {
             float gz = ck_get<DT>(gy, e) * act_slope<ACT>(z);
-            if constexpr (DROP) gz = m >> e & 1 ? gz * a.drop.scale : 0.f;
+            if constexpr (DROP) gz = drop_masked(m, e, gz * a.drop.scale);
             if constexpr (OUT) {
               o[e] = fmaf(rw[e], gz, fmaf(d, c2[e], c1[e]));
             } else {
@@ -542,8 +542,22 @@ __global__ __launch_bounds__(kThreads) void fno_gnorm_cols(GnArgs a) {
           if constexpr (BWD) v.x += o.x, v.y += o.y;
           else join_moments(nn, v.x, v.y, cnt[q * kn + l], o.x, o.y);
         }
-        a.part[u * a.C + kb * V + i] = v;
+        if (!BWD && a.whole) red[e * kn + l] = v;  // nobody else reads this place
+        else a.part[u * a.C + kb * V + i] = v;
       }
+      if constexpr (!BWD)
+        if (a.whole) {  // the channels' moments, of as many values each, joined to the groups'
+          __syncthreads();
+          for (int g = threadIdx.x; g < a.G; g += kThreads) {
+            float nn = 0.f, m = 0.f, q = 0.f;
+            for (int i = 0; i < a.Cg; ++i) {
+              const int c = g * a.Cg + i;
+              const float2 o = red[c % V * kn + c / V];
+              join_moments(nn, m, q, (float)(r1 - r0), o.x, o.y);
+            }
+            a.part[u * a.G + g] = make_float2(m, q);
+          }
+        }
     }
   }
 }
@@ -609,7 +623,7 @@ __global__ __launch_bounds__(kJoin) void fno_gnorm_join(GnArgs a, int groups, in
         v0 = fmaf(w, p.x, v0);
         v1 = fmaf(w, p.y, v1);
       } else {
-        join_moments(n, v0, v1, (float)(min(a.P, (s + 1) * piece) - s * piece), p.x, p.y);
+        join_moments(n, v0, v1, (float)((min(a.P, (s + 1) * piece) - s * piece) * a.whole), p.x, p.y);
       }
     }
     if constexpr (BWD) {
@@ -719,11 +733,17 @@ hipError_t gn_forward(GnArgs a, void *workspace, hipStream_t s) {
   a.last = p.last;
   if (p.team) return p.last ? gn_small<DT, true, false>(a, p.team, s) : gn_small<DT, false, false>(a, p.team, s);
   gn_attach(a, p, workspace, false);
+  // Channels last, few channels a group: the first pass joins them, and the pieces are of groups
+  const bool groups = p.last && a.Cg <= 16 && a.C <= kThreads * ck_vec<DT>();
+  a.whole = groups ? a.Cg : 0;
   hipError_t e = p.last ? gn_cols<DT, false, false, false>(a, s) : gn_rows<DT, false, false, false>(a, p.T, false, s);
   if (e != hipSuccess) return e;
   if (gn_fold(a, p)) return gn_rows<DT, false, true, true>(a, p.T, false, s);
   if (!a.stats) a.stats = a.gsum;  // kept for nobody
-  e = gn_join<DT, false>(a, true, 0, s);
+  GnArgs j = a;
+  if (groups) j.C = a.G, j.Cg = 1, j.sb = (long)a.G * a.S, j.ss = a.G;
+  else j.whole = 1;
+  e = gn_join<DT, false>(j, true, 0, s);
   if (e != hipSuccess) return e;
   return p.last ? gn_cols<DT, false, true, false>(a, s) : gn_rows<DT, false, true, false>(a, p.T, false, s);
 }
