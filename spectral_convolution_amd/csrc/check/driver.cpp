@@ -265,6 +265,12 @@ void trace_call(const std::string &op, int dt, const std::vector<long> &v) {
     EXPECT(fno_channel_mix_save(far(nx), A, bias, add ? far(ny) : nullptr, far(ny), saved, B, I, O, P, act, d, nullptr) == FNO_OK);
     EXPECT(fno_channel_mix_backward_saved(saved, A, bias, far(ny), far(nx), far(na), far(O * es), add ? far(ny) : nullptr,
                                           far(wb), B, I, O, P, act, add, d, nullptr) == FNO_OK);
+  } else if (op == "gnorm") {
+    run_gnorm((int)v[0], (int)v[1], v[2], (int)v[3], (int)v[4], d);
+  } else if (op == "drop") {
+    run_drop((int)v[0], (int)v[1], v[2], d);
+  } else if (op == "mx4") {
+    run_mx4((int)v[0], (int)v[1], (int)v[2], v[3], d);
   } else {
     run_checkpoint_far(v[0], v[1], d);
   }
@@ -276,7 +282,7 @@ void trace_calls() {
   int dt;
   while (std::scanf("%15s %d", op, &dt) == 2) {
     const std::string name = op;
-    std::vector<long> v(name == "norm" ? 4 : name == "mix" ? 6 : 2);
+    std::vector<long> v(name == "norm" || name == "mx4" ? 4 : name == "mix" ? 6 : name == "gnorm" ? 5 : name == "drop" ? 3 : 2);
     for (long &x : v) EXPECT(std::scanf("%ld", &x) == 1);
     trace_call(name, dt, v);
   }

@@ -695,9 +695,9 @@ hipError_t gn_rows(const GnArgs &a, int T, bool params, hipStream_t s) {
   // no gx: the parameters' sums alone, in the order that they have beside it
   arg.main = BWD && OUT && !a.gx ? 0 : (int)std::min(up((long)a.B * a.C, kThreads / T) * a.S, kMaxGrid);
   void *args[] = {(void *)&arg};
-  const void *k = T == 8 ? (const void *)fno_gnorm_rows<DT, BWD, OUT, FOLD, 8>
-                  : T == 64 ? (const void *)fno_gnorm_rows<DT, BWD, OUT, FOLD, 64>
-                            : (const void *)fno_gnorm_rows<DT, BWD, OUT, FOLD, 256>;
+  const void *k = T == 64 ? (const void *)fno_gnorm_rows<DT, BWD, OUT, FOLD, 64> : (const void *)fno_gnorm_rows<DT, BWD, OUT, FOLD, 256>;
+  if constexpr (!FOLD)
+    if (T == 8) k = (const void *)fno_gnorm_rows<DT, BWD, OUT, FOLD, 8>;
   FNO_BOUNDS(check_gnorm_rows(arg, BWD, OUT, FOLD, params, T, DT);)
   return hipLaunchKernel(k, dim3((unsigned)(arg.main + (params ? up(a.C, 8) : 0))), dim3(kThreads), args, 0, s);
 }
@@ -725,7 +725,8 @@ hipError_t gn_join(const GnArgs &a, bool group, int samples, hipStream_t s) {
 }
 
 // channels first: a group's pieces are few enough for each of its second pass's teams to join them
-inline bool gn_fold(const GnArgs &a, const GnPlan &p) { return !p.last && (long)a.Cg * a.S <= 4 * p.T; }
+// (of short rows, T = 8, a group that a team does not hold whole has too many)
+inline bool gn_fold(const GnArgs &a, const GnPlan &p) { return !p.last && p.T > 8 && (long)a.Cg * a.S <= 4 * p.T; }
 
 template <int DT>
 hipError_t gn_forward(GnArgs a, void *workspace, hipStream_t s) {

@@ -15,11 +15,12 @@ DEV = "cuda:0"
 EPS = 1e-5
 # (B, C, P, groups): groups of one value, teams of 16, 64, 256 and 1024 threads, chunk and
 # row ends, groups past a workgroup's registers with short, middle and long rows, with
-# more channels than 256 chunks, many samples, tokens
+# more channels than 256 chunks, many samples, tokens, teams of 1024 for enough groups, many channels of long rows
 SHAPES = [(1, 1, 1, 1), (2, 4, 256, 2), (1, 1, 2, 1), (5, 64, 1, 8), (3, 6, 2, 3), (2, 48, 33, 3), (1, 61, 97, 1),
           (2, 12, 100, 4), (9, 257, 1, 1), (1, 96, 1000, 3), (2, 48, 3721, 3), (1, 3, 70001, 1), (2, 512, 300, 1),
           (1, 4096, 20, 2), (300, 40, 1, 5), (1, 8192, 1, 1), (2, 8192, 9, 4), (70, 24, 50, 24), (3, 2, 40000, 2),
-          (2, 1000, 3, 1), (17, 16, 16, 2), (1, 6, 32771, 2)]
+          (2, 1000, 3, 1), (17, 16, 16, 2), (1, 6, 32771, 2), (24, 32, 1500, 4), (12, 64, 4500, 8),
+          (12, 64, 2101, 8), (1, 1030, 2060, 1)]
 
 
 def case(dtype, B, C, P, last, seed, mean=0.5):

@@ -133,9 +133,13 @@ def random_packed(gen, rows, C):
 
 # rows of either operand and the sum's length: tiles of 128 and 256 whole and cut, sums that end in the
 # first and second half of a stage of 256, one to many stages, and the kernels beside
-@pytest.mark.parametrize("shape", [(65, 128, 512), (128, 256, 640), (129, 127, 768), (300, 200, 896), (257, 700, 1024),
-                                   (96, 1000, 1152), (400, 300, 4096), (3000, 3100, 512), (2900, 3300, 1920), (4096, 2304, 640),
-                                   (130, 140, 500), (300, 300, 600), (70, 66, 992), (64, 4096, 4096), (40, 3000, 1100)], ids=str)
+LARGE = [(65, 128, 512), (128, 256, 640), (129, 127, 768), (300, 200, 896), (257, 700, 1024),
+         (96, 1000, 1152), (400, 300, 4096), (3000, 3100, 512), (2900, 3300, 1920), (4096, 2304, 640),
+         (130, 140, 500), (300, 300, 600), (70, 66, 992), (64, 4096, 4096), (40, 3000, 1100), (3, 500, 1100),
+         (20, 300, 1024), (20, 300, 1100), (3600, 3500, 640), (3500, 3600, 1408), (2100, 2100, 100)]
+
+
+@pytest.mark.parametrize("shape", LARGE, ids=str)
 def test_large_products(shape):
     B, O, I = shape
     gen = torch.Generator(device=DEV).manual_seed(B)
