@@ -38,6 +38,7 @@ struct GnArgs {
   void *gw, *gb;         // NULL: not wanted
   float2 *stats;         // [B][G] (mean, 1 / sqrt(variance + eps))
   float2 *part;          // sums of rows or runs
+  float2 *gpart;         // channels last: [B][S][G] sums of the groups in the pieces
   float2 *gsum;          // [B][G] backward: means of w gz and of w gz x^
   int B, C, G, Cg;
   long P;
@@ -47,7 +48,7 @@ struct GnArgs {
   int S;                 // pieces of a row (channels first) or of a sample (channels last), or runs
   long per;              // 16-byte chunks of such a piece (channels first), rows of it (channels last)
   long sb, sc, ss;       // strides of part: sample, channel, piece
-  int whole;             // channels last, forward: channels of a group whose sums are joined to one, else 0 (join: 1)
+  int whole;             // channels last: the first pass leaves gpart (a workgroup has all channels)
   int main;              // channels first: workgroups of the rows, in front of those of the parameters' sums
 };
 

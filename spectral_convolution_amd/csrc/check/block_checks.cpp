@@ -130,7 +130,10 @@ void check_gnorm_cols(const GnArgs &a, bool bwd, bool out, bool runs, int dtype)
     c.need("lanes of a row", PL >= 1 && ((PL - 1) * V + V - 1) * kn + kn - 1 < 256 * V && (kb + kn - 1) * V < a.C);
   }
   if (!out) c.span("sums", a.part, (size_t)(runs ? 1 : a.B) * a.S * a.C * 8);
-  if (!out && !bwd && a.whole) c.need("a workgroup has all channels", a.whole == a.Cg && cpr <= 256 && !runs);
+  if (!out && a.whole) {
+    c.need("a workgroup has all channels", cpr <= 256 && !runs);
+    c.span("groups' sums", a.gpart, (size_t)a.B * a.S * a.G * 8);
+  }
   if (bwd && out) c.span("group sums", a.gsum, (size_t)a.B * a.G * 8);
   c.need("strides of the sums", a.sb == (runs ? 0 : (long)a.C * a.S) && a.sc == 1 && a.ss == a.C);
 }
@@ -141,7 +144,7 @@ void check_gnorm_join(const GnArgs &a, bool bwd, bool group, int samples, int dt
   c.need("something to join", group || samples);
   if (group) {
     c.span("sums", a.part, (size_t)a.B * a.C * a.S * 8);
-    c.need("channels of the sums", bwd || a.whole >= 1);
+    if (a.whole) c.span("groups' sums", a.gpart, (size_t)a.B * a.S * a.G * 8);
     c.span(bwd ? "group sums" : "stats", bwd ? a.gsum : a.stats, groups * 8);
     c.need("last sum of a sample", (a.C - 1) * a.sc + (a.S - 1) * a.ss < a.sb && a.sb == (long)a.C * a.S);
     const long piece = a.last ? a.per : a.per * (dtype == DT_F32 ? 4 : 8);

@@ -62,12 +62,13 @@ GnPlan gn_plan(const GnArgs &a, int dtype) {
   p.per_run = up(all, R);
   p.runs = (int)up(all, p.per_run);
   p.parts = std::max(p.bteam ? 0 : (size_t)bc * p.S, (size_t)a.C * p.runs);
+  p.gparts = !p.bteam && blocks == 1 ? (size_t)a.B * p.S * a.G : 0;
   return p;
 }
 
 size_t gnorm_workspace_bytes(const GnArgs &a, int dtype) {
   const GnPlan p = gn_plan(a, dtype);
-  return (p.parts + (p.bteam ? 0 : (size_t)a.B * a.G)) * sizeof(float2);
+  return (p.parts + p.gparts + (p.bteam ? 0 : (size_t)a.B * a.G)) * sizeof(float2);
 }
 
 hipError_t gnorm_f32(const GnArgs &a, bool fwd, void *workspace, hipStream_t s);

@@ -22,7 +22,7 @@ struct GnPlan {
   int T;           // lanes of a row (channels first)
   int S, runs;     // pieces of a row or sample; channels last, small groups: runs of the parameters' sums
   long per, per_run;
-  size_t parts;    // sums in the workspace
+  size_t parts, gparts;  // sums in the workspace: of channels' pieces or runs, of groups' pieces
 };
 
 GnPlan gn_plan(const GnArgs &a, int dtype);
@@ -90,7 +90,7 @@ template <int DT>
 __device__ __forceinline__ void store_chunk(void *p, size_t i, int n, const ck_u32x4 &r) {
   using E = typename std::conditional<DT == DT_F32, float, uint16_t>::type;
   if (n == ck_vec<DT>()) __builtin_nontemporal_store((ck_u32x4_any)r, reinterpret_cast<ck_u32x4_any *>(reinterpret_cast<E *>(p) + i));
-  else ck_store<DT>(p, i, n, r);
+  else ck_store_row<DT>(p, i, n, r);
 }
 
 template <int W>

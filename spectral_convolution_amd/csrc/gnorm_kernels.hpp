@@ -68,12 +68,14 @@ __global__ __launch_bounds__(T > kThreads ? T : kThreads) void fno_gnorm_small(G
         rx[i] = ck_shift(rx[i], gone);
         if constexpr (BWD) rg[i] = ck_shift(rg[i], gone);
       }
-    } else {
+    } else {  // rows shorter than a chunk: 16 bytes all the same, of which the first values count
+      const size_t last = (size_t)a.B * a.C * a.P;
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         const Place p = place(i);
-        rx[i] = ck_load<DT>(a.x, p.at, p.n);
-        if constexpr (BWD) rg[i] = ck_load<DT>(a.gy, p.at, p.n);
+        const int n = p.at + V <= last ? V : p.n;
+        rx[i] = ck_load<DT>(a.x, p.at, n);
+        if constexpr (BWD) rg[i] = ck_load<DT>(a.gy, p.at, n);
       }
     }
     float mean, r;
@@ -485,22 +487,22 @@ __global__ __launch_bounds__(kThreads) void fno_gnorm_cols(GnArgs a) {
       if constexpr ((BWD || OUT) && !RUNS) stats(b);
       long seen = -1;
       long row = r0 + pl;
-      if (n == V) {
-        for (; row + (AHEAD - 1) * PL < r1; row += AHEAD * PL) {
-          ck_u32x4 x[AHEAD], g[AHEAD];
+      // 16 bytes also where fewer of their values count, up to the rows at whose end the field ends
+      const long safe = n == V ? r1 : all * a.C < V + c0 ? 0 : min(r1, (all * a.C - V - c0) / a.C + 1);
+      for (; row + (AHEAD - 1) * PL < safe; row += AHEAD * PL) {
+        ck_u32x4 x[AHEAD], g[AHEAD];
 #pragma unroll
-          for (int i = 0; i < AHEAD; ++i) x[i] = load(a.x, (size_t)(row + i * PL) * a.C + c0);
+        for (int i = 0; i < AHEAD; ++i) x[i] = load(a.x, (size_t)(row + i * PL) * a.C + c0);
 #pragma unroll
-          for (int i = 0; i < AHEAD; ++i) g[i] = BWD ? load(a.gy, (size_t)(row + i * PL) * a.C + c0) : none;
+        for (int i = 0; i < AHEAD; ++i) g[i] = BWD ? load(a.gy, (size_t)(row + i * PL) * a.C + c0) : none;
 #pragma unroll
-          for (int i = 0; i < AHEAD; ++i) {
-            if constexpr (RUNS) {
-              b = (row + i * PL) / a.P;
-              if (b != seen) stats(b);
-              seen = b;
-            }
-            chunk(x[i], g[i], row + i * PL);
+        for (int i = 0; i < AHEAD; ++i) {
+          if constexpr (RUNS) {
+            b = (row + i * PL) / a.P;
+            if (b != seen) stats(b);
+            seen = b;
           }
+          chunk(x[i], g[i], row + i * PL);
         }
       }
       for (; row < r1; row += PL) {
@@ -542,20 +544,26 @@ __global__ __launch_bounds__(kThreads) void fno_gnorm_cols(GnArgs a) {
           if constexpr (BWD) v.x += o.x, v.y += o.y;
           else join_moments(nn, v.x, v.y, cnt[q * kn + l], o.x, o.y);
         }
-        if (!BWD && a.whole) red[e * kn + l] = v;  // nobody else reads this place
-        else a.part[u * a.C + kb * V + i] = v;
+        if (!RUNS && a.whole) red[e * kn + l] = v;  // nobody else reads this place
+        if (BWD || !a.whole) a.part[u * a.C + kb * V + i] = v;
       }
-      if constexpr (!BWD)
-        if (a.whole) {  // the channels' moments, of as many values each, joined to the groups'
+      if constexpr (!RUNS)
+        if (a.whole) {  // the channels' sums joined to the groups', a wave a group
           __syncthreads();
-          for (int g = threadIdx.x; g < a.G; g += kThreads) {
-            float nn = 0.f, m = 0.f, q = 0.f;
-            for (int i = 0; i < a.Cg; ++i) {
+          for (int g = threadIdx.x >> 6; g < a.G; g += kThreads / 64) {
+            float nn = 0.f, v0 = 0.f, v1 = 0.f;
+            for (int i = threadIdx.x & 63; i < a.Cg; i += 64) {
               const int c = g * a.Cg + i;
               const float2 o = red[c % V * kn + c / V];
-              join_moments(nn, m, q, (float)(r1 - r0), o.x, o.y);
+              if constexpr (BWD) {
+                const float wc = param(a.w, DT, c, 1.f);
+                v0 = fmaf(wc, o.x, v0), v1 = fmaf(wc, o.y, v1);
+              } else {
+                join_moments(nn, v0, v1, (float)(r1 - r0), o.x, o.y);
+              }
             }
-            a.part[u * a.G + g] = make_float2(m, q);
+            team_join<BWD, 64>(nn, v0, v1, nullptr);
+            if ((threadIdx.x & 63) == 0) a.gpart[u * a.G + g] = make_float2(v0, v1);
           }
         }
     }
@@ -607,7 +615,8 @@ __global__ __launch_bounds__(kJoin) void fno_gnorm_join(GnArgs a, int groups, in
   }
   const long piece = a.last ? a.per : a.per * ck_vec<DT>(), all = (long)a.B * a.G;
   const int step = WIDE ? kJoin : 64, me = WIDE ? threadIdx.x : lane;
-  const uint32_t n_part = (uint32_t)a.Cg * (uint32_t)a.S, inner = a.last ? (uint32_t)a.Cg : (uint32_t)a.S;
+  // a.whole: the pieces' sums are the groups' already
+  const uint32_t n_part = (uint32_t)(a.whole ? 1 : a.Cg) * (uint32_t)a.S, inner = a.last && !a.whole ? (uint32_t)a.Cg : (uint32_t)a.S;
   for (long id = WIDE ? blockIdx.x : blockIdx.x * 16L + wave; id < all; id += WIDE ? groups : groups * 16L) {
     const long b = id / a.G;
     const int c0 = (int)(id - b * a.G) * a.Cg;
@@ -616,14 +625,15 @@ __global__ __launch_bounds__(kJoin) void fno_gnorm_join(GnArgs a, int groups, in
     for (uint32_t i = me; i < n_part; i += step) {  // neighbours in memory one after the other
       const uint32_t outer = i / inner, in = i - outer * inner;
       const int c = c0 + (int)(a.last ? in : outer);
-      const long s = a.last ? outer : in;
-      const float2 p = a.part[b * a.sb + c * a.sc + s * a.ss];
+      const long s = a.last && !a.whole ? outer : in;
+      const float2 p = a.whole ? a.gpart[(b * a.S + s) * a.G + id - b * a.G] : a.part[b * a.sb + c * a.sc + s * a.ss];
       if constexpr (BWD) {
-        const float w = param(a.w, DT, c, 1.f);
+        const float w = a.whole ? 1.f : param(a.w, DT, c, 1.f);
         v0 = fmaf(w, p.x, v0);
         v1 = fmaf(w, p.y, v1);
       } else {
-        join_moments(n, v0, v1, (float)((min(a.P, (s + 1) * piece) - s * piece) * a.whole), p.x, p.y);
+        const long rows = min(a.P, (s + 1) * piece) - s * piece;
+        join_moments(n, v0, v1, (float)(a.whole ? rows * a.Cg : rows), p.x, p.y);
       }
     }
     if constexpr (BWD) {
@@ -658,7 +668,9 @@ __global__ __launch_bounds__(kJoin) void fno_gnorm_join(GnArgs a, int groups, in
 
 inline void gn_attach(GnArgs &a, const GnPlan &p, void *workspace, bool runs) {
   a.part = static_cast<float2 *>(workspace);
-  a.gsum = a.part + p.parts;
+  a.gpart = a.part + p.parts;
+  a.gsum = a.gpart + p.gparts;
+  a.whole = p.gparts != 0 && !runs;
   a.last = p.last;
   if (!p.last) {
     a.S = p.S, a.per = p.per;
@@ -715,7 +727,7 @@ hipError_t gn_cols(const GnArgs &a, hipStream_t s) {
 template <int DT, bool BWD>
 hipError_t gn_join(const GnArgs &a, bool group, int samples, hipStream_t s) {
   GnArgs arg = a;
-  const bool wide = (long)a.Cg * a.S > 1024;
+  const bool wide = (long)(a.whole ? 1 : a.Cg) * a.S > 256;
   const long all = (long)a.B * a.G;
   int groups = group ? (int)std::min(wide ? all : up(all, 16), kMaxGrid / 4) : 0;
   void *args[] = {(void *)&arg, (void *)&groups, (void *)&samples};
@@ -734,17 +746,11 @@ hipError_t gn_forward(GnArgs a, void *workspace, hipStream_t s) {
   a.last = p.last;
   if (p.team) return p.last ? gn_small<DT, true, false>(a, p.team, s) : gn_small<DT, false, false>(a, p.team, s);
   gn_attach(a, p, workspace, false);
-  // Channels last, few channels a group: the first pass joins them, and the pieces are of groups
-  const bool groups = p.last && a.Cg <= 16 && a.C <= kThreads * ck_vec<DT>();
-  a.whole = groups ? a.Cg : 0;
   hipError_t e = p.last ? gn_cols<DT, false, false, false>(a, s) : gn_rows<DT, false, false, false>(a, p.T, false, s);
   if (e != hipSuccess) return e;
   if (gn_fold(a, p)) return gn_rows<DT, false, true, true>(a, p.T, false, s);
   if (!a.stats) a.stats = a.gsum;  // kept for nobody
-  GnArgs j = a;
-  if (groups) j.C = a.G, j.Cg = 1, j.sb = (long)a.G * a.S, j.ss = a.G;
-  else j.whole = 1;
-  e = gn_join<DT, false>(j, true, 0, s);
+  e = gn_join<DT, false>(a, true, 0, s);
   if (e != hipSuccess) return e;
   return p.last ? gn_cols<DT, false, true, false>(a, s) : gn_rows<DT, false, true, false>(a, p.T, false, s);
 }
