@@ -99,6 +99,23 @@ __global__ __launch_bounds__(kDropThreads) void fno_drop(DropArgs a) {
     }
     return;
   }
+  // Rows that end inside a chunk: 16 bytes all the same, which end inside the field except in the last workgroups.
+  const long tail = rem0 + kDropSpan - 1, down = tail / cpr;  // the workgroup's last chunk
+  if (base + kDropSpan <= total && (row0 + down) * a.n + (tail - down * cpr + 1) * V <= a.rows * a.n) {
+    ck_u32x4 x[kDropRuns], v[kDropRuns];
+    size_t at[kDropRuns];
+#pragma unroll
+    for (int i = 0; i < kDropRuns; ++i) {
+      at[i] = (size_t)row[i] * a.n + k[i] * V;
+      v[i] = ck_load<DT>(a.v, at[i], V);
+    }
+#pragma unroll
+    for (int i = 0; i < kDropRuns; ++i) x[i] = a.x ? ck_load<DT>(a.x, at[i], V) : none;
+#pragma unroll
+    for (int i = 0; i < kDropRuns; ++i)
+      ck_store_row<DT>(a.y, at[i], a.n - k[i] * V, drop_apply<DT>(x[i], v[i], kept(i), scale));
+    return;
+  }
 #pragma unroll 1
   for (int i = 0; i < kDropRuns; ++i) {
     if (base + i * kDropThreads + threadIdx.x >= total) return;

@@ -35,7 +35,7 @@ GnPlan gn_plan(const GnArgs &a, int dtype) {
   const long V = gn_vec(dtype);
   p.last = a.last || a.P == 1;
   const long len = p.last ? a.Cg : a.P, rows = p.last ? a.P : a.Cg, chunks = up(len, V) * rows;
-  p.team = chunks <= 64 ? 16 : chunks <= 256 ? 64 : chunks <= 1024 ? 256 : chunks <= 4096 ? 1024 : chunks <= 8192 ? 2048 : 0;
+  p.team = chunks <= 16 ? 8 : chunks <= 64 ? 16 : chunks <= 256 ? 64 : chunks <= 1024 ? 256 : chunks <= 4096 ? 1024 : chunks <= 8192 ? 2048 : 0;
   // one compute unit a group: few large ones would leave the others idle
   if (p.team >= 1024 && (long)a.B * a.G < 96) p.team = 0;
   p.bteam = chunks <= 4096 ? p.team : 0;  // the backward holds two fields

@@ -10,7 +10,8 @@ namespace fno {
 
 // ------------------------------------------------------------ small groups
 
-// T threads hold a group, NC chunks of 16 bytes each.
+// T threads hold a group, NC chunks of 16 bytes each (8192 x 1024 bf16 in 16 groups of 8 chunks, a step: 112 us by
+// teams of 16 with four chunks, 66 by teams of 8 with two).
 template <int DT, bool LAST, bool BWD, int T, int NC>
 __global__ __launch_bounds__(T > kThreads ? T : kThreads) void fno_gnorm_small(GnArgs a) {
   constexpr int V = ck_vec<DT>(), TEAMS = T > kThreads ? 1 : kThreads / T;
@@ -534,12 +535,34 @@ __global__ __launch_bounds__(kThreads) void fno_gnorm_cols(GnArgs a) {
         }
       }
       __syncthreads();
+      int left = PL;  // lanes' sums of a channel: halved until one thread's turn through them is short
+      while (left > 16) {
+        const int h = (left + 1) / 2;
+        if (pl + h < left) {
+          const float nb = BWD ? 0.f : cnt[(pl + h) * kn + kl];
+          float na = BWD ? 0.f : cnt[threadIdx.x];
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            float2 &v = red[(pl * V + e) * kn + kl];
+            const float2 o = red[((pl + h) * V + e) * kn + kl];
+            if constexpr (BWD) {
+              v.x += o.x, v.y += o.y;
+            } else {
+              float n1 = na;
+              join_moments(n1, v.x, v.y, nb, o.x, o.y);
+            }
+          }
+          if constexpr (!BWD) cnt[threadIdx.x] = na + nb;
+        }
+        left = h;
+        __syncthreads();
+      }
       for (int i = threadIdx.x; i < kn * V; i += kThreads) {  // channel kb V + i
         const int e = i % V, l = i / V;
         if (kb * V + i >= a.C) continue;
         float2 v = red[e * kn + l];
         float nn = BWD ? 0.f : cnt[l];
-        for (int q = 1; q < PL; ++q) {
+        for (int q = 1; q < left; ++q) {
           const float2 o = red[(q * V + e) * kn + l];
           if constexpr (BWD) v.x += o.x, v.y += o.y;
           else join_moments(nn, v.x, v.y, cnt[q * kn + l], o.x, o.y);
@@ -689,14 +712,15 @@ template <int DT, bool LAST, bool BWD>
 hipError_t gn_small(const GnArgs &a, int team, hipStream_t s) {
   GnArgs arg = a;
   void *args[] = {(void *)&arg};
-  const void *k = team == 16 ? (const void *)fno_gnorm_small<DT, LAST, BWD, 16, 4>
+  const void *k = team == 8 ? (const void *)fno_gnorm_small<DT, LAST, BWD, 8, 2>
+                  : team == 16 ? (const void *)fno_gnorm_small<DT, LAST, BWD, 16, 4>
                   : team == 64 ? (const void *)fno_gnorm_small<DT, LAST, BWD, 64, 4>
                   : team == 256 ? (const void *)fno_gnorm_small<DT, LAST, BWD, 256, 4>
                                 : (const void *)fno_gnorm_small<DT, LAST, BWD, 1024, 4>;
   if constexpr (!BWD)
     if (team > 1024) k = (const void *)fno_gnorm_small<DT, LAST, BWD, 1024, 8>;
   const int threads = std::max(kThreads, std::min(team, 1024));
-  FNO_BOUNDS(check_gnorm_small(a, LAST, BWD, std::min(team, 1024), team > 1024 ? 8 : 4, DT);)
+  FNO_BOUNDS(check_gnorm_small(a, LAST, BWD, std::min(team, 1024), team > 1024 ? 8 : team == 8 ? 2 : 4, DT);)
   return gn_run(k, up((long)a.B * a.G, std::max(1, threads / team)), 1, threads, args, s);
 }
 

@@ -11,6 +11,7 @@
 
 #include "gelu.hpp"
 #include "mx4.hpp"
+#include "norm_common.hpp"
 
 namespace fno {
 
@@ -44,51 +45,27 @@ __device__ __forceinline__ float value_at(const void *p, size_t i) {
   else return bf16_to_f32(reinterpret_cast<const uint16_t *>(p)[i]);
 }
 
-// four neighbouring results z at y[at] .., n of them there
-template <int DT>
-__device__ __forceinline__ void mx4_finish(const Gemm &g, const v4f &acc, const float *bias, size_t at, int n) {
-  typedef unsigned u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
-  float o[4];
-#pragma unroll
-  for (int r = 0; r < 4; ++r) o[r] = acc[r] + bias[r];
-  if (n >= 4) {
-    if (g.add) {
-      if constexpr (DT == DT_F32) {
-        const ck_u32x4 v = *reinterpret_cast<const ck_u32x4_any *>(reinterpret_cast<const float *>(g.add) + at);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) o[r] += __uint_as_float(v[r]);
-      } else {
-        const u32x2_any v = *reinterpret_cast<const u32x2_any *>(reinterpret_cast<const uint16_t *>(g.add) + at);
-        const ck_u32x4 w{v[0], v[1], 0u, 0u};
-#pragma unroll
-        for (int r = 0; r < 4; ++r) o[r] += ck_get<DT>(w, r);
-      }
-    }
-    if (g.act)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) o[r] = gelu_train(o[r]);
-    if constexpr (DT == DT_F32) {
-      *reinterpret_cast<ck_u32x4_any *>(reinterpret_cast<float *>(g.y) + at) = ck_raw<DT>(o);
-    } else {
-      *reinterpret_cast<u32x2_any *>(reinterpret_cast<uint16_t *>(g.y) + at) =
-          u32x2_any{ck_pair<DT>(o[0], o[1]), ck_pair<DT>(o[2], o[3])};
-    }
-  } else {
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-      if (r < n) {
-        if (g.add) o[r] += value_at<DT>(g.add, at + r);
-        if (g.act) o[r] = gelu_train(o[r]);
-        if constexpr (DT == DT_F32) reinterpret_cast<float *>(g.y)[at + r] = o[r];
-        else if constexpr (DT == DT_F16) reinterpret_cast<_Float16 *>(g.y)[at + r] = (_Float16)o[r];
-        else reinterpret_cast<uint16_t *>(g.y)[at + r] = (uint16_t)f32_to_bf16(o[r]);
-      }
-  }
-}
-
 template <int DT>
 __device__ __forceinline__ float bias_at(const Gemm &g, long i, long n) {
   return g.bias ? value_at<DT>(g.bias, (size_t)min(i, n - 1)) : 0.f;
+}
+
+// neighbouring sums o of row s at y[at] .., n of them there: bias (bf: of their f), addition, activation
+template <int DT, int N>
+__device__ __forceinline__ void mx4_finish(const Gemm &g, float (&o)[N], const float *bf, long s, size_t at, int n) {
+  static_assert(N == ck_vec<DT>(), "16 bytes");
+  const float bs = g.bias_f ? 0.f : bias_at<DT>(g, s, g.ns);
+#pragma unroll
+  for (int e = 0; e < N; ++e) o[e] += bf[e] + bs;
+  if (g.add) {
+    const ck_u32x4 d = ck_load<DT>(g.add, at, n);
+#pragma unroll
+    for (int e = 0; e < N; ++e) o[e] += ck_get<DT>(d, e);
+  }
+  if (g.act)
+#pragma unroll
+    for (int e = 0; e < N; ++e) o[e] = gelu_train(o[e]);
+  ck_store_row<DT>(g.y, at, n, ck_raw<DT>(o));
 }
 
 }  // namespace
@@ -96,7 +73,8 @@ __device__ __forceinline__ float bias_at(const Gemm &g, long i, long n) {
 // Short sums: a wave has 16 F f x 16 S s, four waves side by side along f; operands straight from memory to
 // registers, the next step's loaded before this one's products.
 template <int DT, int F, int S>
-__global__ __launch_bounds__(kThreads) void fno_mx4_mix(Gemm g) {
+__global__ __launch_bounds__(kThreads, 3) void fno_mx4_mix(Gemm g) {
+  __shared__ __attribute__((aligned(16))) float stage[4][16 * (16 * F + 4)];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, quad = lane >> 4;
   const long ft = (g.nf + 64 * F - 1) / (64 * F), st = (g.ns + 16 * S - 1) / (16 * S), tiles = ft * st * g.batches, steps = (g.nb + 3) / 4;
   for (long t = blockIdx.x; t < tiles; t += gridDim.x) {
@@ -147,18 +125,33 @@ __global__ __launch_bounds__(kThreads) void fno_mx4_mix(Gemm g) {
 #pragma unroll
         for (int j = 0; j < S; ++j) acc[i][j] = mx4_product(fn[i], fxn[i], sn[j], sxn[j], acc[i][j]);
     }
+    // 16 columns at a time through LDS, so that lanes finish and store whole 16 bytes of neighbours
+    constexpr int N = ck_vec<DT>(), FW = 16 * F, PITCH = FW + 4, LANES = FW / N;
+    const long fl = f0 + lane % LANES * N;
+    const int there = (int)max(0L, min((long)N, g.nf - fl));
+    float bf[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) bf[e] = g.bias_f && there > 0 ? bias_at<DT>(g, fl + e, g.nf) : 0.f;
+    float *part = stage[wave];
 #pragma unroll
     for (int j = 0; j < S; ++j) {
-      const long s = s0 + 16 * j + l16;
 #pragma unroll
-      for (int i = 0; i < F; ++i) {
-        const long f = f0 + 16 * i + 4 * quad;
-        if (s >= g.ns || f >= g.nf) continue;
-        float bias[4];
+      for (int i = 0; i < F; ++i) *reinterpret_cast<v4f *>(part + l16 * PITCH + 16 * i + 4 * quad) = acc[i][j];
+      __builtin_amdgcn_wave_barrier();
 #pragma unroll
-        for (int r = 0; r < 4; ++r) bias[r] = g.bias_f ? bias_at<DT>(g, f + r, g.nf) : bias_at<DT>(g, s, g.ns);
-        mx4_finish<DT>(g, acc[i][j], bias, (size_t)(b * g.ybatch + s * g.ys + f), (int)min(4L, g.nf - f));
+      for (int c = lane / LANES; c < 16; c += 64 / LANES) {
+        const long s = s0 + 16 * j + c;
+        if (s >= g.ns || there == 0) continue;
+        float o[N];
+#pragma unroll
+        for (int e = 0; e < N; e += 4) {
+          const v4f v = *reinterpret_cast<const v4f *>(part + c * PITCH + lane % LANES * N + e);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) o[e + r] = v[r];
+        }
+        mx4_finish<DT>(g, o, bf, s, (size_t)(b * g.ybatch + s * g.ys + fl), there);
       }
+      __builtin_amdgcn_wave_barrier();
     }
   }
 }
@@ -234,11 +227,15 @@ __global__ __launch_bounds__(512) void fno_mx4_mix_few(Gemm g) {
 #pragma unroll
       for (int w = 1; w < W; ++w) v += red[w][wave][lane];
       const long s = 16 * wave + l16, f = f0 + 4 * quad;
-      if (s < g.ns && f < g.nf) {
-        float bias[4];
+      if (s < g.ns) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) bias[r] = g.bias_f ? bias_at<DT>(g, f + r, g.nf) : bias_at<DT>(g, s, g.ns);
-        mx4_finish<DT>(g, v, bias, (size_t)(b * g.ybatch + s * g.ys + f), (int)min(4L, g.nf - f));
+        for (int r = 0; r < 4; ++r)
+          if (f + r < g.nf) {
+            const size_t at = (size_t)(b * g.ybatch + s * g.ys + f + r);
+            float o = v[r] + (g.bias_f ? bias_at<DT>(g, f + r, g.nf) : bias_at<DT>(g, s, g.ns));
+            if (g.add) o += value_at<DT>(g.add, at);
+            put<DT>(g.y, at, g.act ? gelu_train(o) : o);
+          }
       }
     }
   }
@@ -482,24 +479,14 @@ void fno_mx4_mix_tiles(Gemm g) {
       for (int c = lane / LANES; c < 32; c += 64 / LANES) {
         const long s = s0 + ws * (32 * WS) + 32 * j + c;
         if (s >= g.ns || there == 0) continue;
-        const float bs = g.bias_f ? 0.f : bias_at<DT>(g, s, g.ns);
         float o[N];
 #pragma unroll
         for (int e = 0; e < N; e += 4) {
           const v4f v = *reinterpret_cast<const v4f *>(part + c * PITCH + lane % LANES * N + e);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) o[e + r] = v[r] + (bf[e + r] + bs);
+          for (int r = 0; r < 4; ++r) o[e + r] = v[r];
         }
-        const size_t y = (size_t)(b * g.ybatch + s * g.ys + fl);
-        if (g.add) {
-          const ck_u32x4 d = ck_load<DT>(g.add, y, there);
-#pragma unroll
-          for (int e = 0; e < N; ++e) o[e] += ck_get<DT>(d, e);
-        }
-        if (g.act)
-#pragma unroll
-          for (int e = 0; e < N; ++e) o[e] = gelu_train(o[e]);
-        ck_store<DT>(g.y, y, there, ck_raw<DT>(o));
+        mx4_finish<DT>(g, o, bf, s, (size_t)(b * g.ybatch + s * g.ys + fl), there);
       }
       __builtin_amdgcn_wave_barrier();
     }
@@ -550,13 +537,14 @@ hipError_t launch_mx4_mix(const Mx4MixArgs &a, int dtype, hipStream_t s) {
     const void *k = dtype == DT_F32 ? tiles_kernel<DT_F32>(w) : dtype == DT_F16 ? tiles_kernel<DT_F16>(w) : tiles_kernel<DT_BF16>(w);
     return hipLaunchKernel(k, dim3((unsigned)tiles(64 * w)), dim3(w == 4 ? 512 : 256), args, 0, s);
   }
-  // tiles of 256 x 64, or of 64 x 32 where those would leave compute units idle (5 x 200 x 72 x 1001 fp32: 17 us, 8)
+  // tiles of 128 x 64 (of 256 x 64, whose registers leave a compute unit half the waves, 32 x 64 x 64 x 65536 fp16 takes
+  // 245 us, so 203), or of 64 x 32 where those would leave compute units idle (5 x 200 x 72 x 1001 fp32: 17 us, 8)
   auto count = [&](long f, long r) { return (g.nf + f - 1) / f * ((g.ns + r - 1) / r) * g.batches; };
-  const bool wide = count(256, 64) >= 256;
-#define FNO_PICK(DT) (wide ? (const void *)fno_mx4_mix<DT, 4, 4> : (const void *)fno_mx4_mix<DT, 1, 2>)
+  const bool wide = count(128, 64) >= 256;
+#define FNO_PICK(DT) (wide ? (const void *)fno_mx4_mix<DT, 2, 4> : (const void *)fno_mx4_mix<DT, 1, 2>)
   const void *k = dtype == DT_F32 ? FNO_PICK(DT_F32) : dtype == DT_F16 ? FNO_PICK(DT_F16) : FNO_PICK(DT_BF16);
 #undef FNO_PICK
-  return hipLaunchKernel(k, dim3((unsigned)std::min(wide ? count(256, 64) : count(64, 32), kMaxGrid)), dim3(kThreads), args, 0, s);
+  return hipLaunchKernel(k, dim3((unsigned)std::min(wide ? count(128, 64) : count(64, 32), kMaxGrid)), dim3(kThreads), args, 0, s);
 }
 
 }  // namespace fno
