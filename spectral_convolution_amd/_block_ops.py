@@ -30,7 +30,7 @@ class Dropout:
     """What a call drops: units ("element", "channel" of a sample, "sample") with
     probability p (to 1/65536), by the random bits that belong to seed and offset
     (each below 2^64). A program moves the offset on with every call; a backward takes
-    the forward's. step: a device int64 tensor of one value that is added to the offset when the
+    the forward's. An object does not change: a backward finds what its forward had. step: a device int64 tensor of one value that is added to the offset when the
     call runs, for captured graphs (not to be moved on between a forward and its backward)."""
 
     __slots__ = ("p", "seed", "offset", "unit", "step", "_s")
@@ -47,8 +47,14 @@ class Dropout:
             torch = base._t()
             if not isinstance(step, torch.Tensor) or step.dtype != torch.int64 or step.numel() != 1:
                 raise ValueError("step must be an int64 tensor of one value")
-        self.p, self.seed, self.offset, self.unit, self.step = p, seed, offset, unit, step
-        self._s = DropoutStruct(p, DROP_UNITS[unit], seed, offset, None)
+        for name, v in zip(self.__slots__, (p, seed, offset, unit, step, DropoutStruct(p, DROP_UNITS[unit], seed, offset, None))):
+            object.__setattr__(self, name, v)
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"a Dropout does not change: make another for another {name}")
+
+    def __reduce__(self):
+        return Dropout, (self.p, self.seed, self.offset, self.unit, self.step)
 
     def _struct(self, ref):
         """fno_dropout_t for a call on ref's device."""

@@ -80,12 +80,7 @@ __device__ __forceinline__ void join_moments(float &n, float &mean, float &m2, f
   n = t;
 }
 
-// A whole chunk loaded for the last time, or stored: past the caches, which keep what is still to be read
-template <int DT>
-__device__ __forceinline__ ck_u32x4 load_last(const void *p, size_t i) {
-  using E = typename std::conditional<DT == DT_F32, float, uint16_t>::type;
-  return __builtin_nontemporal_load(reinterpret_cast<const ck_u32x4_any *>(reinterpret_cast<const E *>(p) + i));
-}
+// A whole chunk goes past the caches, which keep what is still to be read
 template <int DT>
 __device__ __forceinline__ void store_chunk(void *p, size_t i, int n, const ck_u32x4 &r) {
   using E = typename std::conditional<DT == DT_F32, float, uint16_t>::type;

@@ -499,7 +499,7 @@ __global__ __launch_bounds__(kThreads) void fno_gnorm_cols(GnArgs a) {
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
           if constexpr (RUNS) {
-            b = (row + i * PL) / a.P;
+            b = a.P == 1 ? row + i * PL : (row + i * PL) / a.P;
             if (b != seen) stats(b);
             seen = b;
           }
@@ -510,7 +510,7 @@ __global__ __launch_bounds__(kThreads) void fno_gnorm_cols(GnArgs a) {
         const ck_u32x4 x = ck_load<DT>(a.x, (size_t)row * a.C + c0, n);
         const ck_u32x4 g = BWD ? ck_load<DT>(a.gy, (size_t)row * a.C + c0, n) : none;
         if constexpr (RUNS) {
-          b = row / a.P;
+          b = a.P == 1 ? row : row / a.P;
           if (b != seen) stats(b);
           seen = b;
         }

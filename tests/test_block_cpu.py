@@ -147,6 +147,18 @@ def test_dropout_residual_refuses(L):
     assert f(over, None, m, o, 2, 4, 16, 0, 0, None) == INVALID
 
 
+def test_a_dropout_does_not_change():
+    """Its backward would draw another mask, or the change would be lost."""
+    import copy
+    d = fno.Dropout(0.25, 3, 7, unit="channel")
+    for name in ("p", "seed", "offset", "unit", "step"):
+        with pytest.raises(AttributeError):
+            setattr(d, name, 1)
+    e = copy.deepcopy(d)
+    assert (e.p, e.seed, e.offset, e.unit, e.step) == (0.25, 3, 7, "channel", None)
+    assert (e._s.p, e._s.unit, e._s.seed, e._s.offset) == (0.25, 1, 3, 7)
+
+
 def test_binding_refuses():
     import torch
     for bad in (-0.1, 1.5, NAN):
