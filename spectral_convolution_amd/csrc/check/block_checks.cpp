@@ -193,11 +193,9 @@ void check_mx4_mix(const Mx4MixArgs &a, int dtype) {
   c.need("codes 16-byte aligned", (((uintptr_t)a.xq | (uintptr_t)a.aq) & 15) == 0);
   if (a.nb % 4 == 0 && a.nb >= 16) {  // what fno_mx4_mix_tiles fetches of a row, in bytes, and its LDS reads
     const long stages = (a.nb + 7) / 8, pairs = (stages + 1) / 2;
-    for (long st : {0L, stages - 1})
-      for (long unit = 0; unit < 8; ++unit) {
-        const long u = 8 * st + unit - (8 * st + 8 > a.nb && (unit & 4) ? 4 : 0);
-        c.need("units of a stage inside the row", u >= 0 && u < a.nb);
-      }
+    const size_t past = 8 * stages > a.nb ? 64 : 0;  // half a stage's units behind the last row
+    c.span("codes of x as fetched", a.xq, rows * a.nb * 16 + past);
+    c.span("codes of A as fetched", a.aq, (size_t)a.O * a.nb * 16 + past);
     for (long pair : {0L, pairs - 1})
       for (long d = 0; d < 4; ++d) c.need("scales inside the row", std::min(16 * pair + 4 * d, a.nb - 4) + 4 <= a.nb);
     c.need("offsets of a tile in 32 bits", 256L * a.nb * 16 + 128 < 1L << 31);

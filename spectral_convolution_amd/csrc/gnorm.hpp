@@ -74,7 +74,7 @@ __device__ __forceinline__ void with_act(const GnArgs &a, F f) {
 __device__ __forceinline__ void join_moments(float &n, float &mean, float &m2, float nb, float meanb, float m2b) {
   const float t = n + nb;
   if (nb == 0.f) return;
-  const float f = nb / t, d = meanb - mean;
+  const float f = nb * __builtin_amdgcn_rcpf(t), d = meanb - mean;  // off by a step or two of the mean's change
   mean = n == 0.f ? meanb : fmaf(d, f, mean);
   m2 = n == 0.f ? m2b : m2 + m2b + d * d * n * f;
   n = t;

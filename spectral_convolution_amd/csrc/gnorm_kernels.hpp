@@ -571,23 +571,30 @@ __global__ __launch_bounds__(kThreads) void fno_gnorm_cols(GnArgs a) {
         if (BWD || !a.whole) a.part[u * a.C + kb * V + i] = v;
       }
       if constexpr (!RUNS)
-        if (a.whole) {  // the channels' sums joined to the groups', a wave a group
+        if (a.whole) {  // the channels' sums joined to the groups', a small group's by fewer lanes (16 x 128^2 x 128 bf16
+                        // in 32 groups: 25 us by a wave each, 16 by 8 lanes)
           __syncthreads();
-          for (int g = threadIdx.x >> 6; g < a.G; g += kThreads / 64) {
-            float nn = 0.f, v0 = 0.f, v1 = 0.f;
-            for (int i = threadIdx.x & 63; i < a.Cg; i += 64) {
-              const int c = g * a.Cg + i;
-              const float2 o = red[c % V * kn + c / V];
-              if constexpr (BWD) {
-                const float wc = param(a.w, DT, c, 1.f);
-                v0 = fmaf(wc, o.x, v0), v1 = fmaf(wc, o.y, v1);
-              } else {
-                join_moments(nn, v0, v1, (float)(r1 - r0), o.x, o.y);
+          auto join = [&](auto width) __attribute__((always_inline)) {
+            constexpr int W = decltype(width)::value;
+            const int me = threadIdx.x % W;
+            for (int g = threadIdx.x / W; g < a.G; g += kThreads / W) {
+              float nn = 0.f, v0 = 0.f, v1 = 0.f;
+              for (int i = me; i < a.Cg; i += W) {
+                const int c = g * a.Cg + i;
+                const float2 o = red[c % V * kn + c / V];
+                if constexpr (BWD) {
+                  const float wc = param(a.w, DT, c, 1.f);
+                  v0 = fmaf(wc, o.x, v0), v1 = fmaf(wc, o.y, v1);
+                } else {
+                  join_moments(nn, v0, v1, (float)(r1 - r0), o.x, o.y);
+                }
               }
+              team_join<BWD, W>(nn, v0, v1, nullptr);
+              if (me == 0) a.gpart[u * a.G + g] = make_float2(v0, v1);
             }
-            team_join<BWD, 64>(nn, v0, v1, nullptr);
-            if ((threadIdx.x & 63) == 0) a.gpart[u * a.G + g] = make_float2(v0, v1);
-          }
+          };
+          if (a.Cg <= 16) join(std::integral_constant<int, 8>{});
+          else join(std::integral_constant<int, 64>{});
         }
     }
   }
