@@ -567,8 +567,9 @@ fno_status_t fno_norm_residual_backward_saved(
  * forward and backward. Fields are [batch][channels][pixels], or with
  * channels_last 1 [batch][pixels][channels]; one pixel: tokens, either way.
  * Fields are 16-byte aligned, parameters to their element; outputs share memory with
- * nothing. Sums and statistics are fp32, results repeat bit for bit, calls
- * can be captured into a graph.
+ * nothing. Sums and statistics are fp32 (squares too: deviations past 1e19 overflow), results
+ * repeat bit for bit, calls can be captured into a graph. Calls that run at the same
+ * time, and graphs that are replayed at the same time, need workspaces of their own.
  *
  * Dropout. What is dropped is a unit: a value, a channel of a sample or a sample,
  * numbered in memory order (value i, b * channels + c, b). Unit u is dropped where its
