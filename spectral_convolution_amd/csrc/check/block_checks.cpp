@@ -87,7 +87,8 @@ void check_gnorm_small(const GnArgs &a, bool last, bool bwd, int T, int NC, int 
     const long b = id / a.G, c0 = (id - b * a.G) * a.Cg, pitch = last ? a.C : a.P;
     const long first = last ? b * a.P * a.C + c0 : (b * a.C + c0) * a.P;
     for (long q = 0; q < (long)T * NC; ++q) {
-      const long qc = std::min(q, chunks - 1), row = qc / cpr, k = (qc - row * cpr) * V;
+      const long qc = std::min(q, chunks - 1), row = (long)((uint64_t)(2 * qc) * ((0x80000000u + cpr - 1) / cpr) >> 32), k = (qc - row * cpr) * V;
+      in = in && row == qc / cpr;
       const long nv = q < chunks ? std::min(len - k, V) : 0, at = first + row * pitch + k;
       in = in && at >= 0 && at + (len % V == 0 ? V : nv) <= n;
       params = params && (last ? c0 + k + std::min(len - k, V) <= a.C : c0 + row < a.C);

@@ -60,7 +60,7 @@ GnPlan gn_plan(const GnArgs &a, int dtype) {
   p.per = up(a.P, S);
   p.S = (int)up(a.P, p.per);
   const long all = a.B * a.P;
-  const long R = std::min({up(kLastUnits, blocks), up(all, 4 * lanes), std::max(1L, kParts / a.C)});
+  const long R = std::min({up(kLastUnits / 2, blocks), up(all, 4 * lanes), std::max(1L, kParts / a.C)});
   p.per_run = up(all, R);
   p.runs = (int)up(all, p.per_run);
   p.parts = std::max(p.bteam ? 0 : (size_t)bc * p.S, (size_t)a.C * p.runs);

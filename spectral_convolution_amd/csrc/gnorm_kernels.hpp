@@ -11,7 +11,7 @@ namespace fno {
 // ------------------------------------------------------------ small groups
 
 // T threads hold a group, NC chunks of 16 bytes each (8192 x 1024 bf16 in 16 groups of 8 chunks, a step: 112 us by
-// teams of 16 with four chunks, 66 by teams of 8 with two).
+// teams of 16 with four chunks, 66 by teams of 8 with two). Bound by vector issue on tokens, by latency on few groups.
 template <int DT, bool LAST, bool BWD, int T, int NC>
 __global__ __launch_bounds__(T > kThreads ? T : kThreads) void fno_gnorm_small(GnArgs a) {
   constexpr int V = ck_vec<DT>(), TEAMS = T > kThreads ? 1 : kThreads / T;
@@ -19,6 +19,7 @@ __global__ __launch_bounds__(T > kThreads ? T : kThreads) void fno_gnorm_small(G
   const int t = threadIdx.x % T;
   const uint32_t len = LAST ? (uint32_t)a.Cg : (uint32_t)a.P, rows = LAST ? (uint32_t)a.P : (uint32_t)a.Cg;
   const uint32_t cpr = (len + V - 1) / V, chunks = rows * cpr;  // at most T NC
+  const uint32_t by_cpr = (0x80000000u + cpr - 1) / cpr;  // q / cpr is the high half of 2 q by_cpr: q cpr < 2^31
   const bool whole = len % V == 0;
   const float n = (float)len * (float)rows;
   const DropKey key = drop_key(a.drop);
@@ -42,7 +43,7 @@ __global__ __launch_bounds__(T > kThreads ? T : kThreads) void fno_gnorm_small(G
     auto place = [&](int i) __attribute__((always_inline)) {
       const uint32_t q = mine + i * T, qc = min(q, chunks - 1);
       Place p;
-      p.row = qc / cpr;
+      p.row = __umulhi(2 * qc, by_cpr);
       p.k = (qc - p.row * cpr) * V;
       p.n = q < chunks ? (int)min(len - p.k, (uint32_t)V) : 0;
       p.at = first + p.row * pitch + p.k;
@@ -144,9 +145,11 @@ __global__ __launch_bounds__(T > kThreads ? T : kThreads) void fno_gnorm_small(G
         }
       });
     } else {
-      // Twice over the values in registers, whose 16-bit forms take half the room of w gz and x^: the second time
-      // with the sums of the first.
-      float s1 = 0.f, s2 = 0.f;
+      // Twice over the values in registers: the second time with the sums of the first. w gz waits in registers of its own
+      // where a team's workgroup leaves room for it; else it is computed again from the values, whose 16-bit forms take
+      // half the room.
+      constexpr bool KEEP = T <= 256;
+      float s1 = 0.f, s2 = 0.f, kept[KEEP ? NC : 1][V];
       auto each = [&](auto out) __attribute__((always_inline)) {
         constexpr bool OUT = decltype(out)::value;
         again();
@@ -166,6 +169,7 @@ __global__ __launch_bounds__(T > kThreads ? T : kThreads) void fno_gnorm_small(G
               if constexpr (OUT) {
                 o[e] = r * (g - s1 - h * s2);
               } else {
+                if constexpr (KEEP) kept[i][e] = g;
                 s1 += g;
                 s2 = e < p.n ? fmaf(g, h, s2) : s2;
               }
@@ -180,8 +184,22 @@ __global__ __launch_bounds__(T > kThreads ? T : kThreads) void fno_gnorm_small(G
       s1 = team_sum<T>(s1, red[0]) / n;
       s2 = team_sum<T>(s2, red[1]) / n;
       fresh<DT>(rx);
-      fresh<DT>(rg);
-      each(std::true_type{});
+      if constexpr (KEEP) {
+        again();
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          if (i * T >= (int)chunks) break;
+          const Place p = place(i);
+          float o[V];
+#pragma unroll
+          for (int e = 0; e < V; ++e) o[e] = r * (kept[i][e] - s1 - (ck_get<DT>(rx[i], e) - mean) * r * s2);
+          if (there && p.n) store_chunk<DT>(a.gx, p.at, p.n, ck_raw<DT>(o));
+          channel_done();
+        }
+      } else {
+        fresh<DT>(rg);
+        each(std::true_type{});
+      }
     }
   }
 }
