@@ -60,6 +60,8 @@ GnPlan gn_plan(const GnArgs &a, int dtype) {
   p.per = up(a.P, S);
   p.S = (int)up(a.P, p.per);
   const long all = a.B * a.P;
+  // half as many runs: twice the sums cost more than the second half of the workgroups gains (8192 x 1024 bf16 in 8
+  // groups, a step: 50 us with all, 45 with half)
   const long R = std::min({up(kLastUnits / 2, blocks), up(all, 4 * lanes), std::max(1L, kParts / a.C)});
   p.per_run = up(all, R);
   p.runs = (int)up(all, p.per_run);

@@ -11,7 +11,8 @@ namespace fno {
 // ------------------------------------------------------------ small groups
 
 // T threads hold a group, NC chunks of 16 bytes each (8192 x 1024 bf16 in 16 groups of 8 chunks, a step: 112 us by
-// teams of 16 with four chunks, 66 by teams of 8 with two). Bound by vector issue on tokens, by latency on few groups.
+// teams of 16 with four chunks, 54 by teams of 8 with two and half the runs of the parameters). Bound by vector issue
+// on tokens, by latency on few groups.
 template <int DT, bool LAST, bool BWD, int T, int NC>
 __global__ __launch_bounds__(T > kThreads ? T : kThreads) void fno_gnorm_small(GnArgs a) {
   constexpr int V = ck_vec<DT>(), TEAMS = T > kThreads ? 1 : kThreads / T;
@@ -31,9 +32,10 @@ __global__ __launch_bounds__(T > kThreads ? T : kThreads) void fno_gnorm_small(G
     const uint32_t b = gid / (uint32_t)a.G, g = gid - b * (uint32_t)a.G, c0 = g * a.Cg;
     // value 0 of the group, and the distance of its rows
     const size_t first = LAST ? (size_t)b * a.P * a.C + c0 : ((size_t)b * a.C + c0) * a.P;
-    const size_t pitch = LAST ? a.C : a.P;
+    const uint32_t pitch = LAST ? (uint32_t)a.C : (uint32_t)a.P;  // a group's values span fewer than 2^28
     ck_u32x4 rx[NC], rg[BWD ? NC : 1];
-    // Where chunk i of a thread lies; each phase works it out again, since the registers go to the values.
+    // Where chunk i of a thread lies; each phase works it out again, since the registers go to the values (kept through the
+    // phases: 8192 x 4096 fp16 in 32 groups, a step, 164 us).
     struct Place {
       uint32_t row, k;
       int n;  // values of the chunk, 0 where there is none
@@ -82,30 +84,36 @@ __global__ __launch_bounds__(T > kThreads ? T : kThreads) void fno_gnorm_small(G
     }
     float mean, r;
     if constexpr (!BWD) {
-      float s = 0.f;
-      again();
+      // sum of f over a thread's values, chosen by chunk where chunks are whole
+      auto sum = [&](auto f) __attribute__((always_inline)) {
+        float s = 0.f;
+        again();
+        if (whole) {
 #pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        const int nv = place(i).n;
+          for (int i = 0; i < NC; ++i) {
+            float c = 0.f;
 #pragma unroll
-        for (int e = 0; e < V; ++e) s += e < nv ? ck_get<DT>(rx[i], e) : 0.f;
-        channel_done();
-      }
-      mean = team_sum<T>(s, red[0]) / n;
-      fresh<DT>(rx);
-      again();
-      s = 0.f;
+            for (int e = 0; e < V; ++e) c = f(ck_get<DT>(rx[i], e), c);
+            s += mine + i * T < chunks ? c : 0.f;
+            channel_done();
+          }
+        } else {
 #pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        const int nv = place(i).n;
+          for (int i = 0; i < NC; ++i) {
+            const int nv = place(i).n;
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float d = ck_get<DT>(rx[i], e) - mean;
-          s = e < nv ? fmaf(d, d, s) : s;
+            for (int e = 0; e < V; ++e) s = e < nv ? f(ck_get<DT>(rx[i], e), s) : s;
+            channel_done();
+          }
         }
-        channel_done();
-      }
-      r = rsq(team_sum<T>(s, red[1]) / n + a.eps);
+        return s;
+      };
+      mean = team_sum<T>(sum([](float v, float s) __attribute__((always_inline)) { return s + v; }), red[0]) / n;
+      fresh<DT>(rx);
+      r = rsq(team_sum<T>(sum([&](float v, float s) __attribute__((always_inline)) {
+                const float d = v - mean;
+                return fmaf(d, d, s);
+              }), red[1]) / n + a.eps);
       fresh<DT>(rx);
       if (a.stats && there && t == 0) a.stats[gid] = make_float2(mean, r);
     } else {
