@@ -370,11 +370,11 @@ __global__ __launch_bounds__(kThreads) void fno_gnorm_rows(GnArgs a) {
         }
       }
       team_join<BWD, T>(n, v0, v1, red);
+      const float size = (float)a.Cg * (float)a.P;  // n has been rounded at every join
       if constexpr (BWD) {
-        const float size = (float)a.Cg * (float)a.P;
         st.use(a.stats[st.group()], make_float2(v0 / size, v1 / size));
       } else {
-        const float2 m = make_float2(v0, rsq(v1 / n + a.eps));
+        const float2 m = make_float2(v0, rsq(v1 / size + a.eps));
         if (a.stats && t == 0 && s == 0 && st.c == c0 && rid < rows) a.stats[st.group()] = m;
         st.use(m, make_float2(0.f, 0.f));
       }
@@ -715,7 +715,7 @@ __global__ __launch_bounds__(kJoin) void fno_gnorm_join(GnArgs a, int groups, in
     if (me == 0) {
       const float size = (float)a.Cg * (float)a.P;
       if constexpr (BWD) a.gsum[id] = make_float2(v0 / size, v1 / size);
-      else a.stats[id] = make_float2(v0, rsq(v1 / n + a.eps));
+      else a.stats[id] = make_float2(v0, rsq(v1 / size + a.eps));  // n has been rounded at every join
     }
   }
 }
