@@ -82,18 +82,23 @@ void check_gnorm_small(const GnArgs &a, bool last, bool bwd, int T, int NC, int 
   c.need("a team holds a group", chunks <= (long)T * NC && T <= 1024);
   c.need("groups in 31 bits", groups < 1L << 31);
   c.need("one pixel: channels last", last || a.P > 1);
-  bool in = true, params = true;
+  bool in = true, loads = true, params = true;
   for (long id : {0L, groups / 2, groups - 1}) {
     const long b = id / a.G, c0 = (id - b * a.G) * a.Cg, pitch = last ? a.C : a.P;
     const long first = last ? b * a.P * a.C + c0 : (b * a.C + c0) * a.P;
-    for (long q = 0; q < (long)T * NC; ++q) {
+    for (long q = 0; q < (long)T * NC; ++q) {  // a lane's slots, those behind the group's last chunk too: they load it again
       const long qc = std::min(q, chunks - 1), row = (long)((uint64_t)(2 * qc) * ((0x80000000u + cpr - 1) / cpr) >> 32), k = (qc - row * cpr) * V;
       in = in && row == qc / cpr;
       const long nv = q < chunks ? std::min(len - k, V) : 0, at = first + row * pitch + k;
-      in = in && at >= 0 && at + (len % V == 0 ? V : nv) <= n;
+      in = in && at >= 0 && at + nv <= n;
+      // the values that its load takes, by the kernel's three branches
+      const long back = len % V != 0 && len >= V ? V - std::min(len - k, V) : 0, from = at - back;
+      const long wide = len >= V || at + V <= n ? V : nv;
+      loads = loads && from >= 0 && from + wide <= n;
       params = params && (last ? c0 + k + std::min(len - k, V) <= a.C : c0 + row < a.C);
     }
   }
+  c.need("loads inside the field", loads);
   c.need("chunks inside the field", in);
   c.need("parameters of existing channels", params);
 }

@@ -59,16 +59,18 @@ __global__ __launch_bounds__(T > kThreads ? T : kThreads) void fno_gnorm_small(G
 #pragma unroll
         for (int i = 0; i < NC; ++i) rg[i] = ck_load<DT>(a.gy, place(i).at, V);
     } else if (len >= V) {  // a row's last chunk as the 16 bytes that end with the row: no load waits for another
+      // by the chunk's own length, also where it is loaded for a slot that has none: the field may end with it
+      auto back = [&](const Place &p) __attribute__((always_inline)) { return V - min(len - p.k, (uint32_t)V); };
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         const Place p = place(i);
-        rx[i] = ck_load<DT>(a.x, p.at - (V - p.n) % V, V);
-        if constexpr (BWD) rg[i] = ck_load<DT>(a.gy, p.at - (V - p.n) % V, V);
+        rx[i] = ck_load<DT>(a.x, p.at - back(p), V);
+        if constexpr (BWD) rg[i] = ck_load<DT>(a.gy, p.at - back(p), V);
       }
       again();
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
-        const int gone = (V - place(i).n) % V * (16 / V);
+        const int gone = (int)back(place(i)) * (16 / V);
         rx[i] = ck_shift(rx[i], gone);
         if constexpr (BWD) rg[i] = ck_shift(rg[i], gone);
       }

@@ -1,0 +1,36 @@
+"""The loads and stores of the block operators' kernels stay inside their buffers: the library's host code
+runs on the CPU against the recording runtime, where every launcher states what its kernel reads and writes as
+the kernel indexes it (csrc/check)."""
+
+import os
+import shutil
+
+import pytest
+
+from spectral_convolution_amd import bounds_check
+from test_training_variants_cpu import _program
+
+pytestmark = pytest.mark.skipif(shutil.which("hipcc") is None and not os.path.exists("/opt/rocm/bin/hipcc"),
+                                reason="needs hipcc (host-only compile)")
+
+
+def _trace(*calls):
+    r = bounds_check.run(_program(), args=["trace"], calls="\n".join(calls) + "\n")
+    assert "bounds:" not in r.stderr, r.stderr[-2000:]
+    assert r.returncode == 0, r.stdout[-500:] + r.stderr[-2000:]
+    return r.stdout
+
+
+# (B, C, P, groups): rows that end inside 16 bytes, fewer chunks a group than its team has room for, in teams of 8, 16,
+# 64, 256 and 1024 lanes, so that the field ends with a chunk that lanes without one load too
+RAGGED = [(32, 64, 9, 16), (97, 61, 97, 1), (2, 48, 33, 3), (3, 33, 1, 3), (9, 257, 1, 1), (61, 2048, 1, 2048 // 32),
+          (1, 4096, 61, 64), (97, 130, 57, 1), (100, 700, 41, 1)]
+
+
+@pytest.mark.parametrize("shape", RAGGED, ids=str)
+def test_small_groups_are_read_inside_the_field(shape):
+    B, C, P, G = shape
+    for d in range(3):
+        for last in (0, 1):
+            out = _trace(f"gnorm {d} {B} {C} {P} {G} {last}")
+            assert "fno_gnorm_small" in out
