@@ -61,6 +61,17 @@ void check_drop(const DropArgs &a, int mode, int dtype) {
       c.need("whole chunks inside the field", (base + span) * V <= a.rows * a.n);
       if (mode != 0) c.need("whole chunks where a flat field has them", base * V == row0 * a.n + rem0 * V);
     }
+    const long tail = rem0 + span - 1, down = tail / cpr, end = a.rows * a.n;
+    // rows that end inside a chunk: 16 bytes all the same where the workgroup's last chunk has them
+    const bool wide = !whole && base + span <= total && (row0 + down) * a.n + (tail - down * cpr + 1) * V <= end;
+    bool loads = true;
+    for (long local = 0; local < span && base + local < total; ++local) {
+      const long v = rem0 + local, d = mode == 0 ? 0 : cpr > span ? (v >= cpr ? 1 : 0) : (uint32_t)v / (uint32_t)cpr;
+      const long k = v - d * cpr, at = whole ? (base + local) * V : (row0 + d) * a.n + k * V;
+      loads = loads && at >= 0 && at + (whole || wide ? V : std::min(a.n - k * V, V)) <= end;
+      loads = loads && k >= 0 && (whole || a.n - k * V > 0);  // a store of a row's own values
+    }
+    c.need("loads inside the field", loads);
     for (long local : {0L, 1L, 255L, 256L, 1022L, 1023L}) {
       if (base + local >= total) continue;
       const long v = rem0 + local, d = mode == 0 ? 0 : cpr > span ? (v >= cpr ? 1 : 0) : (uint32_t)v / (uint32_t)cpr;
@@ -110,6 +121,7 @@ void check_gnorm_rows(const GnArgs &a, bool bwd, bool out, bool fold, bool param
   c.need("pieces cover the row", a.S >= 1 && a.per >= 1 && a.S * a.per >= cpr && (a.S - 1) * a.per < cpr);
   c.need("a row of lanes or a workgroup", T == 8 || T == 64 || T == 256);
   c.need("offsets of a row in 32 bits", cpr * V + 4L * T * V < 1L << 32);
+  c.need("whole chunks inside the row", a.P / V * V <= a.P && a.P - (cpr - 1) * V >= 1);
   if (!out || fold) c.span("sums", a.part, (size_t)rows * a.S * 8);
   if (bwd && out && !fold) c.span("group sums", a.gsum, (size_t)a.B * a.G * 8);
   c.need("strides of the sums", a.sb == (long)a.C * a.S && a.sc == a.S && a.ss == 1);
@@ -134,6 +146,20 @@ void check_gnorm_cols(const GnArgs &a, bool bwd, bool out, bool runs, int dtype)
   for (long kb = 0; kb < cpr; kb += 256) {
     const long kn = std::min(256L, cpr - kb), PL = 256 / kn;
     c.need("lanes of a row", PL >= 1 && ((PL - 1) * V + V - 1) * kn + kn - 1 < 256 * V && (kb + kn - 1) * V < a.C);
+    // the loads of a lane: 16 bytes of its channels in the rows below `safe`, its own values in the others
+    bool loads = true;
+    const long all = (long)a.B * a.P, units = runs ? a.S : (long)a.B * a.S;
+    for (long u : {0L, units / 2, units - 1}) {
+      const long b = runs ? 0 : u / a.S, p0 = runs ? u * a.per : (u - b * a.S) * a.per;
+      const long r0 = runs ? p0 : b * a.P + p0, r1 = runs ? std::min(all, p0 + a.per) : b * a.P + std::min(a.P, p0 + a.per);
+      loads = loads && r0 >= 0 && r0 < r1 && r1 <= all;
+      for (long kl = 0; kl < kn; ++kl) {
+        const long c0 = (kb + kl) * V, nv = std::min(V, a.C - c0);
+        const long safe = nv == V ? r1 : all * a.C < V + c0 ? 0 : std::min(r1, (all * a.C - V - c0) / a.C + 1);
+        loads = loads && nv >= 1 && safe <= r1 && (safe <= r0 || (safe - 1) * a.C + c0 + V <= all * a.C);
+      }
+    }
+    c.need("loads inside the field", loads);
   }
   if (!out) c.span("sums", a.part, (size_t)(runs ? 1 : a.B) * a.S * a.C * 8);
   if (!out && a.whole) {
@@ -197,6 +223,23 @@ void check_mx4_mix(const Mx4MixArgs &a, int dtype) {
   c.span("y", a.y, n);
   c.need("blocks cover the row", a.nb == (a.I + 31) / 32);
   c.need("codes 16-byte aligned", (((uintptr_t)a.xq | (uintptr_t)a.aq) & 15) == 0);
+  if (a.nb >= 32) {  // what a lane of fno_mx4_mix_few reads of its two rows: whole and clamped steps of four blocks
+    const bool steps4 = a.nb % 4 == 0;
+    const long steps = (a.nb + 3) / 4, per = (steps + 7) / 8;
+    bool codes = true, scales = true;
+    for (long wave = 0; wave < 8; ++wave) {
+      const long k0 = wave * per, k1 = std::min(steps, k0 + per);
+      for (long k = k0; k < k1; k += 4)
+        for (long u = 0; u < 4; ++u)
+          for (long quad = 0; quad < 4; ++quad) {
+            const long step = std::min(k + u, k1 - 1), kb = 4 * step + quad, kc = steps4 ? kb : std::min(kb, a.nb - 1);
+            codes = codes && step >= k0 && kc < a.nb;
+            scales = scales && (steps4 ? (k + 4 <= steps ? 4 * k + 16 : 4 * step + 4) <= a.nb : kc < a.nb);
+          }
+    }
+    c.need("few rows: codes inside the row", codes);
+    c.need("few rows: scales inside the row", scales);
+  }
   if (a.nb % 4 == 0 && a.nb >= 16) {  // what fno_mx4_mix_tiles fetches of a row, in bytes, and its LDS reads
     const long stages = (a.nb + 7) / 8, pairs = (stages + 1) / 2;
     const size_t past = 8 * stages > a.nb ? 64 : 0;  // half a stage's units behind the last row

@@ -354,7 +354,7 @@ int main(int argc, char **argv) {
       for (int k = 0; k < 4; ++k) trace_call("mix", dt, {c.B, c.I, c.O, c.P, k & 1, k >> 1});
   struct D { int B, C; long P; };
   const D dd[] = {{1, 1, 1}, {2, 4, 256}, {3, 7, 33}, {5, 1001, 1}, {32, 64, 65536}, {4, 3, 3721}, {7, 130, 9}, {1, 1, 1L << 31},
-                  {1 << 30, 1, 1024}, {2, 8192, 1L << 26}, {65536, 4096, 4096}, {2000000000, 3, 5}};
+                  {1 << 30, 1, 1024}, {15, 189, 2622}, {2000, 3, 3}, {1, 37, 5000}, {2, 8192, 1L << 26}, {65536, 4096, 4096}, {2000000000, 3, 5}};
   for (const D &c : dd)
     for (fno_dtype_t dt : dts) run_drop(c.B, c.C, c.P, dt);
   struct G { int B, C; long P; int G; };
@@ -362,14 +362,15 @@ int main(int argc, char **argv) {
                   {3, 33, 1, 3}, {9, 257, 1, 1}, {1, 96, 1000, 3}, {2, 48, 3721, 3}, {1, 3, 70000, 1}, {2, 512, 300, 1}, {1, 4096, 20, 2}, {300, 40, 1, 5},
                   {1, 8192, 1, 1}, {2, 8192, 9, 4}, {20, 64, 65536, 8}, {16, 128, 16384, 32}, {8192, 1024, 1, 16},
                   {1, 8192, fno::kGnMaxPixels, 1}, {3, 5, fno::kGnMaxPixels - 3, 5}, {1 << 30, 4, 3, 1}, {1 << 28, 8, 511, 4},
-                  {2, 8191, 65537, 1}, {1000000, 100, 70, 100}, {134217728, 8192, 1, 8}};
+                  {2, 8191, 65537, 1}, {1000000, 100, 70, 100}, {5, 61, 20000, 1}, {5, 4, 56935, 2}, {1, 3, 90001, 1}, {1, 2057, 9001, 1}, {134217728, 8192, 1, 8}};
   for (const G &c : gg)
     for (fno_dtype_t dt : dts)
       for (int last = 0; last < 2; ++last) run_gnorm(c.B, c.C, c.P, c.G, last, dt);
   struct X { int B, I, O; long P; };
   const X xx[] = {{1, 1, 1, 1}, {2, 4, 4, 256}, {3, 33, 70, 7}, {5, 200, 72, 1001}, {8192, 4096, 4096, 1}, {1, 8192, 8192, 1},
                   {32, 64, 64, 65536}, {16, 65536, 3, 1}, {2, 31, 129, 2}, {700, 96, 40, 1}, {1, 64, 512, 1L << 31},
-                  {2147483647, 32, 64, 1}, {1 << 20, 17, 5, 2047}};
+                  {2147483647, 32, 64, 1}, {1 << 20, 17, 5, 2047},
+                  {3, 1100, 70, 1}, {1, 4001, 300, 1}, {20, 1024, 31, 1}, {2, 1056, 16, 33}};
   for (const X &c : xx)
     for (fno_dtype_t dt : dts) run_mx4(c.B, c.I, c.O, c.P, dt);
   const long reports = check_reports();

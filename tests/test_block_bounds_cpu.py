@@ -34,3 +34,26 @@ def test_small_groups_are_read_inside_the_field(shape):
         for last in (0, 1):
             out = _trace(f"gnorm {d} {B} {C} {P} {G} {last}")
             assert "fno_gnorm_small" in out
+
+
+# channels last and groups past a team's registers: rows that end inside 16 bytes, up to the field's end
+COLUMNS = [(5, 61, 20000, 1), (5, 4, 56935, 2), (1, 3, 90001, 1), (1, 2057, 9001, 1), (2, 8191, 65537, 1)]
+
+
+@pytest.mark.parametrize("shape", COLUMNS, ids=str)
+def test_large_groups_are_read_inside_the_field(shape):
+    B, C, P, G = shape
+    for d in range(3):
+        out = _trace(f"gnorm {d} {B} {C} {P} {G} 1", f"gnorm {d} {B} {C} {P} {G} 0")
+        assert "fno_gnorm_cols" in out and "fno_gnorm_rows" in out
+
+
+@pytest.mark.parametrize("shape", [(3, 7, 33), (15, 189, 2622), (2000, 3, 3), (1, 37, 5000), (7, 130, 9), (1, 1, 1)], ids=str)
+def test_dropout_reads_inside_the_field(shape):
+    _trace(*(f"drop {d} {' '.join(map(str, shape))}" for d in range(3)))
+
+
+@pytest.mark.parametrize("shape", [(1, 8192, 8192, 1), (3, 1100, 70, 1), (1, 4001, 300, 1), (20, 1024, 31, 1), (2, 1056, 16, 33)], ids=str)
+def test_few_rows_are_read_inside_their_operands(shape):
+    out = _trace(*(f"mx4 {d} {' '.join(map(str, shape))}" for d in range(3)))
+    assert "fno_mx4_mix_few" in out
