@@ -361,7 +361,7 @@ int main(int argc, char **argv) {
   const G gg[] = {{2, 4, 256, 2}, {1, 1, 1, 1}, {1, 1, 2, 1}, {5, 64, 1, 8}, {3, 6, 2, 3}, {2, 48, 33, 3}, {1, 61, 97, 1}, {32, 64, 9, 16},
                   {3, 33, 1, 3}, {9, 257, 1, 1}, {1, 96, 1000, 3}, {2, 48, 3721, 3}, {1, 3, 70000, 1}, {2, 512, 300, 1}, {1, 4096, 20, 2}, {300, 40, 1, 5},
                   {1, 8192, 1, 1}, {2, 8192, 9, 4}, {20, 64, 65536, 8}, {16, 128, 16384, 32}, {8192, 1024, 1, 16},
-                  {1, 8192, fno::kGnMaxPixels, 1}, {3, 5, fno::kGnMaxPixels - 3, 5}, {1 << 30, 4, 3, 1}, {1 << 28, 8, 511, 4},
+                  {1, 8192, fno::kGnMaxPixels, 1}, {3, 5, fno::kGnMaxPixels - 3, 5}, {1 << 30, 4, 3, 1}, {1 << 28, 8, 511, 4}, {1 << 22, 1, 8200, 1}, {1 << 22, 16, 1500, 1},
                   {2, 8191, 65537, 1}, {1000000, 100, 70, 100}, {5, 61, 20000, 1}, {5, 4, 56935, 2}, {1, 3, 90001, 1}, {1, 2057, 9001, 1}, {134217728, 8192, 1, 8}};
   for (const G &c : gg)
     for (fno_dtype_t dt : dts)

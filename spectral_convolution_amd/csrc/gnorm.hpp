@@ -10,7 +10,8 @@
 namespace fno {
 
 constexpr int kThreads = 256;
-constexpr long kMaxGrid = 1L << 22;  // workgroups of a launch: the kernels loop past it
+constexpr long kMaxGrid = 1L << 22;      // workgroups of a launch: the kernels loop past it
+constexpr long kMaxLaunch = 1L << 31;    // threads of it: the runtime takes fewer than 2^32
 
 inline int gn_vec(int dtype) { return dtype == DT_F32 ? 4 : 8; }
 inline long up(long a, long b) { return (a + b - 1) / b; }

@@ -740,7 +740,7 @@ inline void gn_attach(GnArgs &a, const GnPlan &p, void *workspace, bool runs) {
 }
 
 inline hipError_t gn_run(const void *k, long gx, long gy, int threads, void **args, hipStream_t s) {
-  return hipLaunchKernel(k, dim3((unsigned)std::min(gx, kMaxGrid), (unsigned)gy), dim3((unsigned)threads), args, 0, s);
+  return hipLaunchKernel(k, dim3((unsigned)std::min({gx, kMaxGrid, kMaxLaunch / threads}), (unsigned)gy), dim3((unsigned)threads), args, 0, s);
 }
 
 template <int DT, bool LAST, bool BWD>

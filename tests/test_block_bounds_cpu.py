@@ -57,3 +57,12 @@ def test_dropout_reads_inside_the_field(shape):
 def test_few_rows_are_read_inside_their_operands(shape):
     out = _trace(*(f"mx4 {d} {' '.join(map(str, shape))}" for d in range(3)))
     assert "fno_mx4_mix_few" in out
+
+
+@pytest.mark.parametrize("shape", [(1 << 22, 1, 8200, 1), (1 << 21, 6, 4100, 2), (1 << 22, 16, 1500, 1)], ids=str)
+def test_millions_of_groups_of_1024_threads(shape):
+    """A launch takes fewer than 2^32 threads, whatever the number of groups."""
+    B, C, P, G = shape
+    for d in (1, 2):
+        out = _trace(f"gnorm {d} {B} {C} {P} {G} 0", f"gnorm {d} {B} {C} {P} {G} 1")
+        assert "fno_gnorm_small" in out
