@@ -56,8 +56,7 @@ GnPlan gn_plan(const GnArgs &a, int dtype) {
   }
   const long cpr = up(a.C, V), lanes = std::max(1L, (long)kThreads / std::min(cpr, (long)kThreads));
   const long blocks = up(cpr, kThreads), most = std::max(1L, kParts / bc);
-  // a lane sums at most 256 rows: 2000 squares of fp16 values, whose ties are many, are off by 13 half steps on average
-  const long S = std::min({std::max(up(kLastUnits, a.B * blocks), up(a.P, 256 * lanes)), up(a.P, 4 * lanes), most});
+  const long S = std::min({up(kLastUnits, a.B * blocks), up(a.P, 4 * lanes), most});
   p.per = up(a.P, S);
   p.S = (int)up(a.P, p.per);
   const long all = a.B * a.P;

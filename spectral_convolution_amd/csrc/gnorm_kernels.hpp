@@ -422,7 +422,10 @@ __global__ __launch_bounds__(kThreads) void fno_gnorm_rows(GnArgs a) {
 
 // A lane has a chunk of V channels and every PL-th of a unit's rows; 256 chunks of channels
 // a workgroup (blockIdx.y). A unit is `per` rows: a piece of a sample, or with
-// RUNS rows of any samples (the parameters' sums of small groups).
+// RUNS rows of any samples (the parameters' sums of small groups). A lane sums kStretch rows at a time and joins
+// what they come to: where values' squares share their last digits every addition to a long sum rounds the same way
+// (2000 squares of fp16 values: 13 half steps off on average).
+constexpr int kStretch = 256;
 template <int DT, bool BWD, bool OUT, bool RUNS>
 __global__ __launch_bounds__(kThreads) void fno_gnorm_cols(GnArgs a) {
   constexpr int V = ck_vec<DT>(), AHEAD = BWD || OUT ? 2 : 4;
@@ -454,6 +457,7 @@ __global__ __launch_bounds__(kThreads) void fno_gnorm_cols(GnArgs a) {
     }
     // z = (x - mean) rw + bias; gx = rw gz + c1 + (x - mean) c2
     float mean[V], r[V], rw[V], c1[V], c2[V], s1[V], s2[V], shift[V], count = 0.f;
+    float joined = 0.f;  // values in the stretches that red and cnt hold already
     auto stats = [&](long sample) {
 #pragma unroll
       for (int e = 0; e < V; ++e) {
@@ -512,56 +516,72 @@ __global__ __launch_bounds__(kThreads) void fno_gnorm_cols(GnArgs a) {
         if constexpr (OUT) store_chunk<DT>(BWD ? a.gx : a.y, at, n, ck_raw<DT>(o));
       });
     };
+    // the sums of a stretch into the lane's own places, to those of the stretches before it
+    auto flush = [&](bool more) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        float2 &v = red[(pl * V + e) * kn + kl];
+        float v0 = s1[e], v1 = s2[e];
+        if constexpr (BWD) {
+          if constexpr (!RUNS) v1 *= r[e];
+          if (more) v0 += v.x, v1 += v.y;
+        } else {
+          const float d = count > 0.f ? v0 / count : 0.f;
+          v1 = fmaxf(v1 - v0 * d, 0.f) + (v1 - v1);  // not below 0, NaN where it is NaN
+          v0 = shift[e] + d;
+          if (more) {
+            float na = joined, m = v.x, q = v.y;
+            join_moments(na, m, q, count, v0, v1);
+            v0 = m, v1 = q;
+          }
+        }
+        v = make_float2(v0, v1);
+        s1[e] = s2[e] = 0.f;
+      }
+      joined += count, count = 0.f;
+    };
+    if constexpr (!OUT) __syncthreads();  // the last unit's sums have been read
     if (lane) {
       if constexpr ((BWD || OUT) && !RUNS) stats(b);
       long seen = -1;
       long row = r0 + pl;
       // 16 bytes also where fewer of their values count, up to the rows at whose end the field ends
-      const long safe = n == V ? r1 : all * a.C < V + c0 ? 0 : min(r1, (all * a.C - V - c0) / a.C + 1);
-      for (; row + (AHEAD - 1) * PL < safe; row += AHEAD * PL) {
-        ck_u32x4 x[AHEAD], g[AHEAD];
+      const long within = n == V ? r1 : all * a.C < V + c0 ? 0 : min(r1, (all * a.C - V - c0) / a.C + 1);
+      for (long from = r0; from < r1; from += (long)kStretch * PL) {
+        const long to = OUT ? r1 : min(r1, from + (long)kStretch * PL), safe = min(to, within);
+        for (; row + (AHEAD - 1) * PL < safe; row += AHEAD * PL) {
+          ck_u32x4 x[AHEAD], g[AHEAD];
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) x[i] = load(a.x, (size_t)(row + i * PL) * a.C + c0);
+          for (int i = 0; i < AHEAD; ++i) x[i] = load(a.x, (size_t)(row + i * PL) * a.C + c0);
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) g[i] = BWD ? load(a.gy, (size_t)(row + i * PL) * a.C + c0) : none;
+          for (int i = 0; i < AHEAD; ++i) g[i] = BWD ? load(a.gy, (size_t)(row + i * PL) * a.C + c0) : none;
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
+          for (int i = 0; i < AHEAD; ++i) {
+            if constexpr (RUNS) {
+              b = a.P == 1 ? row + i * PL : (row + i * PL) / a.P;
+              if (b != seen) stats(b);
+              seen = b;
+            }
+            chunk(x[i], g[i], row + i * PL);
+          }
+        }
+        for (; row < to; row += PL) {
+          const ck_u32x4 x = ck_load<DT>(a.x, (size_t)row * a.C + c0, n);
+          const ck_u32x4 g = BWD ? ck_load<DT>(a.gy, (size_t)row * a.C + c0, n) : none;
           if constexpr (RUNS) {
-            b = a.P == 1 ? row + i * PL : (row + i * PL) / a.P;
+            b = a.P == 1 ? row : row / a.P;
             if (b != seen) stats(b);
             seen = b;
           }
-          chunk(x[i], g[i], row + i * PL);
+          chunk(x, g, row);
         }
-      }
-      for (; row < r1; row += PL) {
-        const ck_u32x4 x = ck_load<DT>(a.x, (size_t)row * a.C + c0, n);
-        const ck_u32x4 g = BWD ? ck_load<DT>(a.gy, (size_t)row * a.C + c0, n) : none;
-        if constexpr (RUNS) {
-          b = a.P == 1 ? row : row / a.P;
-          if (b != seen) stats(b);
-          seen = b;
-        }
-        chunk(x, g, row);
+        if constexpr (OUT) break;
+        flush(from > r0);
       }
     }
     if constexpr (!OUT) {
-      __syncthreads();  // the last unit's sums have been read
-      if (lane) {
-        if constexpr (!BWD) cnt[threadIdx.x] = count;
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          float v0 = s1[e], v1 = s2[e];
-          if constexpr (!BWD) {
-            const float d = count > 0.f ? v0 / count : 0.f;
-            v1 = fmaxf(v1 - v0 * d, 0.f) + (v1 - v1);
-            v0 = shift[e] + d;
-          } else if constexpr (!RUNS) {
-            v1 *= r[e];
-          }
-          red[(pl * V + e) * kn + kl] = make_float2(v0, v1);
-        }
-      }
+      if constexpr (!BWD)
+        if (lane) cnt[threadIdx.x] = joined;
       __syncthreads();
       int left = PL;  // lanes' sums of a channel: halved until one thread's turn through them is short
       while (left > 16) {
