@@ -8,9 +8,10 @@
 //   s1[b][c] = sum gz,  s2[b][c] = sum gz x^:
 //   gb = sum_b s1,  gw = sum_b s2,
 //   gx = r (w gz - M1 - x^ M2),  M1 = sum_c w s1 / n,  M2 = sum_c w s2 / n.
-// The mask of D is computed again. Statistics and sums are fp32: squares are summed about a value
-// from among those summed, and partial moments joined by Chan's formula, so that neither a large mean nor
-// an outlier costs digits. No atomics: results repeat bit for bit.
+// The mask of D is computed again. Statistics and sums are fp32. A group that is read once has its mean corrected by its values'
+// deviations from it, so the mean is off by half a step; pieces of a larger one have their squares summed about a value from among
+// those summed, which an outlier or a large mean does not cost digits, and are joined by Chan's formula, where each join
+// moves the mean by up to half a step. No atomics: results repeat bit for bit.
 //
 // A group that fits a workgroup's registers is read once (fno_gnorm_small). Of larger ones a first
 // kernel leaves the moments (forward) or s1, s2 (backward) of every channel's pieces, a small one joins

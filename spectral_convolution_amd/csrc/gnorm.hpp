@@ -114,6 +114,22 @@ __device__ __forceinline__ float team_sum(float v, float *red) {
   }
 }
 
+// the same of two at once
+template <int T>
+__device__ __forceinline__ float2 team_sums(float2 v, float (*red)[16]) {
+  v = make_float2(lane_sum<(T < 64 ? T : 64)>(v.x), lane_sum<(T < 64 ? T : 64)>(v.y));
+  if constexpr (T > 64) {
+    const int wave = threadIdx.x >> 6;
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) red[0][wave] = v.x, red[1][wave] = v.y;
+    __syncthreads();
+    v = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < T / 64; ++i) v.x += red[0][i], v.y += red[1][i];
+  }
+  return v;
+}
+
 // V consecutive parameters p[i] .. as fp32, `none` where there is no p or i + e >= n
 template <int DT>
 __device__ __forceinline__ void param_piece(const void *p, size_t i, long n, float none, float *o) {

@@ -66,3 +66,12 @@ def test_millions_of_groups_of_1024_threads(shape):
     for d in (1, 2):
         out = _trace(f"gnorm {d} {B} {C} {P} {G} 0", f"gnorm {d} {B} {C} {P} {G} 1")
         assert "fno_gnorm_small" in out
+
+
+def test_groups_that_a_team_holds():
+    """The shapes of the tests of levels far from zero are held by a team, or are not, as those tests take it."""
+    import test_gpu_group_norm_levels as levels
+    for shapes, held in ((levels.HELD, True), (levels.SPLIT, False)):
+        for B, C, P, G in shapes:
+            for last in (0, 1):
+                assert ("fno_gnorm_small" in _trace(f"gnorm 0 {B} {C} {P} {G} {last}")) == held, (B, C, P, G, last)
