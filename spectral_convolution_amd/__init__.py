@@ -304,6 +304,8 @@ def fno_weights_unpack(plan, layout, w, re, im, stream=None):
 def _autograd_function():
     import torch
 
+    from ._capture import check_backward
+
     class SpectralConvFunction(torch.autograd.Function):
         """The layer as a PyTorch autograd Function on split weights, the
         integration the TurboFNO write-up describes (section 4.3): forward
@@ -335,6 +337,7 @@ def _autograd_function():
         def backward(ctx, grad_y):
             # first derivatives only: a second backward raises instead of
             # silently returning no higher-order terms
+            check_backward(ctx, grad_y)
             kept, w = ctx.saved_tensors
             plan = ctx.plan
             need_x, need_re, need_im = ctx.needs_input_grad[:3]

@@ -7,18 +7,8 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _block_ops as ops
+from ._capture import check_backward
 from ._training_autograd import _dense
-
-
-def _check_capture(*inputs):
-    """Refuse a call that is captured into a graph while an autograd graph made before, on another stream, still
-    holds one of its leaves: the captured backward would wait for that stream, and the capture's end would
-    end the process."""
-    if inputs[0].is_cuda and torch.is_grad_enabled() and torch.cuda.is_current_stream_capturing():
-        ops.base._t()
-        if ops.base._native.elsewhere(*inputs):
-            raise RuntimeError("a leaf of this call belongs to an autograd graph that lives on another stream: drop "
-                               "that graph (its outputs) before capturing a backward of the same leaves")
 
 
 class GroupNormFunction(torch.autograd.Function):
@@ -41,6 +31,7 @@ class GroupNormFunction(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, gy):
+        check_backward(ctx, gy)
         x, weight, bias, stats = ctx.saved_tensors
         need = ctx.needs_input_grad
         groups, eps, act, last = ctx.spec
@@ -70,6 +61,7 @@ class DropoutResidualFunction(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, gy):
+        check_backward(ctx, gy)
         gv = None
         if ctx.needs_input_grad[0]:
             g = _dense(gy)

@@ -241,13 +241,15 @@ def channel_mix_mx4(x, weight, bias=None, add=None, act=0):
 def group_norm(x, params, dropout=None):
     """D(act(group norm of x)), differentiable in x, params.weight and params.bias; x and
     the groups' statistics are kept for the backward, no mask is."""
-    from ._block_autograd import GroupNormFunction, _check_capture
-    _check_capture(x, params.weight, params.bias)
+    from ._block_autograd import GroupNormFunction
+    from ._capture import check_call
+    check_call(x, params.weight, params.bias)
     return GroupNormFunction.apply(x, params.weight, params.bias, params, dropout)
 
 
 def dropout_residual(v, dropout, x=None, channels_last=False):
     """x + D(v) (x None: D(v)), differentiable in both; nothing is kept for the backward."""
-    from ._block_autograd import DropoutResidualFunction, _check_capture
-    _check_capture(v, x)
+    from ._block_autograd import DropoutResidualFunction
+    from ._capture import check_call
+    check_call(v, x)
     return DropoutResidualFunction.apply(v, x, dropout, channels_last)

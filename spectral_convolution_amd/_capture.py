@@ -1,0 +1,32 @@
+"""Captured graphs and autograd. A leaf's gradient accumulator belongs to the stream that was current when the first
+autograd graph holding the leaf was made, and lives as long as something keeps it: that graph (its outputs), a hook on it.
+A backward that is captured on another stream would wait for that one, which is not captured, and the end of the capture would
+end the process; these checks raise an error before."""
+
+import torch
+
+from . import _training as ops
+
+
+def _raise():
+    raise RuntimeError("a leaf of this call belongs to an autograd graph that lives on another stream: drop "
+                       "that graph (its outputs, and hooks on the leaf's gradient accumulator) before capturing a backward of "
+                       "the same leaves, or run it on the stream that captures")
+
+
+def check_call(*inputs):
+    """Refuse a captured call of leaves that belong elsewhere, at the call. A captured forward whose
+    backward is not wanted runs under torch.no_grad()."""
+    if inputs[0].is_cuda and torch.is_grad_enabled() and torch.cuda.is_current_stream_capturing():
+        ops._t()
+        if ops._native.elsewhere(*inputs):
+            _raise()
+
+
+def check_backward(ctx, grad):
+    """Refuse, from inside a captured backward, to pass gradients on to leaves that belong elsewhere."""
+    if grad is not None and grad.is_cuda and torch.cuda.is_current_stream_capturing():
+        ops._t()
+        leaves = [node.variable for node, _ in ctx.next_functions if hasattr(node, "variable")]
+        if ops._native.elsewhere(*leaves):
+            _raise()

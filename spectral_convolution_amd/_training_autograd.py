@@ -7,6 +7,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _training as ops
+from ._capture import check_backward
 
 
 def _dense(t):
@@ -37,6 +38,7 @@ class ChannelMixFunction(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, gy):
+        check_backward(ctx, gy)
         saved, A, bias = ctx.saved_tensors
         need = ctx.needs_input_grad
         if not any(need[:4]):
@@ -79,6 +81,7 @@ class NormResidualFunction(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, gy, gu):
+        check_backward(ctx, gu if gy is None else gy)
         none = (None,) * 6
         saved = ctx.saved_tensors
         kept, prm = saved[:ctx.n_kept], saved[ctx.n_kept:]
