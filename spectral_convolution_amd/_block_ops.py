@@ -240,7 +240,8 @@ def channel_mix_mx4(x, weight, bias=None, add=None, act=0):
 
 def group_norm(x, params, dropout=None):
     """D(act(group norm of x)), differentiable in x, params.weight and params.bias; x and
-    the groups' statistics are kept for the backward, no mask is."""
+    the groups' statistics are kept for the backward, no mask is. A call captured into a graph
+    whose leaves an autograd graph on another stream holds is refused; under torch.no_grad() it is not."""
     from ._block_autograd import GroupNormFunction
     from ._capture import check_call
     check_call(x, params.weight, params.bias)
@@ -248,7 +249,8 @@ def group_norm(x, params, dropout=None):
 
 
 def dropout_residual(v, dropout, x=None, channels_last=False):
-    """x + D(v) (x None: D(v)), differentiable in both; nothing is kept for the backward."""
+    """x + D(v) (x None: D(v)), differentiable in both; nothing is kept for the backward.
+    Captured calls: as group_norm."""
     from ._block_autograd import DropoutResidualFunction
     from ._capture import check_call
     check_call(v, x)

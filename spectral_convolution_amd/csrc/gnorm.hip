@@ -16,9 +16,9 @@
 // A group that fits a workgroup's registers is read once (fno_gnorm_small). Of larger ones a first
 // kernel leaves the moments (forward) or s1, s2 (backward) of every channel's pieces, a small one joins
 // them, a third reads the field again. A backward of small groups still needs s1, s2 for the
-// parameters, summed over runs of whole rows. Bound by memory and by the vector units alike: 20 x 64 x 256^2 fp16 with GELU
-// 35 us (the moments, 4.8 TB/s), 76 (values, 4.4), 83 (sums, 4.0), 95 (gx, 5.3), vector issue 94 to 98 % in the middle two;
-// 4 x 64^3 x 32 fp32, channels last, dropout: 29, 57, 58 and 72 (5.6 TB/s).
+// parameters, summed over runs of whole rows. Bound by memory and by the vector units alike: a step of 20 x 64 x 256^2 fp16 with
+// GELU takes 254 us, its kernels at their fastest 33 (the moments, 5.1 TB/s), 66 (values, 5.1), 73 (sums, 4.6) and 90 (gx, 5.6), vector
+// issue 94 and 97 % in the middle two; of 4 x 64^3 x 32 fp32, channels last, dropout, 215 us: 28, 54, 56 and 70 (5.8 TB/s).
 
 #include <algorithm>
 

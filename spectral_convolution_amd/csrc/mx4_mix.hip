@@ -3,8 +3,10 @@
 // on the scaled matrix instructions v_mfma_scale_f32_16x16x128_f8f6f4, which take the blocks' powers of two with
 // the codes: lane l has row l % 16 and block l / 16 of four, 16 bytes of codes and one scale byte of either operand.
 // Products of codes are exact, sums are fp32 (a product of 128 off by up to 4e-8 of its terms' sizes, measured).
-// 8192 x 4096 x 4096 bf16 with GELU: 93 us, 2.96 PFLOP/s; the instruction alone runs at 6.6 on random codes, at 8 to 9 on
-// constant ones: what bounds it most is power (zeros instead of random codes: 71 us). One token, 8192 x 8192: 10 us
+// 8192 x 4096 x 4096 bf16 with GELU: 96 us, 2.9 PFLOP/s; the instruction alone runs at 6.6 on random codes, at 8 to 9 on
+// constant ones. On zeros it takes 71 to 79 us, again less than half of the instruction's rate, so power is not what bounds it: a step of
+// 64 of a 256^2 tile's sum reads 48 KB of LDS and fills 16, 512 clocks at 128 bytes, as long as its matrix instructions
+// take, and the tile's GELU runs behind the last of them. One token, 8192 x 8192: 10 us
 // for 36 MB. 32 x 64 x 64 x 256^2 fp16, GELU and addition: 203 us, 3 TB/s, bound by GELU behind one step of products.
 //
 // The rows that are neighbours in y are the instruction's first operand (pixels of a field, output
