@@ -126,9 +126,10 @@ __global__ __launch_bounds__(T > kThreads ? T : kThreads) void fno_gnorm_small(G
         s.y = fmaf(d, d, s.y);
       });
       dev = team_sums<T>(dev, red);
-      const float off = dev.x / n, var = dev.y / n - off * off;
+      const float off = dev.x / n, off2 = off * off, var = dev.y / n;
       mean += off;
-      r = rsq((var < 0.f ? 0.f : var) + a.eps);  // NaN stays NaN
+      // less the correction's square, not below 0; what overflowed stays infinite, a NaN stays one
+      r = rsq((off2 < var ? var - off2 : var < __builtin_inff() ? 0.f : var) + a.eps);
       fresh<DT>(rx);
       if (a.stats && there && t == 0) a.stats[gid] = make_float2(mean, r);
     } else {

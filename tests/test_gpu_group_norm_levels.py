@@ -55,3 +55,15 @@ def test_small_deviations(shape, level, spread, last):
     size = abs(ry - per(b[1])) + abs(per(b[1]))
     bound = of(m_off * r) * abs(per(w[1])) + CHAIN * size + half_step("f32") * abs(ry)
     assert (abs(f64(y) - ry) <= bound).all()
+
+
+@pytest.mark.parametrize("last", [False, True])
+@pytest.mark.parametrize("shape", HELD, ids=str)
+def test_constant_groups_whose_squares_overflow(shape, last):
+    """At 1e30 a step of the level squared is past fp32: y is the bias all the same."""
+    B, C, P, G = shape
+    rng = np.random.default_rng(3)
+    x = torch.full((B, P, C) if last else (B, C, P), 1.1e30)
+    w, b, gy = stored(rng, (C,), "f32"), stored(rng, (C,), "f32"), stored(rng, tuple(x.shape), "f32")
+    y, *_ = run("f32", B, C, P, G, last, 0, None, dict(x=(x, None), gy=gy, w=w, b=b))
+    assert (y == b[0].to(y.device).view((1, 1, C) if last else (1, C, 1))).all()
