@@ -15,9 +15,10 @@
 //
 //   elsewhere(t, t, ...)
 //
-// Whether one of the tensors (or None) is a leaf whose gradient accumulator lives, in an autograd graph made
-// before, and belongs to another stream than the device's current one. A backward captured into a
-// graph would wait for that stream, which is not captured, and the end of the capture ends the process.
+// For each of the tensors (or None) that is a leaf whose gradient accumulator lives, in an autograd graph made
+// before, and belongs to another stream than the device's current one, that stream as (id, device index, device type), in a
+// list. A backward captured into a graph would wait for it; where it is not captured itself, the end of the capture
+// ends the process.
 
 #include <c10/core/impl/VirtualGuardImpl.h>
 #include <torch/csrc/autograd/function.h>
@@ -86,6 +87,8 @@ PyObject *buffer(PyObject *, PyObject *const *args, Py_ssize_t n) {
 }
 
 PyObject *elsewhere(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  std::unique_ptr<PyObject, Release> out(PyList_New(0));
+  if (!out) return nullptr;
   try {
     for (Py_ssize_t i = 0; i < n; ++i) {
       if (!THPVariable_Check(args[i])) continue;
@@ -94,9 +97,12 @@ PyObject *elsewhere(PyObject *, PyObject *const *args, Py_ssize_t n) {
       const auto node = torch::autograd::impl::try_get_grad_accumulator(t);
       if (!node) continue;
       const auto its = node->stream();
-      if (its && *its != c10::impl::VirtualGuardImpl(t.device().type()).getStream(t.device())) Py_RETURN_TRUE;
+      if (!its || *its == c10::impl::VirtualGuardImpl(t.device().type()).getStream(t.device())) continue;
+      const c10::StreamData3 s = its->pack3();
+      std::unique_ptr<PyObject, Release> one(Py_BuildValue("(Lii)", (long long)s.stream_id, (int)s.device_index, (int)s.device_type));
+      if (!one || PyList_Append(out.get(), one.get()) < 0) return nullptr;
     }
-    Py_RETURN_FALSE;
+    return out.release();
   } catch (const std::exception &e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
     return nullptr;

@@ -22,11 +22,14 @@ class Pass(torch.autograd.Function):
         return gy, gy, gy
 
 
+ELSEWHERE = ((0, 0, 1),)  # the default stream
+
+
 def _backward(monkeypatch, capturing, elsewhere):
     seen = []
     _training._t()
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing)
-    monkeypatch.setattr(_training, "_native", SimpleNamespace(elsewhere=lambda *t: seen.extend(t) or elsewhere))
+    monkeypatch.setattr(_training, "_native", SimpleNamespace(elsewhere=lambda *t: seen.extend(t) or list(elsewhere)))
     a, b = torch.ones(3, requires_grad=True), torch.ones(3, requires_grad=True)
     got = torch.autograd.grad(Pass.apply(a, 2 * b, torch.ones(3)).sum(), (a, b))
     assert all((g == k).all() for g, k in zip(got, (1, 2)))
@@ -34,14 +37,29 @@ def _backward(monkeypatch, capturing, elsewhere):
 
 
 def test_leaves_are_looked_at_in_a_capture(monkeypatch):
-    seen, a = _backward(monkeypatch, True, False)
+    seen, a = _backward(monkeypatch, True, ())
     assert len(seen) == 1 and seen[0] is a  # not what was computed from b, not the constant
-    assert _backward(monkeypatch, False, True)[0] == []
+    assert _backward(monkeypatch, False, ELSEWHERE)[0] == []
 
 
 def test_leaves_elsewhere_are_refused(monkeypatch):
     with pytest.raises(RuntimeError, match="belongs to an autograd graph"):
-        _backward(monkeypatch, True, True)
+        _backward(monkeypatch, True, ELSEWHERE)
+
+
+def test_streams_of_the_capture_are_no_reason(monkeypatch):
+    """A stream that has joined the capture is part of it; one that has not is refused, among others too."""
+    monkeypatch.setattr(_capture, "_captured", lambda stream_id, *_: stream_id == 5)
+    _backward(monkeypatch, True, ((5, 0, 1),))
+    with pytest.raises(RuntimeError, match="belongs to an autograd graph"):
+        _backward(monkeypatch, True, ((5, 0, 1), (6, 0, 1)))
+
+
+def test_leaves_of_the_current_stream():
+    _training._t()
+    a = torch.ones(2, requires_grad=True)
+    kept = a * 2
+    assert _training._native.elsewhere(a, None, kept) == []
 
 
 def test_no_gradient(monkeypatch):

@@ -101,3 +101,45 @@ def test_captured_forward_without_gradients(op):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, eager)
+
+
+@pytest.mark.parametrize("op", ["mix", "norm", "group norm", "dropout"])
+def test_streams_that_joined_the_capture(op):
+    """Two calls of the same leaves on two streams of one capture, the accumulators of the first's."""
+    leaves, call, _ = _case(op)
+    first = call()
+    gy, gz = torch.randn_like(first), torch.randn_like(first)
+    del first
+    want = torch.autograd.grad((call(), call()), leaves, (gy, gz))
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=main):
+        y = call()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            z = call()
+        main.wait_stream(side)
+        got = torch.autograd.grad((y, z), leaves, (gy, gz))
+    for _ in range(3):
+        g.replay()
+        torch.cuda.synchronize()
+        for a, r in zip(got, want):
+            # two terms, added in either order
+            assert (a - r).abs().max() <= 2.0 ** -23 * r.abs().max()
+
+
+@pytest.mark.parametrize("op", ["mix", "group norm"])
+def test_another_stream_than_the_default(op):
+    """An eager graph on a stream of its own, which has not joined the capture."""
+    leaves, call, _ = _case(op)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        eager = call()
+    torch.cuda.synchronize()
+    gy = torch.ones_like(eager)
+    torch.cuda.synchronize()
+    with pytest.raises(RuntimeError, match="belongs to an autograd graph"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            torch.autograd.grad(call(), leaves, gy)
+    assert torch.isfinite(eager).all()
